@@ -385,13 +385,163 @@ int fp8rl_quant_kv_tensor_noalloc(const uint16_t* KV, int64_t R, int64_t C, int6
                                   uint8_t* KVq, float* scale, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions.  The first R values of every head are R/2 pairs (x1, x2):
+ * (i, i + R/2), or (2i, 2i + 1) with FP8RL_ROPE_INTERLEAVED.  With c, s the
+ * table's cosine and sine at the token's position,
+ *   y1 = c x1 - s x2,   y2 = s x1 + c x2,
+ * and with FP8RL_ROPE_INVERSE the gradient of that with respect to x (s taken
+ * with the other sign; any magnitude in the table stays).  Values past R are
+ * copied.  Computed in fp32, each product and sum rounded once, and rounded
+ * once to bf16: bit-exact given the table.
+ * X, Y bf16, value d of head h of token t at [t * token + h * head + d]
+ *      (strides in elements, any that are >= 0, so that the heads of a fused
+ *      projection's output can be given in place); 2-byte aligned.  Y may be X
+ *      with the same strides; any other overlap is undefined.
+ * positions int32 [T].  One outside [0, max_pos) is taken as the nearest valid
+ *      one and recorded (fp8rl_check_device_error: FP8RL_ERR_DEVICE).
+ * table fp32 [max_pos][R]: R/2 cosines, then R/2 sines (fp8rl_rope_table).
+ * R even, 0 <= R <= D.  Fastest where D % 8 == 0, R % 16 == 0 (interleaved:
+ * R % 8 == 0), pointers are 16-byte aligned and strides multiples of 8.
+ * Limits: T < 2^31, H * D <= 2^24.  T == 0 launches nothing.
+ * ---------------------------------------------------------------------- */
+#define FP8RL_ROPE_INTERLEAVED 1u
+#define FP8RL_ROPE_INVERSE 2u
+int fp8rl_rope(const uint16_t* X, int64_t T, int64_t H, int64_t D, int64_t x_token, int64_t x_head,
+               const int32_t* positions, const float* table, int64_t max_pos, int64_t R, unsigned flags,
+               uint16_t* Y, int64_t y_token, int64_t y_head, void* stream);
+
+/* The table of fp8rl_rope: table[p][i] = magnitude * cos(p * freq[i]),
+ * table[p][R/2 + i] = magnitude * sin(p * freq[i]), in fp64 and rounded once.
+ * freq: fp64 [R/2] in DEVICE memory, radians a position; a scaled context is in
+ * the frequencies and the magnitude.  table fp32 [max_pos][R].  Made once a model. */
+int fp8rl_rope_table(const double* freq, int64_t max_pos, int64_t R, double magnitude, float* table,
+                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged key-value cache: num_pages pages of page_size tokens of kv_heads
+ * heads of head_dim values, keys in K and values in V with the same strides
+ * (elements): value d of head h of token r of page g is at
+ *   [g * page_stride + r * token_stride + h * head_stride + d],
+ * so pages may be laid out token by token or head by head, and K and V may be
+ * halves of one pool.  dtype FP8RL_KV_BF16: bf16 values (scales unused);
+ * FP8RL_KV_E4M3: codes c of the values c * *k_scale and c * *v_scale, one fp32
+ * > 0 each in device memory, as fp8rl_quant_kv_tensor writes them (FP8-RL,
+ * Abstract, contribution (ii): FP8 KV-cache).
+ * head_dim a multiple of 16 up to 256; K and V 16-byte aligned and every stride
+ * a multiple of 16 bytes.  Limits: page_size <= 2^20, kv_heads <= 65535.
+ * The struct is read during the call (host memory).
+ * ---------------------------------------------------------------------- */
+#define FP8RL_KV_BF16 0
+#define FP8RL_KV_E4M3 1
+typedef struct {
+    void *K, *V;
+    const float *k_scale, *v_scale;
+    int64_t num_pages, page_size, kv_heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    int32_t dtype;
+} fp8rl_paged_kv;
+
+/* ------------------------------------------------------------------------
+ * One step's queries, keys and values into place: q rotated to q_out, k rotated
+ * and stored, v stored.  Rotation as in fp8rl_rope (R = 0: none); a stored value
+ * is bf16_rn(x) or E4M3FN_rn_satfinite(fl32(x / scale)) of the fp32 x (a rotated
+ * key is rounded once, not through bf16).  Bit-exact.
+ * q bf16 [T][Hq][head_dim], k and v bf16 [T][kv_heads][head_dim], token and head
+ *   strides in elements; 2-byte aligned (fast path as in fp8rl_rope).  Hq may
+ *   be 0 (q, q_out unused).  q_out may be q with the same strides; q, k, v must
+ *   not overlap the cache.
+ * slots int64 [T]: slot page * page_size + row of each token; a negative one is
+ *   not stored (its query is still rotated), one past the pool is not stored
+ *   and recorded (FP8RL_ERR_DEVICE).  Which of two equal slots stays is
+ *   undefined.
+ * flags: FP8RL_ROPE_INTERLEAVED.  Limits: T < 2^31, (Hq + 2 kv_heads) * head_dim
+ * <= 2^24.
+ * ---------------------------------------------------------------------- */
+int fp8rl_rope_append_paged(const uint16_t* q, int64_t Hq, int64_t q_token, int64_t q_head,
+                            const uint16_t* k, int64_t k_token, int64_t k_head, const uint16_t* v,
+                            int64_t v_token, int64_t v_head, int64_t T, const int32_t* positions,
+                            const float* table, int64_t max_pos, int64_t R, unsigned flags,
+                            uint16_t* q_out, int64_t qo_token, int64_t qo_head,
+                            const fp8rl_paged_kv* cache, const int64_t* slots, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of the Lq newest tokens of each of B sequences over the paged cache
+ * (which holds them already).  Sequence b has len = seq_lens[b] cached tokens,
+ * token j in row j % page_size of page block_table[b][j / page_size]; query i
+ * stands at position p = len - Lq + i and sees the tokens j <= p, with a window
+ * W > 0 those with j > p - W.  Query head h reads kv head h / (Hq / kv_heads):
+ *   o = sum_j softmax_j(scale q.k_j) v_j,   lse = log sum_j exp(scale q.k_j).
+ * A query that sees nothing (len 0, or i < Lq - len) gets o = 0, lse = -inf.
+ * Rows of the cache that no query of the sequence sees are never read into a
+ * result, whatever they hold.
+ * Scores, maxima, sums and o are held in fp32, o rounded once to bf16.  The
+ * probabilities are rounded to the cache's product type (bf16; for E4M3 caches
+ * fp16), relative to the row's running maximum.  Deterministic.
+ * q   bf16 [B][Lq][Hq][head_dim] by strides (elements, multiples of 8), 16-byte
+ *     aligned; Hq a multiple of kv_heads.
+ * block_table int32 [B][table_stride], DEVICE; table_stride >= max_len /
+ *     page_size rounded up (not checked for B == 1).  A page outside
+ *     the pool is taken as page 0 and recorded (FP8RL_ERR_DEVICE).
+ * seq_lens int32 [B], DEVICE; max_len: a host-side bound on them.  A length
+ *     outside [0, max_len] is taken as the nearest valid one and recorded.
+ * o bf16 [B][Lq][Hq][head_dim] contiguous, 16-byte aligned; lse fp32
+ *     [B][Lq][Hq] or NULL.
+ * workspace: at least fp8rl_attn_paged_workspace_bytes bytes, 16-byte aligned,
+ *     no zeroing, nothing kept between calls; calls in flight at once need
+ *     their own.
+ * Limits: max_len <= 2^30, Lq <= 2^20, B * Lq * Hq < 2^31.
+ * ---------------------------------------------------------------------- */
+size_t fp8rl_attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
+                                        int64_t max_len);
+/* Kernels fp8rl_attn_paged launches for these sizes; 0 for B == 0; -FP8RL_ERR_SHAPE for invalid ones. */
+int fp8rl_attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
+                                  int64_t max_len);
+int fp8rl_attn_paged(const uint16_t* q, int64_t B, int64_t Lq, int64_t Hq, int64_t q_seq,
+                     int64_t q_token, int64_t q_head, const fp8rl_paged_kv* cache,
+                     const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens,
+                     int64_t max_len, int64_t window, float scale, uint16_t* o, float* lse_or_null,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Verification of drafted tokens with given random numbers.  Sequence b has
+ * len <= K drafts t_0 .. t_{len-1} (rows q_i of the drafter's probabilities) and
+ * rows p_0 .. p_len of the target's.  Draft i is kept while
+ *   u_i * q_i(t_i) < p_i(t_i)      (compared exactly);
+ * n drafts are kept.  The next token is the winner argmax_v w_v / e_v (one IEEE
+ * fp32 division; equal scores: lowest v; entries with w_v <= 0 take no part, and
+ * without any it is token 0) of
+ *   w = max(p_n - q_n, 0)  for n < len (or p_n, where that has no positive entry),
+ *   w = p_len              for n = len.
+ * With e_v independent Exp(1) that draws v with probability w_v / sum w.
+ * Q == NULL: a drafter that only proposes tokens; q_i is 1 at t_i and 0 elsewhere.
+ * P [B][K+1][V], Q [B][K][V], sequence and step strides in elements, dtype
+ *   FP8RL_PROB_F32 or FP8RL_PROB_BF16 for both, rows contiguous.
+ * drafts int32 [B][K]; one outside [0, V) is refused and recorded
+ *   (FP8RL_ERR_DEVICE).  draft_lens int32 [B] or NULL (all K); one outside
+ *   [0, K] is taken as the nearest valid one and recorded.
+ * u fp32 [B][K]; noise e fp32 [B][V] with its sequence stride.
+ * tokens int32 [B][K+1]: the kept drafts, the new token, then -1.
+ * accepted int32 [B]: n.
+ * Rows past len are never read.  Bit-exact.  Limits: K <= 32, V < 2^31,
+ * B <= 65535.
+ * ---------------------------------------------------------------------- */
+#define FP8RL_PROB_F32 0
+#define FP8RL_PROB_BF16 1
+int fp8rl_spec_verify(const void* P, int64_t p_seq, int64_t p_step, const void* Q_or_null, int64_t q_seq,
+                      int64_t q_step, int dtype, const int32_t* drafts,
+                      const int32_t* draft_lens_or_null, const float* u, const float* noise,
+                      int64_t noise_seq, int64_t B, int64_t K, int64_t V, int32_t* tokens,
+                      int32_t* accepted, void* stream);
+
+/* ------------------------------------------------------------------------
  * Every wait inside the library's kernels (on an mbarrier filled by TMA or by
  * the tensor core) is bounded.  A wait that runs out records a code in a
  * device-side word, abandons the tile and lets the kernel exit, so the CUDA
  * context stays usable.  This call SYNCHRONIZES the current device, reads and
  * clears that word, and returns FP8RL_OK, FP8RL_ERR_TIMEOUT (a wait ran out)
  * or FP8RL_ERR_DEVICE (a device-side check of the data failed: an expert of
- * the grouped GEMM with more tokens than max_tokens_per_expert).  *detail
+ * the grouped GEMM with more tokens than max_tokens_per_expert; a position, slot,
+ * page, length or draft out of range in the rotary, paged and verification calls).  *detail
  * (may be NULL) receives the raw word (0 if none: kernel id in bits 24..31,
  * the site in bits 16..23, 1 = timeout / 2 = data check in bits 0..15).
  * ---------------------------------------------------------------------- */

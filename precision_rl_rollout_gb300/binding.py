@@ -34,7 +34,10 @@ EXPORTS = ("fp8rl_status_string", "fp8rl_abi_version", "fp8rl_quant_weight_block
            "fp8rl_gemm_kernel_count", "int8rl_gemm_kernel_count",
            "fp8rl_kv_workspace_bytes", "fp8rl_quant_kv_tensor", "fp8rl_quant_kv_with_scale",
            "fp8rl_quant_kv_tensor_noalloc", "fp8rl_rollout_is_workspace_bytes",
-           "fp8rl_rollout_is_weights", "fp8rl_logits_kl_workspace_bytes", "fp8rl_logits_kl")
+           "fp8rl_rollout_is_weights", "fp8rl_logits_kl_workspace_bytes", "fp8rl_logits_kl",
+           "fp8rl_rope", "fp8rl_rope_table", "fp8rl_rope_append_paged",
+           "fp8rl_attn_paged_workspace_bytes", "fp8rl_attn_paged_kernel_count", "fp8rl_attn_paged",
+           "fp8rl_spec_verify")
 
 
 class Fp8rlError(RuntimeError):
@@ -47,6 +50,13 @@ class Fp8rlError(RuntimeError):
 class FP8RL_WDESC(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("Wq", ctypes.c_void_p), ("Ws", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("ldw", ctypes.c_int64)]
+
+
+class FP8RL_PAGED_KV(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "page_stride",
+                                              "token_stride", "head_stride")] + [("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -107,11 +117,20 @@ def load(path: str | None = None):
         lib.fp8rl_rollout_is_workspace_bytes.restype = Z
         lib.fp8rl_rollout_is_workspace_bytes.argtypes = [I]
         lib.fp8rl_rollout_is_weights.argtypes = [P, P, P, I, ctypes.c_float, ctypes.c_int, P, P, P, Z, S]
+        U, F, D, KV = ctypes.c_uint, ctypes.c_float, ctypes.c_double, ctypes.POINTER(FP8RL_PAGED_KV)
+        lib.fp8rl_rope.argtypes = [P, I, I, I, I, I, P, P, I, I, U, P, I, I, S]
+        lib.fp8rl_rope_table.argtypes = [P, I, I, D, P, S]
+        lib.fp8rl_rope_append_paged.argtypes = [P, I, I, I, P, I, I, P, I, I, I, P, P, I, I, U, P, I, I, KV, P, S]
+        lib.fp8rl_attn_paged_workspace_bytes.restype = Z
+        lib.fp8rl_attn_paged_workspace_bytes.argtypes = [I] * 6
+        lib.fp8rl_attn_paged_kernel_count.argtypes = [I] * 6
+        lib.fp8rl_attn_paged.argtypes = [P, I, I, I, I, I, I, KV, P, I, P, I, I, F, P, P, P, Z, S]
+        lib.fp8rl_spec_verify.argtypes = [P, I, I, P, I, I, ctypes.c_int, P, P, P, P, I, I, I, I, P, P, S]
         for name in EXPORTS:
             if name not in ("fp8rl_status_string", "fp8rl_abi_version", "fp8rl_gemm_workspace_bytes",
                             "int8rl_gemm_workspace_bytes", "fp8rl_kv_workspace_bytes",
                             "fp8rl_rollout_is_workspace_bytes", "fp8rl_linear_workspace_bytes",
-                            "fp8rl_logits_kl_workspace_bytes"):
+                            "fp8rl_logits_kl_workspace_bytes", "fp8rl_attn_paged_workspace_bytes"):
                 getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -459,3 +478,249 @@ def fp8rl_logits_kl(P, Q, kl=None, workspace=None, stream=None):
     _ck(lib.fp8rl_logits_kl(_p(P), ldp, _p(Q), ldq, M, V, _p(kl), _p(workspace), wbytes, _stream(P, stream)),
         "fp8rl_logits_kl")
     return kl
+
+
+# ------------------------------------------------------- rollout step: positions, paged cache, drafts
+# These calls also check what only Python can see (types, shapes, devices); what
+# they allocate while a stream is given is recorded on that stream, so that the
+# caching allocator does not hand it out again before the stream is done with it.
+
+def _is(t, dtype, dim, dev, name):
+    if t.dtype is not dtype or t.dim() != dim or t.device != dev:
+        raise ValueError(f"{name}: expected a {dim}-D {dtype} tensor on {dev}, got {t.dim()}-D {t.dtype} on {t.device}")
+
+
+def _is_full(t, dtype, shape, dev, name):
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} {shape} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _heads(t, dim, dev, name):
+    """bf16, heads of contiguous values."""
+    _is(t, torch.bfloat16, dim, dev, name)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _given(stream, *made):
+    """Outputs and workspaces made for a call on a stream of the caller's."""
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        for t in made:
+            if t is not None:
+                t.record_stream(s)
+
+
+FP8RL_ROPE_INTERLEAVED = 1
+FP8RL_ROPE_INVERSE = 2
+
+
+def fp8rl_rope_table(freq, max_pos: int, magnitude: float = 1.0, table=None, stream=None):
+    """freq fp64 [R/2] (radians a position) -> table fp32 [max_pos, R]: cosines, then sines."""
+    lib = load()
+    dev = _cuda(freq, "freq")
+    _is(freq, torch.float64, 1, dev, "freq")
+    R = 2 * freq.shape[0]
+    made = table is None
+    if made:
+        table = torch.empty((max_pos, R), dtype=torch.float32, device=dev)
+    _is_full(freq, torch.float64, (R // 2,), dev, "freq")
+    _is_full(table, torch.float32, (max_pos, R), dev, "table")
+    _ck(lib.fp8rl_rope_table(_p(freq), max_pos, R, magnitude, _p(table), _stream(freq, stream)), "fp8rl_rope_table")
+    if made:
+        _given(stream, table)
+    return table
+
+
+def fp8rl_rope(X, positions, table, interleaved=False, inverse=False, Y=None, stream=None):
+    """X bf16 [T, H, D] (token and head strides free), positions int32 [T], table fp32
+    [max_pos, R] -> Y bf16 [T, H, D]; inverse=True: the gradient.  Y may be X."""
+    lib = load()
+    dev = _cuda(X, "X")
+    _heads(X, 3, dev, "X")
+    T, H, D = X.shape
+    _is_full(positions, torch.int32, (T,), dev, "positions")
+    _is(table, torch.float32, 2, dev, "table")
+    max_pos, R = table.shape
+    _is_full(table, torch.float32, (max_pos, R), dev, "table")
+    made = Y is None
+    if made:
+        Y = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _heads(Y, 3, dev, "Y")
+        if Y.shape != X.shape:
+            raise ValueError("Y must have X's shape")
+    flags = (FP8RL_ROPE_INTERLEAVED if interleaved else 0) | (FP8RL_ROPE_INVERSE if inverse else 0)
+    _ck(lib.fp8rl_rope(_p(X), T, H, D, X.stride(0), X.stride(1), _p(positions), _p(table), max_pos, R, flags, _p(Y),
+                       Y.stride(0), Y.stride(1), _stream(X, stream)), "fp8rl_rope")
+    if made:
+        _given(stream, Y)
+    return Y
+
+
+FP8RL_KV_BF16 = 0
+FP8RL_KV_E4M3 = 1
+
+
+def _paged_kv(K, V, k_scale, v_scale, dev):
+    """Pools [pages, page_size, kv_heads, head_dim] (a page laid out head by head is
+    the transposed view) -> the C struct."""
+    if K.dtype is torch.uint8:
+        dtype = FP8RL_KV_E4M3
+        _is_full(k_scale, torch.float32, (1,), dev, "k_scale")
+        _is_full(v_scale, torch.float32, (1,), dev, "v_scale")
+    else:
+        dtype = FP8RL_KV_BF16
+        k_scale = v_scale = None
+        _is(K, torch.bfloat16, 4, dev, "K")
+    _is(K, K.dtype, 4, dev, "K")
+    _is(V, K.dtype, 4, dev, "V")
+    st = K.stride()
+    if V.shape != K.shape or V.stride() != st or st[3] != 1:
+        raise ValueError("K and V must have the same shape and strides, and contiguous head values")
+    n, page, heads, D = K.shape
+    return FP8RL_PAGED_KV(K.data_ptr(), V.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                          None if v_scale is None else v_scale.data_ptr(), n, page, heads, D, st[0], st[1], st[2],
+                          dtype)
+
+
+def fp8rl_rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale=None, v_scale=None, interleaved=False,
+                            q_out=None, stream=None):
+    """q bf16 [T, Hq, D], k and v bf16 [T, kv_heads, D] (strides free), slots int64 [T]
+    -> q rotated; k rotated and v stored in the pools K, V [pages, page_size, kv_heads, D]
+    (bf16, or uint8 E4M3 codes under k_scale, v_scale fp32 [1]).  table None: no rotation."""
+    lib = load()
+    dev = _cuda(q, "q")
+    _heads(q, 3, dev, "q")
+    _heads(k, 3, dev, "k")
+    _heads(v, 3, dev, "v")
+    T, Hq, D = q.shape
+    kv = _paged_kv(K, V, k_scale, v_scale, dev)
+    if tuple(k.shape) != (T, kv.kv_heads, D) or k.shape != v.shape or kv.head_dim != D:
+        raise ValueError("k and v must be [T, kv_heads, D] with the cache's heads and q's T and D")
+    _is_full(slots, torch.int64, (T,), dev, "slots")
+    max_pos = R = 0
+    if table is not None:
+        max_pos, R = table.shape
+        _is_full(table, torch.float32, (max_pos, R), dev, "table")
+        _is_full(positions, torch.int32, (T,), dev, "positions")
+    made = q_out is None
+    if made:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _heads(q_out, 3, dev, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    _ck(lib.fp8rl_rope_append_paged(_p(q), Hq, q.stride(0), q.stride(1), _p(k), k.stride(0), k.stride(1), _p(v),
+                                    v.stride(0), v.stride(1), T, None if table is None else _p(positions), _p(table),
+                                    max_pos, R, FP8RL_ROPE_INTERLEAVED if interleaved else 0, _p(q_out),
+                                    q_out.stride(0), q_out.stride(1), kv, _p(slots), _stream(q, stream)),
+        "fp8rl_rope_append_paged")
+    if made:
+        _given(stream, q_out)
+    return q_out
+
+
+def fp8rl_attn_paged_workspace_bytes(B: int, Lq: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    return int(load().fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, Hkv, D, max_len))
+
+
+def fp8rl_attn_paged_kernel_count(B: int, Lq: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    return int(load().fp8rl_attn_paged_kernel_count(B, Lq, Hq, Hkv, D, max_len))
+
+
+def fp8rl_attn_paged(q, K, V, block_table, seq_lens, max_len: int, scale=None, window: int = 0, k_scale=None,
+                     v_scale=None, o=None, lse=None, want_lse=False, workspace=None, stream=None):
+    """q bf16 [B, Lq, Hq, D]: the newest Lq tokens of B sequences, whose keys and values
+    are in the pools K, V [pages, page_size, kv_heads, D] already; block_table int32
+    [B, >= max_len / page_size], seq_lens int32 [B] (at most max_len).  scale: D^-1/2
+    unless given.  -> o bf16 [B, Lq, Hq, D] (and lse fp32 [B, Lq, Hq] when want_lse or
+    lse is given)."""
+    lib = load()
+    dev = _cuda(q, "q")
+    _heads(q, 4, dev, "q")
+    B, Lq, Hq, D = q.shape
+    kv = _paged_kv(K, V, k_scale, v_scale, dev)
+    if kv.head_dim != D:
+        raise ValueError("q and the cache must have the same head width")
+    _is(block_table, torch.int32, 2, dev, "block_table")
+    if block_table.shape[0] != B or block_table.shape[1] * kv.page_size < max_len or \
+            (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table must be [B, columns] with contiguous rows covering max_len tokens")
+    _is_full(seq_lens, torch.int32, (B,), dev, "seq_lens")
+    made_o, made_l = o is None, lse is None and want_lse
+    if made_o:
+        o = torch.empty((B, Lq, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _is_full(o, torch.bfloat16, (B, Lq, Hq, D), dev, "o")
+    if made_l:
+        lse = torch.empty((B, Lq, Hq), dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _is_full(lse, torch.float32, (B, Lq, Hq), dev, "lse")
+    made_w = workspace is None
+    if made_w:
+        need = lib.fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, kv.kv_heads, D, max_len)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = q.stride()
+    _ck(lib.fp8rl_attn_paged(_p(q), B, Lq, Hq, st[0], st[1], st[2], kv, _p(block_table),
+                             max(block_table.stride(0), block_table.shape[1]) if B == 1 else block_table.stride(0),
+                             _p(seq_lens), max_len, window, D ** -0.5 if scale is None else scale, _p(o), _p(lse),
+                             _p(workspace), wbytes, _stream(q, stream)), "fp8rl_attn_paged")
+    if stream is not None:
+        _given(stream, o if made_o else None, lse if made_l else None, workspace if made_w else None)
+    return o if lse is None else (o, lse)
+
+
+FP8RL_PROB_F32 = 0
+FP8RL_PROB_BF16 = 1
+
+
+def fp8rl_spec_verify(P, drafts, u, noise, Q=None, draft_lens=None, tokens=None, accepted=None, stream=None):
+    """P fp32 or bf16 [B, K+1, V] and Q [B, K, V] (None: a drafter without probabilities),
+    drafts int32 [B, K], u fp32 [B, K] in [0, 1), noise fp32 [B, V] of Exp(1) draws,
+    draft_lens int32 [B] (None: K) -> (tokens int32 [B, K+1]: kept drafts, the next
+    token, then -1; accepted int32 [B])."""
+    lib = load()
+    dev = _cuda(P, "P")
+    if P.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("P must be float32 or bfloat16")
+    _is(P, P.dtype, 3, dev, "P")
+    B, K, V = P.shape[0], P.shape[1] - 1, P.shape[2]
+    if (P.stride(2) != 1 and V > 1) or (Q is not None and Q.stride(2) != 1 and V > 1):
+        raise ValueError("rows of P and Q must be contiguous")
+    if Q is not None:
+        _is(Q, P.dtype, 3, dev, "Q")
+        if tuple(Q.shape) != (B, K, V):
+            raise ValueError("Q must be [B, K, V]")
+    _is_full(drafts, torch.int32, (B, K), dev, "drafts")
+    _is_full(u, torch.float32, (B, K), dev, "u")
+    _is(noise, torch.float32, 2, dev, "noise")
+    if tuple(noise.shape) != (B, V) or (noise.stride(1) != 1 and V > 1):
+        raise ValueError("noise must be [B, V] with contiguous rows")
+    if draft_lens is not None:
+        _is_full(draft_lens, torch.int32, (B,), dev, "draft_lens")
+    made_t, made_a = tokens is None, accepted is None
+    if made_t:
+        tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
+    else:
+        _is_full(tokens, torch.int32, (B, K + 1), dev, "tokens")
+    if made_a:
+        accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+    else:
+        _is_full(accepted, torch.int32, (B,), dev, "accepted")
+    qs = (0, 0) if Q is None else (Q.stride(0), Q.stride(1))
+    _ck(lib.fp8rl_spec_verify(_p(P), P.stride(0), P.stride(1), _p(Q), qs[0], qs[1],
+                              FP8RL_PROB_F32 if P.dtype is torch.float32 else FP8RL_PROB_BF16, _p(drafts),
+                              _p(draft_lens), _p(u), _p(noise), noise.stride(0), B, K, V, _p(tokens), _p(accepted),
+                              _stream(P, stream)), "fp8rl_spec_verify")
+    if stream is not None:
+        _given(stream, tokens if made_t else None, accepted if made_a else None)
+    return tokens, accepted

@@ -46,6 +46,36 @@ int check_gemm_common(const void* Xq, const float* Xs, const void* Wq, const flo
     return FP8RL_OK;
 }
 
+// A paged cache's geometry and pointers: heads of D values at 16-byte offsets.
+int check_paged_kv(const fp8rl_paged_kv* c) {
+    if (!c) return FP8RL_ERR_NULL;
+    if (c->num_pages <= 0 || c->page_size <= 0 || c->kv_heads <= 0 || c->head_dim <= 0 || c->head_dim % 16 ||
+        c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0)
+        return FP8RL_ERR_SHAPE;
+    if (c->dtype != FP8RL_KV_BF16 && c->dtype != FP8RL_KV_E4M3) return FP8RL_ERR_UNSUPPORTED;
+    if (!c->K || !c->V || (c->dtype == FP8RL_KV_E4M3 && (!c->k_scale || !c->v_scale))) return FP8RL_ERR_NULL;
+    const int64_t unit = c->dtype == FP8RL_KV_E4M3 ? 16 : 8;
+    if (!aligned16(c->K) || !aligned16(c->V) || c->page_stride % unit || c->token_stride % unit ||
+        c->head_stride % unit || !aligned4(c->k_scale) || !aligned4(c->v_scale))
+        return FP8RL_ERR_ALIGN;
+    if (c->head_dim > 256 || c->num_pages > INT32_MAX || c->page_size > (1 << 20) || c->kv_heads > 65535)
+        return FP8RL_ERR_UNSUPPORTED;
+    return FP8RL_OK;
+}
+
+// Rotation arguments shared by fp8rl_rope and fp8rl_rope_append_paged.
+int check_rope(int64_t T, int64_t D, const int32_t* pos, const float* table, int64_t max_pos, int64_t R,
+               unsigned flags, unsigned known) {
+    if (T < 0 || D <= 0 || R < 0 || R > D || R % 2) return FP8RL_ERR_SHAPE;
+    if (flags & ~known) return FP8RL_ERR_UNSUPPORTED;
+    if (R > 0 && max_pos <= 0) return FP8RL_ERR_SHAPE;
+    if (T > 0 && R > 0 && (!pos || !table)) return FP8RL_ERR_NULL;
+    if (!aligned4(pos) || !aligned4(table)) return FP8RL_ERR_ALIGN;
+    return FP8RL_OK;
+}
+inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+constexpr int64_t kMaxTokens = INT32_MAX, kMaxTokenValues = 1 << 24;
+
 }  // namespace
 
 extern "C" {
@@ -293,6 +323,130 @@ int fp8rl_quant_kv_tensor_noalloc(const uint16_t* KV, int64_t R, int64_t C, int6
     if (!aligned4(scale)) return FP8RL_ERR_ALIGN;
     if (R > 0 && R > kv_noalloc_max_values() / C) return FP8RL_ERR_UNSUPPORTED;   // R * C above the limit
     return cuda_status(launch_quant_kv_tensor_noalloc(KV, R, C, ld, KVq, scale, as_stream(stream)));
+}
+
+int fp8rl_rope_table(const double* freq, int64_t max_pos, int64_t R, double magnitude, float* table, void* stream) {
+    if (max_pos < 0 || R <= 0 || R % 2) return FP8RL_ERR_SHAPE;
+    if (!freq || (max_pos > 0 && !table)) return FP8RL_ERR_NULL;
+    if (!aligned8(freq) || !aligned4(table)) return FP8RL_ERR_ALIGN;
+    if (R > kMaxTokenValues || max_pos > (int64_t)INT32_MAX * 128 / R) return FP8RL_ERR_UNSUPPORTED;
+    if (max_pos == 0) return FP8RL_OK;
+    return cuda_status(launch_rope_table(freq, max_pos, R, magnitude, table, as_stream(stream)));
+}
+
+int fp8rl_rope(const uint16_t* X, int64_t T, int64_t H, int64_t D, int64_t x_token, int64_t x_head,
+               const int32_t* positions, const float* table, int64_t max_pos, int64_t R, unsigned flags, uint16_t* Y,
+               int64_t y_token, int64_t y_head, void* stream) {
+    int rc = check_rope(T, D, positions, table, max_pos, R, flags, FP8RL_ROPE_INTERLEAVED | FP8RL_ROPE_INVERSE);
+    if (rc) return rc;
+    if (H <= 0 || x_token < 0 || x_head < 0 || y_token < 0 || y_head < 0) return FP8RL_ERR_SHAPE;
+    if (T > 0 && (!X || !Y)) return FP8RL_ERR_NULL;
+    if (!aligned2(X) || !aligned2(Y)) return FP8RL_ERR_ALIGN;
+    if (T > kMaxTokens || H > kMaxTokenValues / D) return FP8RL_ERR_UNSUPPORTED;
+    if (T == 0) return FP8RL_OK;
+    RopeParams p{};
+    p.q = X, p.y = Y, p.pos = positions, p.table = table;
+    p.T = T, p.max_pos = max_pos, p.q_token = x_token, p.q_head = x_head, p.y_token = y_token, p.y_head = y_head;
+    p.Hq = (int)H, p.D = (int)D, p.R = (int)R;
+    p.sign = flags & FP8RL_ROPE_INVERSE ? -1.f : 1.f;
+    p.in_place = X == Y && x_token == y_token && x_head == y_head;
+    return cuda_status(launch_rope(p, flags & FP8RL_ROPE_INTERLEAVED, false, as_stream(stream)));
+}
+
+int fp8rl_rope_append_paged(const uint16_t* q, int64_t Hq, int64_t q_token, int64_t q_head, const uint16_t* k,
+                            int64_t k_token, int64_t k_head, const uint16_t* v, int64_t v_token, int64_t v_head,
+                            int64_t T, const int32_t* positions, const float* table, int64_t max_pos, int64_t R,
+                            unsigned flags, uint16_t* q_out, int64_t qo_token, int64_t qo_head,
+                            const fp8rl_paged_kv* cache, const int64_t* slots, void* stream) {
+    int rc = check_paged_kv(cache);
+    if (rc) return rc;
+    rc = check_rope(T, cache->head_dim, positions, table, max_pos, R, flags, FP8RL_ROPE_INTERLEAVED);
+    if (rc) return rc;
+    if (Hq < 0 || q_token < 0 || q_head < 0 || k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0 ||
+        qo_token < 0 || qo_head < 0)
+        return FP8RL_ERR_SHAPE;
+    if (T > 0 && (!k || !v || !slots || (Hq > 0 && (!q || !q_out)))) return FP8RL_ERR_NULL;
+    if (!aligned2(q) || !aligned2(k) || !aligned2(v) || !aligned2(q_out) || !aligned8(slots)) return FP8RL_ERR_ALIGN;
+    if (T > kMaxTokens || Hq + 2 * cache->kv_heads > kMaxTokenValues / cache->head_dim) return FP8RL_ERR_UNSUPPORTED;
+    if (T == 0) return FP8RL_OK;
+    RopeParams p{};
+    p.q = q, p.k = k, p.v = v, p.y = q_out, p.kpool = cache->K, p.vpool = cache->V;
+    p.k_scale = cache->k_scale, p.v_scale = cache->v_scale, p.pos = positions, p.table = table, p.slots = slots;
+    p.T = T, p.max_pos = max_pos, p.q_token = q_token, p.q_head = q_head, p.k_token = k_token, p.k_head = k_head;
+    p.v_token = v_token, p.v_head = v_head, p.y_token = qo_token, p.y_head = qo_head;
+    p.num_pages = cache->num_pages, p.page_size = cache->page_size;
+    p.c_page = cache->page_stride, p.c_token = cache->token_stride, p.c_head = cache->head_stride;
+    p.Hq = (int)Hq, p.Hkv = (int)cache->kv_heads, p.D = (int)cache->head_dim, p.R = (int)R;
+    p.sign = 1.f;
+    p.in_place = q == q_out && q_token == qo_token && q_head == qo_head;
+    return cuda_status(launch_rope(p, flags & FP8RL_ROPE_INTERLEAVED, cache->dtype == FP8RL_KV_E4M3,
+                                   as_stream(stream)));
+}
+
+size_t fp8rl_attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
+    if (B <= 0 || Lq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || D <= 0 || max_len <= 0) return 0;
+    return attn_paged_workspace_bytes(B, Lq, Hq, Hkv, D, max_len);
+}
+
+int fp8rl_attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
+    if (B < 0 || Lq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || D <= 0 || max_len < 0) return -FP8RL_ERR_SHAPE;
+    return B == 0 ? 0 : attn_paged_kernel_count(B, Lq, Hq, Hkv, D, max_len);
+}
+
+int fp8rl_attn_paged(const uint16_t* q, int64_t B, int64_t Lq, int64_t Hq, int64_t q_seq, int64_t q_token,
+                     int64_t q_head, const fp8rl_paged_kv* cache, const int32_t* block_table, int64_t table_stride,
+                     const int32_t* seq_lens, int64_t max_len, int64_t window, float scale, uint16_t* o,
+                     float* lse_or_null, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_paged_kv(cache);
+    if (rc) return rc;
+    if (B < 0 || Lq <= 0 || Hq <= 0 || Hq % cache->kv_heads || q_seq < 0 || q_token < 0 || q_head < 0 ||
+        max_len < 0 || window < 0 || table_stride < 0)
+        return FP8RL_ERR_SHAPE;
+    if (B > 0 && (!q || !seq_lens || !o || (max_len > 0 && !block_table))) return FP8RL_ERR_NULL;
+    if (!aligned16(q) || !aligned16(o) || (q_seq | q_token | q_head) % 8 || !aligned4(block_table) ||
+        !aligned4(seq_lens) || !aligned4(lse_or_null) || !aligned16(workspace))
+        return FP8RL_ERR_ALIGN;
+    if (max_len > (1 << 30) || Lq > (1 << 20) || B > INT32_MAX || Hq > (1 << 20) ||
+        B * Lq > INT32_MAX / Hq)
+        return FP8RL_ERR_UNSUPPORTED;
+    if (B > 1 && table_stride < (max_len + cache->page_size - 1) / cache->page_size) return FP8RL_ERR_SHAPE;
+    const size_t need = fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, cache->kv_heads, cache->head_dim, max_len);
+    if (workspace_bytes < need || (need && !workspace)) return FP8RL_ERR_WORKSPACE;
+    if (B == 0) return FP8RL_OK;
+    AttnParams p{};
+    p.q = q, p.kpool = cache->K, p.vpool = cache->V, p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
+    p.pages = block_table, p.lens = seq_lens, p.o = o, p.lse = lse_or_null, p.ws = static_cast<float*>(workspace);
+    p.q_seq = q_seq, p.q_token = q_token, p.q_head = q_head, p.pages_seq = table_stride;
+    p.num_pages = cache->num_pages, p.c_page = cache->page_stride, p.c_token = cache->token_stride;
+    p.c_head = cache->head_stride;
+    p.B = (int)B, p.Lq = (int)Lq, p.Hq = (int)Hq, p.Hkv = (int)cache->kv_heads, p.D = (int)cache->head_dim;
+    p.page_size = (int)cache->page_size, p.max_len = (int)max_len;
+    p.window = (int)(window < max_len ? window : 0);    // a window of max_len or more hides nothing
+    p.scale = scale;
+    return cuda_status(launch_attn_paged(p, cache->dtype == FP8RL_KV_E4M3, as_stream(stream)));
+}
+
+int fp8rl_spec_verify(const void* P, int64_t p_seq, int64_t p_step, const void* Q_or_null, int64_t q_seq,
+                      int64_t q_step, int dtype, const int32_t* drafts, const int32_t* draft_lens_or_null,
+                      const float* u, const float* noise, int64_t noise_seq, int64_t B, int64_t K, int64_t V,
+                      int32_t* tokens, int32_t* accepted, void* stream) {
+    if (B < 0 || K < 0 || V <= 0 || p_seq < 0 || p_step < 0 || q_seq < 0 || q_step < 0 || noise_seq < 0)
+        return FP8RL_ERR_SHAPE;
+    if (dtype != FP8RL_PROB_F32 && dtype != FP8RL_PROB_BF16) return FP8RL_ERR_UNSUPPORTED;
+    if (B > 0 && (!P || !noise || !tokens || !accepted || (K > 0 && (!drafts || !u)))) return FP8RL_ERR_NULL;
+    const bool f32 = dtype == FP8RL_PROB_F32;
+    if (f32 ? !aligned4(P) || !aligned4(Q_or_null) : !aligned2(P) || !aligned2(Q_or_null)) return FP8RL_ERR_ALIGN;
+    if (!aligned4(drafts) || !aligned4(draft_lens_or_null) || !aligned4(u) || !aligned4(noise) || !aligned4(tokens) ||
+        !aligned4(accepted))
+        return FP8RL_ERR_ALIGN;
+    if (K > 32 || V > INT32_MAX || B > 65535) return FP8RL_ERR_UNSUPPORTED;
+    if (B == 0) return FP8RL_OK;
+    VerifyParams p{};
+    p.P = P, p.Q = Q_or_null, p.drafts = drafts, p.lens = draft_lens_or_null, p.u = u, p.noise = noise;
+    p.out = tokens, p.accepted = accepted;
+    p.p_seq = p_seq, p.p_step = p_step, p.q_seq = q_seq, p.q_step = q_step, p.e_seq = noise_seq;
+    p.B = B, p.V = V, p.K = (int)K;
+    return cuda_status(launch_spec_verify(p, !f32, as_stream(stream)));
 }
 
 int fp8rl_check_device_error(uint32_t* detail) {

@@ -55,6 +55,59 @@ size_t kl_partial_bytes();
 cudaError_t launch_logits_kl(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int64_t M,
                              int64_t V, float* kl, void* ws, cudaStream_t st);
 
+// Rotary positions over p.Hq heads of p.q into p.y, and, where p.Hkv > 0, over
+// the keys, which are stored with the values in the cache's slots.  Strides in
+// elements; c_*: the cache's.
+struct RopeParams {
+    const uint16_t *q, *k, *v;
+    uint16_t* y;
+    void *kpool, *vpool;
+    const float *k_scale, *v_scale;
+    const int32_t* pos;
+    const float* table;
+    const int64_t* slots;
+    uint32_t* err;
+    int64_t T, max_pos, q_token, q_head, k_token, k_head, v_token, v_head, y_token, y_head;
+    int64_t num_pages, page_size, c_page, c_token, c_head;
+    int Hq, Hkv, D, R;
+    float sign;         // -1: the gradient
+    bool in_place;      // y is q: what lies past R stays as it is
+};
+cudaError_t launch_rope(const RopeParams& p, bool interleaved, bool e4m3, cudaStream_t st);
+cudaError_t launch_rope_table(const double* freq, int64_t max_pos, int64_t R, double mag, float* table,
+                              cudaStream_t st);
+
+// Attention of Lq new tokens a sequence over a paged cache (strides in elements).
+struct AttnParams {
+    const uint16_t* q;
+    const void *kpool, *vpool;
+    const float *k_scale, *v_scale;
+    const int32_t *pages, *lens;
+    uint16_t* o;
+    float* lse;
+    float* ws;
+    uint32_t* err;
+    int64_t q_seq, q_token, q_head, pages_seq, num_pages, c_page, c_token, c_head;
+    int B, Lq, Hq, Hkv, D, page_size, max_len, window;
+    float scale;
+};
+size_t attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
+int attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
+cudaError_t launch_attn_paged(const AttnParams& p, bool e4m3, cudaStream_t st);
+
+// Verification of drafted tokens (strides in elements).
+struct VerifyParams {
+    const void *P, *Q;
+    const int32_t *drafts, *lens;
+    const float *u, *noise;
+    int32_t *out, *accepted;
+    uint32_t* err;
+    int64_t p_seq, p_step, q_seq, q_step, e_seq;
+    int64_t B, V;
+    int K;
+};
+cudaError_t launch_spec_verify(const VerifyParams& p, bool bf16, cudaStream_t st);
+
 // FP8 block-scaled GEMM: dispatch by M (tcgen05 decode kernel for M <= 256).
 // weights_stable: the kernel immediately preceding the call in the stream did
 // not write Wq, so small weights may start streaming before the dependency wait.

@@ -362,6 +362,14 @@ __device__ __forceinline__ void cluster_sync_all() {
                      "memory");
 }
 
+// The two halves of cluster_sync_all: every thread of the cluster arrives, then waits.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Address of the same shared-memory offset in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t rank) {
     uint32_t r;
@@ -376,6 +384,10 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
 // Named barrier over `count` threads (a multiple of 32).

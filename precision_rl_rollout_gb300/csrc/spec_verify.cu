@@ -1,0 +1,147 @@
+// spec_verify.cu -- verification of drafted tokens against the target model's
+// probabilities, with every random number given.
+//
+// Draft i of a sequence (token t_i, drawn from q_i) is kept while
+// u_i q_i(t_i) < p_i(t_i); both factors are fp32 or bf16, so the product is
+// exact in fp64 and the decision is exact.  At the first refusal n the sequence
+// gets one token from the residual max(p_n - q_n, 0), after len accepted drafts
+// one from p_len: as an exponential race, argmax_v w_v / e_v with e_v ~ Exp(1)
+// given.  Each score is one IEEE division, so the winner does not depend on how
+// the vocabulary is split; equal scores go to the lowest index.
+//
+// Only row n of p and q and the sequence's e are read: 12 bytes a vocabulary
+// entry, bound by HBM in a batch and by latency for one sequence.  A cluster of
+// CTAs shares a row; each finds n for itself and takes part of the row, the
+// parts' winners meet in the CTAs' shared memory.
+#include "common.cuh"
+#include "internal.h"
+#include "sm100_ptx.cuh"
+
+namespace fp8rl {
+
+namespace {
+
+constexpr uint32_t kKernelVerify = 9;
+constexpr int kVThreads = 512;
+constexpr int kVWarps = kVThreads / 32;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+
+// The race so far: score bits (scores are >= 0, so they order as integers) and
+// the complement of the index, as one 64-bit key; larger wins.
+__device__ __forceinline__ uint64_t race_key(float score, uint32_t idx) {
+    return ((uint64_t)__float_as_uint(score) << 32) | (uint32_t)~idx;
+}
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return ((uint64_t)hi << 32) | lo;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kVThreads)
+spec_verify_kernel(const __grid_constant__ VerifyParams p) {
+    __shared__ uint64_t wkey[kVWarps];
+    __shared__ uint64_t part[2][16];           // [round][cluster rank], written by every CTA of the cluster
+    __shared__ int s_n, s_len;
+    sm100::cluster_arrive();                    // every CTA of the cluster has started (waited for below)
+    pdl_wait_then_release();
+    const uint32_t rank = sm100::cluster_ctarank(), ranks = gridDim.x;
+    const int64_t b = blockIdx.y;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T* P = static_cast<const T*>(p.P) + b * p.p_seq;
+    const T* Q = p.Q ? static_cast<const T*>(p.Q) + b * p.q_seq : nullptr;
+    if (warp == 0) {
+        int len = p.lens ? p.lens[b] : p.K;
+        if (len < 0 || len > p.K) {
+            if (lane == 0) atomicCAS(p.err, 0u, (kKernelVerify << 24) | (1u << 16) | 2u);
+            len = len < 0 ? 0 : p.K;
+        }
+        bool keep = false;
+        if (lane < len) {
+            const int32_t tok = p.drafts[b * p.K + lane];
+            if (tok >= 0 && tok < p.V) {
+                const double u = (double)p.u[b * p.K + lane];
+                const double pt = (double)to_f32(P[lane * p.p_step + tok]);
+                const double qt = Q ? (double)to_f32(Q[lane * p.q_step + tok]) : 1.0;
+                keep = u * qt < pt;
+            } else {
+                atomicCAS(p.err, 0u, (kKernelVerify << 24) | (2u << 16) | 2u);
+            }
+        }
+        const uint32_t refused = ~__ballot_sync(0xffffffffu, keep);   // lanes from len on count as refused
+        if (lane == 0) {
+            s_len = len;
+            s_n = refused ? __ffs((int)refused) - 1 : 32;
+        }
+    }
+    __syncthreads();
+    const int n = s_n, len = s_len;
+    bool residual = n < len;
+    const T* pr = P + n * p.p_step;
+    const T* qr = residual && Q ? Q + n * p.q_step : nullptr;
+    const int32_t drop = residual && !Q ? p.drafts[b * p.K + n] : -1;   // a drafter without probabilities: q is 1 there
+    const float* e = p.noise + b * p.e_seq;
+    uint64_t best = 0;
+    for (int round = 0;; ++round) {
+        float top = 0.f;
+        uint32_t at = 0;
+        for (int64_t v = (int64_t)rank * kVThreads + threadIdx.x; v < p.V; v += (int64_t)ranks * kVThreads) {
+            float w = to_f32(pr[v]);
+            if (residual) {
+                if (qr) w = __fsub_rn(w, to_f32(qr[v]));
+                if (v == drop) w = 0.f;
+            }
+            if (w > 0.f) {
+                const float s = __fdiv_rn(w, e[v]);
+                if (s > top) top = s, at = (uint32_t)v;
+            }
+        }
+        uint64_t key = warp_max_key(race_key(top, at));
+        if (lane == 0) wkey[warp] = key;
+        __syncthreads();
+        if (round == 0) sm100::cluster_wait();
+        if (warp == 0) {
+            key = warp_max_key(lane < kVWarps ? wkey[lane] : 0ull);
+            if (lane < ranks) sm100::st_cluster_u64(sm100::map_to_rank(sm100::smem_u32(&part[round][rank]), lane), key);
+        }
+        __syncwarp();
+        sm100::cluster_arrive();
+        sm100::cluster_wait();
+        best = part[round][0];
+        for (uint32_t r = 1; r < ranks; ++r) best = part[round][r] > best ? part[round][r] : best;
+        // a residual with nothing in it (p <= q everywhere, by rounding): draw from p
+        if (!residual || (best >> 32)) break;
+        residual = false;
+        __syncthreads();
+    }
+    if (rank == 0) {
+        const int32_t token = (int32_t)~(uint32_t)best;
+        for (int i = threadIdx.x; i <= p.K; i += kVThreads)
+            p.out[b * (p.K + 1) + i] = i < n ? p.drafts[b * p.K + i] : i == n ? token : -1;
+        if (threadIdx.x == 0) p.accepted[b] = n;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_spec_verify(const VerifyParams& a, bool bf16, cudaStream_t st) {
+    VerifyParams p = a;
+    p.err = device_error_word();
+    if (!p.err) return cudaErrorUnknown;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(8, (unsigned)p.B);
+    cfg.blockDim = dim3(kVThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {8, 1, 1};
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, bf16 ? spec_verify_kernel<uint16_t> : spec_verify_kernel<float>, p);
+}
+
+}  // namespace fp8rl
