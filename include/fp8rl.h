@@ -489,13 +489,16 @@ int fp8rl_rope_append_paged(const uint16_t* q, int64_t Hq, int64_t q_token, int6
  * workspace: at least fp8rl_attn_paged_workspace_bytes bytes, 16-byte aligned,
  *     no zeroing, nothing kept between calls; calls in flight at once need
  *     their own.
- * Limits: max_len <= 2^30, Lq <= 2^20, B * Lq * Hq < 2^31.
+ * Limits: max_len <= 2^30, Lq <= 2^20, B * Lq * Hq < 2^31, and B * Lq * Hq *
+ * max_len <= 2^42.
  * ---------------------------------------------------------------------- */
 size_t fp8rl_attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
                                         int64_t max_len);
-/* Kernels fp8rl_attn_paged launches for these sizes; 0 for B == 0; -FP8RL_ERR_SHAPE for invalid ones. */
+/* Kernels fp8rl_attn_paged launches for these sizes and cache dtype: 1 where
+ * max_len is a tile at most, else 2.  0 for B == 0; a negated status for invalid
+ * sizes. */
 int fp8rl_attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
-                                  int64_t max_len);
+                                  int64_t max_len, int dtype);
 int fp8rl_attn_paged(const uint16_t* q, int64_t B, int64_t Lq, int64_t Hq, int64_t q_seq,
                      int64_t q_token, int64_t q_head, const fp8rl_paged_kv* cache,
                      const int32_t* block_table, int64_t table_stride, const int32_t* seq_lens,

@@ -123,7 +123,7 @@ def load(path: str | None = None):
         lib.fp8rl_rope_append_paged.argtypes = [P, I, I, I, P, I, I, P, I, I, I, P, P, I, I, U, P, I, I, KV, P, S]
         lib.fp8rl_attn_paged_workspace_bytes.restype = Z
         lib.fp8rl_attn_paged_workspace_bytes.argtypes = [I] * 6
-        lib.fp8rl_attn_paged_kernel_count.argtypes = [I] * 6
+        lib.fp8rl_attn_paged_kernel_count.argtypes = [I] * 6 + [ctypes.c_int]
         lib.fp8rl_attn_paged.argtypes = [P, I, I, I, I, I, I, KV, P, I, P, I, I, F, P, P, P, Z, S]
         lib.fp8rl_spec_verify.argtypes = [P, I, I, P, I, I, ctypes.c_int, P, P, P, P, I, I, I, I, P, P, S]
         for name in EXPORTS:
@@ -632,8 +632,9 @@ def fp8rl_attn_paged_workspace_bytes(B: int, Lq: int, Hq: int, Hkv: int, D: int,
     return int(load().fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, Hkv, D, max_len))
 
 
-def fp8rl_attn_paged_kernel_count(B: int, Lq: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
-    return int(load().fp8rl_attn_paged_kernel_count(B, Lq, Hq, Hkv, D, max_len))
+def fp8rl_attn_paged_kernel_count(B: int, Lq: int, Hq: int, Hkv: int, D: int, max_len: int,
+                                  dtype: int = FP8RL_KV_BF16) -> int:
+    return int(load().fp8rl_attn_paged_kernel_count(B, Lq, Hq, Hkv, D, max_len, dtype))
 
 
 def fp8rl_attn_paged(q, K, V, block_table, seq_lens, max_len: int, scale=None, window: int = 0, k_scale=None,

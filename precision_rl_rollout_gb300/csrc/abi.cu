@@ -388,9 +388,11 @@ size_t fp8rl_attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64
     return attn_paged_workspace_bytes(B, Lq, Hq, Hkv, D, max_len);
 }
 
-int fp8rl_attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
+int fp8rl_attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len,
+                                  int dtype) {
     if (B < 0 || Lq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || D <= 0 || max_len < 0) return -FP8RL_ERR_SHAPE;
-    return B == 0 ? 0 : attn_paged_kernel_count(B, Lq, Hq, Hkv, D, max_len);
+    if (dtype != FP8RL_KV_BF16 && dtype != FP8RL_KV_E4M3) return -FP8RL_ERR_UNSUPPORTED;
+    return B == 0 ? 0 : attn_paged_kernel_count(B, Lq, Hq, Hkv, D, max_len, dtype == FP8RL_KV_E4M3);
 }
 
 int fp8rl_attn_paged(const uint16_t* q, int64_t B, int64_t Lq, int64_t Hq, int64_t q_seq, int64_t q_token,
@@ -406,8 +408,8 @@ int fp8rl_attn_paged(const uint16_t* q, int64_t B, int64_t Lq, int64_t Hq, int64
     if (!aligned16(q) || !aligned16(o) || (q_seq | q_token | q_head) % 8 || !aligned4(block_table) ||
         !aligned4(seq_lens) || !aligned4(lse_or_null) || !aligned16(workspace))
         return FP8RL_ERR_ALIGN;
-    if (max_len > (1 << 30) || Lq > (1 << 20) || B > INT32_MAX || Hq > (1 << 20) ||
-        B * Lq > INT32_MAX / Hq)
+    if (max_len > (1 << 30) || Lq > (1 << 20) || B > INT32_MAX || Hq > (1 << 20) || B * Lq > INT32_MAX / Hq ||
+        B * Lq * Hq > ((int64_t)1 << 42) / (max_len + 1))
         return FP8RL_ERR_UNSUPPORTED;
     if (B > 1 && table_stride < (max_len + cache->page_size - 1) / cache->page_size) return FP8RL_ERR_SHAPE;
     const size_t need = fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, cache->kv_heads, cache->head_dim, max_len);

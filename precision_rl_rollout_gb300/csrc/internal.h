@@ -92,7 +92,7 @@ struct AttnParams {
     float scale;
 };
 size_t attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
-int attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
+int attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, bool e4m3);
 cudaError_t launch_attn_paged(const AttnParams& p, bool e4m3, cudaStream_t st);
 
 // Verification of drafted tokens (strides in elements).

@@ -86,7 +86,9 @@ def test_attn_validation(lib):
         if need:
             assert f(B=B, max_len=L, ts=10000, wb=need - 1) == 4 and f(B=B, max_len=L, ts=10000, ws=None) == 4
     c = lib.fp8rl_attn_paged_kernel_count
-    assert c(0, 1, 4, 2, 64, 100) == 0 and c(2, 1, 3, 2, 64, 100) == -2 and c(2, 1, 4, 2, 64, 100) in (1, 2)
+    assert c(0, 1, 4, 2, 64, 100, 0) == 0 and c(2, 1, 3, 2, 64, 100, 0) == -2 and c(2, 1, 4, 2, 64, 100, 2) == -6
+    for dtype in (0, 1):
+        assert c(2, 1, 4, 2, 64, 16, dtype) == 1 and c(2, 1, 4, 2, 64, 100000, dtype) == 2
 
 
 def test_verify_validation(lib):
