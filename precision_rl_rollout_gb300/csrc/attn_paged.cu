@@ -1,25 +1,43 @@
-// attn_paged.cu -- the paged attention call: its sizes and its two cache types
-// (attn_paged.cuh has the kernels).
+// attn_paged.cu -- the paged attention call: its sizes, and which loader a cache
+// takes (attn_paged.cuh has the kernels).
 #include "attn_paged.cuh"
 
 namespace fp8rl {
 
+namespace {
+
+attn::Plan plan_of(int64_t D, int64_t rows, int64_t max_len, bool e4m3) {
+    auto f = [&](auto c) { return attn::plan<decltype(c)>(max_len); };
+    return e4m3 ? attn::pick<true, true>(D, rows, f) : attn::pick<false, true>(D, rows, f);
+}
+
+// The copy engine loads boxes of 8 tokens or more of one page, by the strides of
+// a tensor map; other pages go 16 bytes a thread.
+bool copy_engine(const AttnParams& p, bool e4m3) {
+    const int64_t es = e4m3 ? 1 : 2, most = (int64_t)1 << 40;
+    return p.page_size % 8 == 0 && p.c_token > 0 && (p.c_head > 0 || p.Hkv == 1) && (p.c_page > 0 || p.num_pages == 1) &&
+           p.c_token * es < most && p.c_head * es < most && p.c_page * es < most && p.c_token * p.page_size * es < most;
+}
+
+}  // namespace
+
 size_t attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
     (void)B;                                   // two slots a CTA, whatever the batch
-    const size_t a = plan_attn_paged_bf16(D, Hq / Hkv * Lq, max_len).ws, b = plan_attn_paged_e4m3(D, Hq / Hkv * Lq, max_len).ws;
+    const size_t a = plan_of(D, Hq / Hkv * Lq, max_len, false).ws, b = plan_of(D, Hq / Hkv * Lq, max_len, true).ws;
     return a > b ? a : b;
 }
 
 int attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, bool e4m3) {
     (void)B;
-    return (e4m3 ? plan_attn_paged_e4m3 : plan_attn_paged_bf16)(D, Hq / Hkv * Lq, max_len).kernels;
+    return plan_of(D, Hq / Hkv * Lq, max_len, e4m3).kernels;
 }
 
 cudaError_t launch_attn_paged(const AttnParams& a, bool e4m3, cudaStream_t st) {
     AttnParams p = a;
     p.err = device_error_word();
     if (!p.err) return cudaErrorUnknown;
-    return e4m3 ? launch_attn_paged_e4m3(p, st) : launch_attn_paged_bf16(p, st);
+    if (copy_engine(p, e4m3)) return e4m3 ? launch_attn_e4m3_tma(p, st) : launch_attn_bf16_tma(p, st);
+    return e4m3 ? launch_attn_e4m3(p, st) : launch_attn_bf16(p, st);
 }
 
 }  // namespace fp8rl

@@ -1,13 +1,12 @@
-// attn_paged_bf16.cu -- paged attention over bf16 caches (attn_paged.cuh).
+// attn_paged_bf16.cu -- paged attention over bf16 caches, pages of any size, loaded 16 bytes a thread
+// (attn_paged.cuh).
 #include "attn_paged.cuh"
 
 namespace fp8rl {
 
-cudaError_t launch_attn_paged_bf16(const AttnParams& p, cudaStream_t st) {
-    return attn::pick<false>(p.D, (int64_t)p.Hq / p.Hkv * p.Lq, [&](auto c) { return attn::launch<decltype(c)>(p, st); });
-}
-attn::Plan plan_attn_paged_bf16(int64_t D, int64_t rows, int64_t max_len) {
-    return attn::pick<false>(D, rows, [&](auto c) { return attn::plan<decltype(c)>(max_len); });
+cudaError_t launch_attn_bf16(const AttnParams& p, cudaStream_t st) {
+    return attn::pick<false, false>(p.D, (int64_t)p.Hq / p.Hkv * p.Lq,
+                                   [&](auto c) { return attn::launch<decltype(c)>(p, st); });
 }
 
 }  // namespace fp8rl

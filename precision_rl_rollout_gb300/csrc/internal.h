@@ -72,6 +72,7 @@ struct RopeParams {
     int Hq, Hkv, D, R;
     float sign;         // -1: the gradient
     bool in_place;      // y is q: what lies past R stays as it is
+    int lanes, cta_tokens;   // threads over the heads, tokens a CTA (set by the launcher)
 };
 cudaError_t launch_rope(const RopeParams& p, bool interleaved, bool e4m3, cudaStream_t st);
 cudaError_t launch_rope_table(const double* freq, int64_t max_pos, int64_t R, double mag, float* table,
@@ -90,6 +91,7 @@ struct AttnParams {
     int64_t q_seq, q_token, q_head, pages_seq, num_pages, c_page, c_token, c_head;
     int B, Lq, Hq, Hkv, D, page_size, max_len, window;
     float scale;
+    int box, order;     // tokens a copy-engine box, 1: heads outside tokens (set by the launcher)
 };
 size_t attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
 int attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, bool e4m3);
@@ -184,6 +186,11 @@ bool make_tmap_f32_store(CUtensorMap* m, const void* base, uint64_t rows, uint64
 // fp16 [rows][cols] row-major (cols % 8 == 0), loaded in boxes of box_rows x 64
 // with the 128-byte swizzle (one UMMA K-major atom of fp16).
 bool make_tmap_f16_load(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// 4-D map of 8- or 16-bit values for loads of boxes whose rows are `swizzle` (64 or
+// 128) bytes, stored with that swizzle; zero fill out of range.  strides: bytes of
+// dimensions 1 .. 3.
+bool make_tmap_4d(CUtensorMap* m, const void* base, bool bytes, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                  const uint32_t (&box)[4], int swizzle);
 int num_sms();
 bool decode_supported(int64_t K);
 bool decode_fits(int64_t M, int64_t N, int64_t K, size_t ws_bytes);

@@ -43,11 +43,14 @@ __device__ __forceinline__ Row token_row(const RopeParams& p, int64_t t, bool fi
     }
     if (p.Hkv) {
         const int64_t slot = p.slots[t];
-        const int64_t page = slot / p.page_size;
-        if (slot >= 0 && page < p.num_pages)
-            r.slot = page * p.c_page + (slot - page * p.page_size) * p.c_token;
-        else if (slot >= 0 && first)
-            record_data_error(p.err, 2);
+        if (slot >= 0) {
+            // a 64-bit division costs a hundred instructions; most pools need none
+            const int64_t page = slot >> 32 ? slot / p.page_size : (uint32_t)slot / (uint32_t)p.page_size;
+            if (page < p.num_pages)
+                r.slot = page * p.c_page + (slot - page * p.page_size) * p.c_token;
+            else if (first)
+                record_data_error(p.err, 2);
+        }
     }
     return r;
 }
@@ -56,10 +59,25 @@ __device__ __forceinline__ void unpack8(uint4 v, float* f) {
     f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
     f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
+// 16 bytes read once, past L1; not the read-only path, the rotation may be in place.
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    return make_uint4(round2(f[0], f[1]), round2(f[2], f[3]), round2(f[4], f[5]), round2(f[6], f[7]));
+}
+// (The packed fp32 forms were tried: a packed product and a packed sum that
+// follow one another came out as one fused rounding in places.)
 __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
     const float ya = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
     const float yb = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
@@ -83,75 +101,106 @@ __device__ __forceinline__ void store_cache8(void* pool, int64_t at, const float
     }
 }
 
-// Work items of a token, 16-byte chunks of 8 values:
-//   per q head: pairs (half layout: chunk j and chunk j + R/16; interleaved:
-//   chunk j alone), then the chunks past R (only when not in place);
-//   per k head: the same, always stored; per v head: D / 8 chunks.
-// threadIdx.y: token of the CTA.
+// A head is cut into columns, one a thread, of 16-byte chunks of 8 values: in the
+// half layout column j < R/16 is the chunks j and j + R/16, whose values pair up;
+// interleaved, a chunk holds its own pairs; what lies past R is one chunk a column.
+// A thread keeps its column's cosines and sines in registers and goes over the
+// token's heads (queries, keys, values) p.lanes apart, kBatch at a time with their
+// loads in flight together; the first batch is in flight while the position and
+// its row come.  Loads pass L1 and stores go out evict-first: nothing is read
+// twice (49 -> 45 us for the gradient below).
+// Bound by HBM: 2 bytes in, 2 (E4M3: 1) out a value.  8192 tokens, 40 + 8 heads of
+// 128: 36 us, 5.8 TB/s; gradient of 16411 tokens, 28 + 4 heads, 64 of 128 values
+// interleaved: 45 us, 6.1 TB/s; append of 8192 tokens, 40 + 2 x 8 heads, bf16
+// pages: 41 us, 5.9 TB/s.  What is left is the start and the last wave.
 template <bool kInter, bool kE4m3>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 2)
 rope_kernel(const __grid_constant__ RopeParams p) {
     pdl_wait_then_release();
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= p.T) return;
-    const Row row = token_row(p, t, threadIdx.x == 0);
-    const int pairs = p.R / (kInter ? 8 : 16);              // pair items per head
-    const int rest = (p.D - p.R) / 8;                       // chunks past R per head
-    const int per_q = pairs + (p.in_place ? 0 : rest), per_k = pairs + rest, per_v = p.D / 8;
-    const int nq = p.Hq * per_q, nk = nq + p.Hkv * per_k, n = nk + p.Hkv * per_v;
-    const int half = p.R / 2;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        if (i >= nk) {                                      // v: stored as it is
-            if (row.slot < 0) break;
-            const int h = (i - nk) / per_v, d = (i - nk - h * per_v) * 8;
-            float f[8];
-            unpack8(*reinterpret_cast<const uint4*>(p.v + t * p.v_token + h * p.v_head + d), f);
-            store_cache8<kE4m3>(p.vpool, row.slot + h * p.c_head + d, f, kE4m3 ? *p.v_scale : 1.f);
-            continue;
-        }
-        const bool is_k = i >= nq;
-        if (is_k && row.slot < 0) break;
-        const int ii = is_k ? i - nq : i, per = is_k ? per_k : per_q;
-        const int h = ii / per, j = ii - h * per;
-        const uint16_t* src = is_k ? p.k + t * p.k_token + h * p.k_head : p.q + t * p.q_token + h * p.q_head;
-        const int64_t dst = is_k ? row.slot + h * p.c_head : t * p.y_token + h * p.y_head;
-        auto put = [&](int d, const float* f) {
-            if (is_k)
-                store_cache8<kE4m3>(p.kpool, dst + d, f, kE4m3 ? *p.k_scale : 1.f);
-            else
-                *reinterpret_cast<uint4*>(p.y + dst + d) = pack8(f);
-        };
-        if (j >= pairs) {
-            const int d = p.R + (j - pairs) * 8;
-            float f[8];
-            unpack8(*reinterpret_cast<const uint4*>(src + d), f);
-            put(d, f);
-        } else if (kInter) {
-            float f[8];
-            unpack8(*reinterpret_cast<const uint4*>(src + j * 8), f);
-            const float4 c = *reinterpret_cast<const float4*>(row.cs + j * 4);
-            const float4 s = *reinterpret_cast<const float4*>(row.cs + half + j * 4);
-            rotate(f[0], f[1], c.x, p.sign * s.x);
-            rotate(f[2], f[3], c.y, p.sign * s.y);
-            rotate(f[4], f[5], c.z, p.sign * s.z);
-            rotate(f[6], f[7], c.w, p.sign * s.w);
-            put(j * 8, f);
-        } else {
-            float a[8], b[8];
-            unpack8(*reinterpret_cast<const uint4*>(src + j * 8), a);
-            unpack8(*reinterpret_cast<const uint4*>(src + half + j * 8), b);
+    const int pairs = p.R / (kInter ? 8 : 16), cols = pairs + (p.D - p.R) / 8;
+    const int j = threadIdx.x % cols, hl = threadIdx.x / cols % p.lanes, tok = threadIdx.x / (cols * p.lanes);
+    const int64_t t = (int64_t)blockIdx.x * p.cta_tokens + tok;
+    if (tok >= p.cta_tokens || t >= p.T) return;
+    const bool turn = j < pairs, two = !kInter && turn;      // a column that rotates; of two chunks
+    const int d0 = turn ? j * 8 : p.R + (j - pairs) * 8, d1 = d0 + p.R / 2;
+    constexpr int NC = kInter ? 4 : 8;
+    float c[NC], s[NC];
+    const uint16_t* const q = p.q + t * p.q_token + d0;
+    const uint16_t* const k = p.k + t * p.k_token + d0;
+    const uint16_t* const v = p.v + t * p.v_token + d0;
+    uint16_t* const y = p.y + t * p.y_token;
+    const int heads = p.Hq + 2 * p.Hkv;
+    // queries rotated in place: their columns past R stay as they are
+    int h0 = hl;
+    if (p.in_place && !turn)
+        while (h0 < p.Hq) h0 += p.lanes;
+    constexpr int kBatch = 4;
+    uint4 x0[kBatch], x1[kBatch];
+    auto load = [&]() {
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const float4 c = *reinterpret_cast<const float4*>(row.cs + j * 8 + e);
-                const float4 s = *reinterpret_cast<const float4*>(row.cs + half + j * 8 + e);
-                rotate(a[e], b[e], c.x, p.sign * s.x);
-                rotate(a[e + 1], b[e + 1], c.y, p.sign * s.y);
-                rotate(a[e + 2], b[e + 2], c.z, p.sign * s.z);
-                rotate(a[e + 3], b[e + 3], c.w, p.sign * s.w);
-            }
-            put(j * 8, a);
-            put(half + j * 8, b);
+        for (int u = 0; u < kBatch; ++u) {
+            const int h = h0 + u * p.lanes;
+            if (h >= heads) break;
+            const uint16_t* src = h < p.Hq ? q + h * p.q_head
+                                           : h < p.Hq + p.Hkv ? k + (h - p.Hq) * p.k_head : v + (h - p.Hq - p.Hkv) * p.v_head;
+            x0[u] = ld_once(src);
+            if (two) x1[u] = ld_once(src + p.R / 2);
         }
+    };
+    load();                                                   // in flight while the position and its row come
+    const Row row = token_row(p, t, threadIdx.x == tok * cols * p.lanes);
+    const float ks = kE4m3 ? *p.k_scale : 1.f, vs = kE4m3 ? *p.v_scale : 1.f;
+    if (turn) {
+#pragma unroll
+        for (int e = 0; e < NC; e += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(row.cs + j * NC + e);
+            const float4 b = *reinterpret_cast<const float4*>(row.cs + p.R / 2 + j * NC + e);
+            c[e] = a.x, c[e + 1] = a.y, c[e + 2] = a.z, c[e + 3] = a.w;
+            s[e] = p.sign * b.x, s[e + 1] = p.sign * b.y, s[e + 2] = p.sign * b.z, s[e + 3] = p.sign * b.w;
+        }
+    }
+    const int stored = row.slot < 0 ? p.Hq : heads;
+    for (;;) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int h = h0 + u * p.lanes;
+            if (h >= stored) break;
+            const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+            if ((is_v || !turn) && (is_q || !kE4m3)) {        // kept as it is
+                uint16_t* to = is_q ? y + h * p.y_head
+                                    : static_cast<uint16_t*>(is_v ? p.vpool : p.kpool) + row.slot +
+                                          (h - p.Hq - (is_v ? p.Hkv : 0)) * p.c_head;
+                __stcs(reinterpret_cast<uint4*>(to + d0), x0[u]);
+                if (two) __stcs(reinterpret_cast<uint4*>(to + d1), x1[u]);
+                continue;
+            }
+            float a[8], b[8];
+            unpack8(x0[u], a);
+            if constexpr (kInter) {
+                if (turn && !is_v) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) rotate(a[2 * e], a[2 * e + 1], c[e], s[e]);
+                }
+            } else {
+                unpack8(x1[u], b);
+                if (turn && !is_v) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) rotate(a[e], b[e], c[e], s[e]);
+                }
+            }
+            if (is_q) {
+                __stcs(reinterpret_cast<uint4*>(y + h * p.y_head + d0), pack8(a));
+                if (two) __stcs(reinterpret_cast<uint4*>(y + h * p.y_head + d1), pack8(b));
+            } else {
+                void* pool = is_v ? p.vpool : p.kpool;
+                const int64_t to = row.slot + (h - p.Hq - (is_v ? p.Hkv : 0)) * p.c_head;
+                store_cache8<kE4m3>(pool, to + d0, a, is_v ? vs : ks);
+                if (two) store_cache8<kE4m3>(pool, to + d1, b, is_v ? vs : ks);
+            }
+        }
+        h0 += kBatch * p.lanes;
+        if (h0 >= stored) return;
+        load();
     }
 }
 
@@ -161,8 +210,7 @@ template <bool kInter, bool kE4m3>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_narrow_kernel(const __grid_constant__ RopeParams p) {
     pdl_wait_then_release();
-    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= p.T) return;
+    const int64_t t = blockIdx.x;
     const Row row = token_row(p, t, threadIdx.x == 0);
     const int half = p.R / 2, rest = p.D - p.R;
     const int per_q = half + (p.in_place ? 0 : rest), per_k = half + rest, per_v = p.D;
@@ -175,14 +223,13 @@ rope_narrow_kernel(const __grid_constant__ RopeParams p) {
             static_cast<uint16_t*>(pool)[at] = (uint16_t)f32_to_bf16_bits(f);
     };
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        if (i >= nq && row.slot < 0) break;
         if (i >= nk) {
-            if (row.slot < 0) break;
             const int h = (i - nk) / per_v, d = i - nk - h * per_v;
             cache(p.vpool, row.slot + h * p.c_head + d, bf(p.v[t * p.v_token + h * p.v_head + d]), p.v_scale);
             continue;
         }
         const bool is_k = i >= nq;
-        if (is_k && row.slot < 0) break;
         const int ii = is_k ? i - nq : i, per = is_k ? per_k : per_q;
         const int h = ii / per, j = ii - h * per;
         const uint16_t* src = is_k ? p.k + t * p.k_token + h * p.k_head : p.q + t * p.q_token + h * p.q_head;
@@ -224,14 +271,22 @@ rope_table_kernel(const double* __restrict__ freq, int64_t max_pos, int half, do
 }
 
 template <bool kInter, bool kE4m3>
-cudaError_t launch_t(const RopeParams& p, bool narrow, int items, cudaStream_t st) {
-    // items over x in whole warps, several tokens in a CTA where one has few
-    const int passes = (items + kRopeThreads - 1) / kRopeThreads;
-    const int tx = ((items + passes - 1) / passes + 31) / 32 * 32;
-    const int ty = kRopeThreads / tx > 1 ? kRopeThreads / tx : 1;
-    const dim3 grid((unsigned)((p.T + ty - 1) / ty)), block((unsigned)tx, (unsigned)ty);
-    return launch_pdl(narrow ? rope_narrow_kernel<kInter, kE4m3> : rope_kernel<kInter, kE4m3>, grid, block, 0, st,
-                      p);
+cudaError_t launch_t(RopeParams& p, bool wide, cudaStream_t st) {
+    const int heads = p.Hq + 2 * p.Hkv;
+    if (!wide) return launch_pdl(rope_narrow_kernel<kInter, kE4m3>, dim3((unsigned)p.T), dim3(kRopeThreads), 0, st, p);
+    // A thread goes over up to 16 heads, fewer where that leaves SMs without two
+    // CTAs: its own work (the token's row, its column's cosines) is then spread over
+    // more bytes.  8192 tokens of 48 heads of 128: 75 us with one head a thread, 41
+    // with four, 36 with 16.
+    const int cols = p.R / (kInter ? 8 : 16) + (p.D - p.R) / 8, most = kRopeThreads / cols;
+    const int64_t room = p.T * heads * cols / (2 * (int64_t)num_sms() * kRopeThreads);
+    const int each = room < 1 ? 1 : room > 16 ? 16 : (int)room;
+    p.lanes = (heads + each - 1) / each;
+    if (p.lanes > most) p.lanes = most;
+    p.cta_tokens = each == 1 ? 1 : most / p.lanes;
+    const dim3 grid((unsigned)((p.T + p.cta_tokens - 1) / p.cta_tokens));
+    const dim3 block((unsigned)((cols * p.lanes * p.cta_tokens + 31) / 32 * 32));
+    return launch_pdl(rope_kernel<kInter, kE4m3>, grid, block, 0, st, p);
 }
 
 }  // namespace
@@ -240,19 +295,14 @@ cudaError_t launch_rope(const RopeParams& a, bool interleaved, bool e4m3, cudaSt
     RopeParams p = a;
     p.err = device_error_word();
     if (!p.err) return cudaErrorUnknown;
+    if (p.Hkv == 0 && (p.Hq == 0 || (p.in_place && p.R == 0))) return cudaSuccess;
     auto aligned = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
-    const int unit = interleaved ? 8 : 16;
-    bool wide = p.D % 8 == 0 && p.R % unit == 0;
+    bool wide = p.D % 8 == 0 && p.R % (interleaved ? 8 : 16) == 0 && p.D / 8 <= kRopeThreads;
     wide = wide && aligned(p.q) && aligned(p.y) && aligned(p.table) &&
            (p.q_token | p.q_head | p.y_token | p.y_head) % 8 == 0;
     wide = wide && aligned(p.k) && aligned(p.v) && (p.k_token | p.k_head | p.v_token | p.v_head) % 8 == 0;
-    const int64_t pairs = wide ? p.R / (interleaved ? 8 : 16) : p.R / 2;
-    const int64_t rest = wide ? (p.D - p.R) / 8 : p.D - p.R, vs = wide ? p.D / 8 : p.D;
-    const int64_t items = p.Hq * (pairs + (p.in_place ? 0 : rest)) + p.Hkv * (pairs + rest + vs);
-    if (items == 0) return cudaSuccess;
-    if (interleaved)
-        return e4m3 ? launch_t<true, true>(p, !wide, (int)items, st) : launch_t<true, false>(p, !wide, (int)items, st);
-    return e4m3 ? launch_t<false, true>(p, !wide, (int)items, st) : launch_t<false, false>(p, !wide, (int)items, st);
+    if (interleaved) return e4m3 ? launch_t<true, true>(p, wide, st) : launch_t<true, false>(p, wide, st);
+    return e4m3 ? launch_t<false, true>(p, wide, st) : launch_t<false, false>(p, wide, st);
 }
 
 cudaError_t launch_rope_table(const double* freq, int64_t max_pos, int64_t R, double mag, float* table,

@@ -84,6 +84,18 @@ bool make_tmap_f16_load(CUtensorMap* m, const void* base, uint64_t rows, uint64_
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_4d(CUtensorMap* m, const void* base, bool bytes, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                  const uint32_t (&box)[4], int swizzle) {
+    auto enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, s[3] = {strides[0], strides[1], strides[2]};
+    cuuint32_t b[4] = {box[0], box[1], box[2], box[3]}, estr[4] = {1, 1, 1, 1};
+    return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+               d, s, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int num_sms() {
     static int cache[kMaxDevices] = {0};
     int dev = 0;
