@@ -50,35 +50,38 @@ namespace fp8rl {
 namespace attn {
 
 constexpr uint32_t kKernelAttn = 10;
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kWarps = 4, kConsumers = kWarps * 32, kThreads = kConsumers + 32;   // and a warp that loads
 constexpr float kLazy = 8.f;                  // log2 by which a score may pass the reference before a rescale
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3.402823466e38f;     // reference of a row that has seen nothing: any score passes it
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far above any legitimate wait
 
-template <bool kE4m3_, bool kTma_, int DP_, int NT_, int WR_>
+template <bool kE4m3_, bool kTma_, int DP_, int RT_>
 struct Config {
     static constexpr bool kE4m3 = kE4m3_, kTma = kTma_;
-    static constexpr int DP = DP_;             // padded head width
-    static constexpr int NT = NT_, WR = WR_;   // 8-row tiles a warp, warps over the rows
-    static constexpr int RT = 8 * NT * WR;     // query rows of a CTA
-    static constexpr int WT = kWarps / WR;     // token groups
+    static constexpr int DP = DP_;                           // padded head width
+    static constexpr int RT = RT_, NT = RT / 8;              // query rows of a CTA, in tiles of eight
     static constexpr int ES = kE4m3 ? 1 : 2, RB = DP * ES;   // bytes of a value, of a cached head
     static constexpr int PB = RB < 128 ? RB : 128;           // row bytes of a piece of a tile
     static constexpr int CPR = RB / 16;                      // 16-byte chunks of a cached head
-    static constexpr int TT = kE4m3 && NT <= 2 ? 32 : 16, MT = TT / 16;   // tokens of a warp's tile
-    static constexpr int CT = TT * WT;                       // tokens of a CTA's tile
-    static constexpr int kStage = 2 * TT * RB;               // K and V of one group's tile
-    static constexpr int kQ = NT * DP > 256 ? NT * WR * (DP / 32) * 512 : 0;   // queries, where registers do not hold them
-    static constexpr int kPass = NT > 2 ? 2 : 1;             // parts in which the groups' sums are added
-    static constexpr int kJoin = (WT / 2) * RT * DP * 4 / kPass, kOut = RT * DP * 4;
-    static constexpr int kMerge = kJoin > kOut ? kJoin : kOut;
-    static constexpr int kCtas = DP > 128 ? 1 : 2;           // CTAs an SM
+    static constexpr int MT = RT <= 16 && RB <= (kE4m3 ? 256 : 128) ? 2 : 1;   // 16-token tiles a warp
+    static constexpr int TT = 16 * MT, CT = kWarps * TT;     // tokens of a warp, of a CTA's tile
+    static constexpr int MW = DP / 64;                       // 16-value tiles of the head a warp sums
+    static constexpr int kTile = CT * RB, kStage = 2 * kTile;
+    static constexpr int kP = RT * CT * 2;                   // probabilities, 16 bits
+    static constexpr int kQ = NT * (DP / 32) * 512;          // query operands
+    static constexpr int kSmall = RT * 4 * (kWarps + 3) + 12 * 8 + 16;
+    static constexpr int kCtas = DP > 128 ? 1 : kE4m3 && RT < 64 ? 3 : 2;   // CTAs an SM
     static constexpr int kBudget = 233472 / kCtas - 1024;    // 228 KB an SM, 1 KB of it kept for each CTA
-    static constexpr int kRest = kMerge + kQ + WT * RT * 8 + 6 * WT * 8 + 16;
-    static constexpr int kFit = (kBudget - kRest - 1024) / (WT * kStage);   // 1 KB to align the ring
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static constexpr int kSmem = kStages * WT * kStage + kRest + 1024;
+    static constexpr int kRest = kP + kQ + kSmall;
+    static constexpr int kFit = (kBudget - kRest) / kStage;
+    // 128 KB in flight on an SM keep HBM busy.  More is slower: three tiles a CTA
+    // instead of two took 698 us where these take 631 (128 sequences, bf16).
+    static constexpr int kWant = 131072 / (kCtas * kStage) > 2 ? 131072 / (kCtas * kStage) : 2;
+    static constexpr int kStages = kFit < kWant ? kFit : kWant < 6 ? kWant : 6;
+    static constexpr int kSmem = kStages * kStage + kRest;
+    // what an item costs a CTA beside its tiles (queries, result), in tiles
+    static constexpr int kItem = 65536 / kStage > 1 ? 65536 / kStage : 1;
     static_assert(kStages >= 2, "too little shared memory for two stages");
 };
 
@@ -88,45 +91,49 @@ struct Config {
 struct Span {
     int start, lo, len, tiles;
 };
+template <bool kL2 = false>
 __device__ __forceinline__ Span span_of(const AttnParams& p, int b, int ct) {
     Span s;
-    s.len = min(max(p.lens[b], 0), p.max_len);
+    s.len = min(max(kL2 ? __ldcg(p.lens + b) : p.lens[b], 0), p.max_len);
     s.lo = p.window ? max(0, s.len - p.Lq + 1 - p.window) : 0;
     s.start = s.lo & -p.box;
     s.tiles = max(1, (s.len - s.start + ct - 1) / ct);
     return s;
 }
 
-// The whole warp: units of sequences [0, b_end), and of all; hr items a sequence.
-__device__ __forceinline__ void count_units(const AttnParams& p, int ct, int hr, int b_end, int64_t* before,
-                                            int64_t* total) {
+// Places in the order of all work: an item takes kItem places, then one a tile.
+// The whole warp: places of sequences [0, b_end), and of all; hr items a sequence.
+template <class C, bool kL2 = false>
+__device__ __forceinline__ void count_places(const AttnParams& p, int hr, int b_end, int64_t* before, int64_t* total) {
     const int lane = threadIdx.x & 31;
     int64_t x = 0, y = 0;
+#pragma unroll 4
     for (int b = lane; b < p.B; b += 32) {
-        const int n = span_of(p, b, ct).tiles;
+        const int n = span_of<kL2>(p, b, C::CT).tiles + C::kItem;
         y += n;
         if (b < b_end) x += n;
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
-        x += __shfl_xor_sync(0xffffffffu, x, off);
+        if (b_end) x += __shfl_xor_sync(0xffffffffu, x, off);
         y += __shfl_xor_sync(0xffffffffu, y, off);
     }
     *before = x * hr;
     *total = y * hr;
 }
 
-__device__ __forceinline__ int64_t chunk_of(int64_t total, int ctas) { return (total + ctas - 1) / ctas; }
+__device__ __forceinline__ int64_t div_ceil(int64_t a, int b) {
+    return (a + b - 1) >> 32 ? (a + b - 1) / b : (uint32_t)(a + b - 1) / (uint32_t)b;
+}
 
 // ---------------------------------------------------------------- PTX
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// The thread's copies so far count as its arrival on the barrier when they are done.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -138,10 +145,8 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
+__device__ __forceinline__ void ldsm2_t(uint32_t (&r)[2], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
 }
 template <bool kF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -163,6 +168,11 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t v, uint32_t& lo, uint32_t& h
         : "=r"(lo), "=r"(hi)
         : "r"(v));
 }
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -181,11 +191,32 @@ __device__ __forceinline__ float ex2(float x) {
 template <class C>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
     if constexpr (C::RB >= 128)
-        return (uint32_t)((c >> 3) * (C::TT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+        return (uint32_t)((c >> 3) * (C::CT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
     else
         return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
+// The same for the probabilities: row of a query, chunk of eight tokens.
+template <class C>
+__device__ __forceinline__ uint32_t swz_p(int r, int c) {
+    return (uint32_t)((c >> 3) * (C::RT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void ldsm2(uint32_t (&r)[2], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+__device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm2_t(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
 
+// Brings an address's sector to L1 (the value is not used).
+__device__ __forceinline__ void touch_l1(const void* p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+}
 __device__ __forceinline__ void st_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
@@ -222,16 +253,19 @@ __device__ __forceinline__ void st_zero(uint32_t addr) {
 
 // ---------------------------------------------------------------- the kernel
 
-// A position in the CTA's range of units.
+// A tile of the CTA's range; `place` counts from the range's first.
 struct Cursor {
     Span s;
-    int b, hr, tile;
-    __device__ __forceinline__ void next(const AttnParams& p, int ct, int hr_n) {
+    int b, hr, tile, place;
+    template <class C>
+    __device__ __forceinline__ void next(const AttnParams& p, int hr_n) {
+        ++place;
         if (++tile < s.tiles) return;
         tile = 0;
+        place += C::kItem;
         if (++hr < hr_n) return;
         hr = 0;
-        if (++b < p.B) s = span_of(p, b, ct);
+        if (++b < p.B) s = span_of(p, b, C::CT);
     }
 };
 
@@ -239,167 +273,172 @@ template <class C>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
 attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];          // the ring first: the swizzle wants 1 KB
     constexpr bool kE = C::kE4m3, kTma = C::kTma;
-    constexpr int NT = C::NT, WR = C::WR, RT = C::RT, WT = C::WT, TT = C::TT, MT = C::MT, CT = C::CT, ES = C::ES;
-    constexpr int KS = C::DP / 16, S = C::kStages, kTile = TT * C::RB;
+    constexpr int NT = C::NT, RT = C::RT, TT = C::TT, MT = C::MT, CT = C::CT, ES = C::ES, MW = C::MW;
+    constexpr int KS = C::DP / 16, S = C::kStages;
     constexpr float kBias = kE ? 6.f : 0.f;
-    uint8_t* const smem = smem_raw + ((1024u - (sm100::smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* at_smem = smem + S * WT * C::kStage;
-    float* const merge = reinterpret_cast<float*>(at_smem);
-    uint4* const sq = reinterpret_cast<uint4*>(at_smem + C::kMerge);          // [row tile][KS / 2][lane]
-    float* const sm_m = reinterpret_cast<float*>(at_smem + C::kMerge + C::kQ);   // [WT][RT]
-    float* const sm_l = sm_m + WT * RT;
-    const uint32_t bars = sm100::smem_u32(sm_l + WT * RT);                    // [S][WT], TMA only
-    volatile int* const abort = reinterpret_cast<int*>(sm_l + WT * RT) + 2 * 6 * WT;
+    uint8_t* const smem_p = smem + S * C::kStage;
+    uint4* const sq = reinterpret_cast<uint4*>(smem_p + C::kP);               // [row tile][KS / 2][lane]
+    float* const s_fac = reinterpret_cast<float*>(smem_p + C::kP + C::kQ);    // [RT] log2 units of a unit of the product
+    int* const s_hi = reinterpret_cast<int*>(s_fac + RT);                     // [RT] tokens lo .. hi - 1 are seen
+    int* const s_lo = s_hi + RT;
+    float* const s_w = reinterpret_cast<float*>(s_lo + RT);                   // [warp][RT] maxima, sums
+    const uint32_t full = sm100::smem_u32(s_w + kWarps * RT), empty = full + 48;   // [S] each
+    volatile int* const abort = reinterpret_cast<int*>(s_w + kWarps * RT) + 24;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int tg = warp / WR, wr = warp % WR;                // token group, row group
     const int group = p.Hq / p.Hkv, rows = group * p.Lq, chunks = (rows + RT - 1) / RT, hr_n = p.Hkv * chunks;
-    if constexpr (kTma) {
-        if (threadIdx.x == 0) {
-            for (int i = 0; i < S * WT; ++i) sm100::mbar_init(bars + 8 * i, 1);
-            *abort = 0;
-            sm100::fence_mbar_init();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            sm100::mbar_init(full + 8 * i, kTma ? 1 : 32);     // one arrival and its bytes, or each lane's copies
+            sm100::mbar_init(empty + 8 * i, kWarps);
+        }
+        *abort = 0;
+        sm100::fence_mbar_init();
+        if constexpr (kTma) {
             sm100::prefetch_tmap(&kmap);
             sm100::prefetch_tmap(&vmap);
         }
-        __syncthreads();
     }
+    __syncthreads();
     pdl_wait_then_release();
 
-    // the CTA's range of units, and where it begins
+    // the CTA's range of places, and its first tile
     int64_t before, total;
-    count_units(p, CT, hr_n, 0, &before, &total);
-    const int64_t chunk = chunk_of(total, gridDim.x), u0 = (int64_t)blockIdx.x * chunk;
-    if (u0 >= total) return;
-    const int count = (int)(total - u0 < chunk ? total - u0 : chunk);
-    Cursor ld;
-    int64_t item0 = 0;                                        // first unit of the sequence the range begins in
-    for (int base = 0;; base += 32) {
-        const int b = base + lane;
-        const int n = b < p.B ? span_of(p, b, CT).tiles : 0;
-        if (blockIdx.x == 0 && warp == 0 && b < p.B && (p.lens[b] < 0 || p.lens[b] > p.max_len))
-            atomicCAS(p.err, 0u, (kKernelAttn << 24) | (1u << 16) | 2u);
+    count_places<C>(p, hr_n, 0, &before, &total);
+    const int64_t chunk = div_ceil(total, gridDim.x), u0 = (int64_t)blockIdx.x * chunk;
+    const int size = (int)(total - u0 < chunk ? total - u0 : chunk);
+    if (sm100::smem_u32(smem) & 1023u) {                       // as the runtime places it; nothing below would fit
+        if (threadIdx.x == 0) atomicCAS(p.err, 0u, (kKernelAttn << 24) | (4u << 16) | 2u);
+        return;
+    }
+    if (blockIdx.x == 0 && warp == 0)
+        for (int b = lane; b < p.B; b += 32)
+            if (p.lens[b] < 0 || p.lens[b] > p.max_len) atomicCAS(p.err, 0u, (kKernelAttn << 24) | (1u << 16) | 2u);
+    if (size <= 0) return;
+    Cursor at;
+    int64_t base = 0;                                         // first place of the sequence the range begins in
+    for (int b0 = 0;; b0 += 32) {
+        const int n = b0 + lane < p.B ? span_of(p, b0 + lane, C::CT).tiles + C::kItem : 0;
         int64_t inc = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += o;
         }
-        const uint32_t in = __ballot_sync(0xffffffffu, item0 + inc * hr_n > u0);
-        if (in && blockIdx.x != 0) {
-            const int l = __ffs((int)in) - 1;
-            item0 += __shfl_sync(0xffffffffu, (inc - n) * hr_n, l);
-            ld.b = base + l;
-            break;
-        }
-        if (blockIdx.x == 0 && base + 32 >= p.B) {            // this one has looked at every length
-            item0 = 0, ld.b = 0;
-            break;
-        }
-        if (blockIdx.x != 0) item0 += __shfl_sync(0xffffffffu, inc * hr_n, 31);
+        const uint32_t in = __ballot_sync(0xffffffffu, base + inc * hr_n > u0);
+        const int l = in ? __ffs((int)in) - 1 : 31;
+        base += __shfl_sync(0xffffffffu, (in ? inc - n : inc) * hr_n, l);
+        at.b = b0 + l;
+        if (in) break;
     }
-    ld.s = span_of(p, ld.b, CT);
-    ld.hr = (int)((u0 - item0) / ld.s.tiles);
-    ld.tile = (int)((u0 - item0) - (int64_t)ld.hr * ld.s.tiles);
-    Cursor at = ld;
+    at.s = span_of(p, at.b, C::CT);
+    {
+        const int64_t in = u0 - base;                         // below 2^31 items of a sequence
+        const int each = at.s.tiles + C::kItem;
+        at.hr = (int)(in >> 32 ? in / each : (uint32_t)in / (uint32_t)each);
+        at.tile = max(0, (int)(in - (int64_t)at.hr * each) - C::kItem);
+        at.place = (int)((int64_t)at.hr * each + C::kItem + at.tile - in);
+    }
+    if (at.place >= size) return;                             // the range ends before its first tile
 
-    // The loader fills the group's ring, a tile a stage, S - 1 tiles ahead.  Pages
-    // are looked up one tile before they are used, by one lane a box (copy engine)
-    // or a lane a token.
-    const uint32_t ring = sm100::smem_u32(smem) + tg * C::kStage;      // stage s: + s * WT * kStage
-    const int unit = kTma ? p.box : 1;                                  // tokens a lane looks up
-    auto lookup = [&](const Cursor& c) -> int64_t {           // -1: nothing to load
-        const int i = kTma ? lane * unit : lane % TT;
-        const int j = c.s.start + c.tile * CT + tg * TT + i;
-        if (i >= TT || j >= c.s.len) return -1;
-        const int pg = j / p.page_size;
-        int page = p.pages[c.b * p.pages_seq + pg];
-        if ((uint32_t)page >= (uint64_t)p.num_pages) {
-            atomicCAS(p.err, 0u, (kKernelAttn << 24) | (2u << 16) | 2u);
-            page = 0;
+    const uint32_t ring = sm100::smem_u32(smem);              // a tile a slot
+    auto head_of = [&](const Cursor& c) { return chunks == 1 ? c.hr : c.hr / chunks; };
+    bool dead = false;                                        // a wait ran out: nothing more is loaded or waited for
+    auto wait = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+        if (!dead && !sm100::mbar_wait_bounded(bar, parity, abort, kWaitLimitNs)) {
+            if (lane == 0) atomicCAS(p.err, 0u, (kKernelAttn << 24) | (site << 16) | 1u);
+            *abort = 1;
+            dead = true;
         }
-        if constexpr (kTma) return ((int64_t)page << 32) | (uint32_t)(j - pg * p.page_size);
-        return (page * p.c_page + (int64_t)(j - pg * p.page_size) * p.c_token + (c.hr / chunks) * p.c_head) * ES;
+        dead = __any_sync(0xffffffffu, dead);
     };
-    const bool loads = !kTma || wr == 0;
-    int issued = 0, armed = 0;
-    bool dead = false;                                        // a wait ran out: nothing more is loaded or computed
-    int64_t off = loads ? lookup(ld) : 0;
-    auto issue = [&]() {
-        if (issued < count && loads && !dead) {
-            const uint32_t slot = issued % S, dst = ring + slot * (WT * C::kStage);
+
+    // The loading warp keeps every slot full; nothing it does is on the other warps'
+    // way (loads issued between their products cost 500 cycles a tile).  By the copy
+    // engine a lane takes a box of one page, else each lane copies 16 bytes a turn.
+    if (warp == kWarps) {
+        auto page_of = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
+        auto page_at = [&](int pg) {
+            int page = p.pages[at.b * p.pages_seq + pg];
+            if ((uint32_t)page >= (uint64_t)p.num_pages) {
+                atomicCAS(p.err, 0u, (kKernelAttn << 24) | (2u << 16) | 2u);
+                page = 0;
+            }
+            return page;
+        };
+        int n = 0;
+#pragma unroll 1
+        for (bool first = true; at.place < size; at.next<C>(p, hr_n), ++n, first = false) {
+            const int c0 = at.s.start + at.tile * CT, h = head_of(at);
+            if (first || (at.tile & 15) == 0) {               // page numbers to L1 ahead of their use, a tile a lane
+                const int64_t j = c0 + (int64_t)lane * CT;
+                if (j < at.s.len) touch_l1(p.pages + at.b * p.pages_seq + page_of((int)j));
+            }
+            const uint32_t slot = n % S, bar = full + 8 * slot, dst = ring + slot * C::kStage;
             if constexpr (kTma) {
-                const uint32_t bar = bars + 8 * (slot * WT + tg);
-                const uint32_t n = __popc(__ballot_sync(0xffffffffu, off >= 0));
-                ++armed;
-                if (lane == 0) sm100::mbar_arrive_expect_tx(bar, n * 2 * unit * C::RB);
+                const int i = lane * p.box, j = c0 + i;
+                const bool load = i < CT && j < at.s.len;
+                const int pg = load ? page_of(j) : 0, page = load ? page_at(pg) : 0, row = j - pg * p.page_size;
+                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, load));
+                if (n >= S) wait(empty + 8 * slot, (n / S - 1) & 1, 5);
+                if (dead) break;
+                if (lane == 0) sm100::mbar_arrive_expect_tx(bar, boxes * 2 * p.box * C::RB);
                 __syncwarp();
-                if (off >= 0) {
-                    const int h = ld.hr / chunks, page = (int)(off >> 32), row = (int)(uint32_t)off;
+                if (load)
 #pragma unroll
                     for (int x = 0; x < C::RB / C::PB; ++x) {
-                        const uint32_t d = dst + x * (TT * C::PB) + lane * unit * C::PB;
+                        const uint32_t d = dst + x * (CT * C::PB) + i * C::PB;
                         tma_load_4d(d, &kmap, bar, x * (C::PB / ES), p.order ? row : h, p.order ? h : row, page);
-                        tma_load_4d(d + kTile, &vmap, bar, x * (C::PB / ES), p.order ? row : h, p.order ? h : row, page);
+                        tma_load_4d(d + C::kTile, &vmap, bar, x * (C::PB / ES), p.order ? row : h, p.order ? h : row, page);
+                    }
+            } else {
+                int64_t off[CT / 32];                          // this lane's tokens' offsets in bytes, -1: no such token
+#pragma unroll
+                for (int i = 0; i < CT / 32; ++i) {
+                    const int j = c0 + i * 32 + lane;
+                    off[i] = -1;
+                    if (j < at.s.len) {
+                        const int pg = page_of(j);
+                        off[i] = (page_at(pg) * p.c_page + (int64_t)(j - pg * p.page_size) * p.c_token + h * p.c_head) * ES;
                     }
                 }
-            } else {
+                if (n >= S) wait(empty + 8 * slot, (n / S - 1) & 1, 5);
+                if (dead) break;
                 const int cpr = p.D * ES / 16;                // chunks the cache has of a head
-                constexpr int RPI = 32 / C::CPR > 0 ? 32 / C::CPR : 1;      // rows a warp covers at once
-                constexpr int kTurns = TT / RPI / WR;
+                constexpr int RPI = 32 / C::CPR;              // rows a turn
 #pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                    const int r = (wr * kTurns + i) * RPI + (C::CPR < 32 ? lane / C::CPR : 0), c = lane % C::CPR;
-                    const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                    const uint32_t n = o >= 0 && c < cpr ? 16u : 0u;
-                    const int64_t src = n ? o + c * 16 : 0;
-                    cp_async16(dst + swz<C>(r, c), static_cast<const uint8_t*>(p.kpool) + src, n);
-                    cp_async16(dst + kTile + swz<C>(r, c), static_cast<const uint8_t*>(p.vpool) + src, n);
-                }
+                for (int i = 0; i < CT / 32; ++i)
+#pragma unroll 4
+                    for (int k = 0; k < 32; k += RPI) {
+                        const int r = k + lane / C::CPR, c = lane % C::CPR;
+                        const int64_t o = __shfl_sync(0xffffffffu, off[i], r);
+                        const uint32_t bytes = o >= 0 && c < cpr ? 16u : 0u;
+                        const int64_t src = bytes ? o + c * 16 : 0;
+                        cp_async16(dst + swz<C>(i * 32 + r, c), static_cast<const uint8_t*>(p.kpool) + src, bytes);
+                        cp_async16(dst + C::kTile + swz<C>(i * 32 + r, c), static_cast<const uint8_t*>(p.vpool) + src, bytes);
+                    }
+                cp_async_arrive(bar);
             }
-            ld.next(p, CT, hr_n);
-            if (issued + 1 < count) off = lookup(ld);
         }
-        ++issued;
-        if constexpr (!kTma) cp_async_commit();
-    };
-    auto group_sync = [&]() {
-        if constexpr (WR == 1)
-            __syncwarp();
-        else
-            sm100::named_bar_sync(1 + tg, WR * 32);
-    };
-    // Tile n has landed for the whole group, whose warps are all past tile n - 1.
-    auto arrived = [&](int n) {
-        if constexpr (kTma) {
-            if (!dead && !sm100::mbar_wait_bounded(bars + 8 * (n % S * WT + tg), (n / S) & 1, abort, kWaitLimitNs)) {
-                if (lane == 0) atomicCAS(p.err, 0u, (kKernelAttn << 24) | (3u << 16) | 1u);
-                *abort = 1;
-                dead = true;
-            }
-            if constexpr (WR == 1)
-                dead = __any_sync(0xffffffffu, dead);
-            else
-                dead = sm100::bar_red_or(1 + tg, WR * 32, dead);
-        } else {
-            cp_async_wait<S - 2>();
-            group_sync();
-        }
-    };
+        if (dead)                                              // copies still in flight write to this CTA's memory
+            for (int k = n > S ? n - S : 0; k < n; ++k) sm100::mbar_drain(full + 8 * (k % S), (k / S) & 1, kWaitLimitNs);
+        return;
+    }
+    auto consumers_sync = [&]() { sm100::named_bar_sync(2, kConsumers); };
 
-    // a segment's queries, bounds and sums; columns 2t and 2t + 1 of each row tile
-    uint32_t q[C::kQ ? 1 : NT][KS][2];
-    float fac[NT][2];                          // log2 units of a unit of the product
-    int hi[NT][2], lo[NT][2];                  // tokens the columns' queries see
-    float o[NT][KS][4], ref[NT][2], sum[NT][2];
-    const float xs = p.scale * kLog2e * (kE ? *p.k_scale : 1.f);
+    // a segment's running reference and sums; columns 2t and 2t + 1 of each row tile
+    float o[NT][MW][4], ref[NT][2], sum[NT][2];
+    auto floor_of = [](float r) { return r == kNone ? 0.f : r; };
 
+    // A segment's queries into shared memory as operands, a row tile a warp, and the
+    // rows' factors and bounds.
     auto begin = [&]() {
-        const int h = at.hr / chunks, r0 = (at.hr - h * chunks) * RT + wr * 8 * NT;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        const int h = head_of(at), r0 = (at.hr - h * chunks) * RT;
+        const float xs = p.scale * kLog2e * (kE ? *p.k_scale : 1.f);
+#pragma unroll 1
+        for (int n = warp; n < NT; n += kWarps) {
             const int r = r0 + n * 8 + g, i = r / group;
             const uint16_t* src = p.q + at.b * p.q_seq + i * p.q_token + (h * group + r - i * group) * p.q_head;
             uint32_t w[KS][2];
@@ -416,7 +455,7 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                     }
                 }
             }
-            fac[n][0] = fac[n][1] = xs;
+            float fac = xs;
             if constexpr (kE) {
                 float top = 0.f;
 #pragma unroll
@@ -426,95 +465,86 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int e = (int)(__float_as_uint(top) >> 23);            // biased exponent
-                // 2^(141 - e) puts the largest at 2^14; its reciprocal goes into the factor
+                // 2^(141 - e) puts the largest in [2^14, 2^15); its reciprocal goes into the factor
                 const int up = e == 0 || e == 255 ? 0 : min(141 - e, 100);
-                const float x = __int_as_float((127 + up) << 23), down = __int_as_float((127 - up) << 23);
+                const float x = __int_as_float((127 + up) << 23);
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) w[k][c] = pack_f16x2(bf16_lo(w[k][c]) * x, bf16_hi(w[k][c]) * x);
-                fac[n][0] *= __shfl_sync(0xffffffffu, down, 8 * t);         // row 2t is held by lanes 8t .. 8t + 3
-                fac[n][1] *= __shfl_sync(0xffffffffu, down, 8 * t + 4);
-            }
-            if constexpr (C::kQ) {
-                if (tg == n % WT)
-#pragma unroll
-                    for (int k = 0; k < KS; k += 2)
-                        sq[((wr * NT + n) * (KS / 2) + k / 2) * 32 + lane] =
-                            make_uint4(w[k][0], w[k][1], w[k + 1][0], w[k + 1][1]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) q[n][k][0] = w[k][0], q[n][k][1] = w[k][1];
+                fac *= __int_as_float((127 - up) << 23);
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int rc = r0 + n * 8 + 2 * t + c;
-                hi[n][c] = rc < rows ? at.s.len - p.Lq + rc / group + 1 : 0;
-                lo[n][c] = p.window ? max(0, hi[n][c] - p.window) : 0;
-                ref[n][c] = kNone;
-                sum[n][c] = 0.f;
+            for (int k = 0; k < KS; k += 2)
+                sq[(n * (KS / 2) + k / 2) * 32 + lane] = make_uint4(w[k][0], w[k][1], w[k + 1][0], w[k + 1][1]);
+            if (t == 0) {
+                const int hi = r < rows ? at.s.len - p.Lq + i + 1 : 0;
+                s_fac[n * 8 + g] = fac;
+                s_hi[n * 8 + g] = hi;
+                s_lo[n * 8 + g] = p.window ? max(0, hi - p.window) : 0;
             }
-#pragma unroll
-            for (int k = 0; k < KS; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
-        if constexpr (C::kQ) __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            ref[n][0] = ref[n][1] = kNone;
+            sum[n][0] = sum[n][1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < MW; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
+        }
+        consumers_sync();
     };
 
-    // What the product must not meet in an edge tile.  Rows of no visible token
-    // (a whole box is loaded) become zero.  A value that only some of the queries
-    // see must not reach the others as 0 x NaN: what is not finite is added where
-    // it is seen, and taken out of the tile.  x: the tile's probabilities.
-    auto hide = [&](uint32_t vb, int t0, const float (&x)[NT][MT][4]) {
-        const int both_lo = p.window ? at.s.len - p.window : 0, both_hi = at.s.len - p.Lq + 1;   // seen by every query
-        bool bad = false;
-        for (int j = 0; j < TT; ++j) {
-            const bool none = t0 + j < at.s.lo || t0 + j >= at.s.len;
-            if (none && kTma) {
-                if (lane < C::CPR) st_zero16(vb + swz<C>(j, lane));
-            } else if (!none && (t0 + j < both_lo || t0 + j >= both_hi)) {
-                for (int d = lane; d < p.D; d += 32)
-                    bad |= !isfinite(ld_value<kE>(vb + swz<C>(j, d * ES / 16) + d * ES % 16));
-            }
-        }
-        bad = __any_sync(0xffffffffu, bad);
-        group_sync();                                         // the group's warps have all looked
-        if (bad) {
-            for (int j = 0; j < TT; ++j)
+    // A lane's row of a matrix load, as an offset in a tile; chunk c (even) is at
+    // (tile + offset) ^ (c & 7) * 16, plus whole pieces.
+    const int lane_vr = kE ? lane & 15 : (lane & 7) + (lane >> 4) * 8, lane_vc = kE ? lane >> 4 : lane >> 3 & 1;
+    const uint32_t lane_k = swz<C>(warp * TT + (lane & 15), lane >> 4), lane_v = swz<C>(lane_vr, lane_vc);
+    auto piece = [](uint32_t at, int c) -> uint32_t { return (at ^ (uint32_t)((c & 7) << 4)) + (c >> 3) * (CT * 128); };
+    // the same for a chunk known at run time
+    auto chunk_at = [](uint32_t at, int c) -> uint32_t { return (at ^ (uint32_t)((c & 7) << 4)) + (c >> 3) * (CT * 128); };
+    const uint32_t sp = sm100::smem_u32(smem_p);
+    // probabilities, stored and loaded by pairs of row tiles (where there are two)
+    const uint32_t p_lane = sp + swz_p<C>((lane >> 4 & (NT > 1 ? 1 : 0)) * 8 + (lane & 7), lane >> 3 & 1);
+    auto p_at = [](uint32_t at, int n, int c) -> uint32_t {   // row tile n, chunk c, both even
+        return (at ^ (uint32_t)((c & 7) << 4)) + (c >> 3) * (RT * 128) + n * 1024;
+    };
+
+    // The tile's values that are not finite and that only some of the queries see:
+    // added where they are seen, then taken out of the warp's part of the tile, which
+    // no other warp reads.
+    auto settle = [&](uint32_t vb, int ct0) {
+        for (int j = 0; j < CT; ++j)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float w0 = 0.f, w1 = 0.f;                  // the token's probabilities in columns 2t, 2t + 1
+            for (int k = 0; k < MW; ++k)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const float y0 = __shfl_sync(0xffffffffu, j & 8 ? x[n][m][2] : x[n][m][0], (j & 7) * 4 + t);
-                        const float y1 = __shfl_sync(0xffffffffu, j & 8 ? x[n][m][3] : x[n][m][1], (j & 7) * 4 + t);
-                        if (m == j >> 4) w0 = y0, w1 = y1;
-                    }
-                    const bool see0 = t0 + j < hi[n][0] && t0 + j >= lo[n][0];
-                    const bool see1 = t0 + j < hi[n][1] && t0 + j >= lo[n][1];
+                for (int e = 0; e < 2; ++e) {
+                    const int d = (warp * MW + k) * 16 + (kE ? 2 * g + e : g + 8 * e);
+                    const uint32_t a = vb + swz<C>(j, d * ES / 16) + d * ES % 16;
+                    const float v = ld_value<kE>(a);
+                    if (isfinite(v)) continue;
 #pragma unroll
-                    for (int k = 0; k < KS; ++k)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int d = kE ? 16 * k + 2 * g + e : 16 * k + g + 8 * e;
-                            const float v = ld_value<kE>(vb + swz<C>(j, d * ES / 16) + d * ES % 16);
-                            if (!isfinite(v) && see0) o[n][k][2 * e] += w0 * v;
-                            if (!isfinite(v) && see1) o[n][k][2 * e + 1] += w1 * v;
+                        for (int c = 0; c < 2; ++c) {
+                            const int r = n * 8 + 2 * t + c;
+                            const uint32_t w = *reinterpret_cast<const uint16_t*>(smem_p + swz_p<C>(r, j / 8) + (j & 7) * 2);
+                            const float pr = kE ? __half2float(__ushort_as_half((unsigned short)w)) : __uint_as_float(w << 16);
+                            if (ct0 + j < s_hi[r] && ct0 + j >= s_lo[r]) o[n][k][2 * e + c] += pr * v;
                         }
                 }
-            group_sync();                                     // and added
-            for (int i = lane; i < TT * p.D; i += 32) {
-                const int j = i / p.D, d = i - j * p.D;
-                const uint32_t a = vb + swz<C>(j, d * ES / 16) + d * ES % 16;
-                if (!isfinite(ld_value<kE>(a))) st_zero<kE>(a);
-            }
-            group_sync();
+        __syncwarp();
+        for (int i = lane; i < CT * 16 * MW; i += 32) {
+            const int j = i / (16 * MW), d = warp * MW * 16 + i - j * (16 * MW);
+            const uint32_t a = vb + swz<C>(j, d * ES / 16) + d * ES % 16;
+            if (!isfinite(ld_value<kE>(a))) st_zero<kE>(a);
         }
-        if constexpr (kTma) sm100::fence_proxy_async_smem();  // the copy engine writes these rows next
+        if constexpr (kTma) sm100::fence_proxy_async_smem();
+        __syncwarp();
     };
 
-    auto compute = [&](uint32_t kb, int t0) {
-        const uint32_t vb = kb + kTile;
-        // S^T = K Q^T
+    auto compute = [&](uint32_t kb, int ct0) {
+        const uint32_t vb = kb + C::kTile, ka = kb + lane_k, va = vb + lane_v;
+        const int t0 = ct0 + warp * TT;                       // this warp's first token
+        // S^T = K Q^T over the warp's tokens
         float s[NT][MT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -522,68 +552,52 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             for (int m = 0; m < MT; ++m) s[n][m][0] = s[n][m][1] = s[n][m][2] = s[n][m][3] = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; k += 2) {
-            uint32_t b[NT][4];                                // queries of steps k and k + 1
+            uint32_t a0[MT][4], a1[MT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if constexpr (C::kQ) {
-                    const uint4 v = sq[((wr * NT + n) * (KS / 2) + k / 2) * 32 + lane];
-                    b[n][0] = v.x, b[n][1] = v.y, b[n][2] = v.z, b[n][3] = v.w;
+            for (int m = 0; m < MT; ++m) {
+                if constexpr (kE) {
+                    uint32_t w[4];
+                    ldsm4(w, piece(ka, k) + m * 16 * C::PB);
+                    e4m3x4_f16(w[0], a0[m][0], a0[m][2]);
+                    e4m3x4_f16(w[1], a0[m][1], a0[m][3]);
+                    e4m3x4_f16(w[2], a1[m][0], a1[m][2]);
+                    e4m3x4_f16(w[3], a1[m][1], a1[m][3]);
                 } else {
-                    b[n][0] = q[n][k][0], b[n][1] = q[n][k][1], b[n][2] = q[n][k + 1][0], b[n][3] = q[n][k + 1][1];
+                    ldsm4(a0[m], piece(ka, 2 * k) + m * 16 * C::PB);
+                    ldsm4(a1[m], piece(ka, 2 * k + 2) + m * 16 * C::PB);
                 }
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int r = m * 16 + (lane & 15);
-                uint32_t a0[4], a1[4];
-                if constexpr (kE) {
-                    uint32_t w[4];
-                    ldsm4(w, kb + swz<C>(r, k + (lane >> 4)));
-                    e4m3x4_f16(w[0], a0[0], a0[2]);
-                    e4m3x4_f16(w[1], a0[1], a0[3]);
-                    e4m3x4_f16(w[2], a1[0], a1[2]);
-                    e4m3x4_f16(w[3], a1[1], a1[3]);
-                } else {
-                    ldsm4(a0, kb + swz<C>(r, 2 * k + (lane >> 4)));
-                    ldsm4(a1, kb + swz<C>(r, 2 * k + 2 + (lane >> 4)));
+            for (int n = 0; n < NT; ++n) {
+                const uint4 v = sq[(n * (KS / 2) + k / 2) * 32 + lane];          // steps k and k + 1
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    mma16816<kE>(s[n][m], a0[m], v.x, v.y);
+                    mma16816<kE>(s[n][m], a1[m], v.z, v.w);
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816<kE>(s[n][m], a0, b[n][0], b[n][1]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816<kE>(s[n][m], a1, b[n][2], b[n][3]);
             }
         }
         // log2 scores above the running reference; tokens that a query does not see at -inf
-        const bool edge = t0 + TT > at.s.len - p.Lq + 1 || (p.window && t0 < at.s.len - p.window);
+        const bool edge = ct0 + CT > at.s.len - p.Lq + 1 || (p.window && ct0 < at.s.len - p.window);
         float x[NT][MT][4];
-        uint32_t seen = 0xffffffffu;
-        if (edge) {
-            seen = 0;
+        auto relative = [&]() {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                const float2 f = *reinterpret_cast<const float2*>(s_fac + n * 8 + 2 * t);
+                int2 hi = make_int2(0, 0), lo = make_int2(0, 0);
+                if (edge) {
+                    hi = *reinterpret_cast<const int2*>(s_hi + n * 8 + 2 * t);
+                    lo = *reinterpret_cast<const int2*>(s_lo + n * 8 + 2 * t);
+                }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
+                        x[n][m][e] = fmaf(s[n][m][e], e & 1 ? f.y : f.x, -ref[n][e & 1]);
                         const int j = t0 + m * 16 + g + 8 * (e >> 1);
-                        seen |= (uint32_t)(j < hi[n][e & 1] && j >= lo[n][e & 1]) << ((n * MT + m) * 4 + e);
+                        if (edge && (j >= (e & 1 ? hi.y : hi.x) || j < (e & 1 ? lo.y : lo.x))) x[n][m][e] = -INFINITY;
                     }
-        }
-        auto relative = [&]() {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[n][m][e] = fmaf(s[n][m][e], fac[n][e & 1], -ref[n][e & 1]);
-            if (edge)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!(seen >> ((n * MT + m) * 4 + e) & 1)) x[n][m][e] = -INFINITY;
+            }
         };
         relative();
         float top = -INFINITY;
@@ -592,8 +606,27 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 top = fmaxf(top, fmaxf(fmaxf(x[n][m][0], x[n][m][1]), fmaxf(x[n][m][2], x[n][m][3])));
-        // the maximum is only reduced over the lanes when some score passes the room
-        if (__any_sync(0xffffffffu, top > kLazy + kBias)) {
+        // The reference is the CTA's; maxima are only taken when some score passes the
+        // room.  This barrier also says that every warp is done with the tile before.
+        if (sm100::bar_red_or(1, kConsumers, top > kLazy + kBias)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 f = *reinterpret_cast<const float2*>(s_fac + n * 8 + 2 * t);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float r = kNone;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = c; e < 4; e += 2)
+                            if (x[n][m][e] != -INFINITY) r = fmaxf(r, s[n][m][e] * (c ? f.y : f.x) - kBias);
+                    r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 4));
+                    r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 8));
+                    r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 16));
+                    if (g == 0) s_w[warp * RT + n * 8 + 2 * t + c] = r;
+                }
+            }
+            consumers_sync();
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float f[2];
@@ -601,25 +634,19 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 for (int c = 0; c < 2; ++c) {
                     float r = ref[n][c];
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int e = c; e < 4; e += 2)
-                            if (seen >> ((n * MT + m) * 4 + e) & 1) r = fmaxf(r, s[n][m][e] * fac[n][c] - kBias);
-                    r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 4));
-                    r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 8));
-                    r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 16));
+                    for (int w = 0; w < kWarps; ++w) r = fmaxf(r, s_w[w * RT + n * 8 + 2 * t + c]);
                     f[c] = ex2(ref[n][c] - r);
                     ref[n][c] = r;
                     sum[n][c] *= f[c];
                 }
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
+                for (int k = 0; k < MW; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[n][k][e] *= f[e & 1];
             }
             relative();
         }
-        uint32_t pt[NT][MT][2];
+        uint32_t pk[NT][MT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -628,40 +655,91 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 for (int e = 0; e < 4; ++e) x[n][m][e] = ex2(x[n][m][e]);
                 sum[n][0] += x[n][m][0] + x[n][m][2];
                 sum[n][1] += x[n][m][1] + x[n][m][3];
-                pt[n][m][0] = transpose8x8(kE ? pack_f16x2(x[n][m][0], x[n][m][1]) : pack_bf16x2(x[n][m][0], x[n][m][1]));
-                pt[n][m][1] = transpose8x8(kE ? pack_f16x2(x[n][m][2], x[n][m][3]) : pack_bf16x2(x[n][m][2], x[n][m][3]));
+                pk[n][m][0] = kE ? pack_f16x2(x[n][m][0], x[n][m][1]) : pack2_bf16(x[n][m][0], x[n][m][1]);
+                pk[n][m][1] = kE ? pack_f16x2(x[n][m][2], x[n][m][3]) : pack2_bf16(x[n][m][2], x[n][m][3]);
             }
-        if (edge) hide(vb, t0, x);
-        // O^T += V^T P^T
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m) {
+            const int c = (warp * MT + m) * 2;
+            if constexpr (NT == 1) {
+                stsm2_t(p_at(p_lane, 0, c), pk[0][m][0], pk[0][m][1]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < KS; k += 2) {
-                uint32_t a0[4], a1[4];
-                if constexpr (kE) {
+                for (int n = 0; n < NT; n += 2)
+                    stsm4_t(p_at(p_lane, n, c), pk[n][m][0], pk[n][m][1], pk[n + 1][m][0], pk[n + 1][m][1]);
+            }
+        }
+        // What the product must not meet.  Rows of no visible token (a whole box is
+        // loaded) become zero.  A value that only some of the queries see must not
+        // reach the others as 0 x NaN: looked for here, settled below.
+        bool bad = false;
+        if (edge) {
+            const int both_lo = p.window ? at.s.len - p.window : 0, both_hi = at.s.len - p.Lq + 1;   // seen by every query
+            for (int i = 0; i < TT; ++i) {
+                const int j = t0 + i, r = warp * TT + i;
+                const bool none = j < at.s.lo || j >= at.s.len;
+                if (none && kTma) {
+                    if (lane < C::CPR) st_zero16(vb + swz<C>(r, lane));
+                } else if (!none && (j < both_lo || j >= both_hi)) {
+                    for (int d = lane; d < p.D; d += 32)
+                        bad |= !isfinite(ld_value<kE>(vb + swz<C>(r, d * ES / 16) + d * ES % 16));
+                }
+            }
+            if constexpr (kTma) sm100::fence_proxy_async_smem();      // the copy engine writes these rows next
+        }
+        if (sm100::bar_red_or(1, kConsumers, bad)) settle(vb, ct0);
+        // O^T += V^T P^T: the warp's part of the head over the CTA's tokens
+#pragma unroll
+        for (int kt = 0; kt < CT / 16; ++kt) {
+            uint32_t b[NT][2];
+            if constexpr (NT == 1) {
+                uint32_t v[2];
+                ldsm2(v, p_at(p_lane, 0, 2 * kt));
+                b[0][0] = v[0], b[0][1] = v[1];
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t v[4];
+                    ldsm4(v, p_at(p_lane, n, 2 * kt));
+                    b[n][0] = v[0], b[n][1] = v[1], b[n + 1][0] = v[2], b[n + 1][1] = v[3];
+                }
+            }
+            const uint32_t row = kt * 16 * C::PB;
+            uint32_t a[MW][4];
+            if constexpr (kE && MW == 1) {                    // one chunk of the head: 16 tokens of it
+                uint32_t w[2];
+                ldsm2_t(w, vb + swz<C>(kt * 16 + (lane & 15), warp));
+                e4m3x4_f16(__byte_perm(w[0], 0, 0x3120), a[0][0], a[0][1]);
+                e4m3x4_f16(__byte_perm(w[1], 0, 0x3120), a[0][2], a[0][3]);
+            } else if constexpr (kE) {
+#pragma unroll
+                for (int k = 0; k < MW; k += 2) {
                     uint32_t w[4];
-                    ldsm4_t(w, vb + swz<C>(m * 16 + (lane & 15), k + (lane >> 4)));
-                    e4m3x4_f16(__byte_perm(w[0], 0, 0x3120), a0[0], a0[1]);
-                    e4m3x4_f16(__byte_perm(w[1], 0, 0x3120), a0[2], a0[3]);
-                    e4m3x4_f16(__byte_perm(w[2], 0, 0x3120), a1[0], a1[1]);
-                    e4m3x4_f16(__byte_perm(w[3], 0, 0x3120), a1[2], a1[3]);
-                } else {
-                    const int r = m * 16 + (lane & 7) + (lane >> 4) * 8;
-                    ldsm4_t(a0, vb + swz<C>(r, 2 * k + ((lane >> 3) & 1)));
-                    ldsm4_t(a1, vb + swz<C>(r, 2 * k + 2 + ((lane >> 3) & 1)));
+                    ldsm4_t(w, chunk_at(va, warp * MW + k) + row);
+                    e4m3x4_f16(__byte_perm(w[0], 0, 0x3120), a[k][0], a[k][1]);
+                    e4m3x4_f16(__byte_perm(w[1], 0, 0x3120), a[k][2], a[k][3]);
+                    e4m3x4_f16(__byte_perm(w[2], 0, 0x3120), a[k + 1][0], a[k + 1][1]);
+                    e4m3x4_f16(__byte_perm(w[3], 0, 0x3120), a[k + 1][2], a[k + 1][3]);
                 }
+            } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma16816<kE>(o[n][k], a0, pt[n][m][0], pt[n][m][1]);
-                    mma16816<kE>(o[n][k + 1], a1, pt[n][m][0], pt[n][m][1]);
-                }
+                for (int k = 0; k < MW; ++k) ldsm4_t(a[k], chunk_at(va, (warp * MW + k) * 2) + row);
             }
+#pragma unroll
+            for (int k = 0; k < MW; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<kE>(o[n][k], a[k], b[n][0], b[n][1]);
+        }
     };
 
-    // The groups' sums of a segment made one and written: the result if the item
-    // lies wholly in this CTA's range, else one of the CTA's two slots.
-    auto finish = [&](int64_t u) {                            // u: the segment's last unit
-        float L[NT][2], M[NT][2];
+    // A segment's sums made one and written: the result if the item lies wholly in
+    // this CTA's range, else one of the CTA's two slots.  Each warp has its part of
+    // the head for every row.
+    auto finish = [&]() {
+        const int first = at.place - at.tile;                 // the item's tiles: first .. first + tiles - 1
+        const bool whole = first >= 0 && first + at.s.tiles <= size;
+        const int h = head_of(at), r0 = (at.hr - h * chunks) * RT;
+        float* const slot = p.ws + ((int64_t)blockIdx.x * 2 + (first <= 0 ? 0 : 1)) * (RT * (C::DP + 2));
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -670,117 +748,79 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                const int r = wr * 8 * NT + n * 8 + 2 * t + c;
-                if (g == 0) sm_m[tg * RT + r] = ref[n][c], sm_l[tg * RT + r] = x;
+                if (g == 0) s_w[warp * RT + n * 8 + 2 * t + c] = x;
             }
-        __syncthreads();
+        consumers_sync();
+        const float vs = kE ? *p.v_scale : 1.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int r = wr * 8 * NT + n * 8 + 2 * t + c;
-                float m = kNone, l = 0.f;
+                const int r = n * 8 + 2 * t + c, rr = r0 + r;
+                float l = 0.f;
 #pragma unroll
-                for (int w = 0; w < WT; ++w) m = fmaxf(m, sm_m[w * RT + r]);
+                for (int w = 0; w < kWarps; ++w) l += s_w[w * RT + r];
+                const bool mine = warp == 0 && g == 0;
+                if (whole) {
+                    if (rr >= rows) continue;
+                    const int qi = rr / group;
+                    const int64_t row = ((int64_t)at.b * p.Lq + qi) * p.Hq + h * group + rr - qi * group;
+                    const float f = l == 0.f ? 0.f : vs / l;
 #pragma unroll
-                for (int w = 0; w < WT; ++w) l += sm_l[w * RT + r] * ex2(sm_m[w * RT + r] - m);
-                const float f = ex2(ref[n][c] - m);
-#pragma unroll
-                for (int k = 0; k < KS; ++k) o[n][k][c] *= f, o[n][k][c + 2] *= f;
-                M[n][c] = m, L[n][c] = l;
-            }
-        // the groups' sums, halved in number at each step, kPass parts of the head a step
-        constexpr int KP = KS / C::kPass;
-        auto place = [&](int n, int k, int e, int width) {     // [row][value] of a sum
-            const int d = kE ? 16 * k + 2 * g + (e >> 1) : 16 * k + g + 8 * (e >> 1);
-            return (wr * 8 * NT + n * 8 + 2 * t + (e & 1)) * width + d;
-        };
-#pragma unroll
-        for (int half = WT / 2; half >= 1; half /= 2)
-#pragma unroll
-            for (int part = 0; part < C::kPass; ++part) {
-                constexpr int W = 16 * KP;
-                if (tg >= half && tg < 2 * half)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < KP; ++k)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                merge[(tg - half) * RT * W + place(n, k, e, W)] = o[n][part * KP + k][e];
-                __syncthreads();
-                if (tg < half)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < KP; ++k)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                o[n][part * KP + k][e] += merge[tg * RT * W + place(n, k, e, W)];
-                __syncthreads();
-            }
-        if (tg == 0) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) merge[place(n, k, e, C::DP)] = o[n][k][e];
-                if (g == 0)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int r = wr * 8 * NT + n * 8 + 2 * t + c;
-                        sm_m[r] = M[n][c], sm_l[r] = L[n][c];
+                    for (int k = 0; k < MW; ++k) {
+                        const int d = (warp * MW + k) * 16 + (kE ? 2 * g : g);
+                        const float v0 = l == 0.f ? 0.f : o[n][k][c] * f, v1 = l == 0.f ? 0.f : o[n][k][c + 2] * f;
+                        uint16_t* to = p.o + row * p.D + d;
+                        if constexpr (kE) {
+                            if (d < p.D) *reinterpret_cast<uint32_t*>(to) = pack2_bf16(v0, v1);
+                        } else if (d < p.D) {
+                            const uint32_t v = pack2_bf16(v0, v1);
+                            to[0] = (uint16_t)v, to[8] = (uint16_t)(v >> 16);
+                        }
                     }
+                    if (p.lse && mine) p.lse[row] = l == 0.f ? -INFINITY : (ref[n][c] + log2f(l)) * kLn2;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < MW; ++k) {
+                        float* to = slot + r * C::DP + (warp * MW + k) * 16 + (kE ? 2 * g : g);
+                        if constexpr (kE)
+                            *reinterpret_cast<float2*>(to) = make_float2(o[n][k][c], o[n][k][c + 2]);
+                        else
+                            to[0] = o[n][k][c], to[8] = o[n][k][c + 2];
+                    }
+                    if (mine) slot[RT * C::DP + r] = ref[n][c], slot[RT * C::DP + RT + r] = l;
+                }
             }
-        }
-        __syncthreads();
-        const int64_t first = u - at.tile;                    // the item's units: first .. first + tiles - 1
-        const bool whole = first >= u0 && first + at.s.tiles <= u0 + count;
-        const int h = at.hr / chunks, r0 = (at.hr - h * chunks) * RT;
-        if (whole) {
-            const float vs = kE ? *p.v_scale : 1.f;
-            for (int i = threadIdx.x; i < RT * (C::DP / 4); i += kThreads) {
-                const int r = i / (C::DP / 4), d = (i - r * (C::DP / 4)) * 4, rr = r0 + r;
-                if (rr >= rows || d >= p.D) continue;
-                const float l = sm_l[r], f = l == 0.f ? 0.f : vs / l;
-                const float4 v = *reinterpret_cast<const float4*>(merge + r * C::DP + d);
-                const int qi = rr / group;
-                const int64_t row = ((int64_t)at.b * p.Lq + qi) * p.Hq + h * group + rr - qi * group;
-                *reinterpret_cast<uint2*>(p.o + row * p.D + d) =
-                    l == 0.f ? make_uint2(0, 0)
-                             : make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
-                if (p.lse && d == 0) p.lse[row] = l == 0.f ? -INFINITY : (sm_m[r] + log2f(l)) * kLn2;
-            }
-        } else {
-            float* slot = p.ws + ((int64_t)blockIdx.x * 2 + (first <= u0 ? 0 : 1)) * (RT * (C::DP + 2));
-            for (int i = threadIdx.x; i < RT * (C::DP / 4); i += kThreads)
-                *reinterpret_cast<float4*>(slot + i * 4) = *reinterpret_cast<const float4*>(merge + i * 4);
-            for (int r = threadIdx.x; r < RT; r += kThreads) {
-                slot[RT * C::DP + r] = sm_m[r];
-                slot[RT * C::DP + RT + r] = sm_l[r];
-            }
-        }
-        __syncthreads();
     };
 
+    // The next segment's queries are brought to L1 while this one finishes.
+    auto touch = [&](const Cursor& c) {
+        const int h = head_of(c), r0 = (c.hr - h * chunks) * RT;
+        for (int n = warp; n < NT; n += kWarps) {
+            const int r = r0 + n * 8 + g, i = r / group;
+            const uint16_t* src = p.q + c.b * p.q_seq + i * p.q_token + (h * group + r - i * group) * p.q_head;
+            for (int d = t * 16; d < p.D; d += 64)            // a 32-byte sector a lane
+                if (r < rows) touch_l1(src + d);
+        }
+    };
+
+    bool fresh = true;
 #pragma unroll 1
-    for (int i = 0; i < S - 1; ++i) issue();
-    begin();
-#pragma unroll 1
-    for (int n = 0; n < count; ++n) {
-        arrived(n);
-        issue();
-        const int t0 = at.s.start + at.tile * CT + tg * TT;
-        if (t0 < at.s.len && !dead) compute(ring + (n % S) * (WT * C::kStage), t0);
-        const bool end = at.tile + 1 == at.s.tiles || n + 1 == count;
-        if (end) finish(u0 + n);
-        at.next(p, CT, hr_n);
-        if (end && n + 1 < count) begin();
+    for (int n = 0; at.place < size; ++n) {
+        if (fresh) begin();
+        wait(full + 8 * (n % S), (n / S) & 1, 3);
+        compute(ring + (n % S) * C::kStage, at.s.start + at.tile * CT);
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(empty + 8 * (n % S));
+        Cursor then = at;
+        then.next<C>(p, hr_n);
+        fresh = then.tile == 0 || then.place >= size;
+        if (fresh) {
+            if (then.place < size) touch(then);
+            finish();
+        }
+        at = then;
     }
-    if (kTma && dead && lane == 0)                             // the copies still in flight write to this CTA's memory
-        for (int n = armed > S ? armed - S : 0; n < armed; ++n)
-            sm100::mbar_drain(bars + 8 * (n % S * WT + tg), (n / S) & 1, kWaitLimitNs);
 }
 
 // Joins the slots of the items that lie in several CTAs' ranges, in CTA order.
@@ -792,15 +832,17 @@ attn_join_kernel(const __grid_constant__ AttnParams p, int ctas, int spread) {
     constexpr int RT = C::RT, DP = C::DP, kW = 8, V4 = DP / 128 > 0 ? DP / 128 : 1;
     __shared__ float4 so[kW][DP / 4];
     __shared__ float sm[kW], sl[kW];
-    pdl_wait_then_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = p.Hq / p.Hkv, rows = group * p.Lq, chunks = (rows + RT - 1) / RT, hr_n = p.Hkv * chunks;
     const int b = blockIdx.x / hr_n, hr = blockIdx.x - b * hr_n;
+    // The lengths were there before the kernel this one follows: it started after
+    // that one had passed its own wait.  Read from L2, where they are.
     int64_t before, total;
-    count_units(p, C::CT, hr_n, b, &before, &total);
-    const Span s = span_of(p, b, C::CT);
-    const int64_t chunk = chunk_of(total, ctas), first = before + (int64_t)hr * s.tiles;
+    count_places<C, true>(p, hr_n, b, &before, &total);
+    const Span s = span_of<true>(p, b, C::CT);
+    const int64_t chunk = div_ceil(total, ctas), first = before + (int64_t)hr * (s.tiles + C::kItem) + C::kItem;
     const int c0 = (int)(first / chunk), c1 = (int)((first + s.tiles - 1) / chunk);
+    pdl_wait_then_release();
     if (c0 == c1) return;
     const int h = hr / chunks, r0 = (hr - h * chunks) * RT;
     auto slot = [&](int c) {
@@ -898,15 +940,16 @@ cudaError_t launch(const AttnParams& a, cudaStream_t st) {
     AttnParams p = a;
     CUtensorMap km = {}, vm = {};
     p.box = 1;
+    p.page_shift = p.page_size & (p.page_size - 1) ? -1 : __builtin_ctz((unsigned)p.page_size);
     if constexpr (C::kTma) {
-        p.box = C::TT;
+        p.box = C::CT;
         while (p.page_size % p.box) p.box /= 2;
         p.order = p.c_token < p.c_head && p.Hkv > 1;
         if (!make_map<C>(&km, p.kpool, p) || !make_map<C>(&vm, p.vpool, p)) return cudaErrorInvalidValue;
     }
     const int rows = p.Hq / p.Hkv * p.Lq, chunks = (rows + C::RT - 1) / C::RT;
     const int64_t items = (int64_t)p.B * p.Hkv * chunks, tiles = (p.max_len + C::CT - 1) / C::CT;
-    const int64_t most = items * (tiles > 1 ? tiles : 1), wave = (int64_t)num_sms() * C::kCtas;
+    const int64_t most = items * (tiles > 1 ? tiles + C::kItem : 1), wave = (int64_t)num_sms() * C::kCtas;
     cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int ctas = (int)(most < wave ? most : wave);
@@ -921,23 +964,18 @@ cudaError_t launch(const AttnParams& a, cudaStream_t st) {
 // a kv head x Lq): as few row tiles as hold them, so that no product is spent on
 // rows that are not there; above the largest the rows go in chunks, each reading
 // the cache again.
+template <bool kE4m3, bool kTma, int DP, class F>
+auto pick_rows(int64_t rows, F f) {
+    if (rows <= 8) return f(Config<kE4m3, kTma, DP, 8>{});
+    if (rows <= 16) return f(Config<kE4m3, kTma, DP, 16>{});
+    if (rows <= 32 || DP > 128) return f(Config<kE4m3, kTma, DP, 32>{});
+    return f(Config<kE4m3, kTma, DP, (DP > 128 ? 32 : 64)>{});
+}
 template <bool kE4m3, bool kTma, class F>
 auto pick(int64_t D, int64_t rows, F f) {
-    if (D <= 64) {
-        if (rows <= 8) return f(Config<kE4m3, kTma, 64, 1, 1>{});
-        if (rows <= 16) return f(Config<kE4m3, kTma, 64, 2, 1>{});
-        if (rows <= 32) return f(Config<kE4m3, kTma, 64, 4, 1>{});
-        return f(Config<kE4m3, kTma, 64, 4, 2>{});
-    }
-    if (D <= 128) {
-        if (rows <= 8) return f(Config<kE4m3, kTma, 128, 1, 1>{});
-        if (rows <= 16) return f(Config<kE4m3, kTma, 128, 2, 1>{});
-        if (rows <= 32) return f(Config<kE4m3, kTma, 128, 4, 1>{});
-        return f(Config<kE4m3, kTma, 128, 4, 2>{});
-    }
-    if (rows <= 8) return f(Config<kE4m3, kTma, 256, 1, 1>{});
-    if (rows <= 16) return f(Config<kE4m3, kTma, 256, 2, 1>{});
-    return f(Config<kE4m3, kTma, 256, 2, 2>{});
+    if (D <= 64) return pick_rows<kE4m3, kTma, 64>(rows, f);
+    if (D <= 128) return pick_rows<kE4m3, kTma, 128>(rows, f);
+    return pick_rows<kE4m3, kTma, 256>(rows, f);
 }
 
 }  // namespace attn
