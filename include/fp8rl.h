@@ -525,7 +525,7 @@ int fp8rl_attn_paged(const uint16_t* q, int64_t B, int64_t Lq, int64_t Hq, int64
  * u fp32 [B][K]; noise e fp32 [B][V] with its sequence stride.
  * tokens int32 [B][K+1]: the kept drafts, the new token, then -1.
  * accepted int32 [B]: n.
- * Rows past len are never read.  Bit-exact.  Limits: K <= 32, V < 2^31,
+ * Rows past len are never read.  Bit-exact.  Limits: K <= 32, V <= 2^30,
  * B <= 65535.
  * ---------------------------------------------------------------------- */
 #define FP8RL_PROB_F32 0

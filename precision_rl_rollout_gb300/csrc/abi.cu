@@ -441,7 +441,7 @@ int fp8rl_spec_verify(const void* P, int64_t p_seq, int64_t p_step, const void* 
     if (!aligned4(drafts) || !aligned4(draft_lens_or_null) || !aligned4(u) || !aligned4(noise) || !aligned4(tokens) ||
         !aligned4(accepted))
         return FP8RL_ERR_ALIGN;
-    if (K > 32 || V > INT32_MAX || B > 65535) return FP8RL_ERR_UNSUPPORTED;
+    if (K > 32 || V > (1 << 30) || B > 65535) return FP8RL_ERR_UNSUPPORTED;
     if (B == 0) return FP8RL_OK;
     VerifyParams p{};
     p.P = P, p.Q = Q_or_null, p.drafts = drafts, p.lens = draft_lens_or_null, p.u = u, p.noise = noise;

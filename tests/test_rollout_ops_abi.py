@@ -100,7 +100,7 @@ def test_verify_validation(lib):
         assert f(**{name: None}) == 1, name
     assert f(B=-1) == 2 and f(K=-1) == 2 and f(V=0) == 2 and f(ps=-1) == 2
     assert f(P=A + 2) == 3 and f(P=A + 1, dtype=1) == 3 and f(noise=A + 2) == 3 and f(tokens=A + 1) == 3
-    assert f(dtype=2) == 6 and f(K=33) == 6 and f(B=65536) == 6
+    assert f(dtype=2) == 6 and f(K=33) == 6 and f(B=65536) == 6 and f(V=(1 << 30) + 1) == 6
 
 
 def test_binding_refusals():
