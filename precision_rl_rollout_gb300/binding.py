@@ -12,9 +12,9 @@ stream of that device unless ``stream`` is given.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
 import torch
@@ -62,7 +62,7 @@ class FP8RL_PAGED_KV(ctypes.Structure):
 
 
 _lib = None
-_rope_append = _attn_paged = None        # the calls that take a cache's struct, taking it as packed bytes
+_calls = None                            # the module _calls.so
 _lock = threading.Lock()
 
 
@@ -72,7 +72,7 @@ def library_path() -> str:
 
 def load(path: str | None = None):
     """Load libfp8rl.so (built by ``precision_rl_rollout_gb300.build``)."""
-    global _lib, _rope_append, _attn_paged
+    global _lib, _calls
     with _lock:
         if _lib is not None:
             return _lib
@@ -136,13 +136,23 @@ def load(path: str | None = None):
                             "fp8rl_logits_kl_workspace_bytes", "fp8rl_attn_paged_workspace_bytes"):
                 getattr(lib, name).restype = ctypes.c_int
 
-        def packed(f):
-            g = lib[f.__name__]                        # a function object of its own
-            g.argtypes, g.restype = [P if t is KV else t for t in f.argtypes], ctypes.c_int
-            return g
-        _rope_append, _attn_paged = packed(lib.fp8rl_rope_append_paged), packed(lib.fp8rl_attn_paged)
+        _calls = _load_calls(lib)
         _lib = lib
         return lib
+
+
+def _load_calls(lib):
+    """The compiled side of the rollout step's calls, given the library's functions."""
+    if not os.path.exists(_build.CALLS_PATH):
+        raise RuntimeError(f"_calls.so not found at {_build.CALLS_PATH}: build it with "
+                           "`python -m precision_rl_rollout_gb300.build` (needs g++ and torch's headers)")
+    loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                  ("fp8rl_rope", "fp8rl_rope_append_paged", "fp8rl_attn_paged", "fp8rl_attn_paged_workspace_bytes",
+                   "fp8rl_spec_verify")), Fp8rlError)
+    return module
 
 
 def _ck(rc: int, where: str):
@@ -490,44 +500,15 @@ def fp8rl_logits_kl(P, Q, kl=None, workspace=None, stream=None):
 
 
 # ------------------------------------------------------- rollout step: positions, paged cache, drafts
-# These calls check what only Python can see (types, shapes, devices).  A decode
-# step makes them with a few microseconds of GPU work behind each, so the checks
-# are plain expressions, pointers go over as integers and the cache's struct as
-# packed bytes.  What a call allocates while a stream is given is recorded on that
-# stream, so that the caching allocator does not hand it out again too early.
+# A decode step makes these calls with a few microseconds of GPU work behind each, so
+# their checks and marshalling are compiled (csrc/calls.cpp -> _calls.so, built with
+# the library).  A wrong type, shape, stride or device is a ValueError; a status of the
+# C ABI an Fp8rlError.  What a call allocates while a stream is given is recorded on
+# that stream, so that the caching allocator does not hand it out again too early.
 
-_BF16, _F32, _F64, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64,
-                                      torch.uint8)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_pack_kv = struct.Struct("4P7qi4x").pack                      # FP8RL_PAGED_KV
-
-
-def _refuse(name, t, want):
-    raise ValueError(f"{name}: expected {want}, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-
-
-def _dense(t, dtype, shape, dev, name):
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _refuse(name, t, f"contiguous {dtype} {shape} on the call's device")
-
-
-def _heads(t, dim, dev, name):
-    """bf16 on a GPU, heads of contiguous values; -> strides."""
-    st = t.stride()
-    if t.dtype is not _BF16 or len(st) != dim or t.get_device() != dev or dev < 0 or (st[-1] != 1 and t.shape[-1] > 1):
-        _refuse(name, t, f"a {dim}-D {_BF16} CUDA tensor with contiguous head values")
-    return st
-
-
-def _on(stream, dev, *made):
-    """The raw stream of a call; tensors it made are recorded on a given one."""
-    if stream is None:
-        return _raw_stream(dev)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
-    for t in made:
-        if t is not None:
-            t.record_stream(s)
-    return s.cuda_stream
+def _given(stream, device):
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    return s, s.cuda_stream
 
 
 FP8RL_ROPE_INTERLEAVED = 1
@@ -537,104 +518,55 @@ FP8RL_ROPE_INVERSE = 2
 def fp8rl_rope_table(freq, max_pos: int, magnitude: float = 1.0, table=None, stream=None):
     """freq fp64 [R/2] (radians a position) -> table fp32 [max_pos, R]: cosines, then sines."""
     lib = load()
-    dev = freq.get_device()
-    if dev < 0 or freq.dtype is not _F64 or freq.dim() != 1 or not freq.is_contiguous():
-        _refuse("freq", freq, "a contiguous 1-D float64 CUDA tensor")
+    if not freq.is_cuda or freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_contiguous():
+        raise ValueError("freq must be a contiguous 1-D float64 CUDA tensor")
     R = 2 * freq.shape[0]
     made = table is None
-    if made:
-        table = torch.empty((max_pos, R), dtype=_F32, device=freq.device)
-    _dense(table, _F32, (max_pos, R), dev, "table")
-    _ck(lib.fp8rl_rope_table(freq.data_ptr(), max_pos, R, magnitude, table.data_ptr(),
-                             _on(stream, dev, table if made else None)), "fp8rl_rope_table")
+    table = _need(table, (max_pos, R), torch.float32, freq.device, "table")
+    if table.device != freq.device:
+        raise ValueError("table must be on freq's device")
+    _ck(lib.fp8rl_rope_table(_p(freq), max_pos, R, magnitude, _p(table), _stream(freq, stream)), "fp8rl_rope_table")
+    if made and stream is not None:
+        table.record_stream(_given(stream, freq.device)[0])
     return table
 
 
 def fp8rl_rope(X, positions, table, interleaved=False, inverse=False, Y=None, stream=None):
     """X bf16 [T, H, D] (token and head strides free), positions int32 [T], table fp32
     [max_pos, R] -> Y bf16 [T, H, D]; inverse=True: the gradient.  Y may be X."""
-    lib = _lib or load()
-    dev = X.get_device()
-    xs = _heads(X, 3, dev, "X")
-    T, H, D = X.shape
-    _dense(positions, _I32, (T,), dev, "positions")
-    max_pos, R = table.shape
-    _dense(table, _F32, (max_pos, R), dev, "table")
-    made = Y is None
-    if made:
-        Y = torch.empty((T, H, D), dtype=_BF16, device=X.device)
-    ys = _heads(Y, 3, dev, "Y")
-    if Y.shape != X.shape:
-        _refuse("Y", Y, "X's shape")
-    rc = lib.fp8rl_rope(X.data_ptr(), T, H, D, xs[0], xs[1], positions.data_ptr(), table.data_ptr(), max_pos, R,
-                        (1 if interleaved else 0) | (2 if inverse else 0), Y.data_ptr(), ys[0], ys[1],
-                        _on(stream, dev, Y if made else None))
-    if rc:
-        raise Fp8rlError(rc, "fp8rl_rope")
-    return Y
+    if _lib is None:
+        load()
+    if stream is None:
+        return _calls.rope(X, positions, table, interleaved, inverse, Y, None)
+    s, raw = _given(stream, X.device)
+    out = _calls.rope(X, positions, table, interleaved, inverse, Y, raw)
+    if Y is None:
+        out.record_stream(s)
+    return out
 
 
 FP8RL_KV_BF16 = 0
 FP8RL_KV_E4M3 = 1
 
 
-def _paged_kv(K, V, k_scale, v_scale, dev):
-    """Pools [pages, page_size, kv_heads, head_dim] (a page laid out head by head is
-    the transposed view) -> the C struct's bytes, (page_size, kv_heads, head_dim)."""
-    n, page, heads, D = K.shape
-    st = K.stride()
-    if V.shape != K.shape or V.stride() != st or st[3] != 1 or V.dtype is not K.dtype or K.get_device() != dev or \
-            V.get_device() != dev:
-        _refuse("V", V, f"K's type, shape, strides and device, {K.dtype} {tuple(K.shape)} {st} on {K.device}, "
-                        "with contiguous head values")
-    if K.dtype is _U8:
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is None:
-                raise ValueError(f"{name}: an E4M3 cache needs its scale, float32 [1]")
-            _dense(t, _F32, (1,), dev, name)
-        kv = _pack_kv(K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, page, heads, D, st[0],
-                      st[1], st[2], FP8RL_KV_E4M3)
-    elif K.dtype is _BF16:
-        kv = _pack_kv(K.data_ptr(), V.data_ptr(), 0, 0, n, page, heads, D, st[0], st[1], st[2], FP8RL_KV_BF16)
-    else:
-        _refuse("K", K, "bfloat16 values or uint8 E4M3 codes")
-    return kv, page, heads, D
-
-
 def fp8rl_rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale=None, v_scale=None, interleaved=False,
                             q_out=None, stream=None):
     """q bf16 [T, Hq, D], k and v bf16 [T, kv_heads, D] (strides free), slots int64 [T]
     -> q rotated; k rotated and v stored in the pools K, V [pages, page_size, kv_heads, D]
-    (bf16, or uint8 E4M3 codes under k_scale, v_scale fp32 [1]).  table None: no rotation."""
-    lib = _lib or load()
-    dev = q.get_device()
-    qs, ks, vs = _heads(q, 3, dev, "q"), _heads(k, 3, dev, "k"), _heads(v, 3, dev, "v")
-    T, Hq, D = q.shape
-    kv, _, kv_heads, head_dim = _paged_kv(K, V, k_scale, v_scale, dev)
-    if head_dim != D or k.shape != (T, kv_heads, D) or v.shape != k.shape:
-        raise ValueError("k and v must be [T, kv_heads, D] with the cache's heads and q's T and D")
-    _dense(slots, _I64, (T,), dev, "slots")
-    max_pos = R = at = rows = 0
-    if table is not None:
-        max_pos, R = table.shape
-        _dense(table, _F32, (max_pos, R), dev, "table")
-        _dense(positions, _I32, (T,), dev, "positions")
-        at, rows = positions.data_ptr(), table.data_ptr()
-    made = q_out is None
-    if made:
-        q_out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
-    os = _heads(q_out, 3, dev, "q_out")
-    if q_out.shape != q.shape:
-        _refuse("q_out", q_out, "q's shape")
-    rc = _rope_append(q.data_ptr(), Hq, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], T, at,
-                      rows, max_pos, R, 1 if interleaved else 0, q_out.data_ptr(), os[0], os[1], kv,
-                      slots.data_ptr(), _on(stream, dev, q_out if made else None))
-    if rc:
-        raise Fp8rlError(rc, "fp8rl_rope_append_paged")
-    return q_out
+    (bf16, or uint8 E4M3 codes under k_scale, v_scale fp32 [1]; a page laid out head by
+    head is the transposed view).  table None: no rotation."""
+    if _lib is None:
+        load()
+    if stream is None:
+        return _calls.rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale, v_scale, interleaved, q_out,
+                                        None)
+    s, raw = _given(stream, q.device)
+    out = _calls.rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale, v_scale, interleaved, q_out, raw)
+    if q_out is None:
+        out.record_stream(s)
+    return out
 
 
-@functools.lru_cache(maxsize=4096)
 def fp8rl_attn_paged_workspace_bytes(B: int, Lq: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
     return int(load().fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, Hkv, D, max_len))
 
@@ -651,41 +583,24 @@ def fp8rl_attn_paged(q, K, V, block_table, seq_lens, max_len: int, scale=None, w
     [B, >= max_len / page_size], seq_lens int32 [B] (at most max_len).  scale: D^-1/2
     unless given.  -> o bf16 [B, Lq, Hq, D] (and lse fp32 [B, Lq, Hq] when want_lse or
     lse is given)."""
-    lib = _lib or load()
-    dev = q.get_device()
-    qs = _heads(q, 4, dev, "q")
-    B, Lq, Hq, D = q.shape
-    kv, page, kv_heads, head_dim = _paged_kv(K, V, k_scale, v_scale, dev)
-    if head_dim != D:
-        raise ValueError("q and the cache must have the same head width")
-    ts = block_table.stride()
-    if block_table.dtype is not _I32 or len(ts) != 2 or block_table.get_device() != dev or \
-            (ts[1] != 1 and block_table.shape[1] > 1) or block_table.shape[0] != B or \
-            block_table.shape[1] * page < max_len:
-        _refuse("block_table", block_table, "int32 [B, columns] with contiguous rows that cover max_len tokens")
-    _dense(seq_lens, _I32, (B,), dev, "seq_lens")
-    made_o, made_l, made_w = o is None, lse is None and want_lse, workspace is None
-    if made_o:
-        o = torch.empty((B, Lq, Hq, D), dtype=_BF16, device=q.device)
-    else:
-        _dense(o, _BF16, (B, Lq, Hq, D), dev, "o")
-    if made_l:
-        lse = torch.empty((B, Lq, Hq), dtype=_F32, device=q.device)
-    elif lse is not None:
-        _dense(lse, _F32, (B, Lq, Hq), dev, "lse")
-    if made_w:
-        n = fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, kv_heads, D, max_len)
-        workspace = torch.empty(n, dtype=_U8, device=q.device) if n else None
-    elif workspace.get_device() != dev:
-        _refuse("workspace", workspace, "a tensor on the call's device")
-    wp, wn = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    rc = _attn_paged(q.data_ptr(), B, Lq, Hq, qs[0], qs[1], qs[2], kv, block_table.data_ptr(),
-                     ts[0] if B != 1 else block_table.shape[1], seq_lens.data_ptr(), max_len, window,
-                     D ** -0.5 if scale is None else scale, o.data_ptr(), 0 if lse is None else lse.data_ptr(), wp, wn,
-                     _on(stream, dev, o if made_o else None, lse if made_l else None, workspace if made_w else None))
-    if rc:
-        raise Fp8rlError(rc, "fp8rl_attn_paged")
-    return o if lse is None else (o, lse)
+    if _lib is None:
+        load()
+    if stream is None:
+        return _calls.attn_paged(q, K, V, block_table, seq_lens, max_len, scale, window, k_scale, v_scale, o, lse,
+                                 want_lse, workspace, None)
+    s, raw = _given(stream, q.device)
+    made = [o is None, lse is None]
+    if workspace is None:
+        B, Lq, Hq, D = q.shape
+        workspace = torch.empty(fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, K.shape[2], D, max_len),
+                                dtype=torch.uint8, device=q.device)
+        workspace.record_stream(s)
+    out = _calls.attn_paged(q, K, V, block_table, seq_lens, max_len, scale, window, k_scale, v_scale, o, lse, want_lse,
+                            workspace, raw)
+    for t, m in zip(out if isinstance(out, tuple) else (out,), made):
+        if m:
+            t.record_stream(s)
+    return out
 
 
 FP8RL_PROB_F32 = 0
@@ -697,38 +612,13 @@ def fp8rl_spec_verify(P, drafts, u, noise, Q=None, draft_lens=None, tokens=None,
     drafts int32 [B, K], u fp32 [B, K] in [0, 1), noise fp32 [B, V] of Exp(1) draws,
     draft_lens int32 [B] (None: K) -> (tokens int32 [B, K+1]: kept drafts, the next
     token, then -1; accepted int32 [B])."""
-    lib = _lib or load()
-    dev, dtype, ps = P.get_device(), P.dtype, P.stride()
-    if dev < 0 or (dtype is not _F32 and dtype is not _BF16) or len(ps) != 3 or (ps[2] != 1 and P.shape[2] > 1):
-        _refuse("P", P, "a 3-D float32 or bfloat16 CUDA tensor with contiguous rows")
-    B, K, V = P.shape
-    K -= 1
-    qs, qp = (0, 0), 0
-    if Q is not None:
-        qs, qp = Q.stride(), Q.data_ptr()
-        if Q.dtype is not dtype or Q.shape != (B, K, V) or Q.get_device() != dev or (qs[2] != 1 and V > 1):
-            _refuse("Q", Q, f"{dtype} {(B, K, V)} with contiguous rows on P's device")
-    _dense(drafts, _I32, (B, K), dev, "drafts")
-    _dense(u, _F32, (B, K), dev, "u")
-    ns = noise.stride()
-    if noise.dtype is not _F32 or noise.shape != (B, V) or noise.get_device() != dev or (ns[1] != 1 and V > 1):
-        _refuse("noise", noise, f"float32 {(B, V)} with contiguous rows on P's device")
-    if draft_lens is not None:
-        _dense(draft_lens, _I32, (B,), dev, "draft_lens")
-    made_t, made_a = tokens is None, accepted is None
-    if made_t:
-        tokens = torch.empty((B, K + 1), dtype=_I32, device=P.device)
-    else:
-        _dense(tokens, _I32, (B, K + 1), dev, "tokens")
-    if made_a:
-        accepted = torch.empty((B,), dtype=_I32, device=P.device)
-    else:
-        _dense(accepted, _I32, (B,), dev, "accepted")
-    rc = lib.fp8rl_spec_verify(P.data_ptr(), ps[0], ps[1], qp, qs[0], qs[1],
-                               FP8RL_PROB_F32 if dtype is _F32 else FP8RL_PROB_BF16, drafts.data_ptr(),
-                               0 if draft_lens is None else draft_lens.data_ptr(), u.data_ptr(), noise.data_ptr(),
-                               ns[0], B, K, V, tokens.data_ptr(), accepted.data_ptr(),
-                               _on(stream, dev, tokens if made_t else None, accepted if made_a else None))
-    if rc:
-        raise Fp8rlError(rc, "fp8rl_spec_verify")
-    return tokens, accepted
+    if _lib is None:
+        load()
+    if stream is None:
+        return _calls.spec_verify(P, drafts, u, noise, Q, draft_lens, tokens, accepted, None)
+    s, raw = _given(stream, P.device)
+    out = _calls.spec_verify(P, drafts, u, noise, Q, draft_lens, tokens, accepted, raw)
+    for t, given in zip(out, (tokens, accepted)):
+        if given is None:
+            t.record_stream(s)
+    return out

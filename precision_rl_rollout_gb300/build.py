@@ -1,5 +1,6 @@
 """Build libfp8rl.so in-tree: every csrc/*.cu compiled for sm_103a in parallel
-with nvcc, then linked into one shared library beside this file.
+with nvcc, then linked into one shared library beside this file; and beside it the
+Python module _calls.so (csrc/calls.cpp, host code only, against torch's headers).
 
     python -m precision_rl_rollout_gb300.build [--force] [--verbose]
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libfp8rl.so")
+CALLS_PATH = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -40,15 +43,33 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
+    return _sources() + [os.path.join(CSRC, "calls.cpp")] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _build_calls():
+    """_calls.so with the host compiler, against the torch that will import it."""
+    import torch
+    cxx = shutil.which("g++") or "g++"
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    home = os.path.dirname(os.path.dirname(_nvcc()))
+    here = os.path.dirname(torch.__file__)
+    inc = [os.path.join(here, "include"), os.path.join(here, "include", "torch", "csrc", "api", "include"),
+           os.path.join(home, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-w", *[f"-I{p}" for p in inc],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "calls.cpp"),
+           "-o", tmp, "-L" + os.path.join(here, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -67,7 +88,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, (r.stdout + r.stderr)
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_build_calls)
         results = list(ex.map(compile_one, _sources()))
+        calls.result()
     if verbose or ptxas_verbose:
         for _, log in results:
             if log.strip():
