@@ -6,37 +6,58 @@
 // a query that sees nothing gets zeros and a log-sum of -inf.
 //
 // What bounds it.  Every cached key and value is read once and meets the group's
-// query rows (query heads of the kv head x Lq): 2 rows flop a bf16 byte, 4 rows
-// an E4M3 byte.  With 5-8 rows that is far below the tensor cores' rate at HBM
-// speed even for mma.sync, so the kernel is a stream from HBM, and the design
-// keeps about 128 KB of loads in flight on every SM.  The tcgen05 form would
-// want 128 query or cache rows an instruction, its scores in tensor memory, and
-// E4M3 operands on both sides (which the queries and probabilities are not).
+// query rows (query heads of the kv head x Lq): 2 rows flop a bf16 byte, 4 rows an
+// E4M3 byte.  With the 5-8 rows of one new token that is far below the tensor
+// cores' rate at HBM speed, and the kernel is a stream: 128 sequences of 40/8 heads
+// of 128 over bf16, 4.3 GB, in 653 us (6.6 TB/s, 98% of a plain copy), one sequence
+// of 131072 tokens in 83 us (6.4 TB/s); 64 ragged sequences of 28/4 heads over E4M3,
+// 270 MB, in 51 us (5.3 TB/s; the start, the last tiles and the join are 11 of it).
+// Five new tokens over E4M3 (25 rows, 32 in the product) take 141 us for 555 MB:
+// m16n8k16 runs at 8.3 cycles a scheduler here, 61 us of it, and the conversions,
+// exponentials and matrix loads around it do not all hide behind one another.
 //
-// Products.  A warp takes 16 (E4M3: 32) tokens at a time: S^T = K Q^T with the
-// tokens as the M side and 8 query rows as the N side of m16n8k16, so a group of
-// 5-8 heads fills the tile; O^T += V^T P^T with 16 head values as the M side.
-// K comes through ldmatrix, V through its transposing form, P^T from the scores'
-// registers through an 8x8 register transpose.  E4M3 is converted to fp16 in
-// registers (exact); the key's values are taken in an order of the head
-// dimension that makes each 4-byte piece of a row two operand words, Q follows
-// the same order, and transposed V comes out as even and odd head values.  For
-// E4M3 caches the bf16 queries are held as fp16, scaled by a power of two that
-// puts the row's largest value at 2^14 (exact down to 2^-28 of it).
-// Probabilities are rounded to the product's type relative to the running
-// maximum (fp16: times 2^6, so that 2^-20 of the maximum is still a normal
-// number); their sum is of the unrounded fp32 values.
+// Why mma.sync.  tcgen05 wants 128 rows an instruction on the M side, 16-bit
+// operands on both sides or 8-bit ones on both.  Tokens or head values can be that
+// side, but E4M3 values would have to go through registers and shared memory again
+// as fp16 (queries and probabilities do not fit 8 bits: the tail of a long row is
+// more than 2^18 below its maximum), and the probabilities through tensor memory
+// and back, for a product that mostly waits for HBM.  mma.sync.m16n8k32 on E4M3 with
+// the queries as two E4M3 parts was tried for the scores: exact enough, but it
+// costs 10-15 cycles with fresh operands, more than fp16 with one conversion
+// shared by all rows (verification 285 us against 149).
 //
-// Running maximum.  Products are rescaled only when a tile's maximum passes the
-// reference by 2^8: exact arithmetic does not change, and fp32 sums, bf16 and
-// fp16 probabilities all have the room.
+// The CTA.  Four warps compute, a fifth loads: it keeps a ring of tiles (K and V of
+// CT tokens) full, by the copy engine where pages hold a multiple of 8 tokens, else
+// 16 bytes a lane.  A tile's work in each warp: S^T = K Q^T for its own tokens
+// (tokens the M side, 8 query rows the N side: a group of 5-8 heads fills it); the
+// probabilities of its tokens into shared memory; then O^T += V^T P^T for its own
+// quarter of the head over all tokens of the tile.  So a warp holds 1/4 of the sums
+// (the same rows summed by four warps over their own tokens took the registers of
+// two CTAs, and a reduction of all sums at every item's end), and the sums need no
+// joining inside the CTA.  The loads were first issued between the products by the
+// warps themselves; that was 500 cycles on every tile's way (63 -> 54 us, 64
+// sequences over E4M3).
 //
-// Work split.  The unit is a tile of the CTA (its token groups side by side) of
-// one item (sequence, kv head, chunk of query rows).  All units of the batch, in
-// item order, are cut into equal ranges, one a CTA, one wave of CTAs: ragged
-// lengths need no plan on the host, and one long sequence spreads over the GPU.
-// The lengths are read on the device.  A CTA writes an item that lies wholly in
-// its range; of items that do not it has at most two, whose unnormalised sums go
+// Operands.  K comes through ldmatrix, V and the probabilities through its and
+// stmatrix's transposing forms.  E4M3 is converted to fp16 in registers (exact);
+// the key's values are taken in an order of the head dimension that makes each
+// 4-byte piece of a row two operand words, Q follows the same order, and transposed
+// V comes out as even and odd head values.  For E4M3 caches the bf16 queries are
+// held as fp16, scaled by a power of two that puts the row's largest value at 2^14
+// (exact down to 2^-28 of it).  Probabilities are rounded to the product's type
+// relative to the running reference (fp16: times 2^6, so that 2^-20 of the maximum
+// is still a normal number); their sum is of the unrounded fp32 values.
+//
+// Running reference.  A row's reference is the CTA's and moves only when some score
+// passes it by 2^8: exact arithmetic does not change, and fp32 sums, bf16 and fp16
+// probabilities all have the room.
+//
+// Work split.  The unit is a tile of one item (sequence, kv head, chunk of query
+// rows).  All tiles of the batch, in item order, with a few places more for each
+// item's start and end, are cut into equal ranges, one a CTA, one wave of CTAs:
+// ragged lengths need no plan on the host, and one long sequence spreads over the
+// GPU.  The lengths are read on the device.  A CTA writes an item that lies wholly
+// in its range; of items that do not it has at most two, whose unnormalised sums go
 // to its two slots of the workspace, joined in a second launch in CTA order.
 #pragma once
 
@@ -50,6 +71,7 @@
 
 namespace fp8rl {
 namespace attn {
+namespace {      // each translation unit its own configurations
 
 constexpr uint32_t kKernelAttn = 10;
 constexpr int kWarps = 4, kConsumers = kWarps * 32, kThreads = kConsumers + 32;   // and a warp that loads
@@ -78,12 +100,13 @@ struct Config {
     static constexpr int kRest = kP + kQ + kSmall;
     static constexpr int kFit = (kBudget - kRest) / kStage;
     // 128 KB in flight on an SM keep HBM busy.  More is slower: three tiles a CTA
-    // instead of two took 698 us where these take 631 (128 sequences, bf16).
+    // instead of two took 703 us where these take 654 (128 sequences, bf16).
     static constexpr int kWant = 131072 / (kCtas * kStage) > 2 ? 131072 / (kCtas * kStage) : 2;
     static constexpr int kStages = kFit < kWant ? kFit : kWant < 6 ? kWant : 6;
     static constexpr int kSmem = kStages * kStage + kRest;
-    // what an item costs a CTA beside its tiles (queries, result), in tiles
-    static constexpr int kItem = 65536 / kStage > 1 ? 65536 / kStage : 1;
+    // what an item costs a CTA beside its tiles (queries, result), in tiles, as the
+    // time of 64 KB (with many rows 96 KB) of the cache
+    static constexpr int kCost = RT > 16 ? 98304 : 65536, kItem = kCost / kStage > 1 ? kCost / kStage : 1;
     static_assert(kStages >= 2, "too little shared memory for two stages");
 };
 
@@ -218,6 +241,7 @@ __device__ __forceinline__ void stsm2_t(uint32_t addr, uint32_t a, uint32_t b) {
 __device__ __forceinline__ void touch_l1(const void* p) {
     uint32_t v;
     asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    (void)v;
 }
 __device__ __forceinline__ void st_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
@@ -432,7 +456,6 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
 
     // a segment's running reference and sums; columns 2t and 2t + 1 of each row tile
     float o[NT][MW][4], ref[NT][2], sum[NT][2];
-    auto floor_of = [](float r) { return r == kNone ? 0.f : r; };
 
     // A segment's queries into shared memory as operands, a row tile a warp, and the
     // rows' factors and bounds.
@@ -857,21 +880,36 @@ attn_join_kernel(const __grid_constant__ AttnParams p, int ctas, int spread) {
 #pragma unroll
         for (int k = 0; k < V4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         const int begin = c0 + (spread ? warp : 0), step = spread ? kW : 1;
-        for (int c = begin + lane * step; c <= c1; c += 32 * step) m = fmaxf(m, slot(c)[RT * DP + r]);
+        constexpr int kBatch = 4;                             // slots whose loads are in flight together
+        for (int c = begin; c <= c1; c += kBatch * step) {
+            float xm[kBatch], xl[kBatch];
+            float4 v[kBatch][V4];
 #pragma unroll
-        for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-#pragma unroll 4
-        for (int c = begin; c <= c1; c += step) {
-            const float* x = slot(c);
-            const float f = ex2(x[RT * DP + r] - m);
-            l += x[RT * DP + RT + r] * f;
+            for (int i = 0; i < kBatch; ++i) {
+                const bool in = c + i * step <= c1;
+                const float* x = slot(in ? c + i * step : c);
+                xm[i] = in ? x[RT * DP + r] : kNone;
+                xl[i] = in ? x[RT * DP + RT + r] : 0.f;
 #pragma unroll
-            for (int k = 0; k < V4; ++k) {
-                const int d = (k * 32 + lane) * 4;
-                if (d < DP) {
-                    const float4 v = *reinterpret_cast<const float4*>(x + r * DP + d);
-                    o[k].x += f * v.x, o[k].y += f * v.y, o[k].z += f * v.z, o[k].w += f * v.w;
-                }
+                for (int k = 0; k < V4; ++k)
+                    v[i][k] = in && (k * 32 + lane) * 4 < DP
+                                  ? *reinterpret_cast<const float4*>(x + r * DP + (k * 32 + lane) * 4)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) top = fmaxf(top, xm[i]);
+            const float f0 = ex2(m - top);
+            m = top, l *= f0;
+#pragma unroll
+            for (int k = 0; k < V4; ++k) o[k].x *= f0, o[k].y *= f0, o[k].z *= f0, o[k].w *= f0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float f = ex2(xm[i] - m);
+                l += xl[i] * f;
+#pragma unroll
+                for (int k = 0; k < V4; ++k)
+                    o[k].x += f * v[i][k].x, o[k].y += f * v[i][k].y, o[k].z += f * v[i][k].z, o[k].w += f * v[i][k].w;
             }
         }
         if (spread) {
@@ -990,6 +1028,7 @@ auto pick(int64_t D, int64_t rows, F f) {
     return pick_rows<kE4m3, kTma, 256>(rows, f);
 }
 
+}  // namespace
 }  // namespace attn
 
 // One translation unit a cache type and loader (they compile side by side).
