@@ -495,7 +495,7 @@ int fp8rl_rope_append_paged(const uint16_t* q, int64_t Hq, int64_t q_token, int6
 size_t fp8rl_attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
                                         int64_t max_len);
 /* Kernels fp8rl_attn_paged launches for these sizes and cache dtype: 1 where
- * max_len is a tile at most, else 2.  0 for B == 0; a negated status for invalid
+ * max_len is short for the batch, else 2.  0 for B == 0; a negated status for invalid
  * sizes. */
 int fp8rl_attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
                                   int64_t max_len, int dtype);

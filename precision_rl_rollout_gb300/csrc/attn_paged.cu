@@ -6,8 +6,9 @@ namespace fp8rl {
 
 namespace {
 
-attn::Plan plan_of(int64_t D, int64_t rows, int64_t max_len, bool e4m3) {
-    auto f = [&](auto c) { return attn::plan<decltype(c)>(max_len); };
+attn::Plan plan_of(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, bool e4m3) {
+    const int64_t rows = Hq / Hkv * Lq;
+    auto f = [&](auto c) { return attn::plan<decltype(c)>(B, Hkv, rows, max_len); };
     return e4m3 ? attn::pick<true, true>(D, rows, f) : attn::pick<false, true>(D, rows, f);
 }
 
@@ -22,14 +23,12 @@ bool copy_engine(const AttnParams& p, bool e4m3) {
 }  // namespace
 
 size_t attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
-    (void)B;                                   // two slots a CTA, whatever the batch
-    const size_t a = plan_of(D, Hq / Hkv * Lq, max_len, false).ws, b = plan_of(D, Hq / Hkv * Lq, max_len, true).ws;
+    const size_t a = plan_of(B, Lq, Hq, Hkv, D, max_len, false).ws, b = plan_of(B, Lq, Hq, Hkv, D, max_len, true).ws;
     return a > b ? a : b;
 }
 
 int attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, bool e4m3) {
-    (void)B;
-    return plan_of(D, Hq / Hkv * Lq, max_len, e4m3).kernels;
+    return plan_of(B, Lq, Hq, Hkv, D, max_len, e4m3).kernels;
 }
 
 cudaError_t launch_attn_paged(const AttnParams& a, bool e4m3, cudaStream_t st) {

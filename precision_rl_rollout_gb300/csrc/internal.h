@@ -92,8 +92,9 @@ struct AttnParams {
     int B, Lq, Hq, Hkv, D, page_size, max_len, window;
     float scale;
     // set by the launcher: tokens a copy-engine box, 1 where heads lie outside
-    // tokens, the page size's logarithm (-1: not a power of two)
-    int box, order, page_shift;
+    // tokens, the page size's logarithm (-1: not a power of two), CTAs a cluster
+    // where each item has one (0: not so)
+    int box, order, page_shift, cluster;
 };
 size_t attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
 int attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, bool e4m3);
