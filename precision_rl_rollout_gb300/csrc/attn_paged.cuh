@@ -92,7 +92,10 @@ struct Config {
     static constexpr int TT = 16 * MT, CT = kWarps * TT;     // tokens of a warp, of a CTA's tile
     static constexpr int MW = DP / 64;                       // 16-value tiles of the head a warp sums
     static constexpr int kTile = CT * RB, kStage = 2 * kTile;
-    static constexpr int kP = RT * CT * 2;                   // probabilities, 16 bits
+    // Probabilities, 16 bits; bf16 ones as the sum of two where a few rows leave the
+    // tensor cores idle: one rounding of 2^-9 beside the result's own made the
+    // output's error 1.4 times a single rounding's.
+    static constexpr int kParts = !kE4m3 && RT <= 16 ? 2 : 1, kPart = RT * CT * 2, kP = kParts * kPart;
     static constexpr int kQ = NT * (DP / 32) * 512;          // query operands
     static constexpr int kSmall = RT * 4 * (kWarps + 3) + 12 * 8 + 16;
     static constexpr int kCtas = DP > 128 ? 1 : kE4m3 && RT < 64 ? 3 : 2;   // CTAs an SM
@@ -540,8 +543,9 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     // the same for a chunk known at run time
     auto chunk_at = [](uint32_t at, int c) -> uint32_t { return (at ^ (uint32_t)((c & 7) << 4)) + (c >> 3) * (CT * 128); };
     const uint32_t sp = sm100::smem_u32(smem_p);
-    // probabilities, stored and loaded by pairs of row tiles (where there are two)
-    const uint32_t p_lane = sp + swz_p<C>((lane >> 4 & (NT > 1 ? 1 : 0)) * 8 + (lane & 7), lane >> 3 & 1);
+    // probabilities, stored and loaded by pairs of row tiles, or both parts of one
+    const uint32_t p_lane = sp + swz_p<C>((NT > 1 ? lane >> 4 : 0) * 8 + (lane & 7), lane >> 3 & 1) +
+                            (NT == 1 && C::kParts == 2 ? (lane >> 4) * C::kPart : 0);
     auto p_at = [](uint32_t at, int n, int c) -> uint32_t {   // row tile n, chunk c, both even
         return (at ^ (uint32_t)((c & 7) << 4)) + (c >> 3) * (RT * 128) + n * 1024;
     };
@@ -684,7 +688,6 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
             }
             relative();
         }
-        uint32_t pk[NT][MT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -693,18 +696,30 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 for (int e = 0; e < 4; ++e) x[n][m][e] = ex2(x[n][m][e]);
                 sum[n][0] += x[n][m][0] + x[n][m][2];
                 sum[n][1] += x[n][m][1] + x[n][m][3];
-                pk[n][m][0] = kE ? pack_f16x2(x[n][m][0], x[n][m][1]) : pack2_bf16(x[n][m][0], x[n][m][1]);
-                pk[n][m][1] = kE ? pack_f16x2(x[n][m][2], x[n][m][3]) : pack2_bf16(x[n][m][2], x[n][m][3]);
             }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int c = (warp * MT + m) * 2;
-            if constexpr (NT == 1) {
-                stsm2_t(p_at(p_lane, 0, c), pk[0][m][0], pk[0][m][1]);
+            auto pack = [&](int n, int e) {
+                return kE ? pack_f16x2(x[n][m][e], x[n][m][e + 1]) : pack2_bf16(x[n][m][e], x[n][m][e + 1]);
+            };
+            auto rest = [&](int n, int e, uint32_t of) {      // what the rounding to `of` leaves
+                return pack2_bf16(x[n][m][e] - bf16_lo(of), x[n][m][e + 1] - bf16_hi(of));
+            };
+            if constexpr (NT == 1 && C::kParts == 1) {
+                stsm2_t(p_at(p_lane, 0, c), pack(0, 0), pack(0, 2));
+            } else if constexpr (NT == 1) {
+                const uint32_t u = pack(0, 0), v = pack(0, 2);
+                stsm4_t(p_at(p_lane, 0, c), u, v, rest(0, 0, u), rest(0, 2, v));
             } else {
 #pragma unroll
-                for (int n = 0; n < NT; n += 2)
-                    stsm4_t(p_at(p_lane, n, c), pk[n][m][0], pk[n][m][1], pk[n + 1][m][0], pk[n + 1][m][1]);
+                for (int n = 0; n < NT; n += 2) {
+                    const uint32_t u[4] = {pack(n, 0), pack(n, 2), pack(n + 1, 0), pack(n + 1, 2)};
+                    stsm4_t(p_at(p_lane, n, c), u[0], u[1], u[2], u[3]);
+                    if constexpr (C::kParts == 2)
+                        stsm4_t(p_at(p_lane, n, c) + C::kPart, rest(n, 0, u[0]), rest(n, 2, u[1]), rest(n + 1, 0, u[2]),
+                                rest(n + 1, 2, u[3]));
+                }
             }
         }
         // What the product must not meet.  Rows of no visible token (a whole box is
@@ -729,18 +744,19 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         // O^T += V^T P^T: the warp's part of the head over the CTA's tokens
 #pragma unroll
         for (int kt = 0; kt < CT / 16; ++kt) {
-            uint32_t b[NT][2];
-            if constexpr (NT == 1) {
-                uint32_t v[2];
-                ldsm2(v, p_at(p_lane, 0, 2 * kt));
-                b[0][0] = v[0], b[0][1] = v[1];
+            uint32_t b[C::kParts][NT][2];
+            if constexpr (NT == 1 && C::kParts == 1) {
+                ldsm2(b[0][0], p_at(p_lane, 0, 2 * kt));
             } else {
 #pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t v[4];
-                    ldsm4(v, p_at(p_lane, n, 2 * kt));
-                    b[n][0] = v[0], b[n][1] = v[1], b[n + 1][0] = v[2], b[n + 1][1] = v[3];
-                }
+                for (int i = 0; i < (NT == 1 ? 1 : C::kParts); ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t v[4];
+                        ldsm4(v, p_at(p_lane, n, 2 * kt) + i * C::kPart);
+                        const int i1 = NT == 1 ? 1 : i, n1 = NT == 1 ? 0 : n + 1;
+                        b[i][n][0] = v[0], b[i][n][1] = v[1], b[i1][n1][0] = v[2], b[i1][n1][1] = v[3];
+                    }
             }
             const uint32_t row = kt * 16 * C::PB;
             uint32_t a[MW][4];
@@ -766,7 +782,9 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < MW; ++k)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816<kE>(o[n][k], a[k], b[n][0], b[n][1]);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < C::kParts; ++i) mma16816<kE>(o[n][k], a[k], b[i][n][0], b[i][n][1]);
         }
     };
 
