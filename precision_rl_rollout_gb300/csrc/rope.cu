@@ -110,11 +110,11 @@ __device__ __forceinline__ void store_cache8(void* pool, int64_t at, const float
 // its row come.  Loads pass L1 and stores go out evict-first: nothing is read
 // twice (49 -> 45 us for the gradient below).
 // Bound by HBM: 2 bytes in, 2 (E4M3: 1) out a value.  8192 tokens, 40 + 8 heads of
-// 128: 36 us, 5.8 TB/s; gradient of 16411 tokens, 28 + 4 heads, 64 of 128 values
-// interleaved: 45 us, 6.1 TB/s; append of 8192 tokens, 40 + 2 x 8 heads, bf16
-// pages: 41 us, 5.9 TB/s.  What is left is the start and the last wave.
+// 128: 34 us, 6.0 TB/s; gradient of 16411 tokens, 28 + 4 heads, 64 of 128 values
+// interleaved: 43 us, 6.3 TB/s; append of 8192 tokens, 40 + 2 x 8 heads, bf16
+// pages: 42 us, 5.7 TB/s.  What is left is the start and the last wave.
 template <bool kInter, bool kE4m3>
-__global__ void __launch_bounds__(kRopeThreads, 2)
+__global__ void __launch_bounds__(kRopeThreads, 3)
 rope_kernel(const __grid_constant__ RopeParams p) {
     pdl_wait_then_release();
     const int pairs = p.R / (kInter ? 8 : 16), cols = pairs + (p.D - p.R) / 8;
@@ -274,13 +274,13 @@ template <bool kInter, bool kE4m3>
 cudaError_t launch_t(RopeParams& p, bool wide, cudaStream_t st) {
     const int heads = p.Hq + 2 * p.Hkv;
     if (!wide) return launch_pdl(rope_narrow_kernel<kInter, kE4m3>, dim3((unsigned)p.T), dim3(kRopeThreads), 0, st, p);
-    // A thread goes over up to 16 heads, fewer where that leaves SMs without two
+    // A thread goes over up to eight heads, fewer where that leaves SMs without two
     // CTAs: its own work (the token's row, its column's cosines) is then spread over
     // more bytes.  8192 tokens of 48 heads of 128: 75 us with one head a thread, 41
-    // with four, 36 with 16.
+    // with four, 34 with eight; with 16 the last wave of 3001 tokens costs 40% more.
     const int cols = p.R / (kInter ? 8 : 16) + (p.D - p.R) / 8, most = kRopeThreads / cols;
     const int64_t room = p.T * heads * cols / (2 * (int64_t)num_sms() * kRopeThreads);
-    const int each = room < 1 ? 1 : room > 16 ? 16 : (int)room;
+    const int each = room < 1 ? 1 : room > 8 ? 8 : (int)room;
     p.lanes = (heads + each - 1) / each;
     if (p.lanes > most) p.lanes = most;
     p.cta_tokens = each == 1 ? 1 : most / p.lanes;
