@@ -475,8 +475,11 @@ int fp8rl_rope_append_paged(const uint16_t* q, int64_t Hq, int64_t q_token, int6
  * Rows of the cache that no query of the sequence sees are never read into a
  * result, whatever they hold.
  * Scores, maxima, sums and o are held in fp32, o rounded once to bf16.  The
- * probabilities are rounded to the cache's product type (bf16; for E4M3 caches
- * fp16), relative to the row's running maximum.  Deterministic.
+ * probabilities meet the values in the cache's product type: bf16 (up to 16 query
+ * rows a kv head, Hq / kv_heads * Lq, as the sum of two, so to 2^-16; above, rounded
+ * to 2^-8), for E4M3 caches fp16 (to 2^-11), relative to the row's running maximum; the
+ * queries as bf16, for E4M3 caches as fp16 scaled by a power of two a row (exact down
+ * to 2^-28 of the row's largest).  Deterministic.
  * q   bf16 [B][Lq][Hq][head_dim] by strides (elements, multiples of 8), 16-byte
  *     aligned; Hq a multiple of kv_heads.
  * block_table int32 [B][table_stride], DEVICE; table_stride >= max_len /

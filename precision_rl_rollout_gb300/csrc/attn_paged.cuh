@@ -9,10 +9,10 @@
 // query rows (query heads of the kv head x Lq): 2 rows flop a bf16 byte, 4 rows an
 // E4M3 byte.  With the 5-8 rows of one new token that is far below the tensor
 // cores' rate at HBM speed, and the kernel is a stream: 128 sequences of 40/8 heads
-// of 128 over bf16, 4.3 GB, in 653 us (6.6 TB/s, 98% of a plain copy), one sequence
-// of 131072 tokens in 83 us (6.4 TB/s); 64 ragged sequences of 28/4 heads over E4M3,
-// 270 MB, in 51 us (5.3 TB/s; the start, the last tiles and the join are 11 of it).
-// Five new tokens over E4M3 (25 rows, 32 in the product) take 141 us for 555 MB:
+// of 128 over bf16, 4.3 GB, in 658 us (6.6 TB/s, 97% of a plain copy), one sequence
+// of 131072 tokens in 84 us (6.4 TB/s); 64 ragged sequences of 28/4 heads over E4M3,
+// 270 MB, in 52 us (5.2 TB/s; the start, the last tiles and the join are 11 of it).
+// Five new tokens over E4M3 (25 rows, 32 in the product) take 140 us for 555 MB:
 // m16n8k16 runs at 8.3 cycles a scheduler here, 61 us of it, and the conversions,
 // exponentials and matrix loads around it do not all hide behind one another.
 //
@@ -58,7 +58,9 @@
 // ragged lengths need no plan on the host, and one long sequence spreads over the
 // GPU.  The lengths are read on the device.  A CTA writes an item that lies wholly
 // in its range; of items that do not it has at most two, whose unnormalised sums go
-// to its two slots of the workspace, joined in a second launch in CTA order.
+// to its two slots of the workspace, joined in a second launch in CTA order.  A
+// short batch is one launch: each item has a cluster of CTAs, whose sums the first
+// takes through shared memory (1 x 777 tokens: 10.3 -> 7.1 us).
 #pragma once
 
 #include <math.h>
@@ -93,7 +95,7 @@ struct Config {
     static constexpr int MW = DP / 64;                       // 16-value tiles of the head a warp sums
     static constexpr int kTile = CT * RB, kStage = 2 * kTile;
     // Probabilities, 16 bits; bf16 ones as the sum of two where a few rows leave the
-    // tensor cores idle: one rounding of 2^-9 beside the result's own made the
+    // tensor cores idle: one rounding of 2^-8 beside the result's own made the
     // output's error 1.4 times a single rounding's.
     static constexpr int kParts = !kE4m3 && RT <= 16 ? 2 : 1, kPart = RT * CT * 2, kP = kParts * kPart;
     static constexpr int kQ = NT * (DP / 32) * 512;          // query operands
