@@ -173,6 +173,60 @@ def test_append_bits(cuda_lib, T, Hq, Hkv, D, R, page, inter, e4m3, heads_first)
     _no_error()
 
 
+@pytest.mark.parametrize("kind", ["boundary", "power of two", "tiny", "huge"])
+def test_append_codes_at_the_boundaries_between_codes(cuda_lib, kind):
+    """Scales that put a value's quotient on a boundary between two codes or a unit or
+    two beside it; and scales whose reciprocal is exact, or out of range."""
+    rng = np.random.default_rng(5)
+    x = _x((1, 4, 64), 9)
+    f = x.float().numpy()[0]
+    normal = [m * 2.0 ** e for e in range(-6, 9) for m in (17 / 16, 19 / 16, 21 / 16, 23 / 16, 25 / 16, 27 / 16, 29 / 16, 31 / 16)]
+    ties = np.array([i * 2.0 ** -10 for i in range(1, 16, 2)] + [t for t in normal if t < 448])
+    zero = torch.zeros((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    for i in range(48):
+        if kind == "boundary":
+            s = np.float32(abs(float(f.flat[i])) / ties[rng.integers(len(ties))])
+            s = np.float32(s * (1 + (i % 5 - 2) * 2.0 ** -24))
+        else:
+            s = np.float32({"power of two": 2.0 ** (i % 12 - 8), "tiny": 2.0 ** -(100 + i % 49), "huge": 1.3 * 2.0 ** (90 + i % 37)}[kind])
+        K, V = (torch.zeros((1, 1, 4, 64), dtype=torch.uint8, device="cuda") for _ in range(2))
+        scale = torch.tensor([s], device="cuda")
+        fb.fp8rl_rope_append_paged(zero, x.cuda(), x.cuda(), None, None, K, V, torch.zeros(1, dtype=torch.int64, device="cuda"),
+                                   k_scale=scale, v_scale=scale)
+        want = ref.e4m3_codes(f, s)
+        assert np.array_equal(K.cpu().numpy()[0, 0], want) and np.array_equal(V.cpu().numpy()[0, 0], want), s
+    _no_error()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D,R,shift", [(80, 56, 0), (80, 40, 0), (96, 24, 0), (64, 64, 4), (128, 72, 4), (48, 8, 0), (16, 16, 4)])
+def test_append_in_8_byte_chunks(cuda_lib, D, R, shift, e4m3, inter):
+    """Halves of R that are no multiple of 8, and heads that begin 8 bytes past a
+    16-byte boundary; an odd number of chunks past R."""
+    T, Hq, Hkv = 37, 5, 2
+    table = _table(300, R)[0]
+    big = _x((T, (Hq + 2 * Hkv) * D + 2 * shift), D + R).cuda()
+    qkv = big[:, shift:shift + (Hq + 2 * Hkv) * D].unflatten(1, (Hq + 2 * Hkv, D))
+    pos = np.random.default_rng(R).integers(0, 300, T).astype(np.int32)
+    slots = np.arange(T, dtype=np.int64)[::-1].copy()
+    K, V = _pools(5, 8, Hkv, D, e4m3, False), _pools(5, 8, Hkv, D, e4m3, False)
+    ks, vs = 0.013, 0.006
+    args = dict(k_scale=torch.tensor([ks], device="cuda"), v_scale=torch.tensor([vs], device="cuda")) if e4m3 else {}
+    q = fb.fp8rl_rope_append_paged(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], torch.from_numpy(pos).cuda(),
+                                   torch.from_numpy(table).cuda(), K, V, torch.from_numpy(slots).cuda(),
+                                   interleaved=inter, **args)
+    f = qkv.cpu().float().numpy()
+    rot = ref.rope(f, pos, table, R, inter, False, np.float32)
+    assert np.array_equal(q.cpu().float().numpy(), ref.bf16(rot[:, :Hq]))
+    for pool, x, s in ((K, rot[:, Hq:Hq + Hkv], ks), (V, f[:, Hq + Hkv:], vs)):
+        got = pool.cpu().reshape(40, Hkv, D)
+        got = got.numpy() if e4m3 else got.float().numpy()
+        for t in range(T):
+            assert np.array_equal(got[slots[t]], ref.e4m3_codes(x[t], np.float32(s)) if e4m3 else ref.bf16(x[t]))
+    _no_error()
+
+
 def test_append_saturates_and_keeps_specials(cuda_lib):
     v = torch.zeros((1, 1, 16), dtype=torch.bfloat16)
     v[0, 0, :6] = torch.tensor([3e38, -3e38, float("inf"), float("-inf"), float("nan"), 1e-30])
