@@ -1,6 +1,6 @@
 // attn_paged.cu -- the paged attention call: its sizes, and which loader a cache
 // takes (attn_paged.cuh has the kernels).
-#include "attn_paged.cuh"
+#include "attn_paged_wide.cuh"
 
 namespace fp8rl {
 
@@ -9,7 +9,12 @@ namespace {
 attn::Plan plan_of(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, bool e4m3) {
     const int64_t rows = Hq / Hkv * Lq;
     auto f = [&](auto c) { return attn::plan<decltype(c)>(B, Hkv, rows, max_len); };
-    return e4m3 ? attn::pick<true, true>(D, rows, f) : attn::pick<false, true>(D, rows, f);
+    if (e4m3) return attn::pick<true, true>(D, rows, f);
+    // what either of the kernels for a bf16 cache takes: the pages tell which
+    const attn::Plan a = attn::pick<false, true>(D, rows, f);
+    if (!attn::is_wide(D, rows)) return a;
+    const attn::Plan b = attn::pick_wide(D, rows, [&](auto c) { return attn::plan_wide<decltype(c)>(max_len); });
+    return attn::Plan{a.ws > b.ws ? a.ws : b.ws, a.kernels > b.kernels ? a.kernels : b.kernels};
 }
 
 // The copy engine loads boxes of 8 tokens or more of one page, by the strides of
@@ -35,7 +40,9 @@ cudaError_t launch_attn_paged(const AttnParams& a, bool e4m3, cudaStream_t st) {
     AttnParams p = a;
     p.err = device_error_word();
     if (!p.err) return cudaErrorUnknown;
-    if (copy_engine(p, e4m3)) return e4m3 ? launch_attn_e4m3_tma(p, st) : launch_attn_bf16_tma(p, st);
+    const bool engine = copy_engine(p, e4m3);
+    if (engine && !e4m3 && attn::is_wide(p.D, (int64_t)p.Hq / p.Hkv * p.Lq)) return launch_attn_wide(p, st);
+    if (engine) return e4m3 ? launch_attn_e4m3_tma(p, st) : launch_attn_bf16_tma(p, st);
     return e4m3 ? launch_attn_e4m3(p, st) : launch_attn_bf16(p, st);
 }
 

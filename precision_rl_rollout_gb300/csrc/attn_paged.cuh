@@ -300,6 +300,40 @@ struct Cursor {
     }
 };
 
+// The CTA's range of places: its length (or 0), and its first tile in `at`.
+template <class C>
+__device__ __forceinline__ int first_tile(const AttnParams& p, int hr_n, Cursor& at) {
+    const int lane = threadIdx.x & 31;
+    at.place = 0;
+    int64_t before, total;
+    count_places<C>(p, hr_n, 0, &before, &total);
+    const int64_t chunk = div_ceil(total, gridDim.x), u0 = (int64_t)blockIdx.x * chunk;
+    const int size = (int)(total - u0 < chunk ? total - u0 : chunk);
+    if (size <= 0) return 0;
+    int64_t base = 0;                                         // first place of the sequence the range begins in
+    for (int b0 = 0;; b0 += 32) {
+        const int n = b0 + lane < p.B ? span_of(p, b0 + lane, C::CT).tiles + C::kItem : 0;
+        int64_t inc = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += o;
+        }
+        const uint32_t in = __ballot_sync(0xffffffffu, base + inc * hr_n > u0);
+        const int l = in ? __ffs((int)in) - 1 : 31;
+        base += __shfl_sync(0xffffffffu, (in ? inc - n : inc) * hr_n, l);
+        at.b = b0 + l;
+        if (in) break;
+    }
+    at.s = span_of(p, at.b, C::CT);
+    const int64_t in = u0 - base;                             // below 2^31 items of a sequence
+    const int each = at.s.tiles + C::kItem;
+    at.hr = (int)(in >> 32 ? in / each : (uint32_t)in / (uint32_t)each);
+    at.tile = max(0, (int)(in - (int64_t)at.hr * each) - C::kItem);
+    at.place = (int)((int64_t)at.hr * each + C::kItem + at.tile - in);
+    return size;
+}
+
 // kCluster: an item a cluster (p.cluster CTAs); else the tiles are cut into ranges.
 template <class C, bool kCluster>
 __global__ void __launch_bounds__(kThreads, C::kCtas)
@@ -353,36 +387,9 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
         at.tile = rank * each;
         at.place = 0;
         size = min(each, at.s.tiles - at.tile);               // none or less: nothing of it
-    } else {                                                  // the CTA's range of places, and its first tile
-        int64_t before, total;
-        count_places<C>(p, hr_n, 0, &before, &total);
-        const int64_t chunk = div_ceil(total, gridDim.x), u0 = (int64_t)blockIdx.x * chunk;
-        size = (int)(total - u0 < chunk ? total - u0 : chunk);
-        if (size <= 0) return;
-        int64_t base = 0;                                         // first place of the sequence the range begins in
-        for (int b0 = 0;; b0 += 32) {
-            const int n = b0 + lane < p.B ? span_of(p, b0 + lane, C::CT).tiles + C::kItem : 0;
-            int64_t inc = n;
-    #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
-                if (lane >= off) inc += o;
-            }
-            const uint32_t in = __ballot_sync(0xffffffffu, base + inc * hr_n > u0);
-            const int l = in ? __ffs((int)in) - 1 : 31;
-            base += __shfl_sync(0xffffffffu, (in ? inc - n : inc) * hr_n, l);
-            at.b = b0 + l;
-            if (in) break;
-        }
-        at.s = span_of(p, at.b, C::CT);
-        {
-            const int64_t in = u0 - base;                         // below 2^31 items of a sequence
-            const int each = at.s.tiles + C::kItem;
-            at.hr = (int)(in >> 32 ? in / each : (uint32_t)in / (uint32_t)each);
-            at.tile = max(0, (int)(in - (int64_t)at.hr * each) - C::kItem);
-            at.place = (int)((int64_t)at.hr * each + C::kItem + at.tile - in);
-        }
-        if (at.place >= size) return;                             // the range ends before its first tile
+    } else {
+        size = first_tile<C>(p, hr_n, at);
+        if (at.place >= size) return;                         // no work, or the range ends before its first tile
     }
 
     const uint32_t ring = sm100::smem_u32(smem);              // a tile a slot
@@ -1164,6 +1171,7 @@ auto pick(int64_t D, int64_t rows, F f) {
 
 // One translation unit a cache type and loader (they compile side by side).
 cudaError_t launch_attn_bf16_tma(const AttnParams& p, cudaStream_t st);
+cudaError_t launch_attn_wide(const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_bf16(const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_e4m3_tma(const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_e4m3(const AttnParams& p, cudaStream_t st);

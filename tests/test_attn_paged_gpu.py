@@ -103,6 +103,59 @@ def test_long_sequences_split_and_joined(cuda_lib, B, L, Lq, Hq, Hkv, D, window,
     _check(c, _q(B, Lq, Hq, D, L, size=3.0), window)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page,Lq,window", [
+    (33, 1, 128, 16, 1, 0), (40, 8, 128, 8, 5, 0), (48, 3, 96, 32, 5, 0), (28, 4, 64, 64, 8, 0), (16, 2, 128, 24, 8, 40),
+    (48, 3, 128, 128, 8, 0), (65, 1, 64, 16, 1, 7), (6, 2, 80, 8, 43, 0), (10, 5, 128, 16, 150, 0), (4, 4, 64, 256, 70, 19),
+    (12, 1, 16, 16, 11, 0)])
+def test_many_query_rows(cuda_lib, Hq, Hkv, D, page, Lq, window):
+    # more than 32 rows a kv head, one and several chunks of them, over bf16
+    lens = [0, 1, 2, 15, 16, 17, 31, 64, 65, 127, 128, 129, 300, 511]
+    c = Cache(lens, Hkv, D, page, False, (Hq + page) % 2 == 0, D + Lq)
+    _check(c, _q(len(lens), Lq, Hq, D, Hq), window)
+
+
+@pytest.mark.parametrize("B,L,Lq,Hq,Hkv,D,window", [(1, 9000, 5, 14, 2, 128, 0), (2, 4001, 9, 40, 8, 128, 0),
+                                                    (3, 3000, 16, 8, 1, 64, 1111), (1, 2500, 300, 2, 1, 96, 0)])
+def test_many_query_rows_of_long_sequences(cuda_lib, B, L, Lq, Hq, Hkv, D, window):
+    lens = [max(1, L - 777 * b) for b in range(B)]
+    c = Cache(lens, Hkv, D, 16, False, False, L)
+    q = _q(B, Lq, Hq, D, L, size=3.0)
+    o, lse = _check(c, q, window)
+    again, lse2 = _check(c, q, window)
+    assert np.array_equal(o, again) and np.array_equal(lse, lse2)
+
+
+@pytest.mark.parametrize("Hq,Lq,D", [(40, 2, 128), (12, 9, 64), (3, 50, 96)])
+def test_many_query_rows_do_not_see_later_values(cuda_lib, Hq, Lq, D):
+    # NaN and infinities among the newest tokens, and below a window's edge
+    lens, page = [200, 133, 129], 8
+    for window in (0, 61):
+        c = Cache(lens, 1, D, page, False, False, 11)
+        q = _q(3, Lq, Hq, D, 12)
+        want, _ = _check(c, q, window)
+        for bad_keys in (False, True):
+            hit = []
+            for b, n in enumerate(lens):
+                for i, t in enumerate([n - 1, n - 2] if not window else [n - Lq - window + 1, n - Lq - window + 2]):
+                    value = float("nan") if i else float("inf")
+                    at = (int(c.table[b, t // page]), t % page)
+                    c.pools[1][at] = value
+                    if bad_keys:
+                        c.pools[0][at] = value
+                    hit.append((b, t))
+            o, _ = fb.fp8rl_attn_paged(q.cuda(), *c.pools, c.table.cuda(), c.lens.cuda(), max(lens), window=window,
+                                       want_lse=True)
+            o = o.cpu().double().numpy()
+            for b, n in enumerate(lens):
+                for i in range(Lq):
+                    p = n - Lq + i
+                    if any(x == b and t <= p and (not window or t > p - window) for x, t in hit):
+                        assert not np.any(np.isfinite(o[b, i])), (window, b, i)
+                    else:
+                        assert np.array_equal(o[b, i], want[b, i]), (window, b, i)
+        assert fb.fp8rl_check_device_error() == 0
+
+
 def test_many_short_sequences(cuda_lib):
     lens = [(37 * i) % 90 for i in range(300)]
     c = Cache(lens, 2, 64, 16, False, True, 3)
