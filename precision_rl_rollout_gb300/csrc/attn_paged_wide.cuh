@@ -14,13 +14,14 @@
 //   O^T [head x rows] += V^T P^T         V and P with the head and rows inside (MN-major),
 // so K and V are operands as the copy engine lays them, 64 values of 128 tokens a piece
 // under the 128-byte swizzle, and nothing is transposed.  Scores and sums are in tensor
-// memory, fp32.  A thread of the eight that have a token's scores on a lane takes half
-// the rows of one token: exponentials, its token's part of the rows' sums, and 16-byte
-// pieces of P (bf16, one rounding: the reference is the running one of attn_paged.cuh,
+// memory, fp32.  Two threads share a token's scores, every other eight rows
+// each: exponentials, their token's part of the rows' sums, and 16-byte pieces of P
+// (bf16, one rounding: the reference is the running one of attn_paged.cuh,
 // moved rarely, and then the sums in tensor memory are scaled).
 //
 // A warp loads, one issues the products: a tile's scores while the tile before is in
-// the exponentials.  The last tile of an item lets go of the queries' buffer, so the
+// the exponentials, and where two buffers of probabilities fit, the exponentials while
+// the product before sums.  The last tile of an item lets go of the queries' buffer, so the
 // next item's first scores are under way while this one's result is written.
 #pragma once
 
@@ -34,16 +35,18 @@ template <int DP_, int RT_>
 struct WideConfig {
     static constexpr bool kE4m3 = false, kTma = true;
     static constexpr int DP = DP_, RT = RT_, ES = 2, RB = DP * ES, PB = 128, CT = 128;
-    static constexpr int kTile = CT * RB, kStage = 2 * kTile, kCtas = 1;
+    static constexpr int kTile = CT * RB, kCtas = 1;
     static constexpr int kPiece = CT * 128;                  // 64 values of a tile's tokens
-    static constexpr int kP = RT / 64 * kPiece, kQ = DP / 64 * RT * 128;
-    static constexpr int kSmall = RT * 4 * 9 + 24 * 8 + 16;
-    static constexpr int kFit = (232448 - kP - kQ - kSmall) / kStage, kStages = kFit < 4 ? kFit : 4;
-    static constexpr int kSmem = kStages * kStage + kP + kQ + kSmall;
-    static constexpr int kItem = 131072 / kStage;            // an item's start and end, in tiles
-    static constexpr int kHalf = RT / 2;                     // rows a thread
+    static constexpr int kPart = RT / 64 * kPiece, kBufs = DP + RT > 192 ? 1 : 2, kP = kBufs * kPart;   // probabilities
+    static constexpr int kQ = DP / 64 * RT * 128;
+    static constexpr int kSmall = RT * 4 * 9 + 28 * 8 + 16;
+    // a tile of keys or of values a slot, let go of by its own product
+    static constexpr int kFit = (232448 - kP - kQ - kSmall) / kTile, kSlots = kFit < 8 ? kFit : 8;
+    static constexpr int kSmem = kSlots * kTile + kP + kQ + kSmall;
+    static constexpr int kItem = 65536 / kTile;              // an item's start and end, in tiles
+    static constexpr int kUnits = RT / 16;                   // eights of rows a thread
     static constexpr uint32_t kCols = 4 * RT;                // two tiles' scores, the sums, what is set apart
-    static_assert(kStages >= 2 && (RT == 64 || RT == 128) && (DP == 64 || DP == 128), "");
+    static_assert(kSlots >= 4 && (RT == 64 || RT == 128) && (DP == 64 || DP == 128), "");
 };
 
 constexpr int kWideWarps = 8, kWideThreads = kWideWarps * 32 + 64;   // and one that loads, one that multiplies
@@ -63,14 +66,50 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, float* r) {
+    uint32_t v[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(v[i]);
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const float* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(__float_as_uint(r[0])), "r"(__float_as_uint(r[1])), "r"(__float_as_uint(r[2])),
+                 "r"(__float_as_uint(r[3])), "r"(__float_as_uint(r[4])), "r"(__float_as_uint(r[5])),
+                 "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
+                 : "memory");
+}
+// Eight values of each lane joined over the warp: lane l gets value (l >> 2)'s.
+template <class Op>
+__device__ __forceinline__ float join8(const float* x, Op op) {
+    const int lane = threadIdx.x & 31;
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        a[i] = op(up ? x[i + 4] : x[i], __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + 4], 16));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        b[i] = op(up ? a[i + 2] : a[i], __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8));
+    }
+    const bool up = lane & 4;
+    float c = op(up ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4));
+    c = op(c, __shfl_xor_sync(0xffffffffu, c, 2));
+    return op(c, __shfl_xor_sync(0xffffffffu, c, 1));
+}
+
 template <class C>
 __global__ void __launch_bounds__(kWideThreads, 1)
 attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int RT = C::RT, CT = C::CT, S = C::kStages, DP = C::DP, HC = C::kHalf, kN = kWideWarps * 32;
-    const uint32_t ring = sm100::smem_u32(smem), sp = ring + S * C::kStage, sq = sp + C::kP;
-    int* const s_hi = reinterpret_cast<int*>(smem + S * C::kStage + C::kP + C::kQ);   // [RT] tokens lo .. hi - 1 are seen
+    constexpr int RT = C::RT, CT = C::CT, S = C::kSlots, DP = C::DP, U = C::kUnits, kN = kWideWarps * 32;
+    const uint32_t ring = sm100::smem_u32(smem), sp = ring + S * C::kTile, sq = sp + C::kP;
+    int* const s_hi = reinterpret_cast<int*>(smem + S * C::kTile + C::kP + C::kQ);   // [RT] tokens lo .. hi - 1 are seen
     int* const s_lo = s_hi + RT;
     int* const s_row = s_lo + RT;                             // [RT] the row's place in its sequence's output
     float* const s_ref = reinterpret_cast<float*>(s_row + RT);   // [RT] running reference
@@ -78,9 +117,9 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
     float* const s_w = s_fac + RT;                            // [quarter of the tokens][RT] maxima, sums
     const uint32_t bars = sm100::smem_u32(s_w + 4 * RT);
     const uint32_t full = bars, empty = full + 8 * S, s_full = empty + 8 * S, s_free = s_full + 16, p_full = s_free + 16,
-                   pv = p_full + 8, q_full = pv + 8, drained = q_full + 8;
-    volatile int* const abort = reinterpret_cast<int*>(s_w + 4 * RT) + 48;
-    volatile uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(s_w + 4 * RT) + 49;
+                   pv = p_full + 16, q_full = pv + 16, drained = q_full + 8;
+    volatile int* const abort = reinterpret_cast<int*>(s_w + 4 * RT) + 56;
+    volatile uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(s_w + 4 * RT) + 57;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = p.Hq / p.Hkv, rows = group * p.Lq, chunks = (rows + RT - 1) / RT, hr_n = p.Hkv * chunks;
@@ -92,9 +131,9 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
         for (int i = 0; i < 2; ++i) {
             sm100::mbar_init(s_full + 8 * i, 1);
             sm100::mbar_init(s_free + 8 * i, kWideWarps);
+            sm100::mbar_init(p_full + 8 * i, kWideWarps);
+            sm100::mbar_init(pv + 8 * i, 1);
         }
-        sm100::mbar_init(p_full, kWideWarps);
-        sm100::mbar_init(pv, 1);
         sm100::mbar_init(q_full, kWideWarps);
         sm100::mbar_init(drained, 1);
         *abort = 0;
@@ -136,15 +175,14 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
 
     if (warp == kWideWarps) {                                 // loads: a box of one page a lane
         auto page_of = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size; };
-        int n = 0;
+        int m = 0;                                            // tile n: 2n its keys, 2n + 1 its values
 #pragma unroll 1
-        for (bool first = true; at.place < size; at.next<C>(p, hr_n), ++n, first = false) {
+        for (bool first = true; at.place < size; at.next<C>(p, hr_n), first = false) {
             const int c0 = at.s.start + at.tile * CT, h = head_of(at);
             if (first || (at.tile & 15) == 0) {               // page numbers to L1 ahead of their use, a tile a lane
                 const int64_t j = c0 + (int64_t)lane * CT;
                 if (j < at.s.len) touch_l1(p.pages + at.b * p.pages_seq + page_of((int)j));
             }
-            const uint32_t slot = n % S, bar = full + 8 * slot, dst = ring + slot * C::kStage;
             const int i = lane * p.box, j = c0 + i;
             const bool load = i < CT && j < at.s.len;
             const int pg = load ? page_of(j) : 0;
@@ -155,65 +193,76 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             }
             const int row = j - pg * p.page_size;
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, load));
-            if (n >= S) wait(empty + 8 * slot, (n / S - 1) & 1, 5);
-            if (dead) break;
-            if (lane == 0) sm100::mbar_arrive_expect_tx(bar, boxes * 2 * p.box * C::RB);
-            __syncwarp();
-            if (load)
+#pragma unroll 1
+            for (int kv = 0; kv < 2 && !dead; ++kv, ++m) {
+                const uint32_t bar = full + 8 * (m % S), dst = ring + m % S * C::kTile + i * 128;
+                if (m >= S) wait(empty + 8 * (m % S), (m / S - 1) & 1, 5);
+                if (dead) break;
+                if (lane == 0) sm100::mbar_arrive_expect_tx(bar, boxes * p.box * C::RB);
+                __syncwarp();
+                if (load)
 #pragma unroll
-                for (int x = 0; x < DP / 64; ++x) {
-                    const uint32_t d = dst + x * C::kPiece + i * 128;
-                    tma_load_4d(d, &kmap, bar, x * 64, p.order ? row : h, p.order ? h : row, page);
-                    tma_load_4d(d + C::kTile, &vmap, bar, x * 64, p.order ? row : h, p.order ? h : row, page);
-                }
+                    for (int x = 0; x < DP / 64; ++x)
+                        tma_load_4d(dst + x * C::kPiece, kv ? &vmap : &kmap, bar, x * 64, p.order ? row : h, p.order ? h : row, page);
+            }
+            if (dead) break;
         }
         if (dead)                                              // copies still in flight write to this CTA's memory
-            for (int k = n > S ? n - S : 0; k < n; ++k) sm100::mbar_drain(full + 8 * (k % S), (k / S) & 1, kWaitLimitNs);
+            for (int k = m > S ? m - S : 0; k < m; ++k) sm100::mbar_drain(full + 8 * (k % S), (k / S) & 1, kWaitLimitNs);
     } else if (warp == kWideWarps + 1) {                      // multiplies
-        // fp32 sums of bf16 products, 128 x RT; for O^T both operands MN-major
-        constexpr uint32_t kS = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(RT >> 3) << 17 | (128u >> 4) << 24;
-        constexpr uint32_t kO = kS | 1u << 15 | 1u << 16;
-        auto scores = [&](int n, bool first, int item) {
-            wait(full + 8 * (n % S), (n / S) & 1, 3);
+        // fp32 sums of bf16 products, 128 x the rows there are (sixteens); for O^T both
+        // operands MN-major
+        auto shape = [&](const Cursor& c) {
+            const int live = min(RT, rows - (c.hr - head_of(c) * chunks) * RT);
+            return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)((live + 15) / 16 * 2) << 17 | (128u >> 4) << 24;
+        };
+        auto scores = [&](int n, bool first, int item, uint32_t idesc) {
+            const int m = 2 * n;
+            wait(full + 8 * (m % S), (m / S) & 1, 3);
             if (first) wait(q_full, item & 1, 6);
             if (n >= 2) wait(s_free + 8 * (n & 1), ((n >> 1) - 1) & 1, 7);
             if (dead) return;
             sm100::tc_fence_after();
             if (lane == 0) {
-                const uint64_t a = sm100::umma_desc_k128_sw128(ring + (n % S) * C::kStage), b = sm100::umma_desc_k128_sw128(sq);
+                const uint64_t a = sm100::umma_desc_k128_sw128(ring + m % S * C::kTile), b = sm100::umma_desc_k128_sw128(sq);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     sm100::mma_f16(tmem + (n & 1) * RT, a + (k >> 2) * (C::kPiece >> 4) + (k & 3) * 2,
-                                   b + (k >> 2) * (RT * 128 >> 4) + (k & 3) * 2, kS, k > 0);
+                                   b + (k >> 2) * (RT * 128 >> 4) + (k & 3) * 2, idesc, k > 0);
+                sm100::tc_commit(empty + 8 * (m % S));
                 sm100::tc_commit(s_full + 8 * (n & 1));
             }
             __syncwarp();
         };
         int item = 0;
         bool first = true;
-        scores(0, true, 0);
+        uint32_t idesc = shape(at);
+        scores(0, true, 0, idesc);
 #pragma unroll 1
         for (int n = 0; at.place < size && !dead; ++n) {
             Cursor then = at;
             then.next<C>(p, hr_n);
             const bool more = then.place < size, fresh = then.tile == 0;
-            if (more && !fresh) scores(n + 1, false, item);
-            wait(p_full, n & 1, 8);
+            if (more && !fresh) scores(n + 1, false, item, idesc);
+            const int m = 2 * n + 1;
+            wait(full + 8 * (m % S), (m / S) & 1, 3);
+            wait(p_full + 8 * (n & 1), (n >> 1) & 1, 8);
             if (dead) break;
             sm100::tc_fence_after();
             if (lane == 0) {
                 // M is 128; a head of 64 has its second half beyond the tile: any
                 // values, on lanes that nobody reads
-                const uint64_t a = wide_desc_mn(ring + (n % S) * C::kStage + C::kTile, C::kPiece);
-                const uint64_t b = wide_desc_mn(sp, C::kPiece);
+                const uint64_t a = wide_desc_mn(ring + m % S * C::kTile, C::kPiece);
+                const uint64_t b = wide_desc_mn(sp + n % C::kBufs * C::kPart, C::kPiece);
 #pragma unroll
                 for (int k = 0; k < CT / 16; ++k)
-                    sm100::mma_f16(t_o, a + k * (16 * 128 >> 4), b + k * (16 * 128 >> 4), kO, !first || k > 0);
-                sm100::tc_commit(empty + 8 * (n % S));
-                sm100::tc_commit(pv);
+                    sm100::mma_f16(t_o, a + k * (16 * 128 >> 4), b + k * (16 * 128 >> 4), idesc | 1u << 15 | 1u << 16,
+                                   !first || k > 0);
+                sm100::tc_commit(empty + 8 * (m % S));
+                sm100::tc_commit(pv + 8 * (n & 1));
             }
             __syncwarp();
-            if (more && fresh) scores(n + 1, true, ++item);
+            if (more && fresh) idesc = shape(then), scores(n + 1, true, ++item, idesc);
             first = fresh;
             at = then;
         }
@@ -225,25 +274,38 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             __syncwarp();
         }
     } else {
-        const int quad = warp & 3, half = warp >> 2, c0 = half * HC, tok = quad * 32 + lane;
+        // eights of rows 2u + half are this thread's, of its token
+        const int quad = warp & 3, half = warp >> 2, c0 = half * 8, tok = quad * 32 + lane;
         const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
         const float xs = p.scale * kLog2e;
         auto sync = [&]() { sm100::named_bar_sync(2, kN); };
-        float sum[HC];
+        auto summed = [&](int n) {                            // tile n's product is in the sums
+            wait(pv + 8 * (n & 1), (n >> 1) & 1, 10);
+            sm100::tc_fence_after();
+        };
+        float sum[8 * U];
+        int live = 0;                                         // rows of the item that are there
+        auto on = [&](int u) { return (2 * u + half) * 8 < live; };
         bool set_apart = false;                               // products with values that are not finite, in t_x
 
         // An item's queries as the N operand, and its rows' bounds.
         auto begin = [&](const Cursor& c) {
             const int h = head_of(c), r0 = (c.hr - h * chunks) * RT;
             sync();                                           // nobody is at the bounds of the item before
-#pragma unroll 1
-            for (int i = threadIdx.x; i < RT * (DP / 8); i += kN) {
-                const int r = i / (DP / 8), k = i % (DP / 8), rr = r0 + r, qi = rr / group;
-                uint4 v = make_uint4(0, 0, 0, 0);
+            constexpr int kEach = RT * (DP / 8) / kN;
+            uint4 v[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {                 // in flight together
+                const int r = (i * kN + threadIdx.x) / (DP / 8), k = threadIdx.x % (DP / 8), rr = r0 + r, qi = rr / group;
+                v[i] = make_uint4(0, 0, 0, 0);
                 if (rr < rows && k * 8 < p.D)
-                    v = *reinterpret_cast<const uint4*>(p.q + c.b * p.q_seq + qi * p.q_token +
-                                                        (h * group + rr - qi * group) * p.q_head + k * 8);
-                st_shared16(sq + (k >> 3) * (RT * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+                    v[i] = *reinterpret_cast<const uint4*>(p.q + c.b * p.q_seq + qi * p.q_token +
+                                                           (h * group + rr - qi * group) * p.q_head + k * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int r = (i * kN + threadIdx.x) / (DP / 8), k = threadIdx.x % (DP / 8);
+                st_shared16(sq + (k >> 3) * (RT * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
             }
             if (threadIdx.x < RT) {
                 const int r = threadIdx.x, hi = r0 + r < rows ? c.s.len - p.Lq + (r0 + r) / group + 1 : 0;
@@ -258,53 +320,64 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
 
         auto compute = [&](int n, bool first) {
             const int t0 = at.s.start + at.tile * CT, j = t0 + tok;
-            const uint32_t t_s = tmem + (n & 1) * RT + c0 + t_lane, vb = ring + (n % S) * C::kStage + C::kTile;
+            const uint32_t t_s = tmem + (n & 1) * RT + c0 + t_lane, vb = ring + (2 * n + 1) % S * C::kTile;
             const bool edge = t0 + CT > at.s.len - p.Lq + 1 || (p.window && t0 < at.s.len - p.window);
             wait(s_full + 8 * (n & 1), (n >> 1) & 1, 9);
             sm100::tc_fence_after();
-            // 32 rows' log2 scores, above the running reference or as they are; tokens
+            // an eight's log2 scores, above the running reference or as they are; tokens
             // that a query does not see at -inf
+            auto raw = [&](int u, float* x) { tmem_ld_x8(t_s + u * 16, x); };
+            auto relative = [&](int u, float* x, bool above) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    const int c = c0 + u * 16 + e;
+                    const float4 r = above ? *reinterpret_cast<const float4*>(s_ref + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[e] = fmaf(x[e], xs, -r.x), x[e + 1] = fmaf(x[e + 1], xs, -r.y);
+                    x[e + 2] = fmaf(x[e + 2], xs, -r.z), x[e + 3] = fmaf(x[e + 3], xs, -r.w);
+                    if (edge) {
+                        const int4 hi = *reinterpret_cast<const int4*>(s_hi + c), lo = *reinterpret_cast<const int4*>(s_lo + c);
+                        if (j >= hi.x || j < lo.x) x[e] = -INFINITY;
+                        if (j >= hi.y || j < lo.y) x[e + 1] = -INFINITY;
+                        if (j >= hi.z || j < lo.z) x[e + 2] = -INFINITY;
+                        if (j >= hi.w || j < lo.w) x[e + 3] = -INFINITY;
+                    }
+                }
+            };
+            // four eights at a time
             float x[32];
-            auto load = [&](int c, bool above) {
-                uint32_t s[32];
-                sm100::tmem_ld_32x32b_x32(t_s + c, s);
+            auto load = [&](int u0, bool above) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (on(u0 + u)) raw(u0 + u, x + 8 * u);
                 sm100::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 r = above ? *reinterpret_cast<const float4*>(s_ref + c0 + c + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    x[e] = fmaf(__uint_as_float(s[e]), xs, -r.x);
-                    x[e + 1] = fmaf(__uint_as_float(s[e + 1]), xs, -r.y);
-                    x[e + 2] = fmaf(__uint_as_float(s[e + 2]), xs, -r.z);
-                    x[e + 3] = fmaf(__uint_as_float(s[e + 3]), xs, -r.w);
-                }
-                if (edge) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (j >= s_hi[c0 + c + e] || j < s_lo[c0 + c + e]) x[e] = -INFINITY;
-                }
+                for (int u = 0; u < 4; ++u)
+                    if (on(u0 + u)) relative(u0 + u, x + 8 * u, above);
             };
             float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < HC; c += 32) {
-                load(c, true);
+            for (int u0 = 0; u0 < U; u0 += 4) {
+                load(u0, true);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
+                for (int u = 0; u < 4; ++u)
+                    if (on(u0 + u))
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) top = fmaxf(top, x[8 * u + e]);
             }
             const bool moved = sm100::bar_red_or(1, kN, top > kLazy);
             if (moved) {                                      // the rows' references move
 #pragma unroll 1
-                for (int c = 0; c < HC; c += 32) {
-                    load(c, false);
+                for (int u0 = 0; u0 < U; u0 += 4) {
+                    load(u0, false);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float r = fmaxf(x[e], kNone);
-#pragma unroll
-                        for (int off = 16; off; off >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, off));
-                        if (lane == 0) s_w[quad * RT + c0 + c + e] = r;
-                    }
+                    for (int u = 0; u < 4; ++u)
+                        if (on(u0 + u)) {
+                            const float r = join8(x + 8 * u, [](float a, float b) { return fmaxf(a, b); });
+                            if ((lane & 3) == 0) s_w[quad * RT + c0 + (u0 + u) * 16 + (lane >> 2)] = fmaxf(r, kNone);
+                        }
                 }
                 sync();
-                if (threadIdx.x < RT) {
+                if (threadIdx.x < (live + 7) / 8 * 8) {
                     const int r = threadIdx.x;
                     const float was = s_ref[r], now = fmaxf(was, fmaxf(fmaxf(s_w[r], s_w[RT + r]),
                                                                        fmaxf(s_w[2 * RT + r], s_w[3 * RT + r])));
@@ -313,37 +386,41 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
                 }
                 sync();
 #pragma unroll
-                for (int c = 0; c < HC; ++c) sum[c] *= s_fac[c0 + c];
+                for (int i = 0; i < 8 * U; ++i) sum[i] *= s_fac[c0 + (i >> 3) * 16 + (i & 7)];
                 if (!first) {
-                    wait(pv, (n - 1) & 1, 10);                // the sums so far are all in
-                    sm100::tc_fence_after();
+                    summed(n - 1);
 #pragma unroll 1
-                    for (int c = 0; c < HC; c += 32) {
-                        uint32_t o[32];
-                        sm100::tmem_ld_32x32b_x32(t_o + t_lane + c0 + c, o);
+                    for (int u = 0; u < U && on(u); ++u) {
+                        float o[8];
+                        tmem_ld_x8(t_o + t_lane + c0 + u * 16, o);
                         sm100::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_fac[c0 + c + e]);
-                        sm100::tmem_st_32x32b_x32(t_o + t_lane + c0 + c, o);
+                        for (int e = 0; e < 8; ++e) o[e] *= s_fac[c0 + u * 16 + e];
+                        tmem_st_x8(t_o + t_lane + c0 + u * 16, o);
                     }
                     sm100::tmem_wait_st();
                 }
             }
-            if (n > 0) wait(pv, (n - 1) & 1, 10);             // the probabilities before are read
-            // row of the token, 64 of the rows a piece
-            const uint32_t pr = sp + c0 / 64 * C::kPiece + tok * 128;
+            // the probabilities of the tile that had this buffer are read
+            if (n >= C::kBufs) summed(n - C::kBufs);
+            // row of the token, eight eights a piece
+            const uint32_t sp_n = sp + n % C::kBufs * C::kPart, pr = sp_n + tok * 128;
 #pragma unroll
-            for (int c = 0; c < HC; c += 32) {
-                if (HC > 32 || moved) load(c, true);          // (64 rows a thread are not kept)
+            for (int u0 = 0; u0 < U; u0 += 4) {
+                if (U > 4 || moved) load(u0, true);           // (more than four are not kept)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    x[e] = ex2(x[e]);
-                    sum[c + e] += x[e];
-                }
+                for (int u = 0; u < 4; ++u)
+                    if (on(u0 + u)) {
+                        float* const y = x + 8 * u;
 #pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    st_shared16(pr + ((((c0 & 63) + c + e) / 8 ^ (tok & 7)) << 4), pack2_bf16(x[e], x[e + 1]),
-                                pack2_bf16(x[e + 2], x[e + 3]), pack2_bf16(x[e + 4], x[e + 5]), pack2_bf16(x[e + 6], x[e + 7]));
+                        for (int e = 0; e < 8; ++e) {
+                            y[e] = ex2(y[e]);
+                            sum[8 * (u0 + u) + e] += y[e];
+                        }
+                        const int cu = 2 * (u0 + u) + half;
+                        st_shared16(pr + (cu >> 3) * C::kPiece + (((cu & 7) ^ (tok & 7)) << 4), pack2_bf16(y[0], y[1]),
+                                    pack2_bf16(y[2], y[3]), pack2_bf16(y[4], y[5]), pack2_bf16(y[6], y[7]));
+                    }
             }
             sm100::tc_fence_before();
             __syncwarp();
@@ -351,6 +428,7 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             // What the product must not meet: rows of no visible token become zero, and
             // values that are not finite and that only some queries see are set apart.
             if (edge) {
+                wait(full + 8 * ((2 * n + 1) % S), ((2 * n + 1) / S) & 1, 3);
                 const int both_lo = p.window ? at.s.len - p.window : 0, both_hi = at.s.len - p.Lq + 1;   // seen by every query
                 auto some = [&](int i) { return i >= at.s.lo && i < at.s.len && (i < both_lo || i >= both_hi); };
                 auto value = [&](int i, int d) {
@@ -370,12 +448,11 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
                 if (sm100::bar_red_or(1, kN, bad)) {
                     const int d = quad * 32 + lane;
 #pragma unroll 1
-                    for (int c = 0; c < HC; c += 32) {
-                        uint32_t y[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) y[e] = 0;
+                    for (int u = 0; u < U && on(u); ++u) {
+                        const int cu = 2 * u + half;
+                        float y[8] = {};
                         if (set_apart) {
-                            sm100::tmem_ld_32x32b_x32(t_x + t_lane + c0 + c, y);
+                            tmem_ld_x8(t_x + t_lane + c0 + u * 16, y);
                             sm100::tmem_wait_ld();
                         }
 #pragma unroll 1
@@ -383,17 +460,14 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
                             if (!some(t0 + i)) continue;
                             const float v = d < DP ? ld_value<false>(value(i, d)) : 0.f;
                             if (isfinite(v)) continue;
-                            const uint32_t pi = sp + c0 / 64 * C::kPiece + i * 128;
+                            const uint32_t pi = sp_n + (cu >> 3) * C::kPiece + i * 128 + (((cu & 7) ^ (i & 7)) << 4);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int r = (c0 & 63) + c + e;
-                                const float q = ld_value<false>(pi + ((r >> 3 ^ (i & 7)) << 4) + (r & 7) * 2);
-                                if (t0 + i < s_hi[c0 + c + e] && t0 + i >= s_lo[c0 + c + e])
-                                    y[e] = __float_as_uint(__uint_as_float(y[e]) + q * v);
-                            }
+                            for (int e = 0; e < 8; ++e)
+                                if (t0 + i < s_hi[cu * 8 + e] && t0 + i >= s_lo[cu * 8 + e])
+                                    y[e] += ld_value<false>(pi + 2 * e) * v;
                         }
                         __syncwarp();
-                        sm100::tmem_st_32x32b_x32(t_x + t_lane + c0 + c, y);
+                        tmem_st_x8(t_x + t_lane + c0 + u * 16, y);
                     }
                     sm100::tmem_wait_st();
                     set_apart = true;
@@ -406,7 +480,7 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             sm100::tc_fence_before();
             sm100::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) sm100::mbar_arrive(p_full);
+            if (lane == 0) sm100::mbar_arrive(p_full + 8 * (n & 1));
         };
 
         // An item's sums written: the result if it lies wholly in this CTA's range,
@@ -417,58 +491,59 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             const int h = head_of(c), r0 = (c.hr - h * chunks) * RT;
             float* const slot = p.ws + ((int64_t)blockIdx.x * 2 + (begun <= 0 ? 0 : 1)) * (RT * (DP + 2));
 #pragma unroll
-            for (int i = 0; i < HC; ++i) {
-                float y = sum[i];
-#pragma unroll
-                for (int off = 16; off; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-                if (lane == 0) s_w[quad * RT + c0 + i] = y;
-                sum[i] = 0.f;
-            }
+            for (int u = 0; u < U; ++u)
+                if (on(u)) {
+                    const float y = join8(sum + 8 * u, [](float a, float b) { return a + b; });
+                    if ((lane & 3) == 0) s_w[quad * RT + c0 + u * 16 + (lane >> 2)] = y;
+                }
             sync();
-            if (threadIdx.x < RT) {
+            if (threadIdx.x < (live + 7) / 8 * 8) {
                 const int r = threadIdx.x, rr = r0 + r, qi = rr / group;
                 const float l = (s_w[r] + s_w[RT + r]) + (s_w[2 * RT + r] + s_w[3 * RT + r]);
-                s_row[r] = rr < rows ? qi * p.Hq + h * group + rr - qi * group : -1;
+                s_row[r] = qi * p.Hq + h * group + rr - qi * group;
                 s_fac[r] = l == 0.f ? 0.f : 1.f / l;
                 if (!whole)
                     slot[RT * DP + r] = s_ref[r], slot[RT * DP + RT + r] = l;
-                else if (p.lse && rr < rows)
+                else if (p.lse && r < live)
                     p.lse[(int64_t)c.b * p.Lq * p.Hq + s_row[r]] = l == 0.f ? -INFINITY : (s_ref[r] + log2f(l)) * kLn2;
                 s_ref[r] = kNone;
             }
-            wait(pv, n & 1, 10);
-            sm100::tc_fence_after();
+            summed(n);
             sync();
             const int d = quad * 32 + lane;
             uint16_t* const out = p.o + (int64_t)c.b * p.Lq * p.Hq * p.D + d;
 #pragma unroll 1
-            for (int i = 0; i < HC; i += 32) {
-                uint32_t o[32], y[32];
-                sm100::tmem_ld_32x32b_x32(t_o + t_lane + c0 + i, o);
-                if (set_apart) sm100::tmem_ld_32x32b_x32(t_x + t_lane + c0 + i, y);
+            for (int u = 0; u < U && on(u); ++u) {
+                float o[8], y[8];
+                tmem_ld_x8(t_o + t_lane + c0 + u * 16, o);
+                if (set_apart) tmem_ld_x8(t_x + t_lane + c0 + u * 16, y);
                 sm100::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int r = c0 + i + e;
-                    float v = __uint_as_float(o[e]);
-                    if (set_apart) v += __uint_as_float(y[e]);
+                for (int e = 0; e < 8; ++e) {
+                    const int r = c0 + u * 16 + e;
+                    if (set_apart) o[e] += y[e];
                     if (!whole) {
-                        if (d < DP) slot[r * DP + d] = v;
-                    } else if (s_row[r] >= 0 && d < p.D) {
+                        if (d < DP) slot[r * DP + d] = o[e];
+                    } else if (r < live && d < p.D) {
                         const float f = s_fac[r];
-                        out[(int64_t)s_row[r] * p.D] = (uint16_t)pack2_bf16(f == 0.f ? 0.f : v * f, 0.f);
+                        out[(int64_t)s_row[r] * p.D] = (uint16_t)pack2_bf16(f == 0.f ? 0.f : o[e] * f, 0.f);
                     }
                 }
             }
             set_apart = false;
         };
 
-#pragma unroll
-        for (int i = 0; i < HC; ++i) sum[i] = 0.f;
+        auto count = [&](const Cursor& c) { return min(RT, rows - (c.hr - head_of(c) * chunks) * RT); };
+        live = count(at);
         begin(at);
         bool first = true;
 #pragma unroll 1
         for (int n = 0; at.place < size; ++n) {
+            if (first) {
+                live = count(at);
+#pragma unroll
+                for (int i = 0; i < 8 * U; ++i) sum[i] = 0.f;
+            }
             compute(n, first);
             Cursor then = at;
             then.next<C>(p, hr_n);
