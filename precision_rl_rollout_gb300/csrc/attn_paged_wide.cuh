@@ -37,16 +37,17 @@ struct WideConfig {
     static constexpr int DP = DP_, RT = RT_, ES = 2, RB = DP * ES, PB = 128, CT = 128;
     static constexpr int kTile = CT * RB, kCtas = 1;
     static constexpr int kPiece = CT * 128;                  // 64 values of a tile's tokens
-    static constexpr int kPart = RT / 64 * kPiece, kBufs = DP + RT > 192 ? 1 : 2, kP = kBufs * kPart;   // probabilities
+    static constexpr int kPart = (RT + 63) / 64 * kPiece, kBufs = DP == 128 && RT == 128 ? 1 : 2, kP = kBufs * kPart;   // probabilities
     static constexpr int kQ = DP / 64 * RT * 128;
     static constexpr int kSmall = RT * 4 * 9 + 28 * 8 + 16;
     // a tile of keys or of values a slot, let go of by its own product
     static constexpr int kFit = (232448 - kP - kQ - kSmall) / kTile, kSlots = kFit < 8 ? kFit : 8;
     static constexpr int kSmem = kSlots * kTile + kP + kQ + kSmall;
     static constexpr int kItem = 65536 / kTile;              // an item's start and end, in tiles
-    static constexpr int kUnits = RT / 16;                   // eights of rows a thread
-    static constexpr uint32_t kCols = 4 * RT;                // two tiles' scores, the sums, what is set apart
-    static_assert(kSlots >= 4 && (RT == 64 || RT == 128) && (DP == 64 || DP == 128), "");
+    static constexpr int kUnits = RT / 16;                   // eights of rows a thread, kept or taken four at a time
+    static constexpr int kGroup = kUnits <= 5 ? kUnits : 4;
+    static constexpr uint32_t kSlice = RT <= 64 ? 64 : 128, kCols = 4 * kSlice;   // two tiles' scores, the sums, what is set apart
+    static_assert(kSlots >= 4 && RT % 16 == 0 && RT <= 128 && kUnits % kGroup == 0 && (DP == 64 || DP == 128), "");
 };
 
 constexpr int kWideWarps = 8, kWideThreads = kWideWarps * 32 + 64;   // and one that loads, one that multiplies
@@ -160,7 +161,7 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
     }
     __syncthreads();
     sm100::tc_fence_after();
-    const uint32_t tmem = *s_tmem, t_o = tmem + 2 * RT, t_x = tmem + 3 * RT;
+    const uint32_t tmem = *s_tmem, t_o = tmem + 2 * C::kSlice, t_x = tmem + 3 * C::kSlice;
 
     auto head_of = [&](const Cursor& c) { return chunks == 1 ? c.hr : c.hr / chunks; };
     bool dead = false;                                        // a wait ran out: nothing more is issued or waited for
@@ -210,13 +211,10 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
         if (dead)                                              // copies still in flight write to this CTA's memory
             for (int k = m > S ? m - S : 0; k < m; ++k) sm100::mbar_drain(full + 8 * (k % S), (k / S) & 1, kWaitLimitNs);
     } else if (warp == kWideWarps + 1) {                      // multiplies
-        // fp32 sums of bf16 products, 128 x the rows there are (sixteens); for O^T both
-        // operands MN-major
-        auto shape = [&](const Cursor& c) {
-            const int live = min(RT, rows - (c.hr - head_of(c) * chunks) * RT);
-            return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)((live + 15) / 16 * 2) << 17 | (128u >> 4) << 24;
-        };
-        auto scores = [&](int n, bool first, int item, uint32_t idesc) {
+        // fp32 sums of bf16 products, 128 x RT; for O^T both operands MN-major
+        constexpr uint32_t kS = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(RT >> 3) << 17 | (128u >> 4) << 24;
+        constexpr uint32_t kO = kS | 1u << 15 | 1u << 16;
+        auto scores = [&](int n, bool first, int item) {
             const int m = 2 * n;
             wait(full + 8 * (m % S), (m / S) & 1, 3);
             if (first) wait(q_full, item & 1, 6);
@@ -227,8 +225,8 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
                 const uint64_t a = sm100::umma_desc_k128_sw128(ring + m % S * C::kTile), b = sm100::umma_desc_k128_sw128(sq);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    sm100::mma_f16(tmem + (n & 1) * RT, a + (k >> 2) * (C::kPiece >> 4) + (k & 3) * 2,
-                                   b + (k >> 2) * (RT * 128 >> 4) + (k & 3) * 2, idesc, k > 0);
+                    sm100::mma_f16(tmem + (n & 1) * C::kSlice, a + (k >> 2) * (C::kPiece >> 4) + (k & 3) * 2,
+                                   b + (k >> 2) * (RT * 128 >> 4) + (k & 3) * 2, kS, k > 0);
                 sm100::tc_commit(empty + 8 * (m % S));
                 sm100::tc_commit(s_full + 8 * (n & 1));
             }
@@ -236,14 +234,13 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
         };
         int item = 0;
         bool first = true;
-        uint32_t idesc = shape(at);
-        scores(0, true, 0, idesc);
+        scores(0, true, 0);
 #pragma unroll 1
         for (int n = 0; at.place < size && !dead; ++n) {
             Cursor then = at;
             then.next<C>(p, hr_n);
             const bool more = then.place < size, fresh = then.tile == 0;
-            if (more && !fresh) scores(n + 1, false, item, idesc);
+            if (more && !fresh) scores(n + 1, false, item);
             const int m = 2 * n + 1;
             wait(full + 8 * (m % S), (m / S) & 1, 3);
             wait(p_full + 8 * (n & 1), (n >> 1) & 1, 8);
@@ -256,13 +253,12 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
                 const uint64_t b = wide_desc_mn(sp + n % C::kBufs * C::kPart, C::kPiece);
 #pragma unroll
                 for (int k = 0; k < CT / 16; ++k)
-                    sm100::mma_f16(t_o, a + k * (16 * 128 >> 4), b + k * (16 * 128 >> 4), idesc | 1u << 15 | 1u << 16,
-                                   !first || k > 0);
+                    sm100::mma_f16(t_o, a + k * (16 * 128 >> 4), b + k * (16 * 128 >> 4), kO, !first || k > 0);
                 sm100::tc_commit(empty + 8 * (m % S));
                 sm100::tc_commit(pv + 8 * (n & 1));
             }
             __syncwarp();
-            if (more && fresh) idesc = shape(then), scores(n + 1, true, ++item, idesc);
+            if (more && fresh) scores(n + 1, true, ++item);
             first = fresh;
             at = then;
         }
@@ -292,20 +288,20 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
         auto begin = [&](const Cursor& c) {
             const int h = head_of(c), r0 = (c.hr - h * chunks) * RT;
             sync();                                           // nobody is at the bounds of the item before
-            constexpr int kEach = RT * (DP / 8) / kN;
+            constexpr int kEach = (RT * (DP / 8) + kN - 1) / kN;
             uint4 v[kEach];
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {                 // in flight together
                 const int r = (i * kN + threadIdx.x) / (DP / 8), k = threadIdx.x % (DP / 8), rr = r0 + r, qi = rr / group;
                 v[i] = make_uint4(0, 0, 0, 0);
-                if (rr < rows && k * 8 < p.D)
+                if (r < RT && rr < rows && k * 8 < p.D)
                     v[i] = *reinterpret_cast<const uint4*>(p.q + c.b * p.q_seq + qi * p.q_token +
                                                            (h * group + rr - qi * group) * p.q_head + k * 8);
             }
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 const int r = (i * kN + threadIdx.x) / (DP / 8), k = threadIdx.x % (DP / 8);
-                st_shared16(sq + (k >> 3) * (RT * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+                if (r < RT) st_shared16(sq + (k >> 3) * (RT * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
             }
             if (threadIdx.x < RT) {
                 const int r = threadIdx.x, hi = r0 + r < rows ? c.s.len - p.Lq + (r0 + r) / group + 1 : 0;
@@ -320,64 +316,57 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
 
         auto compute = [&](int n, bool first) {
             const int t0 = at.s.start + at.tile * CT, j = t0 + tok;
-            const uint32_t t_s = tmem + (n & 1) * RT + c0 + t_lane, vb = ring + (2 * n + 1) % S * C::kTile;
+            const uint32_t t_s = tmem + (n & 1) * C::kSlice + c0 + t_lane, vb = ring + (2 * n + 1) % S * C::kTile;
             const bool edge = t0 + CT > at.s.len - p.Lq + 1 || (p.window && t0 < at.s.len - p.window);
             wait(s_full + 8 * (n & 1), (n >> 1) & 1, 9);
             sm100::tc_fence_after();
-            // an eight's log2 scores, above the running reference or as they are; tokens
+            // a group's log2 scores, above the running reference or as they are; tokens
             // that a query does not see at -inf
-            auto raw = [&](int u, float* x) { tmem_ld_x8(t_s + u * 16, x); };
-            auto relative = [&](int u, float* x, bool above) {
+            constexpr int G = C::kGroup;
+            float x[8 * G];
+            auto load = [&](int u0, bool above) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const int c = c0 + u * 16 + e;
-                    const float4 r = above ? *reinterpret_cast<const float4*>(s_ref + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int u = 0; u < G; ++u) tmem_ld_x8(t_s + (u0 + u) * 16, x + 8 * u);
+                sm100::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8 * G; e += 4) {
+                    const float4 r = above ? *reinterpret_cast<const float4*>(s_ref + c0 + (u0 + e / 8) * 16 + e % 8)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
                     x[e] = fmaf(x[e], xs, -r.x), x[e + 1] = fmaf(x[e + 1], xs, -r.y);
                     x[e + 2] = fmaf(x[e + 2], xs, -r.z), x[e + 3] = fmaf(x[e + 3], xs, -r.w);
-                    if (edge) {
+                }
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 8 * G; e += 4) {
+                        const int c = c0 + (u0 + e / 8) * 16 + e % 8;
                         const int4 hi = *reinterpret_cast<const int4*>(s_hi + c), lo = *reinterpret_cast<const int4*>(s_lo + c);
-                        if (j >= hi.x || j < lo.x) x[e] = -INFINITY;
-                        if (j >= hi.y || j < lo.y) x[e + 1] = -INFINITY;
-                        if (j >= hi.z || j < lo.z) x[e + 2] = -INFINITY;
-                        if (j >= hi.w || j < lo.w) x[e + 3] = -INFINITY;
+                        x[e] = j >= hi.x || j < lo.x ? -INFINITY : x[e];
+                        x[e + 1] = j >= hi.y || j < lo.y ? -INFINITY : x[e + 1];
+                        x[e + 2] = j >= hi.z || j < lo.z ? -INFINITY : x[e + 2];
+                        x[e + 3] = j >= hi.w || j < lo.w ? -INFINITY : x[e + 3];
                     }
                 }
             };
-            // four eights at a time
-            float x[32];
-            auto load = [&](int u0, bool above) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (on(u0 + u)) raw(u0 + u, x + 8 * u);
-                sm100::tmem_wait_ld();
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (on(u0 + u)) relative(u0 + u, x + 8 * u, above);
-            };
             float top = -INFINITY;
 #pragma unroll
-            for (int u0 = 0; u0 < U; u0 += 4) {
+            for (int u0 = 0; u0 < U; u0 += G) {
                 load(u0, true);
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (on(u0 + u))
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top = fmaxf(top, x[8 * u + e]);
+                for (int e = 0; e < 8 * G; ++e) top = fmaxf(top, x[e]);
             }
             const bool moved = sm100::bar_red_or(1, kN, top > kLazy);
             if (moved) {                                      // the rows' references move
 #pragma unroll 1
-                for (int u0 = 0; u0 < U; u0 += 4) {
+                for (int u0 = 0; u0 < U; u0 += G) {
                     load(u0, false);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (on(u0 + u)) {
-                            const float r = join8(x + 8 * u, [](float a, float b) { return fmaxf(a, b); });
-                            if ((lane & 3) == 0) s_w[quad * RT + c0 + (u0 + u) * 16 + (lane >> 2)] = fmaxf(r, kNone);
-                        }
+                    for (int u = 0; u < G; ++u) {
+                        const float r = join8(x + 8 * u, [](float a, float b) { return fmaxf(a, b); });
+                        if ((lane & 3) == 0) s_w[quad * RT + c0 + (u0 + u) * 16 + (lane >> 2)] = fmaxf(r, kNone);
+                    }
                 }
                 sync();
-                if (threadIdx.x < (live + 7) / 8 * 8) {
+                if (threadIdx.x < RT) {
                     const int r = threadIdx.x;
                     const float was = s_ref[r], now = fmaxf(was, fmaxf(fmaxf(s_w[r], s_w[RT + r]),
                                                                        fmaxf(s_w[2 * RT + r], s_w[3 * RT + r])));
@@ -390,7 +379,7 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
                 if (!first) {
                     summed(n - 1);
 #pragma unroll 1
-                    for (int u = 0; u < U && on(u); ++u) {
+                    for (int u = 0; u < U; ++u) {
                         float o[8];
                         tmem_ld_x8(t_o + t_lane + c0 + u * 16, o);
                         sm100::tmem_wait_ld();
@@ -406,21 +395,20 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             // row of the token, eight eights a piece
             const uint32_t sp_n = sp + n % C::kBufs * C::kPart, pr = sp_n + tok * 128;
 #pragma unroll
-            for (int u0 = 0; u0 < U; u0 += 4) {
-                if (U > 4 || moved) load(u0, true);           // (more than four are not kept)
+            for (int u0 = 0; u0 < U; u0 += G) {
+                if (U > G || moved) load(u0, true);           // (more than a group is not kept)
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (on(u0 + u)) {
-                        float* const y = x + 8 * u;
+                for (int u = 0; u < G; ++u) {
+                    float* const y = x + 8 * u;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            y[e] = ex2(y[e]);
-                            sum[8 * (u0 + u) + e] += y[e];
-                        }
-                        const int cu = 2 * (u0 + u) + half;
-                        st_shared16(pr + (cu >> 3) * C::kPiece + (((cu & 7) ^ (tok & 7)) << 4), pack2_bf16(y[0], y[1]),
-                                    pack2_bf16(y[2], y[3]), pack2_bf16(y[4], y[5]), pack2_bf16(y[6], y[7]));
+                    for (int e = 0; e < 8; ++e) {
+                        y[e] = ex2(y[e]);
+                        sum[8 * (u0 + u) + e] += y[e];
                     }
+                    const int cu = 2 * (u0 + u) + half;
+                    st_shared16(pr + (cu >> 3) * C::kPiece + (((cu & 7) ^ (tok & 7)) << 4), pack2_bf16(y[0], y[1]),
+                                pack2_bf16(y[2], y[3]), pack2_bf16(y[4], y[5]), pack2_bf16(y[6], y[7]));
+                }
             }
             sm100::tc_fence_before();
             __syncwarp();
@@ -491,13 +479,12 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             const int h = head_of(c), r0 = (c.hr - h * chunks) * RT;
             float* const slot = p.ws + ((int64_t)blockIdx.x * 2 + (begun <= 0 ? 0 : 1)) * (RT * (DP + 2));
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (on(u)) {
-                    const float y = join8(sum + 8 * u, [](float a, float b) { return a + b; });
-                    if ((lane & 3) == 0) s_w[quad * RT + c0 + u * 16 + (lane >> 2)] = y;
-                }
+            for (int u = 0; u < U; ++u) {
+                const float y = join8(sum + 8 * u, [](float a, float b) { return a + b; });
+                if ((lane & 3) == 0) s_w[quad * RT + c0 + u * 16 + (lane >> 2)] = y;
+            }
             sync();
-            if (threadIdx.x < (live + 7) / 8 * 8) {
+            if (threadIdx.x < RT) {
                 const int r = threadIdx.x, rr = r0 + r, qi = rr / group;
                 const float l = (s_w[r] + s_w[RT + r]) + (s_w[2 * RT + r] + s_w[3 * RT + r]);
                 s_row[r] = qi * p.Hq + h * group + rr - qi * group;
@@ -600,12 +587,19 @@ Plan plan_wide(int64_t max_len) {
     return Plan{(size_t)num_sms() * 2 * C::RT * (C::DP + 2) * sizeof(float), 2};
 }
 
-// Where it is taken, and its configuration.
+// Where it is taken, and its configuration: as few rows as hold them, above the
+// largest in chunks of 128, each reading the cache again.
 inline bool is_wide(int64_t D, int64_t rows) { return rows > 32 && D <= 128; }
+template <int DP, class F>
+auto pick_wide_rows(int64_t rows, F f) {
+    if (rows <= 48) return f(WideConfig<DP, 48>{});
+    if (rows <= 64) return f(WideConfig<DP, 64>{});
+    if (rows <= 80) return f(WideConfig<DP, 80>{});
+    return f(WideConfig<DP, 128>{});
+}
 template <class F>
 auto pick_wide(int64_t D, int64_t rows, F f) {
-    if (D <= 64) return rows <= 64 ? f(WideConfig<64, 64>{}) : f(WideConfig<64, 128>{});
-    return rows <= 64 ? f(WideConfig<128, 64>{}) : f(WideConfig<128, 128>{});
+    return D <= 64 ? pick_wide_rows<64>(rows, f) : pick_wide_rows<128>(rows, f);
 }
 
 }  // namespace
