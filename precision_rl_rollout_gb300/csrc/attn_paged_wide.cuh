@@ -45,7 +45,7 @@ struct WideConfig {
     static constexpr int kSmem = kSlots * kTile + kP + kQ + kSmall;
     static constexpr int kItem = 65536 / kTile;              // an item's start and end, in tiles
     static constexpr int kUnits = RT / 16;                   // eights of rows a thread, kept or taken four at a time
-    static constexpr int kGroup = kUnits <= 5 ? kUnits : 4;
+    static constexpr int kGroup = kUnits <= 6 ? kUnits : 4;
     static constexpr uint32_t kSlice = RT <= 64 ? 64 : 128, kCols = 4 * kSlice;   // two tiles' scores, the sums, what is set apart
     static_assert(kSlots >= 4 && RT % 16 == 0 && RT <= 128 && kUnits % kGroup == 0 && (DP == 64 || DP == 128), "");
 };
@@ -281,6 +281,7 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
         };
         float sum[8 * U];
         int live = 0;                                         // rows of the item that are there
+        int both_lo = 0, both_hi = 0;
         auto on = [&](int u) { return (2 * u + half) * 8 < live; };
         bool set_apart = false;                               // products with values that are not finite, in t_x
 
@@ -317,7 +318,8 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
         auto compute = [&](int n, bool first) {
             const int t0 = at.s.start + at.tile * CT, j = t0 + tok;
             const uint32_t t_s = tmem + (n & 1) * C::kSlice + c0 + t_lane, vb = ring + (2 * n + 1) % S * C::kTile;
-            const bool edge = t0 + CT > at.s.len - p.Lq + 1 || (p.window && t0 < at.s.len - p.window);
+            // tokens both_lo .. both_hi - 1 are seen by every row of the item
+            const bool edge = t0 + CT > both_hi || t0 < both_lo;
             wait(s_full + 8 * (n & 1), (n >> 1) & 1, 9);
             sm100::tc_fence_after();
             // a group's log2 scores, above the running reference or as they are; tokens
@@ -417,7 +419,6 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             // values that are not finite and that only some queries see are set apart.
             if (edge) {
                 wait(full + 8 * ((2 * n + 1) % S), ((2 * n + 1) / S) & 1, 3);
-                const int both_lo = p.window ? at.s.len - p.window : 0, both_hi = at.s.len - p.Lq + 1;   // seen by every query
                 auto some = [&](int i) { return i >= at.s.lo && i < at.s.len && (i < both_lo || i >= both_hi); };
                 auto value = [&](int i, int d) {
                     return vb + (d >> 6) * C::kPiece + i * 128 + (((d >> 3 & 7) ^ (i & 7)) << 4) + (d & 7) * 2;
@@ -520,14 +521,15 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
             set_apart = false;
         };
 
-        auto count = [&](const Cursor& c) { return min(RT, rows - (c.hr - head_of(c) * chunks) * RT); };
-        live = count(at);
         begin(at);
         bool first = true;
 #pragma unroll 1
         for (int n = 0; at.place < size; ++n) {
             if (first) {
-                live = count(at);
+                const int r0 = (at.hr - head_of(at) * chunks) * RT, p0 = at.s.len - p.Lq + 1;
+                live = min(RT, rows - r0);
+                both_hi = p0 + r0 / group;
+                both_lo = p.window ? p0 + (r0 + live - 1) / group - p.window : 0;
 #pragma unroll
                 for (int i = 0; i < 8 * U; ++i) sum[i] = 0.f;
             }
@@ -587,15 +589,20 @@ Plan plan_wide(int64_t max_len) {
     return Plan{(size_t)num_sms() * 2 * C::RT * (C::DP + 2) * sizeof(float), 2};
 }
 
-// Where it is taken, and its configuration: as few rows as hold them, above the
-// largest in chunks of 128, each reading the cache again.
+// Where it is taken, and its configuration: as few rows as hold them, in chunks of up
+// to 96, each reading the cache again; up to 128 in one, whose scores a thread cannot
+// keep, so that it reads them twice.  120 rows, 32 sequences to 16384: 354 us in one,
+// 396 in two chunks; 320 rows, 16 sequences: 525 us in chunks of 128, 462 in ones of 80;
+// prompt chunks of 512 behind up to 3488 tokens, 7 heads a kv head: 724 and 640.
 inline bool is_wide(int64_t D, int64_t rows) { return rows > 32 && D <= 128; }
 template <int DP, class F>
 auto pick_wide_rows(int64_t rows, F f) {
-    if (rows <= 48) return f(WideConfig<DP, 48>{});
-    if (rows <= 64) return f(WideConfig<DP, 64>{});
-    if (rows <= 80) return f(WideConfig<DP, 80>{});
-    return f(WideConfig<DP, 128>{});
+    if (rows > 96 && rows <= 128) return f(WideConfig<DP, 128>{});
+    const int64_t chunks = (rows + 95) / 96, each = (rows + chunks - 1) / chunks;
+    if (each <= 48) return f(WideConfig<DP, 48>{});
+    if (each <= 64) return f(WideConfig<DP, 64>{});
+    if (each <= 80) return f(WideConfig<DP, 80>{});
+    return f(WideConfig<DP, 96>{});
 }
 template <class F>
 auto pick_wide(int64_t D, int64_t rows, F f) {

@@ -114,6 +114,14 @@ def test_many_query_rows(cuda_lib, Hq, Hkv, D, page, Lq, window):
     _check(c, _q(len(lens), Lq, Hq, D, Hq), window)
 
 
+@pytest.mark.parametrize("D,window", [(128, 0), (64, 30), (112, 200)])
+@pytest.mark.parametrize("rows", [48, 49, 80, 81, 96, 97, 112, 129, 192, 193, 385])
+def test_row_counts_at_the_edges_of_the_configurations(cuda_lib, rows, D, window):
+    lens = [rows + 1, 130, 256, 257, 1000]
+    c = Cache(lens, 1, D, 16, False, False, rows + D)
+    _check(c, _q(len(lens), rows, 1, D, rows), window)
+
+
 @pytest.mark.parametrize("B,L,Lq,Hq,Hkv,D,window", [(1, 9000, 5, 14, 2, 128, 0), (2, 4001, 9, 40, 8, 128, 0),
                                                     (3, 3000, 16, 8, 1, 64, 1111), (1, 2500, 300, 2, 1, 96, 0)])
 def test_many_query_rows_of_long_sequences(cuda_lib, B, L, Lq, Hq, Hkv, D, window):
