@@ -401,7 +401,8 @@ int fp8rl_quant_kv_tensor_noalloc(const uint16_t* KV, int64_t R, int64_t C, int6
  *      one and recorded (fp8rl_check_device_error: FP8RL_ERR_DEVICE).
  * table fp32 [max_pos][R]: R/2 cosines, then R/2 sines (fp8rl_rope_table).
  * R even, 0 <= R <= D.  Fastest where D % 8 == 0, R % 16 == 0 (interleaved:
- * R % 8 == 0), pointers are 16-byte aligned and strides multiples of 8.
+ * R % 8 == 0), pointers are 16-byte aligned and strides multiples of 8; nearly so
+ * with half of each of these.
  * Limits: T < 2^31, H * D <= 2^24.  T == 0 launches nothing.
  * ---------------------------------------------------------------------- */
 #define FP8RL_ROPE_INTERLEAVED 1u
@@ -497,8 +498,8 @@ int fp8rl_rope_append_paged(const uint16_t* q, int64_t Hq, int64_t q_token, int6
  * ---------------------------------------------------------------------- */
 size_t fp8rl_attn_paged_workspace_bytes(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
                                         int64_t max_len);
-/* Kernels fp8rl_attn_paged launches for these sizes and cache dtype: 1 where
- * max_len is short for the batch, else 2.  0 for B == 0; a negated status for invalid
+/* Kernels fp8rl_attn_paged launches at most for these sizes and cache dtype: 1
+ * where max_len is short for the batch, else 2.  0 for B == 0; a negated status for invalid
  * sizes. */
 int fp8rl_attn_paged_kernel_count(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D,
                                   int64_t max_len, int dtype);

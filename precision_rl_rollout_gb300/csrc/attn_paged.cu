@@ -1,5 +1,5 @@
-// attn_paged.cu -- the paged attention call: its sizes, and which loader a cache
-// takes (attn_paged.cuh has the kernels).
+// attn_paged.cu -- the paged attention call: its sizes, and which loader and kernel a
+// cache takes (attn_paged.cuh and attn_paged_wide.cuh have the kernels).
 #include "attn_paged_wide.cuh"
 
 namespace fp8rl {
@@ -11,7 +11,7 @@ attn::Plan plan_of(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv, int64_t D, in
     auto f = [&](auto c) { return attn::plan<decltype(c)>(B, Hkv, rows, max_len); };
     if (e4m3) return attn::pick<true, true>(D, rows, f);
     // what either of the kernels for a bf16 cache takes: the pages tell which
-    const attn::Plan a = attn::pick<false, true>(D, rows, f);
+    const attn::Plan a = attn::pick<false, false>(D, rows, f);
     if (!attn::is_wide(D, rows)) return a;
     const attn::Plan b = attn::pick_wide(D, rows, [&](auto c) { return attn::plan_wide<decltype(c)>(max_len); });
     return attn::Plan{a.ws > b.ws ? a.ws : b.ws, a.kernels > b.kernels ? a.kernels : b.kernels};
@@ -41,6 +41,7 @@ cudaError_t launch_attn_paged(const AttnParams& a, bool e4m3, cudaStream_t st) {
     p.err = device_error_word();
     if (!p.err) return cudaErrorUnknown;
     const bool engine = copy_engine(p, e4m3);
+    // many rows over bf16 by tcgen05, whose operands are as the copy engine lays them
     if (engine && !e4m3 && attn::is_wide(p.D, (int64_t)p.Hq / p.Hkv * p.Lq)) return launch_attn_wide(p, st);
     if (engine) return e4m3 ? launch_attn_e4m3_tma(p, st) : launch_attn_bf16_tma(p, st);
     return e4m3 ? launch_attn_e4m3(p, st) : launch_attn_bf16(p, st);

@@ -1155,7 +1155,8 @@ auto pick_rows(int64_t rows, F f) {
     if (rows <= 16) return f(Config<kE4m3, kTma, DP, 16>{});
     // 64 rows at once only where their sums and scores leave room for the operands:
     // 40 rows over E4M3 took 299 us so and 267 us in two chunks, over bf16 325 and 358
-    if constexpr (!kE4m3 && DP <= 128)
+    // (there only without the copy engine: attn_paged_wide.cuh has the rest)
+    if constexpr (!kE4m3 && !kTma && DP <= 128)
         if (rows > 32) return f(Config<kE4m3, kTma, DP, 64>{});
     return f(Config<kE4m3, kTma, DP, 32>{});
 }

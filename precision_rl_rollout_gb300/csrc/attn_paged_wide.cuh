@@ -3,11 +3,13 @@
 // a prompt behind a cached prefix).  Mathematics, work split and workspace are those
 // of attn_paged.cuh.
 //
-// What bounds it.  128 rows flop 128 a cached byte: at HBM's speed 0.87 PFLOP/s with the
-// products that padding adds, above what mma.sync reaches here (with 64 rows at once,
-// their sums spilled, it made 0.14).  tcgen05 has the rate, so the work becomes a
-// stream again, with the exponentials next: 128 tokens x 128 rows in 1024 cycles of a
-// tile's 3000 at HBM's speed.
+// What bounds it.  Each cached byte meets 2 rows flop; 40 rows at HBM's speed are 0.3
+// PFLOP/s, more than mma.sync makes here beside its matrix loads (64 rows at once, their
+// sums spilled: 0.14).  tcgen05 has the rate, so the work is a stream again, and beyond
+// that the threads' part: a tile of 128 tokens takes them 1.4 us with 40 rows, 2.0 with
+// 80, where HBM takes 1.5.  32 sequences to 16384, 8 kv heads of 128, 1.1 GB: 40 rows in
+// 187 us (5.9 TB/s; by mma.sync 314), 80 in 228 (610), 120 in 364 (649).  Prompt chunks
+// of 512 behind up to 3488 tokens, 8 sequences, 28/4 heads: 421 us, 0.29 PFLOP/s (1170).
 //
 // Products.  Tokens, then head values are the M side, the rows the N side:
 //   S^T [128 tokens x rows] = K Q^T      K and Q with the head inside (K-major),
@@ -43,7 +45,9 @@ struct WideConfig {
     // a tile of keys or of values a slot, let go of by its own product
     static constexpr int kFit = (232448 - kP - kQ - kSmall) / kTile, kSlots = kFit < 8 ? kFit : 8;
     static constexpr int kSmem = kSlots * kTile + kP + kQ + kSmall;
-    static constexpr int kItem = 65536 / kTile;              // an item's start and end, in tiles
+    // An item's start and end, in tiles: 100 sequences to 1500, 40 rows, heads of 128:
+    // 104 us with two, 93 with four, 95 with six; prompt chunks of 512: 527, 466, 421.
+    static constexpr int kItem = 6;
     static constexpr int kUnits = RT / 16;                   // eights of rows a thread, kept or taken four at a time
     static constexpr int kGroup = kUnits <= 6 ? kUnits : 4;
     static constexpr uint32_t kSlice = RT <= 64 ? 64 : 128, kCols = 4 * kSlice;   // two tiles' scores, the sums, what is set apart
