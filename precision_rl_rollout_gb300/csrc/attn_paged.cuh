@@ -90,7 +90,7 @@ struct Config {
     static constexpr int ES = kE4m3 ? 1 : 2, RB = DP * ES;   // bytes of a value, of a cached head
     static constexpr int PB = RB < 128 ? RB : 128;           // row bytes of a piece of a tile
     static constexpr int CPR = RB / 16;                      // 16-byte chunks of a cached head
-    static constexpr int MT = RT <= 16 && RB <= (kE4m3 ? 256 : 128) ? 2 : 1;   // 16-token tiles a warp
+    static constexpr int MT = RT <= 16 && RB <= 128 ? 2 : 1;   // 16-token tiles a warp
     static constexpr int TT = 16 * MT, CT = kWarps * TT;     // tokens of a warp, of a CTA's tile
     static constexpr int MW = DP / 64;                       // 16-value tiles of the head a warp sums
     static constexpr int kTile = CT * RB, kStage = 2 * kTile;
@@ -100,7 +100,10 @@ struct Config {
     static constexpr int kParts = !kE4m3 && RT <= 16 ? 2 : 1, kPart = RT * CT * 2, kP = kParts * kPart;
     static constexpr int kQ = NT * (DP / 32) * 512;          // query operands
     static constexpr int kSmall = RT * 4 * (kWarps + 3) + 12 * 8 + 16;
-    static constexpr int kCtas = DP > 128 ? 1 : kE4m3 && RT < 64 ? 3 : 2;   // CTAs an SM
+    // CTAs an SM.  Two for heads of 256 over E4M3, of 64 tokens a tile, rather than one
+    // of 128: 120 sequences to 57, 16/16 heads: 63 -> 30 us; 64 of 8191, 28/4: 171 -> 169
+    // (three: 25 and 176).
+    static constexpr int kCtas = DP > 128 ? (kE4m3 ? 2 : 1) : kE4m3 && RT < 64 ? 3 : 2;
     static constexpr int kBudget = 233472 / kCtas - 1024;    // 228 KB an SM, 1 KB of it kept for each CTA
     static constexpr int kRest = kP + kQ + kSmall;
     static constexpr int kFit = (kBudget - kRest) / kStage;
