@@ -24,7 +24,8 @@
 // and back, for a product that mostly waits for HBM.  mma.sync.m16n8k32 on E4M3 with
 // the queries as two E4M3 parts was tried for the scores: exact enough, but it
 // costs 10-15 cycles with fresh operands, more than fp16 with one conversion
-// shared by all rows (verification 285 us against 149).
+// shared by all rows (verification 285 us against 149).  More than 32 rows over
+// bf16 are worth tcgen05, with tokens as that side: attn_paged_wide.cuh.
 //
 // The CTA.  Four warps compute, a fifth loads: it keeps a ring of tiles (K and V of
 // CT tokens) full, by the copy engine where pages hold a multiple of 8 tokens, else

@@ -191,7 +191,8 @@ __device__ __forceinline__ void mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uin
         : "memory");
 }
 
-// D[tmem] (+)= A * B^T with fp16 operands (kind::f16, A = B = f16) -> fp32.
+// D[tmem] (+)= A * B^T with 16-bit operands (kind::f16; fp16 or bf16 by the instruction
+// descriptor, both the same) -> fp32.
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {
     asm volatile(
