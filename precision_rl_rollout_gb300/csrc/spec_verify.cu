@@ -108,12 +108,13 @@ spec_verify_kernel(const __grid_constant__ VerifyParams p) {
     const float* e = p.noise + b * p.e_seq;
     const int32_t V = (int32_t)p.V, step = (int32_t)(ranks * kVThreads), v_first = (int32_t)(rank * kVThreads + threadIdx.x);
     // This thread's part of the race, several entries a turn with their loads in
-    // flight together.  A score above the best has w > top * e up to three
-    // roundings of 2^-24: one product settles nearly every entry without dividing.
+    // flight together.  A quotient that rounds to more than top is more than top, so
+    // w > top * e, and all the more w > top * e rounded down (subnormal numbers too):
+    // one product settles nearly every entry without dividing.
     float top = 0.f;
     uint32_t at = 0;
     auto entry = [&](int32_t v, float w, float d) {
-        if (w > __fmul_rn(top, d) * (1.f - 0x1p-20f) && w > 0.f) {
+        if (w > __fmul_rd(top, d) && w > 0.f) {
             const float s = __fdiv_rn(w, d);
             if (s > top) top = s, at = (uint32_t)v;
         }

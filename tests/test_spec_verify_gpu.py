@@ -170,3 +170,26 @@ def test_the_race_draws_the_targets_distribution(cuda_lib):
     n = np.bincount(t[:, 0], minlength=V)
     want = p.numpy() * B
     assert np.all(np.abs(n - want) <= 5 * np.sqrt(want)), (n, want)
+
+
+def test_scores_among_subnormal_numbers(cuda_lib):
+    # products and quotients below 2^-126 have no relative rounding error: nothing that
+    # spares divisions may assume one.  Units of the smallest number, 2^-149: 7 / 1.2627378
+    # is 6, 2 / 0.3063047 is 7, and the second wins
+    tiny = 2.0 ** -149
+    V = 8
+    P, noise = torch.zeros((1, 1, V)), torch.ones((1, V))
+    P[0, 0, 0], P[0, 0, 1] = 7 * tiny, 2 * tiny
+    noise[0, 0], noise[0, 1] = 1.2627378, 0.3063047
+    z = torch.zeros((1, 0))
+    t, _ = fb.fp8rl_spec_verify(P.cuda(), z.int().cuda(), z.cuda(), noise.cuda())
+    assert t.tolist() == [[1]]
+    # rows of such numbers, 8 and 16 entries a thread and unaligned ones
+    for B, V in ((600, 61), (3, 4096), (200, 16001)):
+        g = torch.Generator().manual_seed(V)
+        P = (torch.randint(0, 9, (B, 1, V), generator=g).double() * tiny).float()
+        noise = torch.empty((B, V)).exponential_(generator=g) + 0.25
+        z = torch.zeros((B, 0))
+        t, _ = fb.fp8rl_spec_verify(P.cuda(), z.int().cuda(), z.cuda(), noise.cuda())
+        want, _ = ref.verify(P.numpy(), None, np.zeros((B, 0), np.int32), np.zeros(B, int), np.zeros((B, 0)), noise.numpy())
+        assert np.array_equal(t.cpu().numpy(), want)
