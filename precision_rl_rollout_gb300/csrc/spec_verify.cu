@@ -51,10 +51,12 @@ struct Quad<uint16_t> {
     __device__ __forceinline__ uint16_t at(int k) const { return (uint16_t)((k < 2 ? x.x : x.y) >> (k & 1 ? 16 : 0)); }
 };
 
-// The race so far: score bits (scores are >= 0, so they order as integers) and
-// the complement of the index, as one 64-bit key; larger wins.
+// The race so far: score bits and one (scores are >= 0, so they order as integers) and
+// the complement of the index, as one 64-bit key; larger wins.  Without an entry that
+// takes part (score -1) the upper half is 0 and the index 0: an entry of positive weight
+// takes part even where its score rounds to 0.
 __device__ __forceinline__ uint64_t race_key(float score, uint32_t idx) {
-    return ((uint64_t)__float_as_uint(score) << 32) | (uint32_t)~idx;
+    return ((uint64_t)(score < 0.f ? 0u : __float_as_uint(score) + 1u) << 32) | (uint32_t)~idx;
 }
 __device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
     const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
@@ -111,7 +113,7 @@ spec_verify_kernel(const __grid_constant__ VerifyParams p) {
     // flight together.  A quotient that rounds to more than top is more than top, so
     // w > top * e, and all the more w > top * e rounded down (subnormal numbers too):
     // one product settles nearly every entry without dividing.
-    float top = 0.f;
+    float top = -1.f;
     uint32_t at = 0;
     auto entry = [&](int32_t v, float w, float d) {
         if (w > __fmul_rd(top, d) && w > 0.f) {
@@ -170,7 +172,7 @@ spec_verify_kernel(const __grid_constant__ VerifyParams p) {
     };
     uint64_t best = 0;
     for (int round = 0;; ++round) {
-        top = 0.f, at = 0;
+        top = -1.f, at = 0;
         if (residual && qr)
             race(std::true_type{});
         else

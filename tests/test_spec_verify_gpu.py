@@ -193,3 +193,22 @@ def test_scores_among_subnormal_numbers(cuda_lib):
         t, _ = fb.fp8rl_spec_verify(P.cuda(), z.int().cuda(), z.cuda(), noise.cuda())
         want, _ = ref.verify(P.numpy(), None, np.zeros((B, 0), np.int32), np.zeros(B, int), np.zeros((B, 0)), noise.numpy())
         assert np.array_equal(t.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("V,at", [(64, 9), (50001, 40000), (152064, 151999)])
+def test_a_residual_whose_scores_underflow_is_not_empty(cuda_lib, V, at):
+    # the residual's only positive entry is two units of 2^-149, its score a quarter of
+    # one, which rounds to 0: it takes part and wins all the same, and the entries without
+    # weight, whose scores are 0 too, do not
+    tiny = 2.0 ** -149
+    for drafter in (True, False):
+        P, Q = torch.zeros((2, 2, V)), torch.zeros((2, 1, V))
+        P[:, 0, 7] = 0.0 if not drafter else 0.5
+        Q[:, 0, 7] = 0.5
+        P[:, 0, at], Q[:, 0, at] = 5 * tiny, 3 * tiny
+        Q[:, 0, 3] = 0.5
+        drafts = torch.full((2, 1), 3, dtype=torch.int32)           # p is 0 there: refused
+        noise = torch.ones((2, V))
+        noise[:, at] = 32.0 if not drafter else 8.0
+        t, a = _run(P, Q if drafter else None, drafts, None, torch.full((2, 1), 0.5), noise)
+        assert a.tolist() == [0, 0] and t.tolist() == [[at, -1]] * 2
