@@ -212,3 +212,15 @@ def test_a_residual_whose_scores_underflow_is_not_empty(cuda_lib, V, at):
         noise[:, at] = 32.0 if not drafter else 8.0
         t, a = _run(P, Q if drafter else None, drafts, None, torch.full((2, 1), 0.5), noise)
         assert a.tolist() == [0, 0] and t.tolist() == [[at, -1]] * 2
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,K,V", [(40, 3, 50257), (200, 2, 32001), (40, 3, 50260)])
+def test_many_entries_a_thread(cuda_lib, B, K, V, dtype):
+    # rows off the boundary of four entries that a thread goes over several times, and
+    # the same for rows on it
+    c = _case(B, K, V, B + V, dtype=dtype)
+    t, a = _run(*c)
+    wt, wa = _want(*c)
+    assert np.array_equal(a, wa) and np.array_equal(t, wt)
+    assert fb.fp8rl_check_device_error() == 0
