@@ -264,3 +264,63 @@ def test_append_on_a_side_stream_and_empty_batch(cuda_lib):
     assert fb.fp8rl_rope_append_paged(e, e, e, None, None, K, V, slots[:0]).shape == (0, 2, 64)
     assert fb.fp8rl_rope(e, slots[:0].int(), torch.zeros((1, 64), device="cuda")).shape == (0, 2, 64)
     _no_error()
+
+
+# ---------------------------------------------------------------- prompt-sized calls
+# Large enough that a thread goes over several batches of heads and a CTA over several
+# tokens, the last of them with tokens that are not there (T is prime).
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,H,D,R", [(1747, 48, 128, 128), (2999, 32, 128, 64), (3001, 36, 80, 56), (1201, 21, 256, 256),
+                                     (2003, 41, 96, 0)])
+def test_rope_of_many_tokens(cuda_lib, T, H, D, R, inter, in_place):
+    table = _table(4099, R, magnitude=1.1)[0] if R else np.zeros((4099, 0), np.float32)
+    x = _x((T, H + 2, D), T + R)
+    pos = np.random.default_rng(T).integers(0, 4099, T).astype(np.int32)
+    d = x.cuda()
+    heads = d[:, 1:1 + H]
+    for inverse in (False, True):
+        if inverse and in_place:
+            heads.copy_(x[:, 1:1 + H])
+        y = fb.fp8rl_rope(heads, torch.from_numpy(pos).cuda(), torch.from_numpy(table).cuda(), interleaved=inter,
+                          inverse=inverse, Y=heads if in_place else None)
+        want = ref.bf16(ref.rope(x[:, 1:1 + H].float().numpy(), pos, table, R, inter, inverse, np.float32))
+        assert np.array_equal(y.cpu().float().numpy(), want)
+    assert torch.equal(d[:, 0].cpu(), x[:, 0]) and torch.equal(d[:, -1].cpu(), x[:, -1])
+    _no_error()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,Hq,Hkv,D,R,in_place", [(2003, 28, 4, 128, 128, False), (1733, 40, 8, 96, 48, True),
+                                                   (3001, 28, 4, 80, 56, True), (1511, 8, 8, 256, 256, False),
+                                                   (2999, 40, 8, 64, 0, False)])
+def test_append_of_many_tokens(cuda_lib, T, Hq, Hkv, D, R, in_place, e4m3, inter):
+    rng = np.random.default_rng(T)
+    table = _table(4099, R)[0] if R else None
+    page, pages = 16, -(-T // 16) + 3
+    x = _x((T, Hq + 2 * Hkv, D), T)
+    pos = rng.integers(0, 4099, T).astype(np.int32)
+    slots = rng.permutation(pages * page)[:T].astype(np.int64)
+    slots[rng.permutation(T)[:T // 7]] = -1                   # padding
+    ks, vs = np.float32(0.011), np.float32(0.007)
+    K, V = _pools(pages, page, Hkv, D, e4m3, inter, 3), _pools(pages, page, Hkv, D, e4m3, inter, 5)
+    args = dict(k_scale=torch.tensor([ks], device="cuda"), v_scale=torch.tensor([vs], device="cuda")) if e4m3 else {}
+    d = x.cuda()
+    q = fb.fp8rl_rope_append_paged(d[:, :Hq], d[:, Hq:Hq + Hkv], d[:, Hq + Hkv:], torch.from_numpy(pos).cuda(),
+                                   None if table is None else torch.from_numpy(table).cuda(), K, V,
+                                   torch.from_numpy(slots).cuda(), interleaved=inter,
+                                   q_out=d[:, :Hq] if in_place else None, **args)
+    f = x.float().numpy()
+    rot = f if R == 0 else ref.rope(f, pos, table, R, inter, False, np.float32)
+    assert np.array_equal(q.cpu().float().numpy(), ref.bf16(rot[:, :Hq]))
+    assert torch.equal(d[:, Hq:].cpu(), x[:, Hq:])
+    keep = slots >= 0
+    for pool, y, s, fill in ((K, rot[:, Hq:Hq + Hkv], ks, 3), (V, f[:, Hq + Hkv:], vs, 5)):
+        got = pool.cpu()
+        got = got.numpy() if e4m3 else got.float().numpy()
+        want = np.full(got.shape, fill, got.dtype)
+        want[slots[keep] // page, slots[keep] % page] = ref.e4m3_codes(y[keep], s) if e4m3 else ref.bf16(y[keep])
+        assert np.array_equal(got, want)
+    _no_error()
