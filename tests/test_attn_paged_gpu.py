@@ -319,3 +319,44 @@ def test_empty_batch_and_zero_bound(cuda_lib):
     assert not o.any() and torch.isneginf(lse).all()
     o = fb.fp8rl_attn_paged(q[:0], *c.pools, c.table[:0].cuda(), torch.zeros(0, dtype=torch.int32).cuda(), 16)
     assert o.shape == (0, 2, 2, 64)
+
+
+@pytest.mark.parametrize("n", [1, 7])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("Hq,D,page,Lq", [(8, 128, 16, 1), (8, 128, 7, 1), (5, 64, 16, 3), (16, 64, 16, 1), (7, 256, 16, 1),
+                                          (4, 256, 16, 4), (8, 96, 32, 2), (25, 128, 16, 1), (40, 128, 16, 1), (9, 256, 16, 5)])
+def test_probabilities_are_as_exact_as_promised(cuda_lib, Hq, D, page, Lq, e4m3, n):
+    """Tokens of value 1 and weight 1 against tokens of value -1 and a weight that bf16
+    and fp16 hold badly, so many of each that they nearly cancel: what the rounding of the
+    weights leaves stands in the result.  Promised: 2^-16 of a weight over bf16 for up to
+    16 query rows a kv head, 2^-8 above; 2^-11 over E4M3."""
+    # 0.70117 + 0.45 of bf16's spacing there (2^-8), and off fp16's grid by 0.4 of its spacing
+    w = 0.69921875 + 0.45 * 2.0 ** -8
+    w = np.floor(w * 2048) / 2048 + 0.4 / 2048
+    na, nb = 70 * n, 100 * n
+    length = na + nb + Lq - 1                                  # the newest Lq - 1 tokens weigh nothing to the last bit
+    pages = -(-length // page)
+    k, v = torch.zeros((pages * page, 1, D)), torch.zeros((pages * page, 1, D))
+    k[na:na + nb, 0, 0] = 1.0
+    k[na + nb:, 0, 0] = 448.0
+    v[:na], v[na:na + nb] = 1.0, -1.0
+    one = torch.ones(1, device="cuda")
+    pools = [x.to(torch.float8_e4m3fn).view(torch.uint8) if e4m3 else x.to(torch.bfloat16) for x in (k, v)]
+    pools = [x.view(pages, page, 1, D).cuda() for x in pools]
+    q = torch.zeros((1, Lq, Hq, D), dtype=torch.bfloat16)
+    q[..., 0] = -1.0
+    scale = float(np.float32(-np.log(w)))
+    o = fb.fp8rl_attn_paged(q.cuda(), *pools, torch.arange(pages, dtype=torch.int32).view(1, -1).cuda(),
+                            torch.tensor([length], dtype=torch.int32).cuda(), length, scale=scale,
+                            **(dict(k_scale=one, v_scale=one) if e4m3 else {}))
+    w = np.exp(-scale)
+    total = na + nb * w
+    want = (na - nb * w) / total
+    rows = Hq * Lq
+    each = 2.0 ** -11 if e4m3 else 2.0 ** -16 if rows <= 16 else 2.0 ** -8
+    # the weights' rounding; a score of at most 0.36 in D fp32 sums and three roundings,
+    # and the exponential's 2^-22; fp32 sums; the result's bf16 rounding
+    tol = each + 2 * (2.0 ** -23 * (D + 8) * 0.36 + 2.0 ** -21) + (na + nb) * 2.0 ** -23 + 2.0 ** -8 * 1.01 * abs(want)
+    err = np.abs(o.cpu().double().numpy() - want).max()
+    assert err <= tol, (err, tol)
+    assert fb.fp8rl_check_device_error() == 0
