@@ -503,12 +503,11 @@ def fp8rl_logits_kl(P, Q, kl=None, workspace=None, stream=None):
 # A decode step makes these calls with a few microseconds of GPU work behind each, so
 # their checks and marshalling are compiled (csrc/calls.cpp -> _calls.so, built with
 # the library).  A wrong type, shape, stride or device is a ValueError; a status of the
-# C ABI an Fp8rlError.  What a call allocates while a stream is given is recorded on
-# that stream, so that the caching allocator does not hand it out again too early.
+# C ABI an Fp8rlError.  What a call allocates while a stream is given is of that
+# stream's memory; outputs are recorded on the caller's current stream as well.
 
-def _given(stream, device):
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
-    return s, s.cuda_stream
+def _raw(stream):
+    return stream if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 FP8RL_ROPE_INTERLEAVED = 1
@@ -527,7 +526,8 @@ def fp8rl_rope_table(freq, max_pos: int, magnitude: float = 1.0, table=None, str
         raise ValueError("table must be on freq's device")
     _ck(lib.fp8rl_rope_table(_p(freq), max_pos, R, magnitude, _p(table), _stream(freq, stream)), "fp8rl_rope_table")
     if made and stream is not None:
-        table.record_stream(_given(stream, freq.device)[0])
+        table.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                            torch.cuda.ExternalStream(int(stream), device=freq.device))
     return table
 
 
@@ -536,13 +536,7 @@ def fp8rl_rope(X, positions, table, interleaved=False, inverse=False, Y=None, st
     [max_pos, R] -> Y bf16 [T, H, D]; inverse=True: the gradient.  Y may be X."""
     if _lib is None:
         load()
-    if stream is None:
-        return _calls.rope(X, positions, table, interleaved, inverse, Y, None)
-    s, raw = _given(stream, X.device)
-    out = _calls.rope(X, positions, table, interleaved, inverse, Y, raw)
-    if Y is None:
-        out.record_stream(s)
-    return out
+    return _calls.rope(X, positions, table, interleaved, inverse, Y, _raw(stream))
 
 
 FP8RL_KV_BF16 = 0
@@ -557,14 +551,8 @@ def fp8rl_rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale=None
     head is the transposed view).  table None: no rotation."""
     if _lib is None:
         load()
-    if stream is None:
-        return _calls.rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale, v_scale, interleaved, q_out,
-                                        None)
-    s, raw = _given(stream, q.device)
-    out = _calls.rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale, v_scale, interleaved, q_out, raw)
-    if q_out is None:
-        out.record_stream(s)
-    return out
+    return _calls.rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale, v_scale, interleaved, q_out,
+                                    _raw(stream))
 
 
 def fp8rl_attn_paged_workspace_bytes(B: int, Lq: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
@@ -585,22 +573,8 @@ def fp8rl_attn_paged(q, K, V, block_table, seq_lens, max_len: int, scale=None, w
     lse is given)."""
     if _lib is None:
         load()
-    if stream is None:
-        return _calls.attn_paged(q, K, V, block_table, seq_lens, max_len, scale, window, k_scale, v_scale, o, lse,
-                                 want_lse, workspace, None)
-    s, raw = _given(stream, q.device)
-    made = [o is None, lse is None]
-    if workspace is None:
-        B, Lq, Hq, D = q.shape
-        workspace = torch.empty(fp8rl_attn_paged_workspace_bytes(B, Lq, Hq, K.shape[2], D, max_len),
-                                dtype=torch.uint8, device=q.device)
-        workspace.record_stream(s)
-    out = _calls.attn_paged(q, K, V, block_table, seq_lens, max_len, scale, window, k_scale, v_scale, o, lse, want_lse,
-                            workspace, raw)
-    for t, m in zip(out if isinstance(out, tuple) else (out,), made):
-        if m:
-            t.record_stream(s)
-    return out
+    return _calls.attn_paged(q, K, V, block_table, seq_lens, max_len, scale, window, k_scale, v_scale, o, lse, want_lse,
+                             workspace, _raw(stream))
 
 
 FP8RL_PROB_F32 = 0
@@ -614,11 +588,4 @@ def fp8rl_spec_verify(P, drafts, u, noise, Q=None, draft_lens=None, tokens=None,
     token, then -1; accepted int32 [B])."""
     if _lib is None:
         load()
-    if stream is None:
-        return _calls.spec_verify(P, drafts, u, noise, Q, draft_lens, tokens, accepted, None)
-    s, raw = _given(stream, P.device)
-    out = _calls.spec_verify(P, drafts, u, noise, Q, draft_lens, tokens, accepted, raw)
-    for t, given in zip(out, (tokens, accepted)):
-        if given is None:
-            t.record_stream(s)
-    return out
+    return _calls.spec_verify(P, drafts, u, noise, Q, draft_lens, tokens, accepted, _raw(stream))

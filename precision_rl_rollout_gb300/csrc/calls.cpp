@@ -106,11 +106,34 @@ fp8rl_paged_kv paged_kv(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso
     return kv;
 }
 
-// None: torch's current stream on the call's device; else the raw stream.
-void* stream_of(PyObject* o, c10::Device dev) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-    return PyLong_AsVoidPtr(o);
-}
+// The call's device and stream (None: torch's current one there; else the raw stream),
+// made current while it lasts, so that what the call allocates is of its own stream's
+// memory: a block of another stream's can have work of that stream still queued on it.
+// Outputs on a given stream are recorded on the caller's, which will read them.
+class Launch {
+public:
+    Launch(PyObject* o, c10::Device dev)
+        : caller_(c10::cuda::getCurrentCUDAStream(dev.index())), stream_(pick(o, dev, caller_)), guard_(stream_) {}
+    void* stream() const { return stream_.stream(); }
+    Tensor empty(at::IntArrayRef shape, const at::TensorOptions& options) const {
+        Tensor t = at::empty(shape, options);
+        if (stream_.stream() != caller_.stream()) t.record_stream(caller_.unwrap());
+        return t;
+    }
+
+private:
+    static c10::cuda::CUDAStream pick(PyObject* o, c10::Device dev, c10::cuda::CUDAStream caller) {
+        if (o == Py_None) return caller;
+        void* const raw = PyLong_AsVoidPtr(o);
+        if (!raw && PyErr_Occurred()) {
+            PyErr_Clear();
+            throw std::invalid_argument("stream: expected a raw stream");
+        }
+        return c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), dev.index());
+    }
+    c10::cuda::CUDAStream caller_, stream_;
+    c10::cuda::CUDAStreamGuard guard_;
+};
 
 // Table [max_pos, R] and positions [T].
 void check_table(const Tensor& positions, const Tensor& table, int64_t T, c10::Device dev) {
@@ -120,15 +143,16 @@ void check_table(const Tensor& positions, const Tensor& table, int64_t T, c10::D
 }
 
 // Y given, or new: [like X].
-Tensor output_like(PyObject* o, const Tensor& X, const char* name) {
-    if (o == Py_None) return at::empty(X.sizes(), X.options());
+Tensor output_like(const Launch& launch, PyObject* o, const Tensor& X, const char* name) {
+    if (o == Py_None) return launch.empty(X.sizes(), X.options());
     const Tensor& Y = tensor(o, name);
     heads(Y, X.dim(), X.device(), name);
     if (Y.sizes() != X.sizes()) refuse(name, Y, "the input's shape");
     return Y;
 }
-Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Tensor& like, const char* name) {
-    if (o == Py_None) return at::empty(shape, like.options().dtype(type));
+Tensor output(const Launch& launch, PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Tensor& like,
+              const char* name) {
+    if (o == Py_None) return launch.empty(shape, like.options().dtype(type));
     const Tensor& t = tensor(o, name);
     dense(t, type, shape, like.device(), name);
     return t;
@@ -144,12 +168,12 @@ PyObject* rope(PyObject* const* a) {
     const Tensor &positions = tensor(a[1], "positions"), &table = tensor(a[2], "table");
     const int64_t T = X.size(0), H = X.size(1), D = X.size(2);
     check_table(positions, table, T, dev);
-    const Tensor Y = output_like(a[5], X, "Y");
+    const Launch launch(a[6], dev);
+    const Tensor Y = output_like(launch, a[5], X, "Y");
     const unsigned flags = (truth(a[3]) ? FP8RL_ROPE_INTERLEAVED : 0) | (truth(a[4]) ? FP8RL_ROPE_INVERSE : 0);
-    c10::cuda::CUDAGuard guard(dev);
     const int rc = fn.rope(ptr<uint16_t>(X), T, H, D, X.stride(0), X.stride(1), ptr<int32_t>(positions),
                            ptr<float>(table), table.size(0), table.size(1), flags, ptr<uint16_t>(Y), Y.stride(0),
-                           Y.stride(1), stream_of(a[6], dev));
+                           Y.stride(1), launch.stream());
     if (rc) throw Status{rc, "fp8rl_rope"};
     return THPVariable_Wrap(Y);
 }
@@ -176,13 +200,13 @@ PyObject* rope_append_paged(PyObject* const* a) {
         check_table(p, table, T, dev);
         positions = ptr<int32_t>(p), rows = ptr<float>(table), max_pos = table.size(0), R = table.size(1);
     }
-    const Tensor out = output_like(a[11], q, "q_out");
-    c10::cuda::CUDAGuard guard(dev);
+    const Launch launch(a[12], dev);
+    const Tensor out = output_like(launch, a[11], q, "q_out");
     const int rc = fn.rope_append_paged(ptr<uint16_t>(q), Hq, q.stride(0), q.stride(1), ptr<uint16_t>(k), k.stride(0),
                                         k.stride(1), ptr<uint16_t>(v), v.stride(0), v.stride(1), T, positions, rows,
                                         max_pos, R, truth(a[10]) ? FP8RL_ROPE_INTERLEAVED : 0, ptr<uint16_t>(out),
                                         out.stride(0), out.stride(1), &kv, ptr<int64_t>(slots),
-                                        stream_of(a[12], dev));
+                                        launch.stream());
     if (rc) throw Status{rc, "fp8rl_rope_append_paged"};
     return THPVariable_Wrap(out);
 }
@@ -211,9 +235,10 @@ PyObject* attn_paged(PyObject* const* a) {
             throw std::invalid_argument("scale: expected a number");
         }
     }
-    const Tensor o = output(a[10], q.sizes(), at::kBFloat16, q, "o");
+    const Launch launch(a[14], dev);
+    const Tensor o = output(launch, a[10], q.sizes(), at::kBFloat16, q, "o");
     Tensor lse, workspace;
-    if (a[11] != Py_None || truth(a[12])) lse = output(a[11], q.sizes().slice(0, 3), at::kFloat, q, "lse");
+    if (a[11] != Py_None || truth(a[12])) lse = output(launch, a[11], q.sizes().slice(0, 3), at::kFloat, q, "lse");
     if (a[13] != Py_None) {
         workspace = tensor(a[13], "workspace");
         if (workspace.device() != dev || !workspace.is_contiguous())
@@ -221,13 +246,12 @@ PyObject* attn_paged(PyObject* const* a) {
     } else if (const size_t need = fn.attn_workspace(B, Lq, Hq, kv.kv_heads, D, max_len)) {
         workspace = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
     }
-    c10::cuda::CUDAGuard guard(dev);
     const int rc = fn.attn_paged(ptr<uint16_t>(q), B, Lq, Hq, q.stride(0), q.stride(1), q.stride(2), &kv,
                                  ptr<int32_t>(table), B == 1 ? table.size(1) : table.stride(0), ptr<int32_t>(lens),
                                  max_len, window, (float)scale, ptr<uint16_t>(o),
                                  lse.defined() ? ptr<float>(lse) : nullptr,
                                  workspace.defined() ? workspace.data_ptr() : nullptr,
-                                 workspace.defined() ? workspace.nbytes() : 0, stream_of(a[14], dev));
+                                 workspace.defined() ? workspace.nbytes() : 0, launch.stream());
     if (rc) throw Status{rc, "fp8rl_attn_paged"};
     if (!lse.defined()) return THPVariable_Wrap(o);
     return Py_BuildValue("(NN)", THPVariable_Wrap(o), THPVariable_Wrap(lse));
@@ -263,13 +287,13 @@ PyObject* spec_verify(PyObject* const* a) {
         dense(t, at::kInt, {B}, dev, "draft_lens");
         lens = ptr<int32_t>(t);
     }
-    const Tensor tokens = output(a[6], {B, K + 1}, at::kInt, P, "tokens");
-    const Tensor accepted = output(a[7], {B}, at::kInt, P, "accepted");
-    c10::cuda::CUDAGuard guard(dev);
+    const Launch launch(a[8], dev);
+    const Tensor tokens = output(launch, a[6], {B, K + 1}, at::kInt, P, "tokens");
+    const Tensor accepted = output(launch, a[7], {B}, at::kInt, P, "accepted");
     const int rc = fn.spec_verify(P.data_ptr(), P.stride(0), P.stride(1), qp, q_seq, q_step,
                                   type == at::kFloat ? FP8RL_PROB_F32 : FP8RL_PROB_BF16, ptr<int32_t>(drafts), lens,
                                   ptr<float>(u), ptr<float>(noise), noise.stride(0), B, K, V, ptr<int32_t>(tokens),
-                                  ptr<int32_t>(accepted), stream_of(a[8], dev));
+                                  ptr<int32_t>(accepted), launch.stream());
     if (rc) throw Status{rc, "fp8rl_spec_verify"};
     return Py_BuildValue("(NN)", THPVariable_Wrap(tokens), THPVariable_Wrap(accepted));
 }
