@@ -7,7 +7,8 @@ Tensors: bf16 inputs are ``torch.bfloat16``; E4M3 codes are ``torch.uint8``
 (view them as ``torch.float8_e4m3fn`` if wanted); INT8 codes ``torch.int8``;
 scales ``torch.float32``.  Outputs that are not passed in are allocated with
 ``torch.empty`` on the input's device.  Work is enqueued on the current torch
-stream of that device unless ``stream`` is given.
+stream of that device unless ``stream`` is given; what a call allocates is then of
+that stream's memory.
 """
 from __future__ import annotations
 
@@ -178,9 +179,31 @@ def _rowmajor(t: torch.Tensor, name: str):
     return t.stride(0)
 
 
-def _need(t, shape, dtype, device, name):
-    if t is None:
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on ``stream`` (None: the current one): of that stream's
+    memory, since a block of the current stream's can have work queued there that still
+    reads it, and recorded on the current stream, which will read the result."""
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if s.cuda_stream != here.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
+def _workspace(t, need, device, stream):
+    """-> (workspace or None, its bytes)"""
+    if t is None and need:
+        t = _empty(need, torch.uint8, device, stream)
+    return t, 0 if t is None else t.numel() * t.element_size()
+
+
+def _need(t, shape, dtype, device, name, stream=None):
+    if t is None:
+        return _empty(shape, dtype, device, stream)
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     return t
@@ -201,8 +224,8 @@ def fp8rl_quant_weight_block(W, Wq=None, Ws=None, stream=None):
     lib = load()
     ldw = _rowmajor(W, "W")
     N, K = W.shape
-    Wq = _need(Wq, (N, K), torch.uint8, W.device, "Wq")
-    Ws = _need(Ws, (N // 128, K // 128), torch.float32, W.device, "Ws")
+    Wq = _need(Wq, (N, K), torch.uint8, W.device, "Wq", stream)
+    Ws = _need(Ws, (N // 128, K // 128), torch.float32, W.device, "Ws", stream)
     _ck(lib.fp8rl_quant_weight_block(_p(W), N, K, ldw, _p(Wq), _p(Ws), _stream(W, stream)),
         "fp8rl_quant_weight_block")
     return Wq, Ws
@@ -252,8 +275,8 @@ def fp8rl_quant_act_group(X, Xq=None, Xs=None, stream=None):
     lib = load()
     ldx = _rowmajor(X, "X")
     M, K = X.shape
-    Xq = _need(Xq, (M, K), torch.uint8, X.device, "Xq")
-    Xs = _need(Xs, (K // 128, M), torch.float32, X.device, "Xs")
+    Xq = _need(Xq, (M, K), torch.uint8, X.device, "Xq", stream)
+    Xs = _need(Xs, (K // 128, M), torch.float32, X.device, "Xs", stream)
     _ck(lib.fp8rl_quant_act_group(_p(X), M, K, ldx, _p(Xq), _p(Xs), _stream(X, stream)),
         "fp8rl_quant_act_group")
     return Xq, Xs
@@ -272,12 +295,10 @@ def fp8rl_gemm_w8a8_block(Xq, Xs, Wq, Ws, Y=None, workspace=None, stream=None, w
     lib = load()
     M, K = Xq.shape
     N = Wq.shape[0]
-    Y = Y if Y is not None else torch.empty((M, N), dtype=torch.bfloat16, device=Wq.device)
+    Y = Y if Y is not None else _empty((M, N), torch.bfloat16, Wq.device, stream)
     ldy = _rowmajor(Y, "Y") if M > 0 else N
     need = lib.fp8rl_gemm_workspace_bytes(M, N, K)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Wq.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wbytes = _workspace(workspace, need, Wq.device, stream)
     if weights_stable:
         _ck(lib.fp8rl_gemm_w8a8_block_ex(_p(Xq), _p(Xs), _p(Wq), _p(Ws), M, N, K, _p(Y), ldy,
                                          _p(workspace), wbytes, FP8RL_GEMM_WEIGHTS_STABLE, _stream(Wq, stream)),
@@ -300,7 +321,7 @@ def fp8rl_gemm_w8a8_block_grouped(Xq, Xs, Wq, Ws, expert_offsets, max_tokens_per
     E, N = Wq.shape[0], Wq.shape[1]
     if expert_offsets.dtype != torch.int32 or not expert_offsets.is_cuda or expert_offsets.numel() != E + 1:
         raise ValueError("expert_offsets must be a CUDA int32 tensor of E+1 entries")
-    Y = Y if Y is not None else torch.empty((T, N), dtype=torch.bfloat16, device=Wq.device)
+    Y = Y if Y is not None else _empty((T, N), torch.bfloat16, Wq.device, stream)
     ldy = _rowmajor(Y, "Y") if T > 0 else N
     bound = T if max_tokens_per_expert is None else int(max_tokens_per_expert)
     _ck(lib.fp8rl_gemm_w8a8_block_grouped(_p(Xq), _p(Xs), _p(Wq), _p(Ws), _p(expert_offsets), E, T, N, K,
@@ -320,15 +341,13 @@ def fp8rl_linear_w8a8_block(X, Wq, Ws, Y=None, Xq=None, Xs=None, want_codes=Fals
     ldx = _rowmajor(X, "X")
     M, K = X.shape
     N = Wq.shape[0]
-    Y = Y if Y is not None else torch.empty((M, N), dtype=torch.bfloat16, device=Wq.device)
+    Y = Y if Y is not None else _empty((M, N), torch.bfloat16, Wq.device, stream)
     ldy = _rowmajor(Y, "Y") if M > 0 else N
     if want_codes or Xq is not None or Xs is not None:
-        Xq = _need(Xq, (M, K), torch.uint8, X.device, "Xq")
-        Xs = _need(Xs, (K // 128, M), torch.float32, X.device, "Xs")
+        Xq = _need(Xq, (M, K), torch.uint8, X.device, "Xq", stream)
+        Xs = _need(Xs, (K // 128, M), torch.float32, X.device, "Xs", stream)
     need = lib.fp8rl_linear_workspace_bytes(M, N, K)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Wq.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wbytes = _workspace(workspace, need, Wq.device, stream)
     _ck(lib.fp8rl_linear_w8a8_block(_p(X), ldx, _p(Wq), _p(Ws), M, N, K, _p(Y), ldy, _p(Xq), _p(Xs),
                                     _p(workspace), wbytes, _stream(Wq, stream)),
         "fp8rl_linear_w8a8_block")
@@ -340,8 +359,8 @@ def int8rl_quant_weight_channel(W, Wq=None, Ws=None, stream=None):
     lib = load()
     ldw = _rowmajor(W, "W")
     N, K = W.shape
-    Wq = _need(Wq, (N, K), torch.int8, W.device, "Wq")
-    Ws = _need(Ws, (N,), torch.float32, W.device, "Ws")
+    Wq = _need(Wq, (N, K), torch.int8, W.device, "Wq", stream)
+    Ws = _need(Ws, (N,), torch.float32, W.device, "Ws", stream)
     _ck(lib.int8rl_quant_weight_channel(_p(W), N, K, ldw, _p(Wq), _p(Ws), _stream(W, stream)),
         "int8rl_quant_weight_channel")
     return Wq, Ws
@@ -352,8 +371,8 @@ def int8rl_quant_act_token(X, Xq=None, Xs=None, stream=None):
     lib = load()
     ldx = _rowmajor(X, "X")
     M, K = X.shape
-    Xq = _need(Xq, (M, K), torch.int8, X.device, "Xq")
-    Xs = _need(Xs, (M,), torch.float32, X.device, "Xs")
+    Xq = _need(Xq, (M, K), torch.int8, X.device, "Xq", stream)
+    Xs = _need(Xs, (M,), torch.float32, X.device, "Xs", stream)
     _ck(lib.int8rl_quant_act_token(_p(X), M, K, ldx, _p(Xq), _p(Xs), _stream(X, stream)),
         "int8rl_quant_act_token")
     return Xq, Xs
@@ -380,14 +399,12 @@ def int8rl_gemm_w8a8(Xq, Xs, Wq, Ws, Y=None, acc=None, want_acc=False, workspace
     lib = load()
     M, K = Xq.shape
     N = Wq.shape[0]
-    Y = Y if Y is not None else torch.empty((M, N), dtype=torch.bfloat16, device=Wq.device)
+    Y = Y if Y is not None else _empty((M, N), torch.bfloat16, Wq.device, stream)
     ldy = _rowmajor(Y, "Y") if M > 0 else N
     if want_acc and acc is None:
-        acc = torch.empty((M, N), dtype=torch.int32, device=Wq.device)
+        acc = _empty((M, N), torch.int32, Wq.device, stream)
     need = lib.int8rl_gemm_workspace_bytes(M, N, K)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Wq.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wbytes = _workspace(workspace, need, Wq.device, stream)
     _ck(lib.int8rl_gemm_w8a8(_p(Xq), _p(Xs), _p(Wq), _p(Ws), M, N, K, _p(Y), ldy, _p(acc),
                              _p(workspace), wbytes, _stream(Wq, stream)), "int8rl_gemm_w8a8")
     return (Y, acc) if acc is not None else Y
@@ -402,12 +419,10 @@ def fp8rl_quant_kv_tensor(KV, KVq=None, scale=None, workspace=None, stream=None)
     lib = load()
     ld = _rowmajor(KV, "KV")
     R, C = KV.shape
-    KVq = _need(KVq, (R, C), torch.uint8, KV.device, "KVq")
-    scale = _need(scale, (1,), torch.float32, KV.device, "scale")
+    KVq = _need(KVq, (R, C), torch.uint8, KV.device, "KVq", stream)
+    scale = _need(scale, (1,), torch.float32, KV.device, "scale", stream)
     need = lib.fp8rl_kv_workspace_bytes(R, C)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=KV.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wbytes = _workspace(workspace, need, KV.device, stream)
     _ck(lib.fp8rl_quant_kv_tensor(_p(KV), R, C, ld, _p(KVq), _p(scale), _p(workspace), wbytes,
                                   _stream(KV, stream)), "fp8rl_quant_kv_tensor")
     return KVq, scale
@@ -418,7 +433,7 @@ def fp8rl_quant_kv_with_scale(KV, scale, KVq=None, stream=None):
     lib = load()
     ld = _rowmajor(KV, "KV")
     R, C = KV.shape
-    KVq = _need(KVq, (R, C), torch.uint8, KV.device, "KVq")
+    KVq = _need(KVq, (R, C), torch.uint8, KV.device, "KVq", stream)
     _need(scale, (1,), torch.float32, KV.device, "scale")
     _ck(lib.fp8rl_quant_kv_with_scale(_p(KV), R, C, ld, _p(scale), _p(KVq), _stream(KV, stream)),
         "fp8rl_quant_kv_with_scale")
@@ -454,14 +469,12 @@ def fp8rl_rollout_is_weights(logp_train, logp_rollout, mask=None, log_clip: floa
     if logp_train.shape != logp_rollout.shape or not logp_train.is_contiguous() or not logp_rollout.is_contiguous():
         raise ValueError("logp_train and logp_rollout must be contiguous tensors of the same shape")
     n = logp_train.numel()
-    weights = _need(weights, tuple(logp_train.shape), torch.float32, logp_train.device, "weights")
-    stats = _need(stats, (4,), torch.float64, logp_train.device, "stats")
+    weights = _need(weights, tuple(logp_train.shape), torch.float32, logp_train.device, "weights", stream)
+    stats = _need(stats, (4,), torch.float64, logp_train.device, "stats", stream)
     if mask is not None and (mask.dtype != torch.uint8 or mask.numel() != n or not mask.is_contiguous()):
         raise ValueError("mask must be a contiguous uint8 tensor with one byte per token")
     need = lib.fp8rl_rollout_is_workspace_bytes(n)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=logp_train.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wbytes = _workspace(workspace, need, logp_train.device, stream)
     _ck(lib.fp8rl_rollout_is_weights(_p(logp_train), _p(logp_rollout), _p(mask), n, float(log_clip), int(mode),
                                      _p(weights), _p(stats), _p(workspace), wbytes,
                                      _stream(logp_train, stream)), "fp8rl_rollout_is_weights")
@@ -489,11 +502,9 @@ def fp8rl_logits_kl(P, Q, kl=None, workspace=None, stream=None):
     if P.shape != Q.shape:
         raise ValueError("P and Q must have the same shape")
     M, V = P.shape
-    kl = _need(kl, (M,), torch.float32, P.device, "kl")
+    kl = _need(kl, (M,), torch.float32, P.device, "kl", stream)
     need = lib.fp8rl_logits_kl_workspace_bytes(M, V)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=P.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, wbytes = _workspace(workspace, need, P.device, stream)
     _ck(lib.fp8rl_logits_kl(_p(P), ldp, _p(Q), ldq, M, V, _p(kl), _p(workspace), wbytes, _stream(P, stream)),
         "fp8rl_logits_kl")
     return kl
@@ -520,14 +531,10 @@ def fp8rl_rope_table(freq, max_pos: int, magnitude: float = 1.0, table=None, str
     if not freq.is_cuda or freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_contiguous():
         raise ValueError("freq must be a contiguous 1-D float64 CUDA tensor")
     R = 2 * freq.shape[0]
-    made = table is None
-    table = _need(table, (max_pos, R), torch.float32, freq.device, "table")
+    table = _need(table, (max_pos, R), torch.float32, freq.device, "table", stream)
     if table.device != freq.device:
         raise ValueError("table must be on freq's device")
     _ck(lib.fp8rl_rope_table(_p(freq), max_pos, R, magnitude, _p(table), _stream(freq, stream)), "fp8rl_rope_table")
-    if made and stream is not None:
-        table.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                            torch.cuda.ExternalStream(int(stream), device=freq.device))
     return table
 
 

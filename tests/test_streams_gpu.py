@@ -16,6 +16,14 @@ def _stream_of(t):
     raise AssertionError("not the caching allocator's")
 
 
+def _unused_stream():
+    """A stream that has no memory yet (they come from a pool, in turn)."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    used = {seg["stream"] for seg in torch.cuda.memory_snapshot()}
+    return next(t for t in (torch.cuda.Stream() for _ in range(64)) if t.cuda_stream not in used)
+
+
 def _rollout_calls():
     g = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn((64, 8, 128), generator=g, device="cuda").to(torch.bfloat16)
@@ -60,10 +68,7 @@ def test_attention_takes_its_workspace_from_the_given_stream(cuda_lib):
     call = _rollout_calls()["attn"]
     o, lse = call()
     assert fb.fp8rl_attn_paged_workspace_bytes(2, 1, 8, 2, 128, 5440) > 0
-    # streams come from a pool: one whose memory nobody has used
-    used = {seg["stream"] for seg in torch.cuda.memory_snapshot()}
-    s = next(t for t in (torch.cuda.Stream() for _ in range(64)) if t.cuda_stream not in used)
-    torch.cuda.synchronize()
+    s = _unused_stream()
     call(o=o, lse=lse, stream=s)
     s.synchronize()
     assert any(seg["stream"] == s.cuda_stream for seg in torch.cuda.memory_snapshot())
@@ -90,3 +95,58 @@ def test_a_freed_tensor_that_is_still_read_is_not_overwritten(cuda_lib):
         torch.cuda.synchronize()
         assert torch.equal(kept.cpu(), want)
         del outs
+
+
+def _layer_calls():
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    W, X, kv, P, Q = rand(512, 1024), rand(32, 1024), rand(8192, 1024), rand(4, 9000), rand(4, 9000)
+    (Wq, Ws), (Xq, Xs) = fb.fp8rl_quant_weight_block(W), fb.fp8rl_quant_act_group(X)
+    (W8, Ws8), (X8, Xs8) = fb.int8rl_quant_weight_channel(W), fb.int8rl_quant_act_token(X)
+    scale = fb.fp8rl_quant_kv_tensor(kv)[1]
+    lt, lr = (torch.randn(5000, generator=g, device="cuda") for _ in range(2))
+    E, offs = Wq.view(4, 128, 1024), torch.tensor([0, 9, 9, 20, 32], dtype=torch.int32, device="cuda")
+    freq = torch.rand(32, generator=g, device="cuda", dtype=torch.float64)
+    return {
+        "quant_weight": lambda **kw: fb.fp8rl_quant_weight_block(W, **kw),
+        "quant_act": lambda **kw: fb.fp8rl_quant_act_group(X, **kw),
+        "gemm": lambda **kw: fb.fp8rl_gemm_w8a8_block(Xq, Xs, Wq, Ws, **kw),
+        "gemm_grouped": lambda **kw: fb.fp8rl_gemm_w8a8_block_grouped(Xq, Xs, E, Ws.view(4, 1, 8), offs, **kw),
+        "linear": lambda **kw: fb.fp8rl_linear_w8a8_block(X, Wq, Ws, want_codes=True, **kw),
+        "int8_quant_weight": lambda **kw: fb.int8rl_quant_weight_channel(W, **kw),
+        "int8_quant_act": lambda **kw: fb.int8rl_quant_act_token(X, **kw),
+        "int8_gemm": lambda **kw: fb.int8rl_gemm_w8a8(X8, Xs8, W8, Ws8, want_acc=True, **kw),
+        "kv": lambda **kw: fb.fp8rl_quant_kv_tensor(kv, **kw),
+        "kv_with_scale": lambda **kw: fb.fp8rl_quant_kv_with_scale(kv, scale, **kw),
+        "importance": lambda **kw: fb.fp8rl_rollout_is_weights(lt, lr, **kw),
+        "kl": lambda **kw: fb.fp8rl_logits_kl(P, Q, **kw),
+        "table": lambda **kw: fb.fp8rl_rope_table(freq, 1000, **kw)}
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_layer_calls_allocate_on_the_given_stream(cuda_lib, raw):
+    for name, call in _layer_calls().items():
+        want = [t.clone() for t in _outputs(call())]
+        s = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        got = _outputs(call(stream=s.cuda_stream if raw else s))
+        assert all(_stream_of(t) == s.cuda_stream for t in got), name
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), name
+    assert fb.fp8rl_check_device_error() == 0
+
+
+@pytest.mark.parametrize("name", ["kv", "importance", "kl"])
+def test_layer_calls_take_workspaces_from_the_given_stream(cuda_lib, name):
+    call = _layer_calls()[name]
+    keys = {"kv": ("KVq", "scale"), "importance": ("weights", "stats"), "kl": ("kl",)}[name]
+    given = dict(zip(keys, _outputs(call())))
+    s = _unused_stream()
+    call(stream=s, **given)
+    s.synchronize()
+    assert any(seg["stream"] == s.cuda_stream for seg in torch.cuda.memory_snapshot())
+    assert fb.fp8rl_check_device_error() == 0
