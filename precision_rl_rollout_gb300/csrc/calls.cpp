@@ -135,6 +135,24 @@ private:
     c10::cuda::CUDAStreamGuard guard_;
 };
 
+// While it lasts other Python threads run: a launch waits where the driver's queue is
+// full or a kernel is loaded for its first call.  The caller holds the tensors.
+class Released {
+public:
+    Released() : state_(PyEval_SaveThread()) {}
+    ~Released() { PyEval_RestoreThread(state_); }
+    Released(const Released&) = delete;
+    Released& operator=(const Released&) = delete;
+
+private:
+    PyThreadState* state_;
+};
+template <typename F, typename... Args>
+int unlocked(F f, Args... args) {
+    const Released released;
+    return f(args...);
+}
+
 // Table [max_pos, R] and positions [T].
 void check_table(const Tensor& positions, const Tensor& table, int64_t T, c10::Device dev) {
     dense(positions, at::kInt, {T}, dev, "positions");
@@ -171,9 +189,9 @@ PyObject* rope(PyObject* const* a) {
     const Launch launch(a[6], dev);
     const Tensor Y = output_like(launch, a[5], X, "Y");
     const unsigned flags = (truth(a[3]) ? FP8RL_ROPE_INTERLEAVED : 0) | (truth(a[4]) ? FP8RL_ROPE_INVERSE : 0);
-    const int rc = fn.rope(ptr<uint16_t>(X), T, H, D, X.stride(0), X.stride(1), ptr<int32_t>(positions),
-                           ptr<float>(table), table.size(0), table.size(1), flags, ptr<uint16_t>(Y), Y.stride(0),
-                           Y.stride(1), launch.stream());
+    const int rc = unlocked(fn.rope, ptr<uint16_t>(X), T, H, D, X.stride(0), X.stride(1), ptr<int32_t>(positions),
+                            ptr<float>(table), table.size(0), table.size(1), flags, ptr<uint16_t>(Y), Y.stride(0),
+                            Y.stride(1), launch.stream());
     if (rc) throw Status{rc, "fp8rl_rope"};
     return THPVariable_Wrap(Y);
 }
@@ -202,11 +220,10 @@ PyObject* rope_append_paged(PyObject* const* a) {
     }
     const Launch launch(a[12], dev);
     const Tensor out = output_like(launch, a[11], q, "q_out");
-    const int rc = fn.rope_append_paged(ptr<uint16_t>(q), Hq, q.stride(0), q.stride(1), ptr<uint16_t>(k), k.stride(0),
-                                        k.stride(1), ptr<uint16_t>(v), v.stride(0), v.stride(1), T, positions, rows,
-                                        max_pos, R, truth(a[10]) ? FP8RL_ROPE_INTERLEAVED : 0, ptr<uint16_t>(out),
-                                        out.stride(0), out.stride(1), &kv, ptr<int64_t>(slots),
-                                        launch.stream());
+    const int rc = unlocked(fn.rope_append_paged, ptr<uint16_t>(q), Hq, q.stride(0), q.stride(1), ptr<uint16_t>(k),
+                            k.stride(0), k.stride(1), ptr<uint16_t>(v), v.stride(0), v.stride(1), T, positions, rows,
+                            max_pos, R, truth(a[10]) ? FP8RL_ROPE_INTERLEAVED : 0, ptr<uint16_t>(out), out.stride(0),
+                            out.stride(1), &kv, ptr<int64_t>(slots), launch.stream());
     if (rc) throw Status{rc, "fp8rl_rope_append_paged"};
     return THPVariable_Wrap(out);
 }
@@ -246,12 +263,11 @@ PyObject* attn_paged(PyObject* const* a) {
     } else if (const size_t need = fn.attn_workspace(B, Lq, Hq, kv.kv_heads, D, max_len)) {
         workspace = at::empty({(int64_t)need}, q.options().dtype(at::kByte));
     }
-    const int rc = fn.attn_paged(ptr<uint16_t>(q), B, Lq, Hq, q.stride(0), q.stride(1), q.stride(2), &kv,
-                                 ptr<int32_t>(table), B == 1 ? table.size(1) : table.stride(0), ptr<int32_t>(lens),
-                                 max_len, window, (float)scale, ptr<uint16_t>(o),
-                                 lse.defined() ? ptr<float>(lse) : nullptr,
-                                 workspace.defined() ? workspace.data_ptr() : nullptr,
-                                 workspace.defined() ? workspace.nbytes() : 0, launch.stream());
+    const int rc = unlocked(fn.attn_paged, ptr<uint16_t>(q), B, Lq, Hq, q.stride(0), q.stride(1), q.stride(2), &kv,
+                            ptr<int32_t>(table), B == 1 ? table.size(1) : table.stride(0), ptr<int32_t>(lens), max_len,
+                            window, (float)scale, ptr<uint16_t>(o), lse.defined() ? ptr<float>(lse) : nullptr,
+                            workspace.defined() ? workspace.data_ptr() : nullptr,
+                            workspace.defined() ? workspace.nbytes() : 0, launch.stream());
     if (rc) throw Status{rc, "fp8rl_attn_paged"};
     if (!lse.defined()) return THPVariable_Wrap(o);
     return Py_BuildValue("(NN)", THPVariable_Wrap(o), THPVariable_Wrap(lse));
@@ -290,10 +306,10 @@ PyObject* spec_verify(PyObject* const* a) {
     const Launch launch(a[8], dev);
     const Tensor tokens = output(launch, a[6], {B, K + 1}, at::kInt, P, "tokens");
     const Tensor accepted = output(launch, a[7], {B}, at::kInt, P, "accepted");
-    const int rc = fn.spec_verify(P.data_ptr(), P.stride(0), P.stride(1), qp, q_seq, q_step,
-                                  type == at::kFloat ? FP8RL_PROB_F32 : FP8RL_PROB_BF16, ptr<int32_t>(drafts), lens,
-                                  ptr<float>(u), ptr<float>(noise), noise.stride(0), B, K, V, ptr<int32_t>(tokens),
-                                  ptr<int32_t>(accepted), launch.stream());
+    const int rc = unlocked(fn.spec_verify, P.data_ptr(), P.stride(0), P.stride(1), qp, q_seq, q_step,
+                            type == at::kFloat ? FP8RL_PROB_F32 : FP8RL_PROB_BF16, ptr<int32_t>(drafts), lens,
+                            ptr<float>(u), ptr<float>(noise), noise.stride(0), B, K, V, ptr<int32_t>(tokens),
+                            ptr<int32_t>(accepted), launch.stream());
     if (rc) throw Status{rc, "fp8rl_spec_verify"};
     return Py_BuildValue("(NN)", THPVariable_Wrap(tokens), THPVariable_Wrap(accepted));
 }

@@ -151,3 +151,56 @@ def test_binding_refusals_on_the_device(cuda_lib):
     with pytest.raises(fb.Fp8rlError):
         fb.fp8rl_attn_paged(x[None, :, :1].repeat(1, 1, 3, 1), pool, pool, bt, pos[:1], 8)   # 3 heads over 2
     assert fb.fp8rl_check_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_other_threads_run_during_a_launch(cuda_lib, tmp_path):
+    """A launch can wait (for room in the driver's queue, for a module to load): other
+    Python threads must run meanwhile.  The calls are bound to libc's poll here, given no
+    descriptors and 300 ms by the arguments that come second and third."""
+    import importlib.machinery
+    import importlib.util
+    import shutil
+    import threading
+    import time
+    dev = dict(device="cuda")
+    x = torch.zeros((0, 300, 64), dtype=torch.bfloat16, **dev)
+    pos, table = torch.zeros(0, dtype=torch.int32, **dev), torch.zeros((4, 64), **dev)
+    binding.fp8rl_rope(x, pos, table)                          # loads the module
+    copy = str(tmp_path / "_calls.so")                         # a module of its own, with its own functions
+    shutil.copy(binding._calls.__spec__.origin, copy)
+    calls = importlib.util.module_from_spec(importlib.util.spec_from_loader(
+        "_calls", importlib.machinery.ExtensionFileLoader("_calls", copy)))
+    calls.__spec__.loader.exec_module(calls)
+    poll = ctypes.cast(ctypes.CDLL(None).poll, ctypes.c_void_p).value
+    calls.bind(poll, poll, poll, poll, poll, binding.Fp8rlError)
+    pool = torch.zeros((2, 4, 2, 64), dtype=torch.bfloat16, **dev)
+    kv = torch.zeros((2, 2, 64), dtype=torch.bfloat16, **dev)
+    buf = torch.zeros(1000, **dev)
+    q = torch.zeros(1000, dtype=torch.bfloat16, **dev).as_strided((2, 0, 64), (300, 64, 1))
+    ws = torch.zeros(16, dtype=torch.uint8, **dev)
+    made = {"rope": lambda: calls.rope(x, pos, table, False, False, None, None),
+            "append": lambda: calls.rope_append_paged(q, kv, kv, None, None, pool, pool, torch.zeros(2, dtype=torch.int64, **dev),
+                                                      None, None, False, None, None),
+            "attn": lambda: calls.attn_paged(x.view(0, 300, 1, 64).expand(0, 300, 2, 64), pool, pool,
+                                             torch.zeros((0, 2), dtype=torch.int32, **dev), pos, 8, None, 0, None, None,
+                                             None, None, False, ws, None),
+            "verify": lambda: calls.spec_verify(buf.as_strided((1, 2, 8), (0, 300, 1)), torch.zeros((1, 1), dtype=torch.int32, **dev),
+                                                buf[:1].view(1, 1), buf[:8].view(1, 8), None, None, None, None, None)}
+    for name, call in made.items():
+        ticks, stop = [0], threading.Event()
+
+        def tick():
+            while not stop.wait(0.002):
+                ticks[0] += 1
+        t = threading.Thread(target=tick)
+        t.start()
+        while not ticks[0]:
+            time.sleep(0.001)
+        before, t0 = ticks[0], time.perf_counter()
+        call()
+        took, ran = time.perf_counter() - t0, ticks[0] - before
+        stop.set()
+        t.join()
+        assert took > 0.25, (name, took)                       # the function did wait
+        assert ran > 20, (name, ran)                           # of some 140
