@@ -63,7 +63,7 @@ class FP8RL_PAGED_KV(ctypes.Structure):
 
 
 _lib = None
-_calls = None                            # the module _calls.so
+_calls = None                            # the module _calls.so, from the first rollout call on
 _lock = threading.Lock()
 
 
@@ -73,7 +73,7 @@ def library_path() -> str:
 
 def load(path: str | None = None):
     """Load libfp8rl.so (built by ``precision_rl_rollout_gb300.build``)."""
-    global _lib, _calls
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -137,23 +137,28 @@ def load(path: str | None = None):
                             "fp8rl_logits_kl_workspace_bytes", "fp8rl_attn_paged_workspace_bytes"):
                 getattr(lib, name).restype = ctypes.c_int
 
-        _calls = _load_calls(lib)
         _lib = lib
         return lib
 
 
-def _load_calls(lib):
-    """The compiled side of the rollout step's calls, given the library's functions."""
-    if not os.path.exists(_build.CALLS_PATH):
-        raise RuntimeError(f"_calls.so not found at {_build.CALLS_PATH}: build it with "
-                           "`python -m precision_rl_rollout_gb300.build` (needs g++ and torch's headers)")
-    loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS_PATH)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
-    loader.exec_module(module)
-    module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
-                  ("fp8rl_rope", "fp8rl_rope_append_paged", "fp8rl_attn_paged", "fp8rl_attn_paged_workspace_bytes",
-                   "fp8rl_spec_verify")), Fp8rlError)
-    return module
+def load_calls():
+    """Load _calls.so, the compiled side of the rollout step's calls.  They load it by
+    themselves at their first use; the other calls do without."""
+    global _calls
+    lib = load()
+    with _lock:
+        if _calls is None:
+            if not os.path.exists(_build.CALLS_PATH):
+                raise RuntimeError(f"_calls.so not found at {_build.CALLS_PATH}: build it with "
+                                   "`python -m precision_rl_rollout_gb300.build` (needs g++ and torch's headers)")
+            loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS_PATH)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
+            loader.exec_module(module)
+            module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                          ("fp8rl_rope", "fp8rl_rope_append_paged", "fp8rl_attn_paged",
+                           "fp8rl_attn_paged_workspace_bytes", "fp8rl_spec_verify")), Fp8rlError)
+            _calls = module
+        return _calls
 
 
 def _ck(rc: int, where: str):
@@ -541,8 +546,8 @@ def fp8rl_rope_table(freq, max_pos: int, magnitude: float = 1.0, table=None, str
 def fp8rl_rope(X, positions, table, interleaved=False, inverse=False, Y=None, stream=None):
     """X bf16 [T, H, D] (token and head strides free), positions int32 [T], table fp32
     [max_pos, R] -> Y bf16 [T, H, D]; inverse=True: the gradient.  Y may be X."""
-    if _lib is None:
-        load()
+    if _calls is None:
+        load_calls()
     return _calls.rope(X, positions, table, interleaved, inverse, Y, _raw(stream))
 
 
@@ -556,8 +561,8 @@ def fp8rl_rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale=None
     -> q rotated; k rotated and v stored in the pools K, V [pages, page_size, kv_heads, D]
     (bf16, or uint8 E4M3 codes under k_scale, v_scale fp32 [1]; a page laid out head by
     head is the transposed view).  table None: no rotation."""
-    if _lib is None:
-        load()
+    if _calls is None:
+        load_calls()
     return _calls.rope_append_paged(q, k, v, positions, table, K, V, slots, k_scale, v_scale, interleaved, q_out,
                                     _raw(stream))
 
@@ -578,8 +583,8 @@ def fp8rl_attn_paged(q, K, V, block_table, seq_lens, max_len: int, scale=None, w
     [B, >= max_len / page_size], seq_lens int32 [B] (at most max_len).  scale: D^-1/2
     unless given.  -> o bf16 [B, Lq, Hq, D] (and lse fp32 [B, Lq, Hq] when want_lse or
     lse is given)."""
-    if _lib is None:
-        load()
+    if _calls is None:
+        load_calls()
     return _calls.attn_paged(q, K, V, block_table, seq_lens, max_len, scale, window, k_scale, v_scale, o, lse, want_lse,
                              workspace, _raw(stream))
 
@@ -593,6 +598,6 @@ def fp8rl_spec_verify(P, drafts, u, noise, Q=None, draft_lens=None, tokens=None,
     drafts int32 [B, K], u fp32 [B, K] in [0, 1), noise fp32 [B, V] of Exp(1) draws,
     draft_lens int32 [B] (None: K) -> (tokens int32 [B, K+1]: kept drafts, the next
     token, then -1; accepted int32 [B])."""
-    if _lib is None:
-        load()
+    if _calls is None:
+        load_calls()
     return _calls.spec_verify(P, drafts, u, noise, Q, draft_lens, tokens, accepted, _raw(stream))
