@@ -16,6 +16,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libfp8rl.so")
 CALLS_PATH = os.path.join(PKG, "_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -43,15 +45,25 @@ def _sources():
 
 
 def _deps():
-    return _sources() + [os.path.join(CSRC, "calls.cpp")] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
+    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def _newer(target: str, deps) -> bool:
+    """target is there and no older than what it is made of."""
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB_PATH, _deps())
+
+
+def _calls_up_to_date() -> bool:
+    return _newer(CALLS_PATH, [CALLS_SOURCE, os.path.join(INCLUDE, "fp8rl.h"), os.path.abspath(__file__)])
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _lib_up_to_date() and _calls_up_to_date()
 
 
 def _build_calls():
@@ -64,7 +76,7 @@ def _build_calls():
     inc = [os.path.join(here, "include"), os.path.join(here, "include", "torch", "csrc", "api", "include"),
            os.path.join(home, "include"), sysconfig.get_paths()["include"], INCLUDE]
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-w", *[f"-I{p}" for p in inc],
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "calls.cpp"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", CALLS_SOURCE,
            "-o", tmp, "-L" + os.path.join(here, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -73,8 +85,24 @@ def _build_calls():
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB_PATH
+    """-> the library's path.  The library needs no torch: where _calls.so cannot be made
+    it is there all the same, and a warning says why the rollout calls will not be."""
+    lib, calls = force or not _lib_up_to_date(), force or not _calls_up_to_date()
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        made = ex.submit(_build_calls) if calls else None
+        if lib:
+            _build_library(verbose, ptxas_verbose)
+        try:
+            if made:
+                made.result()
+        except Exception as e:
+            if os.path.exists(CALLS_PATH):
+                os.remove(CALLS_PATH)                  # made for another library
+            warnings.warn(f"_calls.so was not built, the rollout step's calls will raise: {e}", RuntimeWarning, stacklevel=2)
+    return LIB_PATH
+
+
+def _build_library(verbose: bool, ptxas_verbose: bool):
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
@@ -88,9 +116,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, (r.stdout + r.stderr)
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        calls = ex.submit(_build_calls)
         results = list(ex.map(compile_one, _sources()))
-        calls.result()
     if verbose or ptxas_verbose:
         for _, log in results:
             if log.strip():
@@ -101,7 +127,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

@@ -36,3 +36,40 @@ def test_other_calls_do_without_the_compiled_ones(built):
                 "else:\n"
                 "    raise SystemExit('a rollout call ran without its module')\n")
     assert r.returncode == 0, r.stderr
+
+
+@pytest.fixture
+def small(monkeypatch, tmp_path):
+    """The build pointed at a folder of its own and two sources that compile at once."""
+    csrc = tmp_path / "csrc"
+    csrc.mkdir()
+    (csrc / "one.cu").write_text('extern "C" int one() { return 1; }\n')
+    (csrc / "calls.cpp").write_text("#error no torch here\n")
+    for name, value in (("CSRC", csrc), ("BUILD_DIR", tmp_path / "objects"), ("LIB_PATH", tmp_path / "lib.so"),
+                        ("CALLS_PATH", tmp_path / "_calls.so"), ("CALLS_SOURCE", csrc / "calls.cpp")):
+        monkeypatch.setattr(build, name, str(value), raising=False)
+    try:
+        build._nvcc()
+    except RuntimeError as e:
+        pytest.skip(str(e))
+    return csrc
+
+
+def test_the_library_is_built_where_the_calls_cannot_be(small):
+    import ctypes
+    open(build.CALLS_PATH, "w").close()                     # of an earlier library: does not stay
+    with pytest.warns(RuntimeWarning, match="no torch here"):
+        path = build.build(force=True)
+    assert path == build.LIB_PATH and ctypes.CDLL(path).one() == 1
+    assert not os.path.exists(build.CALLS_PATH)
+    # the library stands; only the calls are tried again
+    when = os.path.getmtime(path)
+    with pytest.warns(RuntimeWarning):
+        build.build()
+    assert os.path.getmtime(path) == when
+
+
+def test_a_library_that_does_not_compile_is_an_error(small):
+    (small / "one.cu").write_text("#error broken\n")
+    with pytest.raises(RuntimeError, match="nvcc failed"):
+        build.build(force=True)
