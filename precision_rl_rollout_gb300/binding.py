@@ -63,7 +63,7 @@ class FP8RL_PAGED_KV(ctypes.Structure):
 
 
 _lib = None
-_calls = None                            # the module _calls.so, from the first rollout call on
+_calls = None                            # the compiled calls, from the first of them on
 _lock = threading.Lock()
 
 
@@ -142,16 +142,17 @@ def load(path: str | None = None):
 
 
 def load_calls():
-    """Load _calls.so, the compiled side of the rollout step's calls.  They load it by
-    themselves at their first use; the other calls do without."""
+    """Load the compiled side of the rollout step's calls.  They load it by themselves
+    at their first use; the other calls do without."""
     global _calls
     lib = load()
     with _lock:
         if _calls is None:
-            if not os.path.exists(_build.CALLS_PATH):
-                raise RuntimeError(f"_calls.so not found at {_build.CALLS_PATH}: build it with "
+            path = _build.calls_path()
+            if not os.path.exists(path):
+                raise RuntimeError(f"no compiled calls for this Python and torch at {path}: build them with "
                                    "`python -m precision_rl_rollout_gb300.build` (needs g++ and torch's headers)")
-            loader = importlib.machinery.ExtensionFileLoader("_calls", _build.CALLS_PATH)
+            loader = importlib.machinery.ExtensionFileLoader("_calls", path)
             module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_calls", loader))
             loader.exec_module(module)
             module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
@@ -517,10 +518,10 @@ def fp8rl_logits_kl(P, Q, kl=None, workspace=None, stream=None):
 
 # ------------------------------------------------------- rollout step: positions, paged cache, drafts
 # A decode step makes these calls with a few microseconds of GPU work behind each, so
-# their checks and marshalling are compiled (csrc/calls.cpp -> _calls.so, built with
-# the library).  A wrong type, shape, stride or device is a ValueError; a status of the
-# C ABI an Fp8rlError.  What a call allocates while a stream is given is of that
-# stream's memory; outputs are recorded on the caller's current stream as well.
+# their checks and marshalling are compiled (csrc/calls.cpp, built with the library).
+# A wrong type, shape, stride or device is a ValueError; a status of the C ABI an
+# Fp8rlError.  What a call allocates while a stream is given is of that stream's
+# memory; outputs are recorded on the caller's current stream as well.
 
 def _raw(stream):
     return stream if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)

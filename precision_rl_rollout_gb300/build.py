@@ -1,6 +1,7 @@
 """Build libfp8rl.so in-tree: every csrc/*.cu compiled for sm_103a in parallel
 with nvcc, then linked into one shared library beside this file; and beside it the
-Python module _calls.so (csrc/calls.cpp, host code only, against torch's headers).
+Python module of the rollout step's calls, _calls.<python>.<torch>.so (csrc/calls.cpp,
+host code only, against torch's headers).
 
     python -m precision_rl_rollout_gb300.build [--force] [--verbose]
 
@@ -24,7 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libfp8rl.so")
-CALLS_PATH = os.path.join(PKG, "_calls.so")
+CALLS_STEM = os.path.join(PKG, "_calls")
 CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -49,6 +50,17 @@ def _deps():
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def calls_path() -> str:
+    """The module of the compiled calls for this Python and this torch: it is compiled
+    against both, and one made for others would crash or not load."""
+    try:
+        import torch
+        tag = f"torch{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    except ImportError:
+        tag = "torchless"
+    return f"{CALLS_STEM}.{sysconfig.get_config_var('SOABI')}.{tag}.so"
+
+
 def _newer(target: str, deps) -> bool:
     """target is there and no older than what it is made of."""
     return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
@@ -59,7 +71,7 @@ def _lib_up_to_date() -> bool:
 
 
 def _calls_up_to_date() -> bool:
-    return _newer(CALLS_PATH, [CALLS_SOURCE, os.path.join(INCLUDE, "fp8rl.h"), os.path.abspath(__file__)])
+    return _newer(calls_path(), [CALLS_SOURCE, os.path.join(INCLUDE, "fp8rl.h"), os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
@@ -67,10 +79,11 @@ def up_to_date() -> bool:
 
 
 def _build_calls():
-    """_calls.so with the host compiler, against the torch that will import it."""
+    """The compiled calls with the host compiler, against the torch that will import them."""
     import torch
     cxx = shutil.which("g++") or "g++"
-    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    path = calls_path()
+    tmp = path + f".tmp{os.getpid()}"
     home = os.path.dirname(os.path.dirname(_nvcc()))
     here = os.path.dirname(torch.__file__)
     inc = [os.path.join(here, "include"), os.path.join(here, "include", "torch", "csrc", "api", "include"),
@@ -81,12 +94,12 @@ def _build_calls():
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS_PATH)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """-> the library's path.  The library needs no torch: where _calls.so cannot be made
-    it is there all the same, and a warning says why the rollout calls will not be."""
+    """-> the library's path.  The library needs no torch: where the compiled calls cannot
+    be made it is there all the same, and a warning says why the rollout calls will not be."""
     lib, calls = force or not _lib_up_to_date(), force or not _calls_up_to_date()
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
         made = ex.submit(_build_calls) if calls else None
@@ -96,9 +109,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             if made:
                 made.result()
         except Exception as e:
-            if os.path.exists(CALLS_PATH):
-                os.remove(CALLS_PATH)                  # made for another library
-            warnings.warn(f"_calls.so was not built, the rollout step's calls will raise: {e}", RuntimeWarning, stacklevel=2)
+            if os.path.exists(calls_path()):
+                os.remove(calls_path())                # made for another library
+            warnings.warn(f"the compiled calls were not built, the rollout step's calls will raise: {e}",
+                          RuntimeWarning, stacklevel=2)
     return LIB_PATH
 
 

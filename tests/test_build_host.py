@@ -25,14 +25,14 @@ def _python(code):
 
 def test_other_calls_do_without_the_compiled_ones(built):
     r = _python("from precision_rl_rollout_gb300 import binding as fb, build\n"
-                "build.CALLS_PATH = '/nowhere/_calls.so'\n"
+                "build.CALLS_STEM = '/nowhere/_calls'\n"
                 "fb.load()\n"
                 "assert fb.fp8rl_abi_version() > 0 and fb.fp8rl_gemm_workspace_bytes(64, 512, 512) >= 0\n"
                 "assert fb.fp8rl_attn_paged_kernel_count(0, 1, 4, 2, 64, 100) == 0\n"
                 "try:\n"
                 "    fb.fp8rl_rope(None, None, None)\n"
                 "except RuntimeError as e:\n"
-                "    assert '_calls.so' in str(e) and 'build' in str(e)\n"
+                "    assert '/nowhere/_calls' in str(e) and 'build' in str(e)\n"
                 "else:\n"
                 "    raise SystemExit('a rollout call ran without its module')\n")
     assert r.returncode == 0, r.stderr
@@ -46,7 +46,7 @@ def small(monkeypatch, tmp_path):
     (csrc / "one.cu").write_text('extern "C" int one() { return 1; }\n')
     (csrc / "calls.cpp").write_text("#error no torch here\n")
     for name, value in (("CSRC", csrc), ("BUILD_DIR", tmp_path / "objects"), ("LIB_PATH", tmp_path / "lib.so"),
-                        ("CALLS_PATH", tmp_path / "_calls.so"), ("CALLS_SOURCE", csrc / "calls.cpp")):
+                        ("CALLS_STEM", tmp_path / "_calls"), ("CALLS_SOURCE", csrc / "calls.cpp")):
         monkeypatch.setattr(build, name, str(value), raising=False)
     try:
         build._nvcc()
@@ -57,11 +57,11 @@ def small(monkeypatch, tmp_path):
 
 def test_the_library_is_built_where_the_calls_cannot_be(small):
     import ctypes
-    open(build.CALLS_PATH, "w").close()                     # of an earlier library: does not stay
+    open(build.calls_path(), "w").close()                     # of an earlier library: does not stay
     with pytest.warns(RuntimeWarning, match="no torch here"):
         path = build.build(force=True)
     assert path == build.LIB_PATH and ctypes.CDLL(path).one() == 1
-    assert not os.path.exists(build.CALLS_PATH)
+    assert not os.path.exists(build.calls_path())
     # the library stands; only the calls are tried again
     when = os.path.getmtime(path)
     with pytest.warns(RuntimeWarning):
@@ -73,3 +73,29 @@ def test_a_library_that_does_not_compile_is_an_error(small):
     (small / "one.cu").write_text("#error broken\n")
     with pytest.raises(RuntimeError, match="nvcc failed"):
         build.build(force=True)
+
+
+def test_calls_built_for_another_torch_or_python_are_not_current(built, monkeypatch):
+    import sysconfig
+    import torch
+    assert build.up_to_date()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "9.9.0")
+        assert not build.up_to_date()
+    with monkeypatch.context() as m:
+        var = sysconfig.get_config_var
+        m.setattr(sysconfig, "get_config_var", lambda n: "cpython-399-none" if n == "SOABI" else var(n))
+        assert not build.up_to_date()
+    assert build.up_to_date()
+    # and are not loaded
+    r = _python("import torch\n"
+                "torch.__version__ = '9.9.0'\n"
+                "from precision_rl_rollout_gb300 import binding as fb\n"
+                "fb.load()\n"
+                "try:\n"
+                "    fb.load_calls()\n"
+                "except RuntimeError as e:\n"
+                "    assert '9.9.0' in str(e)\n"
+                "else:\n"
+                "    raise SystemExit('loaded')\n")
+    assert r.returncode == 0, r.stderr
