@@ -104,7 +104,7 @@ struct Config {
     // CTAs an SM.  Two for heads of 256 over E4M3, of 64 tokens a tile, rather than one
     // of 128: 120 sequences to 57, 16/16 heads: 63 -> 30 us; 64 of 8191, 28/4: 171 -> 169
     // (three: 25 and 176).
-    static constexpr int kCtas = DP > 128 ? (kE4m3 ? 2 : 1) : kE4m3 && RT < 64 ? 3 : 2;
+    static constexpr int kCtas = DP > 128 ? (kE4m3 ? 2 : 1) : kE4m3 ? 3 : 2;
     static constexpr int kBudget = 233472 / kCtas - 1024;    // 228 KB an SM, 1 KB of it kept for each CTA
     static constexpr int kRest = kP + kQ + kSmall;
     static constexpr int kFit = (kBudget - kRest) / kStage;
@@ -553,8 +553,6 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
     const int lane_vr = kE ? lane & 15 : (lane & 7) + (lane >> 4) * 8, lane_vc = kE ? lane >> 4 : lane >> 3 & 1;
     const uint32_t lane_k = swz<C>(warp * TT + (lane & 15), lane >> 4), lane_v = swz<C>(lane_vr, lane_vc);
     auto piece = [](uint32_t at, int c) -> uint32_t { return (at ^ (uint32_t)((c & 7) << 4)) + (c >> 3) * (CT * 128); };
-    // the same for a chunk known at run time
-    auto chunk_at = [](uint32_t at, int c) -> uint32_t { return (at ^ (uint32_t)((c & 7) << 4)) + (c >> 3) * (CT * 128); };
     const uint32_t sp = sm100::smem_u32(smem_p);
     // probabilities, stored and loaded by pairs of row tiles, or both parts of one
     const uint32_t p_lane = sp + swz_p<C>((NT > 1 ? lane >> 4 : 0) * 8 + (lane & 7), lane >> 3 & 1) +
@@ -782,7 +780,7 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
 #pragma unroll
                 for (int k = 0; k < MW; k += 2) {
                     uint32_t w[4];
-                    ldsm4_t(w, chunk_at(va, warp * MW + k) + row);
+                    ldsm4_t(w, piece(va, warp * MW + k) + row);
                     e4m3x4_f16(__byte_perm(w[0], 0, 0x3120), a[k][0], a[k][1]);
                     e4m3x4_f16(__byte_perm(w[1], 0, 0x3120), a[k][2], a[k][3]);
                     e4m3x4_f16(__byte_perm(w[2], 0, 0x3120), a[k + 1][0], a[k + 1][1]);
@@ -790,7 +788,7 @@ attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ 
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < MW; ++k) ldsm4_t(a[k], chunk_at(va, (warp * MW + k) * 2) + row);
+                for (int k = 0; k < MW; ++k) ldsm4_t(a[k], piece(va, (warp * MW + k) * 2) + row);
             }
 #pragma unroll
             for (int k = 0; k < MW; ++k)
