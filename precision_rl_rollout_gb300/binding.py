@@ -8,7 +8,9 @@ Tensors: bf16 inputs are ``torch.bfloat16``; E4M3 codes are ``torch.uint8``
 scales ``torch.float32``.  Outputs that are not passed in are allocated with
 ``torch.empty`` on the input's device.  Work is enqueued on the current torch
 stream of that device unless ``stream`` is given; what a call allocates is then of
-that stream's memory.
+that stream's memory.  No call takes part in autograd, whether or not its inputs
+require a gradient: a training step makes the call of the gradient itself
+(``fp8rl_rope`` with ``inverse=True``).
 """
 from __future__ import annotations
 
@@ -546,7 +548,8 @@ def fp8rl_rope_table(freq, max_pos: int, magnitude: float = 1.0, table=None, str
 
 def fp8rl_rope(X, positions, table, interleaved=False, inverse=False, Y=None, stream=None):
     """X bf16 [T, H, D] (token and head strides free), positions int32 [T], table fp32
-    [max_pos, R] -> Y bf16 [T, H, D]; inverse=True: the gradient.  Y may be X."""
+    [max_pos, R] -> Y bf16 [T, H, D]; inverse=True: the gradient, given that of Y (not
+    recorded by autograd).  Y may be X."""
     if _calls is None:
         load_calls()
     return _calls.rope(X, positions, table, interleaved, inverse, Y, _raw(stream))

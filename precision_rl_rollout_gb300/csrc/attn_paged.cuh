@@ -6,8 +6,8 @@
 // a query that sees nothing gets zeros and a log-sum of -inf.
 //
 // What bounds it.  Every cached key and value is read once and meets the group's
-// query rows (query heads of the kv head x Lq): 2 rows flop a bf16 byte, 4 rows an
-// E4M3 byte.  With the 5-8 rows of one new token that is far below the tensor
+// query rows (query heads of the kv head x Lq): rows flop a bf16 byte, 2 rows an E4M3
+// byte.  With the 5-8 rows of one new token that is far below the tensor
 // cores' rate at HBM speed, and the kernel is a stream: 128 sequences of 40/8 heads
 // of 128 over bf16, 4.3 GB, in 658 us (6.6 TB/s, 97% of a plain copy), one sequence
 // of 131072 tokens in 84 us (6.4 TB/s); 64 ragged sequences of 28/4 heads over E4M3,
@@ -60,8 +60,10 @@
 // GPU.  The lengths are read on the device.  A CTA writes an item that lies wholly
 // in its range; of items that do not it has at most two, whose unnormalised sums go
 // to its two slots of the workspace, joined in a second launch in CTA order.  A
-// short batch is one launch: each item has a cluster of CTAs, whose sums the first
-// takes through shared memory (1 x 777 tokens: 10.3 -> 7.1 us).
+// short batch is one launch: each item has a cluster of CTAs, which join their sums
+// through each other's shared memory, a part of the rows each (1 x 777 tokens: 10.3 ->
+// 7.1 us).  "Short" goes by the host's bound max_len: under a loose one the same batch
+// takes the two launches.
 #pragma once
 
 #include <math.h>

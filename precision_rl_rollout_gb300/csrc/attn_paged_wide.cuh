@@ -3,13 +3,15 @@
 // a prompt behind a cached prefix).  Mathematics, work split and workspace are those
 // of attn_paged.cuh.
 //
-// What bounds it.  Each cached byte meets 2 rows flop; 40 rows at HBM's speed are 0.3
+// What bounds it.  Each cached byte meets rows flop; 40 rows at HBM's speed are 0.3
 // PFLOP/s, more than mma.sync makes here beside its matrix loads (64 rows at once, their
 // sums spilled: 0.14).  tcgen05 has the rate, so the work is a stream again, and beyond
 // that the threads' part: a tile of 128 tokens takes them 1.4 us with 40 rows, 2.0 with
-// 80, where HBM takes 1.5.  32 sequences to 16384, 8 kv heads of 128, 1.1 GB: 40 rows in
-// 187 us (5.9 TB/s; by mma.sync 314), 80 in 228 (610), 120 in 364 (649).  Prompt chunks
-// of 512 behind up to 3488 tokens, 8 sequences, 28/4 heads: 421 us, 0.29 PFLOP/s (1170).
+// 80, where HBM takes 1.5.  32 sequences to 16384, 8 kv heads of 128, pages of 64, 1.1 GB:
+// 40 rows in 186 us (5.9 TB/s; by mma.sync in chunks of 32 335), 80 in 211 (530), 120 in
+// 294 (707).  Prompt chunks of 512 behind up to 3488 tokens, 8 sequences, 28/4 heads: 420
+// us, 0.29 PFLOP/s (1534), every chunk of rows over all of its sequence's tiles.  Pages of
+// 16 tokens are eight boxes a tile instead of two: 40 rows 238 us, 80 rows 260.
 //
 // Products.  Tokens, then head values are the M side, the rows the N side:
 //   S^T [128 tokens x rows] = K Q^T      K and Q with the head inside (K-major),
@@ -46,7 +48,7 @@ struct WideConfig {
     static constexpr int kFit = (232448 - kP - kQ - kSmall) / kTile, kSlots = kFit < 8 ? kFit : 8;
     static constexpr int kSmem = kSlots * kTile + kP + kQ + kSmall;
     // An item's start and end, in tiles: 100 sequences to 1500, 40 rows, heads of 128:
-    // 104 us with two, 93 with four, 95 with six; prompt chunks of 512: 527, 466, 421.
+    // 105 us with two, 92 with four, 96 with six; prompt chunks of 512: 528, 466, 420.
     static constexpr int kItem = 6;
     static constexpr int kUnits = RT / 16;                   // eights of rows a thread, kept or taken four at a time
     static constexpr int kGroup = kUnits <= 6 ? kUnits : 4;
@@ -56,8 +58,8 @@ struct WideConfig {
 
 constexpr int kWideWarps = 8, kWideThreads = kWideWarps * 32 + 64;   // and one that loads, one that multiplies
 
-// A K-major operand of 128-byte rows, and an MN-major one of pieces of 64 (rows of
-// the K side 128 bytes apart in eights, the next 64 a piece on).
+// An MN-major operand of pieces of 64 values (rows of the K side 128 bytes apart, in
+// eights; the next 64 values a piece on).
 __device__ __forceinline__ uint64_t wide_desc_mn(uint32_t addr, uint32_t piece) {
     return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(piece >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
@@ -595,9 +597,9 @@ Plan plan_wide(int64_t max_len) {
 
 // Where it is taken, and its configuration: as few rows as hold them, in chunks of up
 // to 96, each reading the cache again; up to 128 in one, whose scores a thread cannot
-// keep, so that it reads them twice.  120 rows, 32 sequences to 16384: 354 us in one,
-// 396 in two chunks; 320 rows, 16 sequences: 525 us in chunks of 128, 462 in ones of 80;
-// prompt chunks of 512 behind up to 3488 tokens, 7 heads a kv head: 724 and 640.
+// keep, so that it reads them twice.  120 rows, 32 sequences to 16384: 294 us in one,
+// 353 in two chunks; 320 rows, 16 sequences: 438 us in chunks of 128, 403 in ones of 80;
+// prompt chunks of 512 behind up to 3488 tokens, 7 heads a kv head: 483 and 420.
 inline bool is_wide(int64_t D, int64_t rows) { return rows > 32 && D <= 128; }
 template <int DP, class F>
 auto pick_wide_rows(int64_t rows, F f) {

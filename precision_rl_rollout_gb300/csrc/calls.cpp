@@ -1,10 +1,11 @@
 // calls.cpp -- the rollout step's calls (rotary positions, the append, paged
 // attention, verification) from torch tensors to the C ABI, as a Python module.
 // A decode step makes these calls with a few microseconds of GPU work behind each;
-// checked and marshalled in Python they took 11 to 23 us of host time, here 5 to
-// 11 (Grace; the launches themselves are 3 to 6 of it).  Everything they refuse is refused with ValueError before any CUDA
-// call; a status of the C ABI becomes the binding's Fp8rlError.  The module links
-// to no part of the library: bind() is given the addresses of its functions.
+// checked and marshalled in Python they took 11 to 23 us of host time, here 4 to
+// 11 (Grace; the launches themselves are 3 to 6 of it).  Everything they refuse is
+// refused with ValueError before any CUDA call; a status of the C ABI becomes the
+// binding's Fp8rlError.  The module links to no part of the library: bind() is given
+// the addresses of its functions.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>

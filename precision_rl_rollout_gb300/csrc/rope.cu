@@ -151,7 +151,9 @@ struct Quant {
 // 128: 32 us, 6.3 TB/s; gradient of 16411 tokens, 28 + 4 heads, 64 of 128 values
 // interleaved: 42 us, 6.5 TB/s; append of 8192 tokens, 40 + 2 x 8 heads, bf16
 // pages: 38 us, 6.3 TB/s; in 8-byte chunks (11041 tokens, 28 + 4 heads, 56 of 80
-// values) 20 us, 5.6 TB/s, a value at a time 82.  What is left is the start and the last wave.
+// values) 22 us, 5.2 TB/s, a value at a time 82.  What is left there is the start and the
+// last wave.  Over E4M3 the append is not HBM's: 8192 tokens of 28 + 2 x 4 heads take 33 us
+// for 147 MB, 4.4 TB/s, with codes leaving 8 bytes at a time and two heads' loads in flight.
 __host__ __device__ inline int rope_columns(int D, int R, bool inter, int W) {
     return inter ? D / W : R / (2 * W) + ((D - R) / W + 1) / 2;
 }
@@ -330,9 +332,10 @@ cudaError_t launch_t(RopeParams& p, int width, cudaStream_t st) {
     if (!width) return launch_pdl(rope_narrow_kernel<kInter, kE4m3>, dim3((unsigned)p.T), dim3(kRopeThreads), 0, st, p);
     // A thread goes over up to eight heads, fewer where that leaves SMs without two
     // CTAs: its own work (the token's row, its column's cosines) is then spread over
-    // more bytes.  8192 tokens of 48 heads of 128: 75 us with one head a thread, 41
-    // with four, 34 with eight; with 16 the last wave of 3001 tokens costs 40% more.
-    // Four where codes are stored (38 -> 36 us for the append over E4M3 above).
+    // more bytes.  us with up to one, four, eight and sixteen heads a thread: 8192 tokens
+    // of 48 heads of 128 41, 32.0, 32.4, 33.3; the gradient above 59, 45, 42, 43; the append
+    // of 40 + 2 x 8 heads 48, 40, 38, 40, but the one of 28 + 2 x 4 heads 42, 27, 26, 22.
+    // Four where codes are stored: that append over E4M3 57, 33, 35, 29.
     const int cols = rope_columns(p.D, p.R, kInter, width), most = kRopeThreads / cols;
     const int64_t room = p.T * heads * cols / (2 * (int64_t)num_sms() * kRopeThreads);
     constexpr int kMost = kE4m3 ? 4 : 8;
