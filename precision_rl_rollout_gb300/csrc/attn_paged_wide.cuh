@@ -150,7 +150,7 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
     }
     if (threadIdx.x < RT) s_ref[threadIdx.x] = kNone;
     __syncthreads();
-    pdl_wait_then_release();
+    sm100::grid_dependency_wait();
     if (ring & 1023u) {                                       // as the runtime places it; nothing below would fit
         if (threadIdx.x == 0) atomicCAS(p.err, 0u, (kKernelAttn << 24) | (4u << 16) | 2u);
         return;
@@ -167,6 +167,9 @@ attn_paged_wide_kernel(const __grid_constant__ AttnParams p, const __grid_consta
     }
     __syncthreads();
     sm100::tc_fence_after();
+    // The next kernel may be scheduled only now: one that takes tensor memory before it
+    // waits for this kernel, on an SM that has room for both, would keep it from this one.
+    sm100::grid_launch_dependents();
     const uint32_t tmem = *s_tmem, t_o = tmem + 2 * C::kSlice, t_x = tmem + 3 * C::kSlice;
 
     auto head_of = [&](const Cursor& c) { return chunks == 1 ? c.hr : c.hr / chunks; };

@@ -99,3 +99,23 @@ def test_calls_built_for_another_torch_or_python_are_not_current(built, monkeypa
                 "else:\n"
                 "    raise SystemExit('loaded')\n")
     assert r.returncode == 0, r.stderr
+
+
+def test_tensor_memory_is_taken_before_the_next_kernel_is_let_in():
+    """A kernel that allocates tensor memory after it has let its dependents in can find
+    it taken by one of them, which holds it while it waits for the first to end: neither
+    would.  Read from the sources: the allocation comes first in each such kernel."""
+    import glob
+    import re
+    release = re.compile(r"pdl_wait_then_release\(|pdl_release_then_wait\(|grid_launch_dependents\(")
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(build.CSRC, "*.cu*"))):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for kernel in re.split(r"\n(?:template[^\n]*\n)?__global__", text)[1:]:
+            alloc = kernel.find("tmem_alloc(")
+            if alloc < 0:
+                continue
+            seen += 1
+            first = release.search(kernel)
+            assert first is None or alloc < first.start(), (os.path.basename(path), kernel[:120])
+    assert seen >= 7
