@@ -541,6 +541,90 @@ int fp8rl_spec_verify(const void* P, int64_t p_seq, int64_t p_step, const void* 
                       int32_t* accepted, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Log-probabilities of chosen tokens under the trainer's policy, straight from the
+ * hidden states and the output matrix: what fp8rl_rollout_is_weights takes as
+ * logp_train.  The logits are never written.  For row m with hidden state h_m, target
+ * t = targets[m] and x_v = scale * h_m . w_v (scale: one over the sampling temperature)
+ *   lse[m] = log sum_v exp x_v,  logp[m] = x_t - lse[m],
+ *   entropy[m] = - sum_v p_v log p_v,  p = exp(x - lse).
+ * A row whose target is outside [0, V) (a prompt's, padding) does not count: its
+ * results are 0, whatever the row of H holds (NaN included).
+ * bf16 products, summed in fp32; maxima, sums and results in fp32.  Deterministic.
+ * H  bf16 [M][ldh], W bf16 [V][ldw], ld >= K, ld % 8 == 0, 16-byte aligned.
+ * K  a multiple of 8 (FP8RL_ERR_SHAPE); V any number.
+ * targets int32 [M]; logp, lse fp32 [M]; entropy fp32 [M] or NULL.
+ * scale: finite and > 0 (FP8RL_ERR_UNSUPPORTED).
+ * workspace: at least fp8rl_linear_logp_workspace_bytes(M, V, K) bytes, 16-byte
+ *     aligned, no zeroing, nothing kept between calls; calls in flight at once need
+ *     their own.
+ * Limits: M, V <= 2^21, K <= 65536, ld <= 2^32 (FP8RL_ERR_UNSUPPORTED).
+ * ---------------------------------------------------------------------- */
+size_t fp8rl_linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K);
+int fp8rl_linear_logp(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, const int32_t* targets,
+                      int64_t M, int64_t V, int64_t K, float scale, float* logp, float* lse,
+                      float* entropy_or_null, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient, given that of logp (g) and, optionally, of the entropy (e): with
+ *   D_mv = g_m (d_vt - p_mv) - e_m p_mv (log p_mv + entropy_m)
+ * (0 in rows that do not count), dH = scale * D W and dW = scale * D^T H.
+ * The logits are computed again, a piece of the vocabulary at a time.  D enters the
+ * products as bf16 relative to the largest |g| and |e| of the call (2^-8 of itself);
+ * the sums are fp32 and the gradients are rounded once to bf16.  Deterministic.
+ * lse, entropy fp32 [M]: the forward's (entropy only with g_entropy).
+ * g_logp fp32 [M]; g_entropy fp32 [M] or NULL.
+ * dH bf16 [M][K], dW bf16 [V][K], contiguous, 16-byte aligned; either may be NULL (not
+ *     wanted: a frozen head, a frozen trunk), not both.  Overwritten, not added to.
+ * With M == 0 dW is set to 0.  Everything else as for fp8rl_linear_logp.
+ * ---------------------------------------------------------------------- */
+size_t fp8rl_linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);
+int fp8rl_linear_logp_backward(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
+                               const int32_t* targets, const float* lse, const float* entropy_or_null,
+                               const float* g_logp, const float* g_entropy_or_null, int64_t M, int64_t V,
+                               int64_t K, float scale, uint16_t* dH_or_null, uint16_t* dW_or_null,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Distillation from a teacher's top logits.  Row m has the student's logits x_v and
+ * k entries of the teacher, a token indices[m][i] and its logit T[m][i]; y = scale * x
+ * (scale: one over the temperature), p = softmax(y), lse = log sum exp y.  The teacher's
+ * probabilities q_i are
+ *   softmax_i(scale * T[m][i]) over the entries, without teacher_lse;
+ *   exp(scale * T[m][i] - teacher_lse[m]) with it (the teacher's log-sum over its whole
+ *   vocabulary, at the same scale).
+ *   loss[m] = sum_i q_i (log q_i - log p_i).
+ * With rest_lse (it needs teacher_lse) the tokens outside the entries are one more
+ * class, q_r = max(0, 1 - sum q_i) against their share p_r of the student:
+ *   loss[m] += q_r (log q_r - log p_r),  rest_lse[m] = log sum_outside exp y.
+ * An entry whose token is outside [0, V) is none; a token named twice counts with both
+ * entries.  A row without entries does not count: loss, lse and rest_lse are 0, whatever
+ * its logits are.  Logits of -inf are probabilities of 0.
+ * The loss is put together in 64 bits from fp32 sums, so that it keeps some 1e-7
+ * absolute where the student is close.  Deterministic.
+ * X  fp32 or bf16 (dtype) [M][ldx], ldx >= V, 16-byte aligned, rows of a multiple of
+ *    16 bytes.  indices int32 [M][k], T fp32 [M][k], teacher_lse fp32 [M] or NULL;
+ *    loss, lse fp32 [M], rest_lse fp32 [M] or NULL.
+ * scale: finite and > 0.  Limits: k <= 1024, V <= 2^20, M < 2^31
+ * (FP8RL_ERR_UNSUPPORTED).
+ * ---------------------------------------------------------------------- */
+#define FP8RL_LOGITS_F32 0
+#define FP8RL_LOGITS_BF16 1
+int fp8rl_distill_topk(const void* X, int64_t ldx, int dtype, const int32_t* indices, const float* T,
+                       const float* teacher_lse_or_null, int64_t M, int64_t V, int64_t k, float scale,
+                       float* loss, float* lse, float* rest_lse_or_null, void* stream);
+
+/* Its gradient: with Q = sum q_i (+ q_r),
+ *   dX[m][v] = g_loss[m] * scale * (Q p_v - q_v)                            inside,
+ *   dX[m][v] = g_loss[m] * scale * (Q p_v - q_r exp(y_v - rest_lse[m]))     outside
+ * (without rest_lse no second term there); 0 in rows that do not count.  Computed in
+ * fp32, rounded once to X's type.  lse, rest_lse: the forward's.
+ * dX [M][lddx] of X's type, lddx >= V, aligned as X; it may be X with the same row
+ * pitch, any other overlap is undefined.  Everything else as for fp8rl_distill_topk. */
+int fp8rl_distill_topk_backward(const void* X, int64_t ldx, int dtype, const int32_t* indices, const float* T,
+                                const float* teacher_lse_or_null, const float* lse,
+                                const float* rest_lse_or_null, const float* g_loss, int64_t M, int64_t V,
+                                int64_t k, float scale, void* dX, int64_t lddx, void* stream);
+
+/* ------------------------------------------------------------------------
  * Every wait inside the library's kernels (on an mbarrier filled by TMA or by
  * the tensor core) is bounded.  A wait that runs out records a code in a
  * device-side word, abandons the tile and lets the kernel exit, so the CUDA

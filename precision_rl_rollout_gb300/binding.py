@@ -10,7 +10,8 @@ scales ``torch.float32``.  Outputs that are not passed in are allocated with
 stream of that device unless ``stream`` is given; what a call allocates is then of
 that stream's memory.  No call takes part in autograd, whether or not its inputs
 require a gradient: a training step makes the call of the gradient itself
-(``fp8rl_rope`` with ``inverse=True``).
+(``fp8rl_rope`` with ``inverse=True``, ``fp8rl_linear_logp_backward``,
+``fp8rl_distill_topk_backward``).
 """
 from __future__ import annotations
 
@@ -42,7 +43,9 @@ EXPORTS = ("fp8rl_status_string", "fp8rl_abi_version", "fp8rl_quant_weight_block
            "fp8rl_rollout_is_weights", "fp8rl_logits_kl_workspace_bytes", "fp8rl_logits_kl",
            "fp8rl_rope", "fp8rl_rope_table", "fp8rl_rope_append_paged",
            "fp8rl_attn_paged_workspace_bytes", "fp8rl_attn_paged_kernel_count", "fp8rl_attn_paged",
-           "fp8rl_spec_verify")
+           "fp8rl_spec_verify", "fp8rl_linear_logp_workspace_bytes", "fp8rl_linear_logp",
+           "fp8rl_linear_logp_backward_workspace_bytes", "fp8rl_linear_logp_backward",
+           "fp8rl_distill_topk", "fp8rl_distill_topk_backward")
 
 
 class Fp8rlError(RuntimeError):
@@ -132,11 +135,19 @@ def load(path: str | None = None):
         lib.fp8rl_attn_paged_kernel_count.argtypes = [I] * 6 + [ctypes.c_int]
         lib.fp8rl_attn_paged.argtypes = [P, I, I, I, I, I, I, KV, P, I, P, I, I, F, P, P, P, Z, S]
         lib.fp8rl_spec_verify.argtypes = [P, I, I, P, I, I, ctypes.c_int, P, P, P, P, I, I, I, I, P, P, S]
+        for name in ("fp8rl_linear_logp_workspace_bytes", "fp8rl_linear_logp_backward_workspace_bytes"):
+            getattr(lib, name).restype = Z
+            getattr(lib, name).argtypes = [I, I, I]
+        lib.fp8rl_linear_logp.argtypes = [P, I, P, I, P, I, I, I, F, P, P, P, P, Z, S]
+        lib.fp8rl_linear_logp_backward.argtypes = [P, I, P, I, P, P, P, P, P, I, I, I, F, P, P, P, Z, S]
+        lib.fp8rl_distill_topk.argtypes = [P, I, ctypes.c_int, P, P, P, I, I, I, F, P, P, P, S]
+        lib.fp8rl_distill_topk_backward.argtypes = [P, I, ctypes.c_int, P, P, P, P, P, P, I, I, I, F, P, I, S]
         for name in EXPORTS:
             if name not in ("fp8rl_status_string", "fp8rl_abi_version", "fp8rl_gemm_workspace_bytes",
                             "int8rl_gemm_workspace_bytes", "fp8rl_kv_workspace_bytes",
                             "fp8rl_rollout_is_workspace_bytes", "fp8rl_linear_workspace_bytes",
-                            "fp8rl_logits_kl_workspace_bytes", "fp8rl_attn_paged_workspace_bytes"):
+                            "fp8rl_logits_kl_workspace_bytes", "fp8rl_attn_paged_workspace_bytes",
+                            "fp8rl_linear_logp_workspace_bytes", "fp8rl_linear_logp_backward_workspace_bytes"):
                 getattr(lib, name).restype = ctypes.c_int
 
         _lib = lib
@@ -144,8 +155,8 @@ def load(path: str | None = None):
 
 
 def load_calls():
-    """Load the compiled side of the rollout step's calls.  They load it by themselves
-    at their first use; the other calls do without."""
+    """Load the compiled side of the rollout step's calls and of the trainer's losses.
+    They load it by themselves at their first use; the other calls do without."""
     global _calls
     lib = load()
     with _lock:
@@ -160,6 +171,10 @@ def load_calls():
             module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
                           ("fp8rl_rope", "fp8rl_rope_append_paged", "fp8rl_attn_paged",
                            "fp8rl_attn_paged_workspace_bytes", "fp8rl_spec_verify")), Fp8rlError)
+            module.bind_losses(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                                 ("fp8rl_linear_logp", "fp8rl_linear_logp_workspace_bytes",
+                                  "fp8rl_linear_logp_backward", "fp8rl_linear_logp_backward_workspace_bytes",
+                                  "fp8rl_distill_topk", "fp8rl_distill_topk_backward")))
             _calls = module
         return _calls
 
@@ -605,3 +620,61 @@ def fp8rl_spec_verify(P, drafts, u, noise, Q=None, draft_lens=None, tokens=None,
     if _calls is None:
         load_calls()
     return _calls.spec_verify(P, drafts, u, noise, Q, draft_lens, tokens, accepted, _raw(stream))
+
+
+# ------------------------------------------------------- the trainer's losses and their gradients
+
+def fp8rl_linear_logp_workspace_bytes(M: int, V: int, K: int) -> int:
+    return int(load().fp8rl_linear_logp_workspace_bytes(M, V, K))
+
+
+def fp8rl_linear_logp(H, W, targets, scale: float = 1.0, logp=None, lse=None, entropy=None, want_entropy=False,
+                      workspace=None, stream=None):
+    """H bf16 [M, K] (hidden states), W bf16 [V, K] (output matrix), targets int32 [M] ->
+    (logp fp32 [M], lse fp32 [M]) of the logits scale * H W^T, which are not kept (and
+    entropy fp32 [M] when want_entropy or entropy is given).  Rows whose target is
+    outside [0, V) do not count: their results are 0."""
+    if _calls is None:
+        load_calls()
+    return _calls.linear_logp(H, W, targets, scale, logp, lse, entropy, want_entropy, workspace, _raw(stream))
+
+
+def fp8rl_linear_logp_backward_workspace_bytes(M: int, V: int, K: int) -> int:
+    return int(load().fp8rl_linear_logp_backward_workspace_bytes(M, V, K))
+
+
+def fp8rl_linear_logp_backward(H, W, targets, lse, g_logp, entropy=None, g_entropy=None, scale: float = 1.0, dH=None,
+                               dW=None, want_dH=True, want_dW=True, workspace=None, stream=None):
+    """The gradient of fp8rl_linear_logp, given that of logp (g_logp fp32 [M]) and, with
+    the forward's entropy, of the entropy (g_entropy fp32 [M]) -> (dH bf16 [M, K] or
+    None, dW bf16 [V, K] or None); one not wanted is None."""
+    if _calls is None:
+        load_calls()
+    return _calls.linear_logp_backward(H, W, targets, lse, g_logp, entropy, g_entropy, scale, dH, dW, want_dH, want_dW,
+                                       workspace, _raw(stream))
+
+
+FP8RL_LOGITS_F32 = 0
+FP8RL_LOGITS_BF16 = 1
+
+
+def fp8rl_distill_topk(X, indices, T, teacher_lse=None, rest=False, scale: float = 1.0, loss=None, lse=None,
+                       rest_lse=None, stream=None):
+    """X fp32 or bf16 [M, V] (student's logits, rows a multiple of 16 bytes apart),
+    indices int32 [M, k] and T fp32 [M, k] (the teacher's tokens and their logits),
+    teacher_lse fp32 [M] (its log-sum over the whole vocabulary; None: its distribution
+    is cut to the entries) -> (loss fp32 [M], lse fp32 [M]) and, when rest or rest_lse is
+    given, rest_lse fp32 [M]: the tokens outside the entries count as one more class."""
+    if _calls is None:
+        load_calls()
+    return _calls.distill_topk(X, indices, T, teacher_lse, rest, scale, loss, lse, rest_lse, _raw(stream))
+
+
+def fp8rl_distill_topk_backward(X, indices, T, lse, g_loss, teacher_lse=None, rest_lse=None, scale: float = 1.0,
+                                dX=None, stream=None):
+    """The gradient of fp8rl_distill_topk with respect to X, given that of the loss
+    (g_loss fp32 [M]) and the forward's lse and rest_lse -> dX of X's type and shape
+    (rows padded to 16 bytes unless given).  dX may be X."""
+    if _calls is None:
+        load_calls()
+    return _calls.distill_topk_backward(X, indices, T, lse, g_loss, teacher_lse, rest_lse, scale, dX, _raw(stream))

@@ -451,6 +451,108 @@ int fp8rl_spec_verify(const void* P, int64_t p_seq, int64_t p_step, const void* 
     return cuda_status(launch_spec_verify(p, !f32, as_stream(stream)));
 }
 
+// Checks that the forward and the backward of fp8rl_linear_logp share.
+static int check_linear_logp(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, const int32_t* targets,
+                             int64_t M, int64_t V, int64_t K, float scale) {
+    if (M < 0 || V <= 0 || K <= 0 || K % 8 || ldh < K || ldw < K) return FP8RL_ERR_SHAPE;
+    if (!W || (M > 0 && (!H || !targets))) return FP8RL_ERR_NULL;
+    if (!aligned16(H) || !aligned16(W) || ldh % 8 || ldw % 8 || !aligned4(targets)) return FP8RL_ERR_ALIGN;
+    if (M > (1 << 21) || V > (1 << 21) || K > (1 << 16) || ldh > (1ll << 32) || ldw > (1ll << 32) || !(scale > 0.f) ||
+        scale > 3e38f)
+        return FP8RL_ERR_UNSUPPORTED;
+    return FP8RL_OK;
+}
+
+size_t fp8rl_linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+    return linear_logp_workspace_bytes(M, V, K);
+}
+
+int fp8rl_linear_logp(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, const int32_t* targets,
+                      int64_t M, int64_t V, int64_t K, float scale, float* logp, float* lse, float* entropy_or_null,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = check_linear_logp(H, ldh, W, ldw, targets, M, V, K, scale);
+    if (rc) return rc;
+    if (M > 0 && (!logp || !lse)) return FP8RL_ERR_NULL;
+    if (!aligned4(logp) || !aligned4(lse) || !aligned4(entropy_or_null) || !aligned16(workspace)) return FP8RL_ERR_ALIGN;
+    const size_t need = linear_logp_workspace_bytes(M, V, K);
+    if (workspace_bytes < need || (need && !workspace)) return FP8RL_ERR_WORKSPACE;
+    if (M == 0) return FP8RL_OK;
+    LogpParams p{};
+    p.H = H, p.W = W, p.targets = targets, p.logp = logp, p.lse = lse, p.entropy = entropy_or_null;
+    p.M = M, p.V = V, p.K = K, p.ldh = ldh, p.ldw = ldw, p.scale = scale;
+    return cuda_status(launch_linear_logp(p, workspace, as_stream(stream)));
+}
+
+size_t fp8rl_linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+    return linear_logp_backward_workspace_bytes(M, V, K);
+}
+
+int fp8rl_linear_logp_backward(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, const int32_t* targets,
+                               const float* lse, const float* entropy_or_null, const float* g_logp,
+                               const float* g_entropy_or_null, int64_t M, int64_t V, int64_t K, float scale,
+                               uint16_t* dH_or_null, uint16_t* dW_or_null, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    const int rc = check_linear_logp(H, ldh, W, ldw, targets, M, V, K, scale);
+    if (rc) return rc;
+    if ((!dH_or_null && !dW_or_null) || (M > 0 && (!lse || !g_logp)) || (g_entropy_or_null && !entropy_or_null))
+        return FP8RL_ERR_NULL;
+    if (!aligned4(lse) || !aligned4(entropy_or_null) || !aligned4(g_logp) || !aligned4(g_entropy_or_null) ||
+        !aligned16(dH_or_null) || !aligned16(dW_or_null) || !aligned16(workspace))
+        return FP8RL_ERR_ALIGN;
+    const size_t need = linear_logp_backward_workspace_bytes(M, V, K);
+    if (workspace_bytes < need || (need && !workspace)) return FP8RL_ERR_WORKSPACE;
+    LogpParams p{};
+    p.H = H, p.W = W, p.targets = targets, p.lse = const_cast<float*>(lse), p.entropy = const_cast<float*>(entropy_or_null);
+    p.g = g_logp, p.ge = g_entropy_or_null, p.dH = dH_or_null, p.dW = dW_or_null;
+    p.M = M, p.V = V, p.K = K, p.ldh = ldh, p.ldw = ldw, p.scale = scale;
+    return cuda_status(launch_linear_logp_backward(p, workspace, as_stream(stream)));
+}
+
+// Checks that the forward and the backward of fp8rl_distill_topk share.
+static int check_distill(const void* X, int64_t ldx, int dtype, const int32_t* indices, const float* T,
+                         const float* teacher_lse, int64_t M, int64_t V, int64_t k, float scale, const float* lse,
+                         const float* rest_lse) {
+    if (M < 0 || V <= 0 || k <= 0 || ldx < V) return FP8RL_ERR_SHAPE;
+    if (dtype != FP8RL_LOGITS_F32 && dtype != FP8RL_LOGITS_BF16) return FP8RL_ERR_UNSUPPORTED;
+    if ((M > 0 && (!X || !indices || !T || !lse)) || (rest_lse && !teacher_lse && M > 0)) return FP8RL_ERR_NULL;
+    if (!aligned16(X) || ldx % (dtype == FP8RL_LOGITS_F32 ? 4 : 8) || !aligned4(indices) || !aligned4(T) ||
+        !aligned4(teacher_lse) || !aligned4(lse) || !aligned4(rest_lse))
+        return FP8RL_ERR_ALIGN;
+    if (M > INT32_MAX || V > (1 << 20) || k > 1024 || !(scale > 0.f) || scale > 3e38f) return FP8RL_ERR_UNSUPPORTED;
+    return FP8RL_OK;
+}
+
+int fp8rl_distill_topk(const void* X, int64_t ldx, int dtype, const int32_t* indices, const float* T,
+                       const float* teacher_lse_or_null, int64_t M, int64_t V, int64_t k, float scale, float* loss,
+                       float* lse, float* rest_lse_or_null, void* stream) {
+    const int rc = check_distill(X, ldx, dtype, indices, T, teacher_lse_or_null, M, V, k, scale, lse, rest_lse_or_null);
+    if (rc) return rc;
+    if (M > 0 && !loss) return FP8RL_ERR_NULL;
+    if (!aligned4(loss)) return FP8RL_ERR_ALIGN;
+    if (M == 0) return FP8RL_OK;
+    DistillParams p{};
+    p.X = X, p.ids = indices, p.t = T, p.teacher_lse = teacher_lse_or_null, p.loss = loss, p.lse = lse;
+    p.rest_lse = rest_lse_or_null, p.M = M, p.V = V, p.ldx = ldx, p.k = (int)k, p.scale = scale;
+    return cuda_status(launch_distill_topk(p, dtype == FP8RL_LOGITS_BF16, false, as_stream(stream)));
+}
+
+int fp8rl_distill_topk_backward(const void* X, int64_t ldx, int dtype, const int32_t* indices, const float* T,
+                                const float* teacher_lse_or_null, const float* lse, const float* rest_lse_or_null,
+                                const float* g_loss, int64_t M, int64_t V, int64_t k, float scale, void* dX,
+                                int64_t lddx, void* stream) {
+    const int rc = check_distill(X, ldx, dtype, indices, T, teacher_lse_or_null, M, V, k, scale, lse, rest_lse_or_null);
+    if (rc) return rc;
+    if (lddx < V || (dX == X && M > 0 && lddx != ldx)) return FP8RL_ERR_SHAPE;
+    if (M > 0 && (!g_loss || !dX)) return FP8RL_ERR_NULL;
+    if (!aligned4(g_loss) || !aligned16(dX) || lddx % (dtype == FP8RL_LOGITS_F32 ? 4 : 8)) return FP8RL_ERR_ALIGN;
+    if (M == 0) return FP8RL_OK;
+    DistillParams p{};
+    p.X = X, p.ids = indices, p.t = T, p.teacher_lse = teacher_lse_or_null, p.g = g_loss;
+    p.lse = const_cast<float*>(lse), p.rest_lse = const_cast<float*>(rest_lse_or_null), p.dX = dX;
+    p.M = M, p.V = V, p.ldx = ldx, p.lddx = lddx, p.k = (int)k, p.scale = scale;
+    return cuda_status(launch_distill_topk(p, dtype == FP8RL_LOGITS_BF16, true, as_stream(stream)));
+}
+
 int fp8rl_check_device_error(uint32_t* detail) {
     uint32_t w = 0;
     cudaError_t e = read_and_clear_device_error(&w);

@@ -1,5 +1,6 @@
 // calls.cpp -- the rollout step's calls (rotary positions, the append, paged
-// attention, verification) from torch tensors to the C ABI, as a Python module.
+// attention, verification) and the trainer's losses (log-probabilities from hidden
+// states, distillation) from torch tensors to the C ABI, as a Python module.
 // A decode step makes these calls with a few microseconds of GPU work behind each;
 // checked and marshalled in Python they took 11 to 23 us of host time, here 4 to
 // 11 (Grace; the launches themselves are 3 to 6 of it).  Everything they refuse is
@@ -29,6 +30,12 @@ struct Functions {
     decltype(&fp8rl_attn_paged) attn_paged;
     decltype(&fp8rl_attn_paged_workspace_bytes) attn_workspace;
     decltype(&fp8rl_spec_verify) spec_verify;
+    decltype(&fp8rl_linear_logp) linear_logp;
+    decltype(&fp8rl_linear_logp_workspace_bytes) linear_logp_workspace;
+    decltype(&fp8rl_linear_logp_backward) linear_logp_backward;
+    decltype(&fp8rl_linear_logp_backward_workspace_bytes) linear_logp_backward_workspace;
+    decltype(&fp8rl_distill_topk) distill_topk;
+    decltype(&fp8rl_distill_topk_backward) distill_topk_backward;
 } fn = {};
 PyObject* status_error = nullptr;                 // binding.Fp8rlError
 
@@ -315,12 +322,184 @@ PyObject* spec_verify(PyObject* const* a) {
     return Py_BuildValue("(NN)", THPVariable_Wrap(tokens), THPVariable_Wrap(accepted));
 }
 
+// ------------------------------------------------------------------ the trainer's losses
+
+double number(PyObject* o, const char* name) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        throw std::invalid_argument(std::string(name) + ": expected a number");
+    }
+    return v;
+}
+// A matrix with contiguous rows.
+void matrix(const Tensor& t, at::ScalarType type, int64_t cols, c10::Device dev, const char* name) {
+    if (t.scalar_type() != type || t.dim() != 2 || t.device() != dev || (cols >= 0 && t.size(1) != cols) ||
+        (t.stride(1) != 1 && t.size(1) > 1)) {
+        std::ostringstream s;
+        s << type << " [rows, " << (cols >= 0 ? std::to_string(cols) : std::string("columns"))
+          << "] with contiguous rows on " << dev;
+        refuse(name, t, s.str());
+    }
+}
+// Its row pitch; a single row's stride says nothing.
+int64_t pitch(const Tensor& t, int64_t multiple) {
+    return t.size(0) > 1 ? t.stride(0) : (t.size(1) + multiple - 1) / multiple * multiple;
+}
+const float* vector_or_null(PyObject* o, int64_t n, c10::Device dev, const char* name) {
+    if (o == Py_None) return nullptr;
+    const Tensor& t = tensor(o, name);
+    dense(t, at::kFloat, {n}, dev, name);
+    return ptr<float>(t);
+}
+Tensor scratch(PyObject* o, size_t need, const Tensor& like) {
+    if (o != Py_None) {
+        const Tensor& t = tensor(o, "workspace");
+        if (t.device() != like.device() || !t.is_contiguous())
+            refuse("workspace", t, "a contiguous tensor on the call's device");
+        return t;
+    }
+    return at::empty({(int64_t)need}, like.options().dtype(at::kByte));
+}
+
+struct Head {                                     // hidden states, output matrix, targets
+    const Tensor &H, &W, &targets;
+    int64_t M, V, K;
+    c10::Device dev;
+    explicit Head(PyObject* const* a)
+        : H(tensor(a[0], "H")), W(tensor(a[1], "W")), targets(tensor(a[2], "targets")), dev(cuda_device(H, "H")) {
+        matrix(H, at::kBFloat16, -1, dev, "H");
+        matrix(W, at::kBFloat16, H.size(1), dev, "W");
+        M = H.size(0), K = H.size(1), V = W.size(0);
+        dense(targets, at::kInt, {M}, dev, "targets");
+    }
+};
+
+// H, W, targets, scale, logp, lse, entropy, want_entropy, workspace, stream
+PyObject* linear_logp(PyObject* const* a) {
+    const Head h(a);
+    const float scale = (float)number(a[3], "scale");
+    const Launch launch(a[9], h.dev);
+    const Tensor logp = output(launch, a[4], {h.M}, at::kFloat, h.H, "logp");
+    const Tensor lse = output(launch, a[5], {h.M}, at::kFloat, h.H, "lse");
+    Tensor entropy;
+    if (a[6] != Py_None || truth(a[7])) entropy = output(launch, a[6], {h.M}, at::kFloat, h.H, "entropy");
+    const Tensor ws = scratch(a[8], fn.linear_logp_workspace(h.M, h.V, h.K), h.H);
+    const int rc = unlocked(fn.linear_logp, ptr<uint16_t>(h.H), pitch(h.H, 8), ptr<uint16_t>(h.W), pitch(h.W, 8),
+                            ptr<int32_t>(h.targets), h.M, h.V, h.K, scale, ptr<float>(logp), ptr<float>(lse),
+                            entropy.defined() ? ptr<float>(entropy) : nullptr, ws.data_ptr(), ws.nbytes(),
+                            launch.stream());
+    if (rc) throw Status{rc, "fp8rl_linear_logp"};
+    if (!entropy.defined()) return Py_BuildValue("(NN)", THPVariable_Wrap(logp), THPVariable_Wrap(lse));
+    return Py_BuildValue("(NNN)", THPVariable_Wrap(logp), THPVariable_Wrap(lse), THPVariable_Wrap(entropy));
+}
+
+// H, W, targets, lse, g_logp, entropy, g_entropy, scale, dH, dW, want_dH, want_dW, workspace, stream
+PyObject* linear_logp_backward(PyObject* const* a) {
+    const Head h(a);
+    const Tensor &lse = tensor(a[3], "lse"), &g = tensor(a[4], "g_logp");
+    dense(lse, at::kFloat, {h.M}, h.dev, "lse");
+    dense(g, at::kFloat, {h.M}, h.dev, "g_logp");
+    const float* entropy = vector_or_null(a[5], h.M, h.dev, "entropy");
+    const float* ge = vector_or_null(a[6], h.M, h.dev, "g_entropy");
+    if (a[6] != Py_None && a[5] == Py_None)
+        throw std::invalid_argument("g_entropy: the gradient of the entropy needs the forward's entropy");
+    const float scale = (float)number(a[7], "scale");
+    const Launch launch(a[13], h.dev);
+    Tensor dH, dW;
+    if (a[8] != Py_None || truth(a[10])) dH = output(launch, a[8], {h.M, h.K}, at::kBFloat16, h.H, "dH");
+    if (a[9] != Py_None || truth(a[11])) dW = output(launch, a[9], {h.V, h.K}, at::kBFloat16, h.H, "dW");
+    if (!dH.defined() && !dW.defined()) throw std::invalid_argument("neither dH nor dW is wanted");
+    const Tensor ws = scratch(a[12], fn.linear_logp_backward_workspace(h.M, h.V, h.K), h.H);
+    const int rc = unlocked(fn.linear_logp_backward, ptr<uint16_t>(h.H), pitch(h.H, 8), ptr<uint16_t>(h.W),
+                            pitch(h.W, 8), ptr<int32_t>(h.targets), ptr<float>(lse), entropy, ptr<float>(g), ge, h.M,
+                            h.V, h.K, scale, dH.defined() ? ptr<uint16_t>(dH) : nullptr,
+                            dW.defined() ? ptr<uint16_t>(dW) : nullptr, ws.data_ptr(), ws.nbytes(), launch.stream());
+    if (rc) throw Status{rc, "fp8rl_linear_logp_backward"};
+    auto wrap = [](const Tensor& t) {
+        if (t.defined()) return THPVariable_Wrap(t);
+        Py_INCREF(Py_None);
+        return Py_None;
+    };
+    return Py_BuildValue("(NN)", wrap(dH), wrap(dW));
+}
+
+struct Logits {                                   // a student's logits and a teacher's entries
+    const Tensor &X, &indices, &T;
+    int64_t M, V, k, multiple;
+    int dtype;
+    c10::Device dev;
+    explicit Logits(PyObject* const* a)
+        : X(tensor(a[0], "X")), indices(tensor(a[1], "indices")), T(tensor(a[2], "T")), dev(cuda_device(X, "X")) {
+        if (X.scalar_type() != at::kFloat && X.scalar_type() != at::kBFloat16)
+            refuse("X", X, "float32 or bfloat16 logits");
+        matrix(X, X.scalar_type(), -1, dev, "X");
+        M = X.size(0), V = X.size(1);
+        if (indices.dim() != 2) refuse("indices", indices, "int32 [M, k]");
+        k = indices.size(1);
+        dense(indices, at::kInt, {M, k}, dev, "indices");
+        dense(T, at::kFloat, {M, k}, dev, "T");
+        dtype = X.scalar_type() == at::kFloat ? FP8RL_LOGITS_F32 : FP8RL_LOGITS_BF16;
+        multiple = X.scalar_type() == at::kFloat ? 4 : 8;
+    }
+};
+
+// X, indices, T, teacher_lse, rest, scale, loss, lse, rest_lse, stream
+PyObject* distill_topk(PyObject* const* a) {
+    const Logits x(a);
+    const float* teacher = vector_or_null(a[3], x.M, x.dev, "teacher_lse");
+    const bool rest = a[8] != Py_None || truth(a[4]);
+    if (rest && a[3] == Py_None) throw std::invalid_argument("rest: what the entries leave needs teacher_lse");
+    const float scale = (float)number(a[5], "scale");
+    const Launch launch(a[9], x.dev);
+    const Tensor loss = output(launch, a[6], {x.M}, at::kFloat, x.X, "loss");
+    const Tensor lse = output(launch, a[7], {x.M}, at::kFloat, x.X, "lse");
+    Tensor rest_lse;
+    if (rest) rest_lse = output(launch, a[8], {x.M}, at::kFloat, x.X, "rest_lse");
+    const int rc = unlocked(fn.distill_topk, x.X.data_ptr(), pitch(x.X, x.multiple), x.dtype, ptr<int32_t>(x.indices),
+                            ptr<float>(x.T), teacher, x.M, x.V, x.k, scale, ptr<float>(loss), ptr<float>(lse),
+                            rest ? ptr<float>(rest_lse) : nullptr, launch.stream());
+    if (rc) throw Status{rc, "fp8rl_distill_topk"};
+    if (!rest) return Py_BuildValue("(NN)", THPVariable_Wrap(loss), THPVariable_Wrap(lse));
+    return Py_BuildValue("(NNN)", THPVariable_Wrap(loss), THPVariable_Wrap(lse), THPVariable_Wrap(rest_lse));
+}
+
+// X, indices, T, lse, g_loss, teacher_lse, rest_lse, scale, dX, stream
+PyObject* distill_topk_backward(PyObject* const* a) {
+    const Logits x(a);
+    const Tensor &lse = tensor(a[3], "lse"), &g = tensor(a[4], "g_loss");
+    dense(lse, at::kFloat, {x.M}, x.dev, "lse");
+    dense(g, at::kFloat, {x.M}, x.dev, "g_loss");
+    const float* teacher = vector_or_null(a[5], x.M, x.dev, "teacher_lse");
+    const float* rest = vector_or_null(a[6], x.M, x.dev, "rest_lse");
+    if (a[6] != Py_None && a[5] == Py_None) throw std::invalid_argument("rest_lse: what the entries leave needs teacher_lse");
+    const float scale = (float)number(a[7], "scale");
+    const Launch launch(a[9], x.dev);
+    Tensor dX;
+    if (a[8] == Py_None) {                        // rows padded to whole 16 bytes
+        const int64_t cols = (x.V + x.multiple - 1) / x.multiple * x.multiple;
+        dX = launch.empty({x.M, cols}, x.X.options());
+        if (cols != x.V) dX = dX.narrow(1, 0, x.V);
+    } else {
+        dX = tensor(a[8], "dX");
+        matrix(dX, x.X.scalar_type(), x.V, x.dev, "dX");
+        if (dX.size(0) != x.M) refuse("dX", dX, "X's shape");
+    }
+    const int rc = unlocked(fn.distill_topk_backward, x.X.data_ptr(), pitch(x.X, x.multiple), x.dtype,
+                            ptr<int32_t>(x.indices), ptr<float>(x.T), teacher, ptr<float>(lse), rest, ptr<float>(g),
+                            x.M, x.V, x.k, scale, dX.data_ptr(), pitch(dX, x.multiple), launch.stream());
+    if (rc) throw Status{rc, "fp8rl_distill_topk_backward"};
+    return THPVariable_Wrap(dX);
+}
+
 // No C++ exception passes into Python.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     try {
         if (n != N) throw std::invalid_argument("expected " + std::to_string(N) + " arguments");
-        if (!status_error) throw std::runtime_error("bind() has not been called");
+        if (!status_error || !fn.distill_topk_backward && (F == linear_logp || F == linear_logp_backward ||
+                                                           F == distill_topk || F == distill_topk_backward))
+            throw std::runtime_error("bind() has not been called");
         return F(args);
     } catch (const Status& s) {
         if (PyObject* e = PyObject_CallFunction(status_error, "is", s.rc, s.where)) {
@@ -350,13 +529,30 @@ PyObject* bind(PyObject*, PyObject* args) {
     Py_RETURN_NONE;
 }
 
+// Addresses of fp8rl_linear_logp, its workspace query, _backward, its query, fp8rl_distill_topk, _backward
+PyObject* bind_losses(PyObject*, PyObject* args) {
+    unsigned long long f[6];
+    if (!PyArg_ParseTuple(args, "KKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5])) return nullptr;
+    fn.linear_logp = reinterpret_cast<decltype(fn.linear_logp)>(f[0]);
+    fn.linear_logp_workspace = reinterpret_cast<decltype(fn.linear_logp_workspace)>(f[1]);
+    fn.linear_logp_backward = reinterpret_cast<decltype(fn.linear_logp_backward)>(f[2]);
+    fn.linear_logp_backward_workspace = reinterpret_cast<decltype(fn.linear_logp_backward_workspace)>(f[3]);
+    fn.distill_topk = reinterpret_cast<decltype(fn.distill_topk)>(f[4]);
+    fn.distill_topk_backward = reinterpret_cast<decltype(fn.distill_topk_backward)>(f[5]);
+    Py_RETURN_NONE;
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyMethodDef fast(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, N>)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {fast<rope, 7>("rope"), fast<rope_append_paged, 13>("rope_append_paged"),
                          fast<attn_paged, 15>("attn_paged"), fast<spec_verify, 9>("spec_verify"),
-                         {"bind", bind, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
+                         fast<linear_logp, 10>("linear_logp"),
+                         fast<linear_logp_backward, 14>("linear_logp_backward"),
+                         fast<distill_topk, 10>("distill_topk"),
+                         fast<distill_topk_backward, 10>("distill_topk_backward"),
+                         {"bind", bind, METH_VARARGS, nullptr}, {"bind_losses", bind_losses, METH_VARARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -113,6 +113,39 @@ struct VerifyParams {
 };
 cudaError_t launch_spec_verify(const VerifyParams& p, bool bf16, cudaStream_t st);
 
+// Log-probabilities of chosen tokens from hidden states and output matrix, and their
+// gradient (strides in elements).
+struct LogpParams {
+    const uint16_t *H, *W;
+    const int32_t* targets;
+    float *logp, *lse, *entropy;      // the forward's results; the backward reads lse and entropy
+    const float *g, *ge;
+    uint16_t *dH, *dW;
+    int64_t M, V, K, ldh, ldw;
+    float scale;
+    // in the workspace, set by the launchers
+    float *part, *picked, *largest, *acc;
+    uint16_t* D;
+    int64_t piece;
+};
+size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K);
+size_t linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);
+cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st);
+cudaError_t launch_linear_logp_backward(LogpParams p, void* ws, cudaStream_t st);
+
+// Distillation from a teacher's top logits, and its gradient (strides in elements).
+struct DistillParams {
+    const void* X;
+    const int32_t* ids;
+    const float *t, *teacher_lse, *g;
+    float *loss, *lse, *rest_lse;     // the forward's results; the backward reads lse and rest_lse
+    void* dX;
+    int64_t M, V, ldx, lddx;
+    int k;
+    float scale;
+};
+cudaError_t launch_distill_topk(const DistillParams& p, bool bf16, bool backward, cudaStream_t st);
+
 // FP8 block-scaled GEMM: dispatch by M (tcgen05 decode kernel for M <= 256).
 // weights_stable: the kernel immediately preceding the call in the stream did
 // not write Wq, so small weights may start streaming before the dependency wait.
