@@ -123,10 +123,20 @@ struct LogpParams {
     uint16_t *dH, *dW;
     int64_t M, V, K, ldh, ldw;
     float scale;
-    // in the workspace, set by the launchers
-    float *part, *picked, *largest, *acc;
-    uint16_t* D;
+    // in the workspace, laid out by the launchers: rows that count, their targets, hidden
+    // states and gradients, one behind the other
+    int *live, *row_of, *row_target;
+    float *row_g, *row_ge, *row_lse, *row_entropy, *largest;
+    uint16_t* rows_h;
+    float *part, *picked;             // forward: each tile's sums of a row, the targets' logits
+    uint16_t* D;                      // backward: a piece's D [rows_pad][piece], dH's fp32 sums [split][rows_pad][K]
+    float* acc;
     int64_t piece;
+    uint32_t* err;
+    int rows_pad, split;
+    // set by the launchers: tiles of the vocabulary, steps of the reduction over K and over
+    // the piece, tiles of K, row tiles a group, the piece's first row of W
+    int tiles, ksteps, steps, ktiles, group, first;
 };
 size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K);
 size_t linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);
@@ -222,6 +232,10 @@ bool make_tmap_f32_store(CUtensorMap* m, const void* base, uint64_t rows, uint64
 // fp16 [rows][cols] row-major (cols % 8 == 0), loaded in boxes of box_rows x 64
 // with the 128-byte swizzle (one UMMA K-major atom of fp16).
 bool make_tmap_f16_load(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// bf16 [rows][cols] row-major (row pitch in elements), loaded in boxes of box_rows x 64
+// with the 128-byte swizzle, zero fill out of range.
+bool make_tmap_bf16_load(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch_elems,
+                         uint32_t box_rows);
 // 4-D map of 8- or 16-bit values for loads of boxes whose rows are `swizzle` (64 or
 // 128) bytes, stored with that swizzle; zero fill out of range.  strides: bytes of
 // dimensions 1 .. 3.

@@ -6,242 +6,843 @@
 //   D_mv = g_m (d_vt - p_mv) - e_m p_mv (log p_mv + entropy_m),
 //   dH = scale D W,   dW = scale D^T H.
 //
-// Forward: tiles of logits, of which each row leaves its maximum, its sum of exponentials
-// and sum of weighted differences; a second launch joins a row's tiles.  Backward: the
-// vocabulary in pieces; a piece's D as bf16 (each D rounded once, relative to the call's
-// largest g or e, to 2^-9 of itself), then its part of dH, summed in fp32 over the pieces, and its rows of dW.
+// Rows that count are brought together first (rows_kernel): prompts and padding take no
+// part in the products, and what they hold reaches nothing.
+//
+// All products are tiles of 256 x 256 by a pair of CTAs (tcgen05.mma.cta_group::2, bf16,
+// sums in tensor memory, fp32): each CTA stages 128 rows of either operand, 64 of the
+// reduction a stage, six stages, and has 128 of the tile's rows in its tensor memory, two
+// tiles of them, so that one tile's threads' part runs under the next one's products.
+//
+// Forward (kLogp): tile by tile each row leaves its maximum, its sum of exponentials and
+// of weighted differences (12 bytes for 256 logits); logp_join_kernel joins a row's tiles.
+// Backward: the vocabulary in pieces, two launches each.  kGrad writes a piece's D as bf16
+// (rounded once, relative to the call's largest |g| and |e|: a mean's gradient, 1/n
+// everywhere, is then exact); kBack multiplies it with W's rows (D as it lies, W with the
+// reduction outside: MN-major) into fp32 sums of dH that the pieces add to, and its
+// transpose with H (both MN-major) into the piece's rows of dW.  Nothing is transposed in
+// memory, and each sum of dH is added to once a launch, so results do not depend on order.
 #include <math.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
+#include "sm100_ptx.cuh"
 
 namespace fp8rl {
 
+using namespace sm100;
+
 namespace {
 
-constexpr int kTile = 64, kDepth = 16, kThreads = 256;
+constexpr uint32_t kKernelLogp = 10;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eRest = 1.9259629911266175e-8f;   // log2(e) - kLog2e
 
-struct Tile {
-    float a[kDepth][kTile + 4], b[kDepth][kTile + 4];
+constexpr int kTile = 256, kHalf = 128, kStep = 64;     // a pair's tile, a CTA's share, the reduction a stage
+constexpr int kStages = 6;
+constexpr int kPiece = 64 * 128;                        // 64 rows of 64 values, as the copy engine lays them
+constexpr int kStageBytes = 4 * kPiece;                 // two pieces of either operand
+constexpr int kEpiWarps = 4, kThreads = 32 * (4 + kEpiWarps);
+constexpr int kOutBytes = 32 * 128;                     // a warp's staging
+constexpr int kOutOffset = kStages * kStageBytes, kBarOffset = kOutOffset + kEpiWarps * kOutBytes;
+constexpr int kSmemBytes = kBarOffset + 256 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+enum Mode { kLogp, kGrad, kBack };
+
+// ------------------------------------------------------------------ pairs of CTAs
+
+// A 64 x 64 box into this CTA's shared memory, counted on the barrier of the pair's first CTA.
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(pol)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs, once the products so far are done.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void pair_arrive(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+// An operand of two pieces with the reduction outside (MN-major): 16 of the reduction are
+// 2048 bytes on, the next 64 values a piece.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(kPiece >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// bf16 x bf16 -> fp32, 256 x 256; bits 15 and 16: A, B are MN-major
+constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (kTile >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+struct Maps {
+    CUtensorMap h, w, d, d_out, acc, dw;
 };
 
-__device__ __forceinline__ float bf(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+// ------------------------------------------------------------------ the work
 
-// c[i][j] += sum_k A(row0 + 16 i + ty, k) B(col0 + 16 j + tx, k), values past the edges zero.
-template <typename FA, typename FB>
-__device__ __forceinline__ void multiply(Tile& s, int64_t K, FA A, FB B, float (&c)[4][4]) {
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t k0 = 0; k0 < K; k0 += kDepth) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < kTile * kDepth; e += kThreads) {
-            const int r = e / kDepth, d = e % kDepth;
-            s.a[d][r] = k0 + d < K ? A(r, k0 + d) : 0.f;
-            s.b[d][r] = k0 + d < K ? B(r, k0 + d) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) c[i][j] = fmaf(s.a[d][16 * i + ty], s.b[d][16 * j + tx], c[i][j]);
+// A tile: rows a of the first operand, rows b of the second, steps [k, k + n) of 64 of
+// the reduction.
+struct Unit {
+    int kind;           // 0: logits, 1: dH, 2: dW
+    int a, b, k, n, slot;
+};
+
+// Tile order of the logits: groups of row tiles whose H stays in L2; in a group the row
+// tile runs fastest, so that a tile of W is read by all of them while it is there.
+__device__ __forceinline__ void tile_of(int u, int rows, int cols, int group, int& r, int& c) {
+    const int g = u / (group * cols), left = u - g * group * cols, here = min(group, rows - g * group);
+    c = left / here;
+    r = g * group + left % here;
+}
+
+template <Mode kMode>
+struct Work {
+    const LogpParams& p;
+    int rows, live, pair, pairs, i;
+
+    __device__ __forceinline__ Work(const LogpParams& p_) : p(p_), i(0) {
+        live = *p.live;
+        rows = (live + kTile - 1) / kTile;
+        pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     }
+    __device__ __forceinline__ bool next(Unit& u) {
+        if constexpr (kMode != kBack) {
+            const int at = pair + i++ * pairs;
+            if (at >= rows * p.tiles) return false;
+            int r, c;
+            const int groups = (rows + p.group - 1) / p.group;
+            tile_of(at, rows, p.tiles, (rows + groups - 1) / max(groups, 1), r, c);
+            u = Unit{0, r * kTile, c * kTile, 0, p.ksteps, c};
+            return true;
+        } else {
+            // dH's units in turn, then dW's: pairs that have one unit of dH less take as
+            // many of dW as last as long first, the others follow in turn
+            const int kt = p.ktiles;
+            const int nh = p.dH ? rows * kt * p.split : 0, nw = p.dW ? p.tiles * kt : 0;
+            int at = pair + i * pairs;
+            if (at < nh) {
+                ++i;
+                const int s = at / (rows * kt), t = at - s * rows * kt;
+                const int k = s * p.steps / p.split, end = (s + 1) * p.steps / p.split;
+                u = Unit{1, t / kt * kTile, t % kt * kTile, k, end - k, s};
+                return true;
+            }
+            const int full = (nh + pairs - 1 - pair) / pairs, wsteps = (live + kStep - 1) / kStep;
+            const int j = i - full;                                                       // the how manieth of dW's
+            const int r = nh % pairs, extra = r && wsteps ? (p.steps / p.split + wsteps / 2) / wsteps : 0;
+            const int head = extra * (pairs - r);
+            if (pair >= r && extra) {
+                const int w = pair - r + j * (pairs - r);
+                if (j < extra) {
+                    if (w >= nw) return false;
+                    at = w;
+                } else {
+                    at = head + pair + (j - extra) * pairs;
+                }
+            } else {
+                at = head + pair + j * pairs;
+            }
+            if (at >= nw) return false;
+            ++i;
+            u = Unit{2, at / kt * kTile, at % kt * kTile, 0, wsteps, 0};
+            return true;
+        }
+    }
+};
+
+// ------------------------------------------------------------------ a tile's threads' part
+
+// The running maximum of a row and its sums, of the unscaled logits: sum of exp(scale (x - top))
+// and of that times (x - top).
+struct Sums {
+    float top = -3.0e38f, sum = 0.f, dev = 0.f;
+};
+// exp(scale d), the constant in two parts: its rounding alone would be a change of temperature
+__device__ __forceinline__ float exp_scaled(float d, float c, float c_rest) { return ex2(fmaf(d, c, d * c_rest)); }
+
+__device__ __forceinline__ void add_sums(Sums& s, float top, float sum, float dev, float c, float c_rest) {
+    const float t = fmaxf(s.top, top);
+    const float d0 = s.top - t, d1 = top - t, f0 = exp_scaled(d0, c, c_rest), f1 = exp_scaled(d1, c, c_rest);
+    s.dev = fmaf(f0, fmaf(d0, s.sum, s.dev), f1 * fmaf(d1, sum, dev));
+    s.sum = fmaf(f0, s.sum, f1 * sum);
+    s.top = t;
 }
 
-__device__ __forceinline__ bool counts(const LogpParams& p, int64_t m) {
-    return m < p.M && p.targets[m] >= 0 && p.targets[m] < p.V;
+// 32 logits of a row, of which the first n are there
+__device__ __forceinline__ void sums_of(Sums& s, const uint32_t (&r)[32], int n, float c, float c_rest, bool entropy) {
+    float most = s.top;
+    if (n >= 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) most = fmaxf(most, __uint_as_float(r[j]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n) most = fmaxf(most, __uint_as_float(r[j]));
+    }
+    if (most > s.top) {
+        const float d = s.top - most, f = exp_scaled(d, c, c_rest);
+        s.dev = s.sum > 0.f ? f * fmaf(d, s.sum, s.dev) : 0.f;
+        s.sum *= f;
+        s.top = most;
+    }
+    float sum = 0.f, dev = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float d = __uint_as_float(r[j]) - most;
+        float e = exp_scaled(d, c, c_rest);
+        if (n < 32 && j >= n) e = 0.f;
+        sum += e;
+        if (entropy) dev = fmaf(e, d, dev);
+    }
+    s.sum += sum, s.dev += dev;
 }
 
-// A tile's logits, rows that do not count as zeros.
-__device__ __forceinline__ void logits(const LogpParams& p, Tile& s, int64_t m0, int64_t v0, float (&c)[4][4]) {
-    multiply(s, p.K, [&](int r, int64_t k) { return counts(p, m0 + r) ? bf(p.H[(m0 + r) * p.ldh + k]) : 0.f; },
-             [&](int r, int64_t k) { return v0 + r < p.V ? bf(p.W[(v0 + r) * p.ldw + k]) : 0.f; }, c);
+// A box of 32 rows of 128 bytes of a warp's own, one row a lane, staged under the 128-byte swizzle.
+__device__ __forceinline__ void stage16(uint8_t* out, int lane, int chunk, uint4 v) {
+    *reinterpret_cast<uint4*>(out + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
 }
 
-__global__ void __launch_bounds__(kThreads)
-logp_tile_kernel(const __grid_constant__ LogpParams p) {
-    __shared__ Tile s;
-    __shared__ float x[kTile][kTile + 1];
-    pdl_wait_then_release();
-    const int64_t v0 = (int64_t)blockIdx.x * kTile, m0 = (int64_t)blockIdx.y * kTile;
-    float c[4][4] = {};
-    logits(p, s, m0, v0, c);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) x[16 * i + ty][16 * j + tx] = c[i][j] * p.scale;
+template <Mode kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOffset);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
+    const uint32_t tfull0 = smem_u32(bars + 2 * kStages), tempty0 = smem_u32(bars + 2 * kStages + 2);
+    const uint32_t warp = warp_id(), lane = lane_id(), rank = cluster_ctarank();
+    auto gave_up = [&](uint32_t site) {
+        atomicCAS(p.err, 0u, kKernelLogp << 24 | site << 16 | 1u);
+        *abort = 1;
+    };
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull0 + 8 * b, 1);
+            mbar_init(tempty0 + 8 * b, 2 * kEpiWarps);
+        }
+        *abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&maps.h);
+        prefetch_tmap(&maps.w);
+        if (kMode != kLogp) prefetch_tmap(&maps.d);
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(2 * kTile)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
     __syncthreads();
-    const int64_t m = m0 + threadIdx.x;
-    if (threadIdx.x >= kTile || m >= p.M) return;
-    const int cols = (int)min((int64_t)kTile, p.V - v0);
-    float top = -INFINITY, sum = 0.f, dev = 0.f;
-    for (int j = 0; j < cols; ++j) top = fmaxf(top, x[threadIdx.x][j]);
-    for (int j = 0; j < cols; ++j) {
-        const float d = x[threadIdx.x][j] - top, e = expf(d);
-        sum += e, dev = fmaf(e, d, dev);
-    }
-    const int64_t at = blockIdx.x * p.M + m, size = (int64_t)gridDim.x * p.M;
-    p.part[at] = top, p.part[size + at] = sum, p.part[2 * size + at] = dev;
-    const int64_t t = p.targets[m] - v0;
-    if (t >= 0 && t < cols) p.picked[m] = x[threadIdx.x][t];
-}
+    cluster_sync_all();                                  // both CTAs' barriers are there
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();
+    grid_launch_dependents();
 
-__global__ void __launch_bounds__(kThreads)
-logp_join_kernel(const __grid_constant__ LogpParams p, int64_t tiles) {
-    pdl_wait_then_release();
-    const int64_t m = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (m >= p.M) return;
-    float logp = 0.f, lse = 0.f, entropy = 0.f;
-    if (counts(p, m)) {
-        float top = -INFINITY;
-        for (int64_t t = 0; t < tiles; ++t) top = fmaxf(top, p.part[t * p.M + m]);
-        float sum = 0.f, dev = 0.f;
-        const int64_t size = tiles * p.M;
-        for (int64_t t = 0; t < tiles; ++t) {
-            const float d = p.part[t * p.M + m] - top, e = expf(d), s = p.part[size + t * p.M + m];
-            sum = fmaf(e, s, sum);
-            dev = fmaf(e, fmaf(d, s, p.part[2 * size + t * p.M + m]), dev);
+    Work<kMode> work(p);
+    Unit u;
+    if (warp == 0 && lane == 0) {
+        // ---------------- loads: this CTA's rows of both operands
+        const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+        const uint32_t bar0 = map_to_rank(full0, 0);
+        uint32_t it = 0;
+        while (!*abort && work.next(u)) {
+            const CUtensorMap* ma = kMode != kBack ? &maps.h : &maps.d;
+            const CUtensorMap* mb = kMode != kBack || u.kind == 1 ? &maps.w : &maps.h;
+            const int a = u.a + (int)rank * kHalf, b = u.b + (int)rank * kHalf + (kMode != kBack ? p.first : 0);
+            for (int k = 0; k < u.n; ++k, ++it) {
+                const int s = it % kStages;
+                if (!mbar_wait_bounded(empty0 + 8 * s, ((it / kStages) & 1) ^ 1, abort, kWaitLimitNs)) {
+                    gave_up(1);
+                    break;
+                }
+                const uint32_t dst = smem_u32(smem + s * kStageBytes), bar = bar0 + 8 * s;
+                if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * kStageBytes);
+                const int at = (u.k + k) * kStep;
+                if (kMode != kBack) {
+                    pair_load(dst, ma, bar, at, a, keep);
+                    pair_load(dst + kPiece, ma, bar, at, a + 64, keep);
+                    pair_load(dst + 2 * kPiece, mb, bar, at, b, once);
+                    pair_load(dst + 3 * kPiece, mb, bar, at, b + 64, once);
+                } else if (u.kind == 1) {
+                    pair_load(dst, ma, bar, at, a, keep);
+                    pair_load(dst + kPiece, ma, bar, at, a + 64, keep);
+                    pair_load(dst + 2 * kPiece, mb, bar, b, p.first + at, keep);
+                    pair_load(dst + 3 * kPiece, mb, bar, b + 64, p.first + at, keep);
+                } else {
+                    pair_load(dst, ma, bar, a, at, keep);
+                    pair_load(dst + kPiece, ma, bar, a + 64, at, keep);
+                    pair_load(dst + 2 * kPiece, mb, bar, b, at, keep);
+                    pair_load(dst + 3 * kPiece, mb, bar, b + 64, at, keep);
+                }
+            }
         }
-        lse = top + logf(sum), logp = p.picked[m] - lse, entropy = logf(sum) - dev / sum;
+        if (*abort && rank == 0)                         // both CTAs' copies in flight land before either ends
+            for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
+                mbar_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kWaitLimitNs);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---------------- products, for both CTAs
+        uint32_t it = 0, tile = 0;
+        while (!*abort && work.next(u)) {
+            if (u.n == 0) continue;
+            const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+            ++tile;
+            if (!mbar_wait_bounded(tempty0 + 8 * buf, use ^ 1, abort, kWaitLimitNs)) {
+                gave_up(3);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + buf * kTile;
+            const bool a_mn = kMode == kBack && u.kind == 2, b_mn = kMode == kBack;
+            const uint32_t idesc = kIdesc | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+            const uint64_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+            for (int k = 0; k < u.n; ++k, ++it) {
+                const int s = it % kStages;
+                if (!mbar_wait_bounded(full0 + 8 * s, (it / kStages) & 1, abort, kWaitLimitNs)) {
+                    gave_up(2);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * kStageBytes);
+                const uint64_t ad = a_mn ? desc_mn(st) : umma_desc_k128_sw128(st);
+                const uint64_t bd = b_mn ? desc_mn(st + 2 * kPiece) : umma_desc_k128_sw128(st + 2 * kPiece);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pair_mma(d, ad + j * a_step, bd + j * b_step, idesc, k > 0 || j > 0);
+                pair_commit(empty0 + 8 * s);
+            }
+            pair_commit(tfull0 + 8 * buf);
+        }
+    } else if (warp >= 4) {
+        // ---------------- the tile's threads' part: a row a thread
+        const int q = warp & 3, row = 32 * q + (int)lane;
+        uint8_t* out = smem + kOutOffset + q * kOutBytes;
+        const uint32_t empty_bar = map_to_rank(tempty0, 0);
+        const float c = p.scale * kLog2e, c_rest = fmaf(p.scale, kLog2e, -c) + p.scale * kLog2eRest;
+        uint32_t tile = 0;
+        while (work.next(u)) {
+            const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+            const int m = u.a + (int)rank * kHalf + row;                 // kLogp, kGrad: the row among those that count
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile;
+            // per row, before the wait
+            float g = 0.f, ge = 0.f, l2 = 0.f, plus = 0.f;
+            int t = -1;
+            if (kMode != kBack) {
+                t = p.row_target[m] - p.first - u.b;
+                if (kMode == kGrad) g = p.row_g[m], ge = p.row_ge[m], l2 = p.row_lse[m] * kLog2e, plus = p.row_entropy[m];
+            }
+            const float f = kMode == kBack ? *p.largest * p.scale : 0.f;
+            if (u.n > 0) {
+                ++tile;
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
+                    if (lane == 0) gave_up(4);
+                    break;
+                }
+                tc_fence_after();
+            }
+            if constexpr (kMode == kLogp) {
+                Sums s;
+                const int cols = min(kTile, (int)p.V - u.b);
+#pragma unroll 1
+                for (int j = 0; j < kTile; j += 32) {
+                    if (j >= cols) break;
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(taddr + j, r);
+                    tmem_wait_ld();
+                    sums_of(s, r, cols - j, c, c_rest, p.entropy != nullptr);
+                    if (t >= j && t < j + 32) {
+                        float x = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e == t - j) x = __uint_as_float(r[e]);
+                        p.picked[m] = x;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+                float* part = p.part + (int64_t)u.slot * p.rows_pad + m;
+                const int64_t size = (int64_t)p.tiles * p.rows_pad;
+                part[0] = s.top, part[size] = s.sum;
+                if (p.entropy) part[2 * size] = s.dev;
+            } else if constexpr (kMode == kGrad) {
+                const int cols = min(kTile, (int)(p.V - p.first) - u.b);
+                const bool entropy = p.ge != nullptr;
+#pragma unroll 1
+                for (int j = 0; j < kTile; j += 64) {
+                    uint32_t packed[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(taddr + j + 32 * h, r);
+                        tmem_wait_ld();
+                        const int j0 = j + 32 * h;
+                        float v[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float x = __uint_as_float(r[e]);
+                            const float a = fmaf(x, c, fmaf(x, c_rest, -l2)), pr = ex2(a);
+                            v[e] = -g * pr;
+                            if (entropy) v[e] = fmaf(-ge * pr, fmaf(a, 0.69314718f, plus), v[e]);
+                        }
+                        if (t >= j0 && t < j0 + 32) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (e == t - j0) v[e] += g;
+                        }
+                        if (cols < j0 + 32) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (j0 + e >= cols) v[e] = 0.f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) packed[16 * h + e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                    }
+                    if (j == kTile - 64) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+                    }
+                    if (lane == 0) bulk_wait_read_all();                 // the box before has left the buffer
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        stage16(out, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&maps.d_out, smem_u32(out), u.b + j, u.a + (int)rank * kHalf + 32 * q);
+                        bulk_commit();
+                    }
+                }
+            } else if (u.kind == 1) {
+                if (u.n == 0) continue;
+#pragma unroll 1
+                for (int j = 0; j < kTile; j += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(taddr + j, r);
+                    tmem_wait_ld();
+                    if (j == kTile - 32) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+                    }
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) stage16(out, lane, e, make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && u.b + j < p.K) {
+                        const int y = u.slot * p.rows_pad + u.a + (int)rank * kHalf + 32 * q;
+                        if (p.first == 0) tma_store_2d(&maps.acc, smem_u32(out), u.b + j, y);
+                        else tma_add_2d(&maps.acc, smem_u32(out), u.b + j, y);
+                        bulk_commit();
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < kTile; j += 64) {
+                    uint32_t packed[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[32];
+                        if (u.n > 0) {
+                            tmem_ld_32x32b_x32(taddr + j + 32 * h, r);
+                            tmem_wait_ld();
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) r[e] = 0;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            packed[16 * h + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+                    }
+                    if (j == kTile - 64 && u.n > 0) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+                    }
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        stage16(out, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    const int y = p.first + u.a + (int)rank * kHalf + 32 * q;
+                    if (lane == 0 && u.b + j < p.K && y < p.V) {
+                        tma_store_2d(&maps.dw, smem_u32(out), u.b + j, y);
+                        bulk_commit();
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
-    p.logp[m] = logp, p.lse[m] = lse;
-    if (p.entropy) p.entropy[m] = entropy;
-}
-
-// The largest |g| and |e| of the rows that count.
-__global__ void __launch_bounds__(1024)
-grad_scale_kernel(const __grid_constant__ LogpParams p) {
-    __shared__ float w[32];
-    pdl_wait_then_release();
-    float a = 0.f;
-    for (int64_t m = threadIdx.x; m < p.M; m += 1024)
-        if (counts(p, m)) a = fmaxf(a, fmaxf(fabsf(p.g[m]), p.ge ? fabsf(p.ge[m]) : 0.f));
-    for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = a;
+    __syncwarp();
+    tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 32; ++i) a = fmaxf(a, w[i]);
-        *p.largest = a > 0.f ? a : 1.f;
+    cluster_sync_all();                                  // neither CTA's memory is in use any more
+    if (warp == 2) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kTile) : "memory");
     }
 }
 
-// D of vocabulary rows [first, first + count), as bf16 [M][count].
-__global__ void __launch_bounds__(kThreads)
-grad_tile_kernel(const __grid_constant__ LogpParams p, int64_t first, int64_t count) {
-    __shared__ Tile s;
+// ------------------------------------------------------------------ before and after the products
+
+__device__ __forceinline__ bool counts(const LogpParams& p, int64_t m) { return p.targets[m] >= 0 && p.targets[m] < p.V; }
+
+// The rows that count, brought together: their hidden states, targets and gradients; zeros
+// for the results of the others.  Every CTA goes over all targets (they are in L2) to find
+// where its own rows go, so nothing is waited for.
+constexpr int kRowThreads = 256, kMostRows = 512;
+
+template <bool kBackward>
+__global__ void __launch_bounds__(kRowThreads)
+rows_kernel(const __grid_constant__ LogpParams p, int rows) {
+    __shared__ int place[kMostRows], before_w[8], all_w[8];
+    __shared__ float largest_w[8];
     pdl_wait_then_release();
-    const int64_t v0 = first + (int64_t)blockIdx.x * kTile, m0 = (int64_t)blockIdx.y * kTile;
-    float c[4][4] = {};
-    logits(p, s, m0, v0, c);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const float largest = *p.largest;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 16 * i + ty;
-        if (m >= p.M) continue;
-        const bool live = counts(p, m);
-        const float g = live ? p.g[m] / largest : 0.f, ge = live && p.ge ? p.ge[m] / largest : 0.f;
-        const float lse = live ? p.lse[m] : 0.f, ent = live && p.ge ? p.entropy[m] : 0.f;
-        for (int j = 0; j < 4; ++j) {
-            const int64_t v = v0 + 16 * j + tx;
-            if (v >= first + count) continue;
-            const float lp = c[i][j] * p.scale - lse, pr = expf(lp);
-            float d = g * ((p.targets[m] == v ? 1.f : 0.f) - pr);
-            if (p.ge) d -= ge * pr * (lp + ent);
-            p.D[m * p.piece + v - first] = live ? (uint16_t)f32_to_bf16_bits(d) : 0;
+    const int M = (int)p.M, m0 = blockIdx.x * rows, mine = min(rows, M - m0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int before = 0, all = 0;
+    float largest = 0.f;
+    for (int m = threadIdx.x; m < M; m += kRowThreads)
+        if (counts(p, m)) {
+            before += m < m0, ++all;
+            if (kBackward) largest = fmaxf(largest, fmaxf(fabsf(p.g[m]), p.ge ? fabsf(p.ge[m]) : 0.f));
+        }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+    }
+    if (lane == 0) before_w[warp] = before, all_w[warp] = all, largest_w[warp] = largest;
+    __syncthreads();
+    before = all = 0, largest = 0.f;
+    for (int w = 0; w < 8; ++w) before += before_w[w], all += all_w[w], largest = fmaxf(largest, largest_w[w]);
+    if (largest == 0.f) largest = 1.f;
+    if (warp == 0)
+        for (int r = 0; r < mine; r += 32) {
+            const bool yes = r + lane < mine && counts(p, m0 + r + lane);
+            const uint32_t those = __ballot_sync(0xffffffffu, yes);
+            if (r + lane < mine) place[r + lane] = yes ? before + __popc(those & ((1u << lane) - 1)) : -1;
+            before += __popc(those);
+        }
+    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *p.live = all;
+        if (kBackward) *p.largest = largest;
+    }
+    const int chunks = (int)(p.K / 8);
+    for (int r = warp; r < mine; r += 8) {
+        const int m = m0 + r, at = place[r];
+        if (at < 0) {
+            if (!kBackward) {
+                if (lane == 0) {
+                    p.logp[m] = 0.f, p.lse[m] = 0.f;
+                    if (p.entropy) p.entropy[m] = 0.f;
+                }
+            } else if (p.dH) {
+                uint4* d = reinterpret_cast<uint4*>(p.dH + (int64_t)m * p.K);
+                for (int i = lane; i < chunks; i += 32) d[i] = make_uint4(0, 0, 0, 0);
+            }
+            continue;
+        }
+        if (lane == 0) {
+            p.row_of[at] = m, p.row_target[at] = p.targets[m];
+            if (kBackward) {
+                p.row_g[at] = p.g[m] / largest, p.row_ge[at] = p.ge ? p.ge[m] / largest : 0.f;
+                p.row_lse[at] = p.lse[m], p.row_entropy[at] = p.ge ? p.entropy[m] : 0.f;
+            }
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(p.H + m * p.ldh);
+        uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.K);
+        for (int i = lane; i < chunks; i += 32) dst[i] = ld_stream_v4(src + i);
+    }
+    // up to the last tile's edge: no target, no gradient, and zeros (past M the copy engine fills them in)
+    const int edge = (all + kTile - 1) / kTile * kTile;
+    for (int at = all + blockIdx.x; at < edge; at += gridDim.x) {
+        if (threadIdx.x == 0) {
+            p.row_target[at] = -1;
+            if (kBackward) p.row_g[at] = 0.f, p.row_ge[at] = 0.f, p.row_lse[at] = 0.f, p.row_entropy[at] = 0.f;
+        }
+        if (at < M) {
+            uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.K);
+            for (int i = threadIdx.x; i < chunks; i += kRowThreads) dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
 }
 
-// acc [M][K] (+)= D W
-__global__ void __launch_bounds__(kThreads)
-grad_h_kernel(const __grid_constant__ LogpParams p, int64_t first, int64_t count) {
-    __shared__ Tile s;
+// Joins a row's tiles: a row a lane, a part of the tiles a warp.
+constexpr int kJoinWarps = 16;
+
+__global__ void __launch_bounds__(32 * kJoinWarps)
+logp_join_kernel(const __grid_constant__ LogpParams p) {
+    __shared__ Sums part[kJoinWarps][32];
     pdl_wait_then_release();
-    const int64_t k0 = (int64_t)blockIdx.x * kTile, m0 = (int64_t)blockIdx.y * kTile;
-    float c[4][4] = {};
-    multiply(s, count, [&](int r, int64_t v) { return m0 + r < p.M ? bf(p.D[(m0 + r) * p.piece + v]) : 0.f; },
-             [&](int r, int64_t v) { return k0 + r < p.K ? bf(p.W[(first + v) * p.ldw + k0 + r]) : 0.f; }, c);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + 16 * i + ty, k = k0 + 16 * j + tx;
-            if (m < p.M && k < p.K) p.acc[m * p.K + k] = (first ? p.acc[m * p.K + k] : 0.f) + c[i][j];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int live = *p.live, m = blockIdx.x * 32 + lane;
+    if (blockIdx.x * 32 >= live) return;
+    const float c = p.scale * kLog2e, c_rest = fmaf(p.scale, kLog2e, -c) + p.scale * kLog2eRest;
+    const int64_t size = (int64_t)p.tiles * p.rows_pad;
+    Sums s;
+    if (m < live)
+        for (int t = warp; t < p.tiles; t += kJoinWarps) {
+            const float* at = p.part + (int64_t)t * p.rows_pad + m;
+            add_sums(s, at[0], at[size], p.entropy ? at[2 * size] : 0.f, c, c_rest);
         }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp > 0 || m >= live) return;
+    for (int w = 1; w < kJoinWarps; ++w) add_sums(s, part[w][lane].top, part[w][lane].sum, part[w][lane].dev, c, c_rest);
+    const float ls = logf(s.sum);
+    const int row = p.row_of[m];
+    p.logp[row] = (float)((double)p.scale * ((double)p.picked[m] - (double)s.top) - (double)ls);
+    p.lse[row] = (float)((double)p.scale * (double)s.top + (double)ls);
+    if (p.entropy) p.entropy[row] = ls - p.scale * s.dev / s.sum;
 }
 
-__global__ void __launch_bounds__(kThreads)
-grad_w_kernel(const __grid_constant__ LogpParams p, int64_t first, int64_t count) {
-    __shared__ Tile s;
+// dH from its fp32 sums, a row a CTA
+__global__ void __launch_bounds__(256)
+grad_h_kernel(const __grid_constant__ LogpParams p) {
     pdl_wait_then_release();
-    const int64_t k0 = (int64_t)blockIdx.x * kTile, v0 = (int64_t)blockIdx.y * kTile;
-    float c[4][4] = {};
-    multiply(s, p.M, [&](int r, int64_t m) { return v0 + r < count ? bf(p.D[m * p.piece + v0 + r]) : 0.f; },
-             [&](int r, int64_t m) { return k0 + r < p.K && counts(p, m) ? bf(p.H[m * p.ldh + k0 + r]) : 0.f; }, c);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int live = *p.live;
     const float f = *p.largest * p.scale;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t v = v0 + 16 * i + ty, k = k0 + 16 * j + tx;
-            if (v < count && k < p.K) p.dW[(first + v) * p.K + k] = (uint16_t)f32_to_bf16_bits(c[i][j] * f);
+    for (int m = blockIdx.x; m < live; m += gridDim.x) {
+        uint2* dst = reinterpret_cast<uint2*>(p.dH + (int64_t)p.row_of[m] * p.K);
+        for (int i = threadIdx.x; i < (int)(p.K / 4); i += 256) {
+            float4 v = *reinterpret_cast<const float4*>(p.acc + (int64_t)m * p.K + 4 * i);
+            for (int s = 1; s < p.split; ++s) {
+                const float4 w = *reinterpret_cast<const float4*>(p.acc + ((int64_t)s * p.rows_pad + m) * p.K + 4 * i);
+                v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+            }
+            dst[i] = make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
         }
+    }
 }
 
-__global__ void __launch_bounds__(kThreads)
-grad_h_round_kernel(const __grid_constant__ LogpParams p) {
-    pdl_wait_then_release();
-    const float f = *p.largest * p.scale;
-    const int64_t step = (int64_t)gridDim.x * kThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < p.M * p.K; i += step)
-        p.dH[i] = (uint16_t)f32_to_bf16_bits(counts(p, i / p.K) ? p.acc[i] * f : 0.f);
+// ------------------------------------------------------------------ host
+
+constexpr int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// A workspace's parts, 256 bytes apart.
+struct Arena {
+    uint8_t* base;
+    size_t used = 0;
+    template <typename T>
+    T* take(int64_t n) {
+        T* at = base ? reinterpret_cast<T*>(base + used) : nullptr;
+        used += (size_t)up(n * (int64_t)sizeof(T), 256);
+        return at;
+    }
+};
+
+void lay_rows(Arena& a, LogpParams& p) {
+    p.rows_pad = (int)up(p.M, kTile);
+    p.live = a.take<int>(1), p.largest = a.take<float>(1);
+    p.row_of = a.take<int>(p.rows_pad), p.row_target = a.take<int>(p.rows_pad);
+    p.rows_h = a.take<uint16_t>(p.M * p.K);
+}
+void lay_forward(Arena& a, LogpParams& p) {
+    lay_rows(a, p);
+    p.tiles = (int)((p.V + kTile - 1) / kTile);
+    p.picked = a.take<float>(p.rows_pad);
+    p.part = a.take<float>(3 * (int64_t)p.tiles * p.rows_pad);
 }
 
-constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
-int64_t piece_of(int64_t M, int64_t V) {
-    int64_t n = (64ll << 20) / (2 * M) / kTile * kTile;
-    n = n < kTile ? kTile : n;
-    return n < V ? n : V;
+// The backward's pieces of the vocabulary: D of a piece is at most 128 MB, about what stays
+// in L2, but at least 4096 wide, so that its launches are long.
+int64_t piece_of(int64_t rows_pad, int64_t V) {
+    const int64_t most = std::max<int64_t>(up((64ll << 20) / rows_pad, kTile), 4096), n = (V + most - 1) / most;
+    return up((V + n - 1) / n, kTile);
+}
+// Parts of a piece that dH's tiles are cut into, summed apart: as many as make the fewest
+// steps for the pair that has the most, with some 8 steps' time for a tile's ends and a
+// hundredth for a part's sums.  The same whether dW is wanted too, whose tiles would fill
+// the gaps: dH has the same bits either way.
+int split_of(int64_t M, int64_t K, int64_t piece, int pairs) {
+    const int64_t tiles = (M + kTile - 1) / kTile * ((K + kTile - 1) / kTile), steps = piece / kStep;
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= 16 && s * 8 <= steps; ++s) {
+        const double turns = (double)((tiles * s + pairs - 1) / pairs);
+        const double cost = turns * ((double)steps / s + 8.0) * (1.0 + 0.01 * s);
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
+}
+void lay_backward(Arena& a, LogpParams& p, int pairs) {
+    lay_rows(a, p);
+    p.row_g = a.take<float>(p.rows_pad), p.row_ge = a.take<float>(p.rows_pad);
+    p.row_lse = a.take<float>(p.rows_pad), p.row_entropy = a.take<float>(p.rows_pad);
+    p.piece = piece_of(p.rows_pad, p.V);
+    p.split = split_of(p.M, p.K, p.piece, pairs);
+    p.D = a.take<uint16_t>((int64_t)p.rows_pad * p.piece);
+    p.acc = a.take<float>((int64_t)p.split * p.rows_pad * p.K);
+}
+
+template <typename K>
+cudaError_t launch_pairs(K kernel, int pairs, cudaStream_t st, const Maps& maps, const LogpParams& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p);
+}
+
+// Pairs of CTAs that run at once on the current device; 0: the kernels do not run there.
+int pairs_here() {
+    static int known[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (!known[dev]) {
+        void (*all[])(Maps, LogpParams) = {logp_pair_kernel<kLogp>, logp_pair_kernel<kGrad>, logp_pair_kernel<kBack>};
+        for (auto* f : all)
+            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * 512);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, logp_pair_kernel<kLogp>, &cfg) != cudaSuccess || n <= 0) return 0;
+        known[dev] = n;
+    }
+    return known[dev];
+}
+
+// 64 x 64 boxes of a row-major bf16 matrix, rows 128 bytes under the 128-byte swizzle, zeros outside
+bool load_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
+    return make_tmap_bf16_load(m, base, (uint64_t)rows, (uint64_t)cols, (uint64_t)pitch, 64);
+}
+
+cudaError_t launch_rows(const LogpParams& p, bool backward, cudaStream_t st) {
+    const int rows = (int)std::max<int64_t>(16, (p.M + 4095) / 4096);
+    const dim3 grid((unsigned)((p.M + rows - 1) / rows));
+    return backward ? launch_pdl(rows_kernel<true>, grid, dim3(kRowThreads), 0, st, p, rows)
+                    : launch_pdl(rows_kernel<false>, grid, dim3(kRowThreads), 0, st, p, rows);
+}
+
+// Row tiles whose hidden states take some 40 MB, a third of L2.
+int group_of(int64_t K) { return (int)std::max<int64_t>(1, (40ll << 20) / (kTile * K * 2)); }
+
+int pairs_or_default() {
+    const int n = num_sms() / 2;
+    return n > 0 ? n : 76;
 }
 
 }  // namespace
 
 size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K) {
     if (M <= 0 || V <= 0 || K <= 0) return 0;
-    return (size_t)up16(4 * (3 * ((V + kTile - 1) / kTile) * M + M));
+    LogpParams p{};
+    p.M = M, p.V = V, p.K = K;
+    Arena a{nullptr};
+    lay_forward(a, p);
+    return a.used;
 }
 
 size_t linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
     if (M <= 0 || V <= 0 || K <= 0) return 0;
-    return (size_t)(16 + up16(M * K * 4) + up16(M * piece_of(M, V) * 2));
+    LogpParams p{};
+    p.M = M, p.V = V, p.K = K;
+    Arena a{nullptr};
+    lay_backward(a, p, pairs_or_default());
+    return a.used;
 }
 
 cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st) {
-    const int64_t tiles = (p.V + kTile - 1) / kTile, mt = (p.M + kTile - 1) / kTile;
-    p.part = static_cast<float*>(ws);
-    p.picked = p.part + 3 * tiles * p.M;
-    cudaError_t e = launch_pdl(logp_tile_kernel, dim3((unsigned)tiles, (unsigned)mt), dim3(kThreads), 0, st, p);
+    const int pairs = pairs_here();
+    if (!pairs) return cudaErrorInvalidDeviceFunction;
+    Arena a{static_cast<uint8_t*>(ws)};
+    lay_forward(a, p);
+    p.err = device_error_word();
+    p.ksteps = (int)((p.K + kStep - 1) / kStep), p.group = group_of(p.K);
+    Maps maps{};
+    if (!p.err || !load_map(&maps.h, p.rows_h, p.M, p.K, p.K) || !load_map(&maps.w, p.W, p.V, p.K, p.ldw))
+        return cudaErrorInvalidValue;
+    cudaError_t e = launch_rows(p, false, st);
+    if (e == cudaSuccess) e = launch_pairs(logp_pair_kernel<kLogp>, pairs, st, maps, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(logp_join_kernel, dim3((unsigned)((p.M + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, p, tiles);
+    return launch_pdl(logp_join_kernel, dim3((unsigned)((p.M + 31) / 32)), dim3(32 * kJoinWarps), 0, st, p);
 }
 
 cudaError_t launch_linear_logp_backward(LogpParams p, void* ws, cudaStream_t st) {
     if (p.M == 0) return p.dW ? cudaMemsetAsync(p.dW, 0, (size_t)(p.V * p.K) * 2, st) : cudaSuccess;
-    uint8_t* b = static_cast<uint8_t*>(ws);
-    p.largest = reinterpret_cast<float*>(b);
-    p.acc = reinterpret_cast<float*>(b + 16);
-    p.D = reinterpret_cast<uint16_t*>(b + 16 + up16(p.M * p.K * 4));
-    p.piece = piece_of(p.M, p.V);
-    auto blocks = [](int64_t n) { return (unsigned)((n + kTile - 1) / kTile); };
-    cudaError_t e = launch_pdl(grad_scale_kernel, dim3(1), dim3(1024), 0, st, p);
+    const int pairs = pairs_here();
+    if (!pairs) return cudaErrorInvalidDeviceFunction;
+    Arena a{static_cast<uint8_t*>(ws)};
+    lay_backward(a, p, pairs_or_default());
+    p.err = device_error_word();
+    p.ksteps = (int)((p.K + kStep - 1) / kStep), p.group = group_of(p.K);
+    p.ktiles = (int)((p.K + kTile - 1) / kTile);
+    Maps maps{};
+    if (!p.err || !load_map(&maps.h, p.rows_h, p.M, p.K, p.K) || !load_map(&maps.w, p.W, p.V, p.K, p.ldw) ||
+        !load_map(&maps.d, p.D, p.rows_pad, p.piece, p.piece) ||
+        !make_tmap_bf16_store(&maps.d_out, p.D, (uint64_t)p.rows_pad, (uint64_t)p.piece, (uint64_t)p.piece, 64, 32) ||
+        !make_tmap_f32_store(&maps.acc, p.acc, (uint64_t)p.split * p.rows_pad, (uint64_t)p.K, (uint64_t)p.K, 32, 32) ||
+        (p.dW && !make_tmap_bf16_store(&maps.dw, p.dW, (uint64_t)p.V, (uint64_t)p.K, (uint64_t)p.K, 64, 32)))
+        return cudaErrorInvalidValue;
+    cudaError_t e = launch_rows(p, true, st);
     for (int64_t v = 0; v < p.V && e == cudaSuccess; v += p.piece) {
-        const int64_t n = p.V - v < p.piece ? p.V - v : p.piece;
-        e = launch_pdl(grad_tile_kernel, dim3(blocks(n), blocks(p.M)), dim3(kThreads), 0, st, p, v, n);
-        if (p.dH && e == cudaSuccess)
-            e = launch_pdl(grad_h_kernel, dim3(blocks(p.K), blocks(p.M)), dim3(kThreads), 0, st, p, v, n);
-        if (p.dW && e == cudaSuccess)
-            e = launch_pdl(grad_w_kernel, dim3(blocks(p.K), blocks(n)), dim3(kThreads), 0, st, p, v, n);
+        const int64_t n = std::min(p.piece, p.V - v);
+        p.first = (int)v, p.tiles = (int)((n + kTile - 1) / kTile), p.steps = (int)((n + kStep - 1) / kStep);
+        e = launch_pairs(logp_pair_kernel<kGrad>, pairs, st, maps, p);
+        if (e == cudaSuccess) e = launch_pairs(logp_pair_kernel<kBack>, pairs, st, maps, p);
     }
     if (!p.dH || e != cudaSuccess) return e;
-    return launch_pdl(grad_h_round_kernel, dim3((unsigned)(4 * num_sms())), dim3(kThreads), 0, st, p);
+    return launch_pdl(grad_h_kernel, dim3((unsigned)std::min<int64_t>(p.M, 8 * num_sms())), dim3(256), 0, st, p);
 }
 
 }  // namespace fp8rl
