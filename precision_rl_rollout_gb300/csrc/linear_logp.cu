@@ -226,6 +226,23 @@ __device__ __forceinline__ void sums_of(Sums& s, const uint32_t (&r)[32], int n,
     s.sum += sum, s.dev += dev;
 }
 
+// r[i] by masks: an index would put the values in memory
+__device__ __forceinline__ uint32_t pick(const uint32_t (&r)[32], int i) {
+    uint32_t x = 0;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        uint32_t same;
+        asm("{\n.reg .pred p;\nsetp.eq.s32 p, %1, %2;\nselp.b32 %0, 0xFFFFFFFF, 0, p;\n}\n" : "=r"(same) : "r"(e), "r"(i));
+        x |= r[e] & same;
+    }
+    return x;
+}
+__device__ __forceinline__ float mask01(int e, int i) {
+    float f;
+    asm("{\n.reg .pred p;\nsetp.eq.s32 p, %1, %2;\nselp.f32 %0, 0f3F800000, 0f00000000, p;\n}\n" : "=f"(f) : "r"(e), "r"(i));
+    return f;
+}
+
 // A box of 32 rows of 128 bytes of a warp's own, one row a lane, staged under the 128-byte swizzle.
 __device__ __forceinline__ void stage16(uint8_t* out, int lane, int chunk, uint4 v) {
     *reinterpret_cast<uint4*>(out + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
@@ -386,13 +403,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                     tmem_ld_32x32b_x32(taddr + j, r);
                     tmem_wait_ld();
                     sums_of(s, r, cols - j, c, c_rest, p.entropy != nullptr);
-                    if (t >= j && t < j + 32) {
-                        float x = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e == t - j) x = __uint_as_float(r[e]);
-                        p.picked[m] = x;
-                    }
+                    if (t >= j && t < j + 32) p.picked[m] = __uint_as_float(pick(r, t - j));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -423,8 +434,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                         }
                         if (t >= j0 && t < j0 + 32) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (e == t - j0) v[e] += g;
+                            for (int e = 0; e < 32; ++e) v[e] = fmaf(g, mask01(e, t - j0), v[e]);
                         }
                         if (cols < j0 + 32) {
 #pragma unroll
