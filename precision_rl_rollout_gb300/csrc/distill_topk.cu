@@ -10,7 +10,7 @@
 // (no q_r without the rest), lse_r the log-sum outside.
 //
 // The loss is a difference of near terms once the student is close, so the logarithms
-// meet in 64 bits; the sums of exponentials are fp32 relative to a maximum.  With the rest
+// are taken to 1e-9 and meet in 64 bits; the sums of exponentials are fp32 relative to a maximum.  With the rest
 // the pass over the logits sums the tokens outside, relative to their own maximum, and the
 // entries are added to that: a difference, or one maximum for both, would lose a small rest.
 // The gradient outside is exp(y_v - lse_r) (Q exp(lse_r - lse) - q_r), no factor above 1.
@@ -22,8 +22,8 @@
 // are bits in shared memory, a byte for the eight bf16 of a load.
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -44,6 +44,24 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+    return sm100::f32x2_pack(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 // exp(scale d) for d <= 0: the constant scale log2(e) in two parts, since its rounding alone
 // would be a change of temperature, some 1e-6 of the sum.
 struct Scale {
@@ -51,19 +69,55 @@ struct Scale {
     __device__ __forceinline__ explicit Scale(float scale)
         : c(scale * kLog2e), rest(fmaf(scale, kLog2e, -(scale * kLog2e)) + scale * kLog2eRest) {}
     __device__ __forceinline__ float exp(float d) const { return ex2(fmaf(d, c, d * rest)); }
+    // of two logits relative to a maximum, given as pairs with -top
+    __device__ __forceinline__ uint64_t exp(uint64_t x, uint64_t low) const {
+        const uint64_t d = add2(x, low), a = fma2(d, pk2(c, c), mul2(d, pk2(rest, rest)));
+        const float2 v = sm100::f32x2_unpack(a);
+        return pk2(ex2(v.x), ex2(v.y));
+    }
 };
 
-// log of a positive fp32 sum to some 1e-8 absolute: the exponent apart, the rest as log1p.
-__device__ __forceinline__ double log_sum(float s) {
-    int e;
-    float f = frexpf(s, &e);                          // [0.5, 1)
-    if (f < 0.70710678f) f *= 2.f, --e;
-    return (double)e * kLn2 + (double)log1pf(f - 1.f);
+// A natural logarithm good to some 1e-9 in mostly 32-bit steps, since 64-bit arithmetic is
+// slow here (three of the library's cost a row 3 us): v = 2^e f, f c = 1 + r with c near
+// 1 / f of ten bits, one of 32, so that r < 1/50 is all but exact; log v = e log 2 - log c +
+// log1p(r), the last by its series, and what v loses as fp32 to first order.
+struct Near {
+    float c;
+    double log;                                        // -log c
+};
+__constant__ Near kNear[32] = {
+    {0.984375, 0.015748356968139168}, {0.955078125, 0.045962135564635756},
+    {0.927734375, 0.07500982100486657}, {0.90234375, 0.10275973395776894},
+    {0.876953125, 0.1313017372972535}, {0.853515625, 0.15839142994391764},
+    {0.83203125, 0.18388527877013736}, {0.810546875, 0.21004610480880948},
+    {0.791015625, 0.23443755793296864}, {0.771484375, 0.2594388601383859},
+    {0.75390625, 0.2824872555746769}, {0.736328125, 0.30607943759149703},
+    {0.71875, 0.33024168687057687}, {0.703125, 0.3522205935893521},
+    {0.6875, 0.3746934494414107}, {0.673828125, 0.394780208008148},
+    {0.66015625, 0.415278729556489}, {0.646484375, 0.43620624966244487},
+    {0.6328125, 0.4575811092471784}, {0.62109375, 0.47627324225933093},
+    {0.609375, 0.4953214372300254}, {0.59765625, 0.514739523087127},
+    {0.587890625, 0.5312143602906321}, {0.576171875, 0.5513492686996879},
+    {0.56640625, 0.5684437020589881}, {0.556640625, 0.5858354447708572},
+    {0.546875, 0.6035350218702582}, {0.537109375, 0.6215535273729365},
+    {0.529296875, 0.6362058041598069}, {0.51953125, 0.6548283162578087},
+    {0.51171875, 0.6699801212784109}, {0.50390625, 0.6853650401178903}};
+__device__ __forceinline__ double log64(double v) {
+    const float s = (float)v, lost = (float)(v - (double)s);
+    if (!(s > 1e-37f && s < 3e38f)) return v > 0.0 ? log(v) : v == 0.0 ? -INFINITY : NAN;
+    const uint32_t b = __float_as_uint(s);
+    const Near& n = kNear[b >> 18 & 31];
+    const float r = fmaf(__uint_as_float((b & 0x007FFFFFu) | 0x3F800000u), n.c, -1.f);
+    const float series = r * r * fmaf(r, fmaf(r, fmaf(r, 0.2f, -0.25f), 1.f / 3.f), -0.5f);
+    return (double)((int)(b >> 23) - 127) * kLn2 + n.log + (double)(r + (series + lost / s));
 }
-// exp of a 64-bit argument as fp32: what its rounding to 32 bits loses, to first order
-__device__ __forceinline__ float exp64(double a) {
-    const float hi = (float)a;
-    return hi < -104.f ? 0.f : expf(hi) * (1.f + (float)(a - (double)hi));
+
+// exp(scale t - shift) as fp32, shift in two parts: what the argument's roundings lose, to
+// first order
+__device__ __forceinline__ float exp_less(float t, float scale, float shift, float shift_rest) {
+    const float y = t * scale, rest = fmaf(t, scale, -y), hi = y - shift, back = hi - y;
+    const float lo = (y - (hi - back)) + (-shift - back) + (rest - shift_rest);
+    return hi < -104.f ? 0.f : expf(hi) * (1.f + lo);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -77,29 +131,6 @@ __device__ __forceinline__ T warp_sum(T v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// Over the CTA, the same for every thread; fixed order.
-template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* buf) {
-    v = warp_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    T r = buf[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) r += buf[w];
-    return r;
-}
-__device__ __forceinline__ float block_max(float v, float* buf) {
-    v = warp_max(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float r = buf[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) r = fmaxf(r, buf[w]);
-    return r;
-}
-
 __device__ __forceinline__ float value(const float* p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float value(const uint16_t* p, int64_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
 __device__ __forceinline__ void put(float* p, int64_t i, float v) { p[i] = v; }
@@ -129,7 +160,7 @@ struct Chunk<uint16_t> {
         asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
         return fmaxf(bf16_lo(a), bf16_hi(a));
     }
-    __device__ __forceinline__ float at(int e) const { return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]); }
+    __device__ __forceinline__ uint64_t pair(int i) const { return pk2(bf16_lo(w[i]), bf16_hi(w[i])); }
     template <typename F>
     __device__ __forceinline__ uint4 map(F f) const {
         uint32_t o[4];
@@ -158,6 +189,7 @@ struct Chunk<float> {
     }
     __device__ __forceinline__ float most() const { return fmaxf(fmaxf(at(0), at(1)), fmaxf(at(2), at(3))); }
     __device__ __forceinline__ float at(int e) const { return __uint_as_float(w[e]); }
+    __device__ __forceinline__ uint64_t pair(int i) const { return sm100::f32x2_pack(w[2 * i], w[2 * i + 1]); }
     template <typename F>
     __device__ __forceinline__ uint4 map(F f) const {
         return make_uint4(__float_as_uint(f(at(0))), __float_as_uint(f(at(1))), __float_as_uint(f(at(2))),
@@ -183,81 +215,106 @@ __device__ __forceinline__ void fetch(Chunk<T> (&b)[kFlight], const T* X, int at
     }
 }
 
-// The teacher's entries of a row in shared memory, and the tokens they name as bits.
+// The teacher's entries of a row in shared memory, and the tokens they name as bits.  A
+// thread's first entry waits in registers until it is used: its token, the teacher's
+// logit and the student's are under way while the row's first logits are.  What is left
+// to do with them then is one warp's: this GPU's 64-bit arithmetic is slow, and eight warps
+// each with the same few steps of it took a CTA 2 us.
 struct Entries {
     int32_t* id;       // [k], -1 where the entry names no token
-    float* q;          // [k], the teacher's probability
+    float* q;          // [k], the teacher's logit, then its probability
     float* x;          // [k], the student's logit
     uint32_t* bits;    // [ceil(V / 32)]
-    float* fbuf;       // [kWarps]
-    double* dbuf;      // [kWarps]
-    int count, distinct;
+    int32_t mine = -1;
+    float my_t = 0.f, my_x = 0.f;
+    bool any, twice = false;       // the row names a token; it names one twice (where there are bits)
+    bool every = false;            // every token is named
     double total;      // sum of q
-    double shift;      // log q_i = scale t_i - shift
+    float shift, shift_rest;       // log q_i = scale t_i - shift
 
-    __device__ __forceinline__ Entries(uint8_t* smem, int k) {
-        dbuf = reinterpret_cast<double*>(smem);
-        fbuf = reinterpret_cast<float*>(dbuf + kWarps);
-        id = reinterpret_cast<int32_t*>(fbuf + kWarps);
-        q = reinterpret_cast<float*>(id + k);
-        x = q + k;
-        bits = reinterpret_cast<uint32_t*>(x + k);
+    __device__ __forceinline__ Entries(uint8_t* smem, const DistillParams& p, int64_t m) {
+        id = reinterpret_cast<int32_t*>(smem);
+        q = reinterpret_cast<float*>(id + p.k);
+        x = q + p.k;
+        bits = reinterpret_cast<uint32_t*>(x + p.k);
+        const int64_t at = m * p.k;
+        if ((int)threadIdx.x < p.k) mine = p.ids[at + threadIdx.x], my_t = p.t[at + threadIdx.x];
+        for (int i = threadIdx.x + kThreads; i < p.k; i += kThreads) id[i] = p.ids[at + i], q[i] = p.t[at + i];
     }
-    // Tokens, and their logits; every thread of the CTA takes part in this and the next.
+    // Tokens, as bits where wanted, and their logits under way.  Every thread takes part.
     template <typename T>
-    __device__ __forceinline__ void load(const DistillParams& p, int64_t m, const T* X) {
-        const int words = (int)((p.V + 31) / 32);
-        for (int w = threadIdx.x; w < words; w += kThreads) bits[w] = 0;
-        __syncthreads();
-        int both = 0;
-        for (int i = threadIdx.x; i < p.k; i += kThreads) {
-            int32_t t = p.ids[m * p.k + i];
-            if (t < 0 || t >= p.V) t = -1;
-            id[i] = t;
-            if (t >= 0) {
-                both += 1 | ((atomicOr(&bits[t >> 5], 1u << (t & 31)) >> (t & 31) & 1) ? 0 : 1 << 16);
-                x[i] = value(X, t);
-            }
+    __device__ __forceinline__ void load(const DistillParams& p, const T* X, bool as_bits) {
+        if (as_bits) {
+            const int words = (int)((p.V + 31) / 32);
+            for (int w = threadIdx.x; w < words; w += kThreads) bits[w] = 0;
+            __syncthreads();
         }
-        both = block_sum(both, reinterpret_cast<int*>(fbuf));
-        count = both & 0xffff, distinct = both >> 16;
+        int named = 0, fresh = 0;
+        for (int i = threadIdx.x; i < p.k; i += kThreads) {
+            int32_t v = i < kThreads ? mine : id[i];
+            if (v < 0 || v >= p.V) v = -1;
+            id[i] = v;
+            if (v < 0) continue;
+            ++named;
+            if (as_bits) fresh += (atomicOr(&bits[v >> 5], 1u << (v & 31)) >> (v & 31) & 1) == 0;
+            if (i < kThreads) my_x = value(X, v);
+            else x[i] = value(X, v);
+        }
+        any = __syncthreads_or(named);
+        if (!as_bits) return;
+        twice = __syncthreads_or(named != fresh);
+        if (p.k >= p.V) {                                  // few tokens: are all of them named?
+            int left = 0;
+            for (int64_t v = threadIdx.x; v < p.V; v += kThreads) left |= !(bits[v >> 5] >> (v & 31) & 1);
+            every = !__syncthreads_or(left);
+        }
     }
-    __device__ __forceinline__ void weigh(const DistillParams& p, int64_t m) {
-        const float* t = p.t + m * p.k;
-        const double scale = (double)p.scale;
+    __device__ __forceinline__ void settle(const DistillParams& p) {
+        if ((int)threadIdx.x < p.k) q[threadIdx.x] = my_t, x[threadIdx.x] = my_x;
+    }
+    // One warp, after settle() and a barrier: the teacher's probabilities; each lane has its
+    // own of `each`, which is called with every entry, its logit and its probability.
+    template <typename F>
+    __device__ __forceinline__ void weigh(const DistillParams& p, int64_t m, F each) {
+        const int lane = threadIdx.x & 31;
         if (p.teacher_lse) {
-            shift = (double)p.teacher_lse[m];
+            shift = p.teacher_lse[m], shift_rest = 0.f;
         } else {
             float top = -INFINITY, s = 0.f;
-            for (int i = threadIdx.x; i < p.k; i += kThreads)
-                if (id[i] >= 0) top = fmaxf(top, t[i]);
-            top = block_max(top, fbuf);
-            for (int i = threadIdx.x; i < p.k; i += kThreads)
-                if (id[i] >= 0) s += exp64(((double)t[i] - (double)top) * scale);
-            s = block_sum(s, fbuf);
-            shift = top > -INFINITY ? (double)top * scale + log_sum(s) : 0.0;   // no entry with any weight: all q 0
+            for (int i = lane; i < p.k; i += 32)
+                if (id[i] >= 0) top = fmaxf(top, q[i]);
+            top = warp_max(top);
+            const float y = top * p.scale, rest = fmaf(top, p.scale, -y);
+            for (int i = lane; i < p.k; i += 32)
+                if (id[i] >= 0) s += exp_less(q[i], p.scale, y, rest);
+            s = warp_sum(s);
+            // no entry with any weight: all q 0
+            const double all = top > -INFINITY ? (double)top * (double)p.scale + log64((double)s) : 0.0;
+            shift = (float)all, shift_rest = (float)(all - (double)shift);
         }
         double sum = 0.0;
-        for (int i = threadIdx.x; i < p.k; i += kThreads) {
-            const float v = id[i] >= 0 ? exp64((double)t[i] * scale - shift) : 0.f;
+        for (int i = lane; i < p.k; i += 32) {
+            const float t = q[i], v = id[i] >= 0 ? exp_less(t, p.scale, shift, shift_rest) : 0.f;
             q[i] = v;
             sum += (double)v;
+            each(i, t, v);
         }
-        total = block_sum(sum, dbuf);
+        total = warp_sum(sum);
+        __syncwarp();
     }
     // What the tokens outside the entries are worth: 1 - sum q, none where every token is an entry.
     __device__ __forceinline__ double rest(const DistillParams& p) const {
-        return p.rest_lse && distinct < p.V ? fmax(1.0 - total, 0.0) : 0.0;
+        return p.rest_lse && !every ? fmax(1.0 - total, 0.0) : 0.0;
     }
     // Whether entry i is the first that names its token.
     __device__ __forceinline__ bool first(int i) const {
-        if (distinct < count)
+        if (twice)
             for (int j = 0; j < i; ++j)
                 if (id[j] == id[i]) return false;
         return true;
     }
 };
-size_t smem_bytes(int64_t k, int64_t V) { return kWarps * 12 + (size_t)k * 12 + (size_t)((V + 31) / 32) * 4; }
+size_t smem_bytes(int64_t k, int64_t V, bool bits) { return (size_t)k * 12 + (bits ? (size_t)((V + 31) / 32) * 4 : 0); }
 
 struct Sum {
     float top, sum;
@@ -284,11 +341,12 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
     int at = (int)((int64_t)chunks * rank / ranks);
     const int end = (int)((int64_t)chunks * (rank + 1) / ranks);
     at += threadIdx.x;
+    Entries n(smem, p, m);
     Chunk<T> now[kFlight];
     fetch(now, X, at, end);
-    Entries n(smem, p.k);
-    n.load(p, m, X);
-    const bool apart = p.rest_lse != nullptr, nobody = n.count == 0;
+    const bool apart = p.rest_lse != nullptr;
+    n.load(p, X, apart);
+    const bool nobody = !n.any;
     const Scale f(p.scale);
     Sum s{kLowest, 0.f};
     const uint8_t* named = reinterpret_cast<const uint8_t*>(n.bits);
@@ -307,16 +365,17 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
             most = fmaxf(most, now[u].most());
         }
         if (most > s.top) s.sum *= f.exp(s.top - most), s.top = most;
-        float part[kFlight];
+        uint64_t part[2] = {0, 0};
+        const uint64_t low = pk2(-s.top, -s.top);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            part[u] = 0.f;
 #pragma unroll
-            for (int e = 0; e < N; ++e) part[u] += f.exp(now[u].at(e) - s.top);
+            for (int e = 0; e < N / 2; ++e) part[u & 1] = add2(part[u & 1], f.exp(now[u].pair(e), low));
             now[u] = next[u];
         }
         // kLowest stands for what is not there: where nothing else is, its terms are not either
-        const float more = (part[0] + part[1]) + (part[2] + part[3]);
+        const float2 sums = sm100::f32x2_unpack(add2(part[0], part[1]));
+        const float more = sums.x + sums.y;
         if (s.top > kLowest || isnan(more)) s.sum += more;
     }
     const int last = chunks * N + (int)threadIdx.x;      // logits past the last whole 16 bytes
@@ -329,8 +388,8 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
         const float t = __shfl_xor_sync(0xffffffffu, s.top, o), v = __shfl_xor_sync(0xffffffffu, s.sum, o);
         s.add(t, v, f);
     }
-    __syncthreads();
     if (lane == 0) warps[warp] = s;
+    n.settle(p);
     __syncthreads();
     s = warps[0];
 #pragma unroll
@@ -342,45 +401,57 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
                                   sm100::f32x2_pack(__float_as_uint(s.top), __float_as_uint(s.sum)));
         sm100::cluster_arrive();
         sm100::cluster_wait();
-        if (rank > 0) return;
         s = Sum{kLowest, 0.f};
-        for (int r = 0; r < ranks; ++r) {
-            const float2 v = sm100::f32x2_unpack(parts[r]);
-            s.add(v.x, v.y, f);
-        }
+        if (rank == 0)
+            for (int r = 0; r < ranks; ++r) {
+                const float2 v = sm100::f32x2_unpack(parts[r]);
+                s.add(v.x, v.y, f);
+            }
     }
+    if (rank > 0 || warp > 0) return;
     if (nobody) {                                        // whatever the row holds
-        if (threadIdx.x == 0) {
+        if (lane == 0) {
             p.loss[m] = 0.f, p.lse[m] = 0.f;
             if (p.rest_lse) p.rest_lse[m] = 0.f;
         }
         return;
     }
-    n.weigh(p, m);
-    const double scale = (double)p.scale;
-    double lse = s.sum == 0.f ? -INFINITY : (double)s.top * scale + log_sum(s.sum);
-    const double rest = lse;
-    if (apart) {                                         // the entries, each token once
-        Sum in{kLowest, 0.f};
-        for (int i = threadIdx.x; i < p.k; i += kThreads)
-            if (n.id[i] >= 0 && n.x[i] != -INFINITY && n.first(i)) in.add(n.x[i], 1.f, f);
-        const float most = block_max(in.top, n.fbuf), sum = block_sum(in.sum * f.exp(in.top - most), n.fbuf);
-        if (sum != 0.f) {
-            const double inside = (double)most * scale + log_sum(sum), far = fmin(inside, rest) - fmax(inside, rest);
-            lse = fmax(inside, rest) + (far < -100.0 ? 0.0 : (double)log1pf(expf((float)far)));
-            if (isnan(sum) || isnan(s.sum)) lse = NAN;
-        }
+    // loss = scale sum_i q_i (t_i - x_i) + sum_i q_i (lse - shift) + q_r (log q_r - lse_r + lse):
+    // the differences in fp32, their weighted sums and the log-sums in 64 bits
+    double far = 0.0;
+    n.weigh(p, m, [&](int i, float t, float q) {
+        if (q > 0.f) far += (double)(q * (t - n.x[i]));
+    });
+    far = warp_sum(far);
+    const double scale = (double)p.scale, qr = n.rest(p);
+    float top = s.top, sum = 0.f;
+    bool above = false;
+    if (apart) {
+        // The entries, each token once, relative to the outside's reference, so that the
+        // whole's sum is that of the two: where the student is near, what the log-sums
+        // share cancels in the loss, and what they do not would stay.  Entries so far
+        // above that it would overflow: relative to their own maximum, and the outside
+        // adds nothing.
+        float most = kLowest;
+        for (int i = lane; i < p.k; i += 32)
+            if (n.id[i] >= 0) most = fmaxf(most, n.x[i]);
+        most = warp_max(most);
+        above = s.sum == 0.f || (most - s.top) * p.scale > 60.f;
+        if (above) top = most;
+        for (int i = lane; i < p.k; i += 32)
+            if (n.id[i] >= 0 && n.x[i] != -INFINITY && n.first(i)) sum += f.exp(n.x[i] - top);
+        sum = warp_sum(sum);
     }
-    double loss = 0.0;
-    for (int i = threadIdx.x; i < p.k; i += kThreads)
-        if (n.q[i] > 0.f)
-            loss += (double)n.q[i] * (((double)p.t[m * p.k + i] * scale - n.shift) - ((double)n.x[i] * scale - lse));
-    loss = block_sum(loss, n.dbuf);
-    if (threadIdx.x == 0) {
-        const double qr = n.rest(p);
-        if (qr > 0.0) loss += qr * ((double)logf((float)qr) - (rest - lse));
+    // three logarithms by three lanes: of the sums outside and of all, of the rest
+    const double all = isnan(s.sum) ? NAN : (double)sum + (above ? 0.0 : (double)s.sum);
+    const double v = log64(lane == 0 ? (double)s.sum : lane == 1 ? all : qr) +
+                     (lane == 0 ? (double)s.top * scale : lane == 1 ? (double)top * scale : 0.0);
+    const double lse = __shfl_sync(0xffffffffu, v, 1), log_qr = __shfl_sync(0xffffffffu, v, 2);
+    if (lane == 0) {
+        double loss = far * scale + n.total * ((lse - (double)n.shift) - (double)n.shift_rest);
+        if (qr > 0.0) loss += qr * (log_qr - (v - lse));
         p.loss[m] = (float)loss, p.lse[m] = (float)lse;
-        if (p.rest_lse) p.rest_lse[m] = (float)rest;
+        if (p.rest_lse) p.rest_lse[m] = (float)v;
     }
 }
 
@@ -388,6 +459,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 4)
 distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
     extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float factors[5];                         // outside: a exp(y - r); inside: g (Q exp(y - l) - q)
     constexpr int N = Chunk<T>::N;
     pdl_wait_then_release();
     const int rank = (int)(blockIdx.x % (unsigned)ranks);
@@ -399,24 +471,32 @@ distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
     // this CTA's logits, the last one's with what is past the last whole 16 bytes
     const int64_t lo = (int64_t)from * N, hi = rank == ranks - 1 ? p.V : (int64_t)end * N;
     int at = from + (int)threadIdx.x;
+    Entries n(smem, p, m);
     Chunk<T> now[kFlight];
     fetch(now, X, at, end);
-    Entries n(smem, p.k);
-    n.load(p, m, X);                                     // before any of this CTA's logits is overwritten
-    n.weigh(p, m);
-    const float c = p.scale * kLog2e;
-    float a = 0.f, r2 = 0.f, g = 0.f, Q = 0.f, l2 = 0.f;
-    if (n.count > 0) {
-        const float qr = (float)n.rest(p), lse = p.lse[m];
-        g = p.g[m] * p.scale, Q = (float)n.total + qr, l2 = lse * kLog2e;
-        a = g * Q, r2 = l2;
-        if (qr > 0.f && p.rest_lse[m] > -INFINITY) {
-            const float rest = p.rest_lse[m];
-            a = g * (Q * expf(rest - lse) - qr), r2 = rest * kLog2e;
+    n.load(p, X, true);
+    n.settle(p);                                         // the entries' logits are read before any of this CTA's is overwritten
+    __syncthreads();
+    if (threadIdx.x < 32 && n.any) {
+        n.weigh(p, m, [](int, float, float) {});
+        if (threadIdx.x == 0) {
+            const float qr = (float)n.rest(p), lse = p.lse[m], g = p.g[m] * p.scale, Q = (float)n.total + qr;
+            float a = g * Q, r2 = lse * kLog2e;
+            if (qr > 0.f && p.rest_lse[m] > -INFINITY) {
+                const float rest = p.rest_lse[m];
+                a = g * (Q * expf(rest - lse) - qr), r2 = rest * kLog2e;
+            }
+            factors[0] = a, factors[1] = r2, factors[2] = g, factors[3] = Q, factors[4] = lse * kLog2e;
         }
     }
-    const bool nobody = n.count == 0;                    // zeros, whatever the row holds
-    auto grad = [&](float x) { return nobody ? 0.f : a * ex2(fmaf(x, c, -r2)); };
+    __syncthreads();
+    const float c = p.scale * kLog2e, a = factors[0], r2 = factors[1], g = factors[2], Q = factors[3], l2 = factors[4];
+    if (!n.any) {                                        // zeros, whatever the row holds
+        for (; at < end; at += kThreads) __stcs(reinterpret_cast<uint4*>(D + (int64_t)at * N), make_uint4(0, 0, 0, 0));
+        for (int64_t v = (int64_t)end * N + threadIdx.x; v < hi; v += kThreads) put(D, v, 0.f);
+        return;
+    }
+    auto grad = [&](float x) { return a * ex2(fmaf(x, c, -r2)); };
     for (; at < end; at += kFlight * kThreads) {
         Chunk<T> next[kFlight];
         fetch(next, X, at + kFlight * kThreads, end);
@@ -427,16 +507,13 @@ distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
             now[u] = next[u];
         }
     }
-    if (chunks * (int64_t)N + threadIdx.x < hi && rank == ranks - 1) {
-        const int64_t v = chunks * (int64_t)N + threadIdx.x;
-        put(D, v, grad(value(X, v)));
-    }
+    for (int64_t v = (int64_t)end * N + threadIdx.x; v < hi; v += kThreads) put(D, v, grad(value(X, v)));
     __syncthreads();
     for (int i = threadIdx.x; i < p.k; i += kThreads) {
         const int64_t t = n.id[i];
         if (t < lo || t >= hi) continue;                 // -1 is below every CTA's
         float q = n.q[i];
-        if (n.distinct < n.count) {                      // a token named twice has both entries' weight
+        if (n.twice) {                                   // a token named twice has both entries' weight
             q = 0.f;
             for (int j = 0; j < p.k; ++j) q += n.id[j] == t ? n.q[j] : 0.f;
         }
@@ -466,13 +543,25 @@ cudaError_t ask() {
 cudaError_t launch(Kernel* f, const DistillParams& p, int per_load, bool cluster, cudaStream_t st) {
     const cudaError_t e = ask();
     if (e != cudaSuccess) return e;
-    // CTAs a row: while all of them find a place at once (four an SM; clusters of 16 only
-    // with an SM a CTA) and each thread keeps two loads
-    const int64_t sms = num_sms();
+    // CTAs a row: as many as make the least of the waves (four CTAs an SM; half a wave more
+    // where there is more than one) times a CTA's time, its bytes at its share of HBM's rate or
+    // at what its own loads in flight allow, and what comes before and after: some 2 us, with
+    // a cluster to join 4.5, in the gradient 1.5.  Measured (1, 2, 4, 8 CTAs a row, us): loss of
+    // 64 rows of 152064 bf16 20, 14, 13, 12, of 777 rows of 50257 27, 31, 43, 64, of 4096 of
+    // 152064 203, 247, 311, 452; gradient of the last 402, 392, 406, 481.  Clusters of 16 only
+    // with an SM a CTA, and each thread keeps two loads.
+    const int64_t sms = num_sms(), row = p.V / per_load * 16, bytes = cluster ? row : 2 * row;
     int ranks = 1;
-    while (2 * ranks <= kMostRanks && 2 * ranks * p.M <= (ranks == 8 ? sms : 4 * sms) && p.V / per_load >= 2 * ranks * kThreads)
-        ranks *= 2;
-    const size_t smem = smem_bytes(p.k, p.V);
+    double least = 1e30;
+    for (int r = 1; r <= kMostRanks; r *= 2) {
+        if (r > 1 && (row < (int64_t)r * 32 * kThreads || (r > 8 && r * p.M > sms))) break;
+        const int64_t ctas = r * p.M, slots = 4 * sms;
+        const double rate = std::min(cluster ? 20e3 : 36e3, 6.7e6 / (double)std::min(ctas, slots));   // bytes a us
+        const double waves = ctas <= slots ? 1.0 : (double)ctas / slots + 0.5;
+        const double cost = waves * ((double)bytes / r / rate + (cluster ? r > 1 ? 4.5 : 2.0 : 1.5));
+        if (cost < least) least = cost, ranks = r;
+    }
+    const size_t smem = smem_bytes(p.k, p.V, !cluster || p.rest_lse);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.M * ranks));
     cfg.blockDim = dim3(kThreads);

@@ -14,8 +14,8 @@
 // reduction a stage, six stages, and has 128 of the tile's rows in its tensor memory, two
 // tiles of them, so that one tile's threads' part runs under the next one's products.
 //
-// Forward (kLogp): tile by tile each row leaves its maximum, its sum of exponentials and
-// of weighted differences (12 bytes for 256 logits); logp_join_kernel joins a row's tiles.
+// Forward (kLogp): tile by tile each row leaves a maximum, its sum of exponentials and
+// of weighted differences (12 bytes for 128 logits); logp_join_kernel joins a row's tiles.
 // Backward: the vocabulary in pieces, two launches each.  kGrad writes a piece's D as bf16
 // (rounded once, relative to the call's largest |g| and |e|: a mean's gradient, 1/n
 // everywhere, is then exact); kBack multiplies it with W's rows (D as it lies, W with the
@@ -25,6 +25,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -39,19 +40,36 @@ namespace {
 constexpr uint32_t kKernelLogp = 10;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLog2eRest = 1.9259629911266175e-8f;   // log2(e) - kLog2e
+constexpr double kLn2 = 0.6931471805599453;
 
 constexpr int kTile = 256, kHalf = 128, kStep = 64;     // a pair's tile, a CTA's share, the reduction a stage
-constexpr int kStages = 6;
 constexpr int kPiece = 64 * 128;                        // 64 rows of 64 values, as the copy engine lays them
-constexpr int kStageBytes = 4 * kPiece;                 // two pieces of either operand
-constexpr int kEpiWarps = 4, kThreads = 32 * (4 + kEpiWarps);
 constexpr int kOutBytes = 32 * 128;                     // a warp's staging
-constexpr int kOutOffset = kStages * kStageBytes, kBarOffset = kOutOffset + kEpiWarps * kOutBytes;
-constexpr int kSmemBytes = kBarOffset + 256 + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 enum Mode { kLogp, kGrad, kBack };
+
+// kLogp: eight warps for the threads' part, half of a row a thread, in registers that the
+// other warps let go of; nothing is staged.  kGrad, kBack: four, a row a thread.
+template <Mode kMode>
+struct Config {
+    static constexpr bool kForward = kMode == kLogp;
+    static constexpr int kStages = kForward ? 6 : 5, kStageBytes = 4 * kPiece;   // two pieces of either operand
+    static constexpr int kEpiWarps = kForward ? 8 : 4, kThreads = 32 * (4 + kEpiWarps);
+    // boxes a warp stages at once: with one, each waits for the copy engine to have read the
+    // one before, 4 us a tile of dW
+    static constexpr int kOuts = kForward ? 0 : 4;
+    static constexpr int kOutOffset = kStages * kStageBytes;
+    static constexpr int kBarOffset = kOutOffset + kEpiWarps * kOuts * kOutBytes;
+    static constexpr int kSmemBytes = kBarOffset + 256 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+};
+constexpr int kLaunchRegs = 168, kOtherRegs = 40, kEpiRegs = 232;   // forward: registers a thread, at launch and after
+static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "the split must fit the launch's registers");
+
+// The tensor cores' fp32 sums lose a little to truncation at each step, towards zero: 5 of
+// 10^6 of a logit over 3584 products.  The forward takes them out of tensor memory every
+// 512 products at most and adds in registers, rounded to nearest (SEGMENT_FIGURES).  The gradient's logits meet a rounding of 2^-9 and are left as they are.
+constexpr int kSegment = 512 / kStep;
 
 // ------------------------------------------------------------------ pairs of CTAs
 
@@ -181,61 +199,105 @@ struct Work {
 
 // ------------------------------------------------------------------ a tile's threads' part
 
-// The running maximum of a row and its sums, of the unscaled logits: sum of exp(scale (x - top))
-// and of that times (x - top).
+// Of a row's logits y = scale log2(e) x: a reference, the sum of 2^(y - top) and that of
+// 2^(y - top) (y - top).
 struct Sums {
     float top = -3.0e38f, sum = 0.f, dev = 0.f;
+    __device__ __forceinline__ void add(float t, float s, float d) {
+        const float most = fmaxf(top, t), d0 = top - most, d1 = t - most, f0 = ex2(d0), f1 = ex2(d1);
+        dev = (sum > 0.f ? f0 * fmaf(d0, sum, dev) : 0.f) + (s > 0.f ? f1 * fmaf(d1, s, d) : 0.f);
+        sum = fmaf(f0, sum, f1 * s);
+        if (isnan(t)) sum = t;
+        top = most;
+    }
 };
-// exp(scale d), the constant in two parts: its rounding alone would be a change of temperature
-__device__ __forceinline__ float exp_scaled(float d, float c, float c_rest) { return ex2(fmaf(d, c, d * c_rest)); }
 
-__device__ __forceinline__ void add_sums(Sums& s, float top, float sum, float dev, float c, float c_rest) {
-    const float t = fmaxf(s.top, top);
-    const float d0 = s.top - t, d1 = top - t, f0 = exp_scaled(d0, c, c_rest), f1 = exp_scaled(d1, c, c_rest);
-    s.dev = fmaf(f0, fmaf(d0, s.sum, s.dev), f1 * fmaf(d1, sum, dev));
-    s.sum = fmaf(f0, s.sum, f1 * sum);
-    s.top = t;
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) { return f32x2_pack(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
+    const float2 f = f32x2_unpack(v);
+    return pk2(ex2(f.x), ex2(f.y));
 }
 
-// 32 logits of a row, of which the first n are there
-__device__ __forceinline__ void sums_of(Sums& s, const uint32_t (&r)[32], int n, float c, float c_rest, bool entropy) {
-    float most = s.top;
-    if (n >= 32) {
+// kCols logits of a row, of which the first n are there, two at a time
+template <int kCols, bool kDev>
+__device__ __forceinline__ void sums_of(Sums& s, const uint64_t (&x)[kCols / 2], int n, float c) {
+    float most = -3.0e38f;
+    if (n >= kCols) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) most = fmaxf(most, __uint_as_float(r[j]));
+        for (int j = 0; j < kCols / 2; ++j) {
+            const float2 v = f32x2_unpack(x[j]);
+            most = fmaxf(most, fmaxf(v.x, v.y));
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < n) most = fmaxf(most, __uint_as_float(r[j]));
+        for (int j = 0; j < kCols / 2; ++j) {
+            const float2 v = f32x2_unpack(x[j]);
+            if (2 * j < n) most = fmaxf(most, v.x);
+            if (2 * j + 1 < n) most = fmaxf(most, v.y);
+        }
     }
-    if (most > s.top) {
-        const float d = s.top - most, f = exp_scaled(d, c, c_rest);
-        s.dev = s.sum > 0.f ? f * fmaf(d, s.sum, s.dev) : 0.f;
-        s.sum *= f;
-        s.top = most;
-    }
-    float sum = 0.f, dev = 0.f;
+    s.top = most * c;
+    const uint64_t cc = pk2(c, c), low = pk2(-s.top, -s.top);
+    uint64_t sum = 0, dev = 0;
+    if (n >= kCols) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float d = __uint_as_float(r[j]) - most;
-        float e = exp_scaled(d, c, c_rest);
-        if (n < 32 && j >= n) e = 0.f;
-        sum += e;
-        if (entropy) dev = fmaf(e, d, dev);
+        for (int j = 0; j < kCols / 2; ++j) {
+            const uint64_t a = fma2(x[j], cc, low), e = ex2_2(a);
+            sum = add2(sum, e);
+            if (kDev) dev = fma2(e, a, dev);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j) {
+            const uint64_t a = fma2(x[j], cc, low);
+            float2 e = f32x2_unpack(ex2_2(a));
+            e.x = 2 * j < n ? e.x : 0.f, e.y = 2 * j + 1 < n ? e.y : 0.f;
+            sum = add2(sum, pk2(e.x, e.y));
+            const float2 d = f32x2_unpack(a);
+            if (kDev) dev = add2(dev, pk2(e.x > 0.f ? e.x * d.x : 0.f, e.y > 0.f ? e.y * d.y : 0.f));
+        }
     }
-    s.sum += sum, s.dev += dev;
+    const float2 t = f32x2_unpack(sum), d = f32x2_unpack(dev);
+    s.sum = t.x + t.y, s.dev = d.x + d.y;
 }
 
-// r[i] by masks: an index would put the values in memory
-__device__ __forceinline__ uint32_t pick(const uint32_t (&r)[32], int i) {
-    uint32_t x = 0;
+// x[i] by masks: an index would put the values in memory
+template <int kCols>
+__device__ __forceinline__ float pick(const uint64_t (&x)[kCols / 2], int i) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) {
+        uint32_t same;
+        asm("{\n.reg .pred p;\nsetp.eq.s32 p, %1, %2;\nselp.b32 %0, 0xFFFFFFFF, 0, p;\n}\n" : "=r"(same) : "r"(e), "r"(i));
+        const float2 v = f32x2_unpack(x[e / 2]);
+        r |= __float_as_uint(e & 1 ? v.y : v.x) & same;
+    }
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ float pick32(const float (&x)[32], int i) {
+    uint32_t r = 0;
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
         uint32_t same;
         asm("{\n.reg .pred p;\nsetp.eq.s32 p, %1, %2;\nselp.b32 %0, 0xFFFFFFFF, 0, p;\n}\n" : "=r"(same) : "r"(e), "r"(i));
-        x |= r[e] & same;
+        r |= __float_as_uint(x[e]) & same;
     }
-    return x;
+    return __uint_as_float(r);
 }
 __device__ __forceinline__ float mask01(int e, int i) {
     float f;
@@ -243,17 +305,25 @@ __device__ __forceinline__ float mask01(int e, int i) {
     return f;
 }
 
+// Wait until at most N of this thread's bulk groups have shared memory left to read.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N < 0 ? 0 : N) : "memory");
+}
 // A box of 32 rows of 128 bytes of a warp's own, one row a lane, staged under the 128-byte swizzle.
 __device__ __forceinline__ void stage16(uint8_t* out, int lane, int chunk, uint4 v) {
     *reinterpret_cast<uint4*>(out + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
 }
 
 template <Mode kMode>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Config<kMode>::kThreads, 1)
 logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpParams p) {
+    using C = Config<kMode>;
+    constexpr int kStages = C::kStages;
+    constexpr bool kForward = C::kForward;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOffset);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
@@ -271,13 +341,13 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, 2 * kEpiWarps);
+            mbar_init(tempty0 + 8 * b, 2 * C::kEpiWarps);
         }
         *abort = 0;
         fence_mbar_init();
         prefetch_tmap(&maps.h);
         prefetch_tmap(&maps.w);
-        if (kMode != kLogp) prefetch_tmap(&maps.d);
+        if (!kForward) prefetch_tmap(&maps.d);
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -295,6 +365,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
 
     Work<kMode> work(p);
     Unit u;
+    if (kForward && warp < 4) regs_dec<kOtherRegs>();
     if (warp == 0 && lane == 0) {
         // ---------------- loads: this CTA's rows of both operands
         const uint64_t keep = policy_evict_last(), once = policy_evict_first();
@@ -304,30 +375,36 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
             const CUtensorMap* ma = kMode != kBack ? &maps.h : &maps.d;
             const CUtensorMap* mb = kMode != kBack || u.kind == 1 ? &maps.w : &maps.h;
             const int a = u.a + (int)rank * kHalf, b = u.b + (int)rank * kHalf + (kMode != kBack ? p.first : 0);
+            // Rows past those that count: 64 of them at once are left as they are in shared
+            // memory (whatever that makes of their products reaches no other row, and nobody
+            // reads theirs), which is faster than filling in zeros: one row 309 -> 175 us.
+            const bool by_row = kMode != kBack || u.kind == 1;
+            const int pieces = by_row ? min(2, max(0, (work.live - a + 63) / 64)) : 2;
+            const int other = by_row ? min(2, max(0, (work.live - a - kHalf + 63) / 64)) : 2;
+            const uint32_t bytes = (uint32_t)(4 + pieces + other) * kPiece;
             for (int k = 0; k < u.n; ++k, ++it) {
                 const int s = it % kStages;
                 if (!mbar_wait_bounded(empty0 + 8 * s, ((it / kStages) & 1) ^ 1, abort, kWaitLimitNs)) {
                     gave_up(1);
                     break;
                 }
-                const uint32_t dst = smem_u32(smem + s * kStageBytes), bar = bar0 + 8 * s;
-                if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * kStageBytes);
+                const uint32_t dst = smem_u32(smem + s * C::kStageBytes), bar = bar0 + 8 * s;
+                if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
                 const int at = (u.k + k) * kStep;
-                if (kMode != kBack) {
-                    pair_load(dst, ma, bar, at, a, keep);
-                    pair_load(dst + kPiece, ma, bar, at, a + 64, keep);
-                    pair_load(dst + 2 * kPiece, mb, bar, at, b, once);
-                    pair_load(dst + 3 * kPiece, mb, bar, at, b + 64, once);
-                } else if (u.kind == 1) {
-                    pair_load(dst, ma, bar, at, a, keep);
-                    pair_load(dst + kPiece, ma, bar, at, a + 64, keep);
-                    pair_load(dst + 2 * kPiece, mb, bar, b, p.first + at, keep);
-                    pair_load(dst + 3 * kPiece, mb, bar, b + 64, p.first + at, keep);
+                if (by_row) {
+                    if (pieces > 0) pair_load(dst, ma, bar, at, a, keep);
+                    if (pieces > 1) pair_load(dst + kPiece, ma, bar, at, a + 64, keep);
                 } else {
                     pair_load(dst, ma, bar, a, at, keep);
                     pair_load(dst + kPiece, ma, bar, a + 64, at, keep);
-                    pair_load(dst + 2 * kPiece, mb, bar, b, at, keep);
-                    pair_load(dst + 3 * kPiece, mb, bar, b + 64, at, keep);
+                }
+                if (kMode != kBack) {
+                    pair_load(dst + 2 * kPiece, mb, bar, at, b, once);
+                    pair_load(dst + 3 * kPiece, mb, bar, at, b + 64, once);
+                } else {
+                    const int y = u.kind == 1 ? p.first + at : at;
+                    pair_load(dst + 2 * kPiece, mb, bar, b, y, keep);
+                    pair_load(dst + 3 * kPiece, mb, bar, b + 64, y, keep);
                 }
             }
         }
@@ -338,51 +415,111 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
         // ---------------- products, for both CTAs
         uint32_t it = 0, tile = 0;
         while (!*abort && work.next(u)) {
-            if (u.n == 0) continue;
-            const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
-            ++tile;
-            if (!mbar_wait_bounded(tempty0 + 8 * buf, use ^ 1, abort, kWaitLimitNs)) {
-                gave_up(3);
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem + buf * kTile;
             const bool a_mn = kMode == kBack && u.kind == 2, b_mn = kMode == kBack;
             const uint32_t idesc = kIdesc | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
             const uint64_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
-            for (int k = 0; k < u.n; ++k, ++it) {
-                const int s = it % kStages;
-                if (!mbar_wait_bounded(full0 + 8 * s, (it / kStages) & 1, abort, kWaitLimitNs)) {
-                    gave_up(2);
+            const int segment = kForward ? p.segment : u.n;
+            for (int k0 = 0; k0 < u.n && !*abort; k0 += segment) {
+                const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+                ++tile;
+                if (!mbar_wait_bounded(tempty0 + 8 * buf, use ^ 1, abort, kWaitLimitNs)) {
+                    gave_up(3);
                     break;
                 }
                 tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * kStageBytes);
-                const uint64_t ad = a_mn ? desc_mn(st) : umma_desc_k128_sw128(st);
-                const uint64_t bd = b_mn ? desc_mn(st + 2 * kPiece) : umma_desc_k128_sw128(st + 2 * kPiece);
+                const uint32_t d = tmem + buf * kTile;
+                const int end = min(u.n, k0 + segment);
+                for (int k = k0; k < end; ++k, ++it) {
+                    const int s = it % kStages;
+                    if (!mbar_wait_bounded(full0 + 8 * s, (it / kStages) & 1, abort, kWaitLimitNs)) {
+                        gave_up(2);
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * C::kStageBytes);
+                    const uint64_t ad = a_mn ? desc_mn(st) : umma_desc_k128_sw128(st);
+                    const uint64_t bd = b_mn ? desc_mn(st + 2 * kPiece) : umma_desc_k128_sw128(st + 2 * kPiece);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) pair_mma(d, ad + j * a_step, bd + j * b_step, idesc, k > 0 || j > 0);
-                pair_commit(empty0 + 8 * s);
+                    for (int j = 0; j < 4; ++j) pair_mma(d, ad + j * a_step, bd + j * b_step, idesc, k > k0 || j > 0);
+                    pair_commit(empty0 + 8 * s);
+                }
+                pair_commit(tfull0 + 8 * buf);
             }
-            pair_commit(tfull0 + 8 * buf);
         }
-    } else if (warp >= 4) {
+    } else if (kForward && warp >= 4) {
+        // ---------------- the tile's threads' part: half of a row a thread
+        if constexpr (kForward) {
+            regs_inc<kEpiRegs>();
+            const int q = warp & 3, half = (int)(warp - 4) >> 2, row = 32 * q + (int)lane;
+            const uint32_t empty_bar = map_to_rank(tempty0, 0);
+            const float c = p.scale * kLog2e;
+            const int64_t size = (int64_t)p.parts * p.rows_pad;
+            uint32_t tile = 0;
+            bool ok = true;
+            while (ok && work.next(u)) {
+                const int m = u.a + (int)rank * kHalf + row;             // the row among those that count
+                const int t = p.row_target[m] - u.b - half * kHalf, cols = (int)p.V - u.b - half * kHalf;
+                uint64_t x[kHalf / 2];
+                for (int k0 = 0; k0 < u.n; k0 += p.segment, ++tile) {
+                    const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
+                        if (lane == 0) gave_up(4);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile + half * kHalf;
+#pragma unroll
+                    for (int j = 0; j < kHalf; j += 32) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(taddr + j, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint64_t v = f32x2_pack(r[2 * e], r[2 * e + 1]);
+                            x[j / 2 + e] = k0 == 0 ? v : add2(x[j / 2 + e], v);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+                }
+                if (!ok) break;
+                Sums s;
+                if (cols > 0) {
+                    if (p.entropy) sums_of<kHalf, true>(s, x, cols, c);
+                    else sums_of<kHalf, false>(s, x, cols, c);
+                    if (t >= 0 && t < kHalf) p.picked[m] = pick<kHalf>(x, t);
+                }
+                float* part = p.part + (int64_t)(2 * u.slot + half) * p.rows_pad + m;
+                part[0] = s.top, part[size] = s.sum;
+                if (p.entropy) part[2 * size] = s.dev;
+            }
+        }
+    } else if (!kForward && warp >= 4) {
         // ---------------- the tile's threads' part: a row a thread
         const int q = warp & 3, row = 32 * q + (int)lane;
-        uint8_t* out = smem + kOutOffset + q * kOutBytes;
+        uint8_t* const outs = smem + C::kOutOffset + q * C::kOuts * kOutBytes;
+        uint32_t box = 0;
+        // the next buffer, once the copy engine has read what was in it
+        auto next_out = [&]() {
+            if (lane == 0) bulk_wait_read<C::kOuts - 1>();
+            __syncwarp();
+            return outs + box++ % C::kOuts * kOutBytes;
+        };
         const uint32_t empty_bar = map_to_rank(tempty0, 0);
-        const float c = p.scale * kLog2e, c_rest = fmaf(p.scale, kLog2e, -c) + p.scale * kLog2eRest;
+        const float c = p.scale * kLog2e;
         uint32_t tile = 0;
         while (work.next(u)) {
             const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
-            const int m = u.a + (int)rank * kHalf + row;                 // kLogp, kGrad: the row among those that count
+            const int m = u.a + (int)rank * kHalf + row;                 // kGrad: the row among those that count
             const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile;
             // per row, before the wait
             float g = 0.f, ge = 0.f, l2 = 0.f, plus = 0.f;
             int t = -1;
-            if (kMode != kBack) {
+            if (kMode == kGrad) {
                 t = p.row_target[m] - p.first - u.b;
-                if (kMode == kGrad) g = p.row_g[m], ge = p.row_ge[m], l2 = p.row_lse[m] * kLog2e, plus = p.row_entropy[m];
+                g = p.row_g[m], ge = p.row_ge[m], l2 = p.row_lse[m] * kLog2e, plus = p.row_entropy[m];
             }
             const float f = kMode == kBack ? *p.largest * p.scale : 0.f;
             if (u.n > 0) {
@@ -393,26 +530,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 }
                 tc_fence_after();
             }
-            if constexpr (kMode == kLogp) {
-                Sums s;
-                const int cols = min(kTile, (int)p.V - u.b);
-#pragma unroll 1
-                for (int j = 0; j < kTile; j += 32) {
-                    if (j >= cols) break;
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(taddr + j, r);
-                    tmem_wait_ld();
-                    sums_of(s, r, cols - j, c, c_rest, p.entropy != nullptr);
-                    if (t >= j && t < j + 32) p.picked[m] = __uint_as_float(pick(r, t - j));
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) pair_arrive(empty_bar + 8 * buf);
-                float* part = p.part + (int64_t)u.slot * p.rows_pad + m;
-                const int64_t size = (int64_t)p.tiles * p.rows_pad;
-                part[0] = s.top, part[size] = s.sum;
-                if (p.entropy) part[2 * size] = s.dev;
-            } else if constexpr (kMode == kGrad) {
+            if constexpr (kMode == kGrad) {
                 const int cols = min(kTile, (int)(p.V - p.first) - u.b);
                 const bool entropy = p.ge != nullptr;
 #pragma unroll 1
@@ -425,12 +543,15 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                         tmem_wait_ld();
                         const int j0 = j + 32 * h;
                         float v[32];
+                        const uint64_t cc = pk2(c, c), low = pk2(-l2, -l2), ng = pk2(-g, -g), ng2 = pk2(-ge, -ge);
+                        const uint64_t ln2 = pk2(0.69314718f, 0.69314718f), pl = pk2(plus, plus);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float x = __uint_as_float(r[e]);
-                            const float a = fmaf(x, c, fmaf(x, c_rest, -l2)), pr = ex2(a);
-                            v[e] = -g * pr;
-                            if (entropy) v[e] = fmaf(-ge * pr, fmaf(a, 0.69314718f, plus), v[e]);
+                        for (int e = 0; e < 16; ++e) {
+                            const uint64_t a = fma2(f32x2_pack(r[2 * e], r[2 * e + 1]), cc, low), pr = ex2_2(a);
+                            uint64_t d = mul2(ng, pr);
+                            if (entropy) d = fma2(mul2(ng2, pr), fma2(a, ln2, pl), d);
+                            const float2 two = f32x2_unpack(d);
+                            v[2 * e] = two.x, v[2 * e + 1] = two.y;
                         }
                         if (t >= j0 && t < j0 + 32) {
 #pragma unroll
@@ -449,8 +570,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                         __syncwarp();
                         if (lane == 0) pair_arrive(empty_bar + 8 * buf);
                     }
-                    if (lane == 0) bulk_wait_read_all();                 // the box before has left the buffer
-                    __syncwarp();
+                    uint8_t* out = next_out();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         stage16(out, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
@@ -473,17 +593,18 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                         __syncwarp();
                         if (lane == 0) pair_arrive(empty_bar + 8 * buf);
                     }
-                    if (lane == 0) bulk_wait_read_all();
-                    __syncwarp();
+                    uint8_t* out = next_out();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) stage16(out, lane, e, make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]));
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && u.b + j < p.K) {
+                    if (lane == 0) {
                         const int y = u.slot * p.rows_pad + u.a + (int)rank * kHalf + 32 * q;
-                        if (p.first == 0) tma_store_2d(&maps.acc, smem_u32(out), u.b + j, y);
-                        else tma_add_2d(&maps.acc, smem_u32(out), u.b + j, y);
-                        bulk_commit();
+                        if (u.b + j < p.K) {
+                            if (p.first == 0) tma_store_2d(&maps.acc, smem_u32(out), u.b + j, y);
+                            else tma_add_2d(&maps.acc, smem_u32(out), u.b + j, y);
+                        }
+                        bulk_commit();                                   // a group a buffer, empty or not
                     }
                 }
             } else {
@@ -509,16 +630,15 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                         __syncwarp();
                         if (lane == 0) pair_arrive(empty_bar + 8 * buf);
                     }
-                    if (lane == 0) bulk_wait_read_all();
-                    __syncwarp();
+                    uint8_t* out = next_out();
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         stage16(out, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
                     fence_proxy_async_smem();
                     __syncwarp();
                     const int y = p.first + u.a + (int)rank * kHalf + 32 * q;
-                    if (lane == 0 && u.b + j < p.K && y < p.V) {
-                        tma_store_2d(&maps.dw, smem_u32(out), u.b + j, y);
+                    if (lane == 0) {
+                        if (u.b + j < p.K && y < p.V) tma_store_2d(&maps.dw, smem_u32(out), u.b + j, y);
                         bulk_commit();
                     }
                 }
@@ -537,6 +657,234 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
     }
 }
 
+// ------------------------------------------------------------------ few rows
+
+// Up to 128 rows: a pass over W that HBM bounds, so the roles change: W's rows are the
+// products' 256, 128 a CTA, the rows that count their 64 or 128 columns, and nearly all of
+// shared memory holds W on its way (11 stages of 16 KB of it, 9 with 128 columns; with rows
+// on the other side it was 6, every product was made for 256 rows, and 48 rows of
+// 152064 x 5120 took 272 us).  A thread has a word of the vocabulary and 32 columns at a time; a
+// column's maximum and sums over a warp's 32 words meet by exchanges that halve the
+// columns at each step, so that lane l ends up with column l, whose sums it keeps over
+// all of its warp's tiles.  W's first stages are loaded before the wait for rows_kernel.
+template <int kN>
+struct FewConfig {
+    static constexpr int kRows = kN / 2;                                  // of H, a CTA's
+    static constexpr int kStageBytes = kHalf * 128 + kRows * 128, kStages = kN == 64 ? 11 : 9;
+    static constexpr int kGroups = kN / 64;                               // of 32 columns, a warp's
+    static constexpr int kThreads = 32 * 12, kBarOffset = kStages * kStageBytes, kSmemBytes = kBarOffset + 256 + 1024;
+    static constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(kN >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
+    static constexpr uint32_t kCols = 2 * kN;
+    static_assert(kSmemBytes <= 232448 && kStageBytes % 1024 == 0, "shared memory per CTA");
+};
+
+// r[j] of every lane to op over the lanes of r[l] in lane l
+template <typename F>
+__device__ __forceinline__ float across(float (&r)[32], int lane, F op) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+            const float keep = upper ? r[j + o] : r[j], send = upper ? r[j] : r[j + o];
+            r[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+    }
+    return r[0];
+}
+
+template <int kN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FewConfig<kN>::kThreads, 1)
+logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpParams p) {
+    using C = FewConfig<kN>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
+    const uint32_t tfull0 = smem_u32(bars + 2 * kStages), tempty0 = smem_u32(bars + 2 * kStages + 2);
+    const uint32_t warp = warp_id(), lane = lane_id(), rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    auto gave_up = [&](uint32_t site) {
+        atomicCAS(p.err, 0u, kKernelLogp << 24 | site << 16 | 1u);
+        *abort = 1;
+    };
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull0 + 8 * b, 1);
+            mbar_init(tempty0 + 8 * b, 2 * 8);
+        }
+        *abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&maps.h);
+        prefetch_tmap(&maps.w);
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(C::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0 && lane == 0) {
+        // ---------------- loads; step i of this pair: step i % ksteps of its tile i / ksteps
+        const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+        const uint32_t bar0 = map_to_rank(full0, 0);
+        const int mine = pair < p.tiles ? (p.tiles - pair + pairs - 1) / pairs : 0;
+        const uint32_t total = (uint32_t)mine * p.ksteps, early = min(total, (uint32_t)kStages);
+        auto load_w = [&](uint32_t i) {
+            const int s = i % kStages, at = (int)(i % p.ksteps) * kStep;
+            const int v = (pair + (int)(i / p.ksteps) * pairs) * kTile + (int)rank * kHalf;
+            const uint32_t dst = smem_u32(smem + s * C::kStageBytes), bar = bar0 + 8 * s;
+            if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * C::kStageBytes);
+            pair_load(dst, &maps.w, bar, at, v, once);
+            pair_load(dst + kPiece, &maps.w, bar, at, v + 64, once);
+        };
+        auto load_h = [&](uint32_t i) {
+            const int s = i % kStages, at = (int)(i % p.ksteps) * kStep;
+            pair_load(smem_u32(smem + s * C::kStageBytes) + 2 * kPiece, &maps.h, bar0 + 8 * s, at, (int)rank * C::kRows, keep);
+        };
+        // (rows_kernel writes no W, and whatever came before it has ended)
+        for (uint32_t i = 0; i < early; ++i) load_w(i);
+        grid_dependency_wait();
+        grid_launch_dependents();
+        for (uint32_t i = 0; i < early; ++i) load_h(i);
+        uint32_t it = early;
+        for (; it < total && !*abort; ++it) {
+            if (!mbar_wait_bounded(empty0 + 8 * (it % kStages), ((it / kStages) & 1) ^ 1, abort, kWaitLimitNs)) {
+                gave_up(1);
+                break;
+            }
+            load_w(it);
+            load_h(it);
+        }
+        if (*abort && rank == 0)
+            for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
+                mbar_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kWaitLimitNs);
+    } else {
+        grid_dependency_wait();
+        grid_launch_dependents();
+        if (warp == 1 && lane == 0 && rank == 0) {
+            uint32_t it = 0, tile = 0;
+            for (int v = pair; v < p.tiles && !*abort; v += pairs)
+                for (int k0 = 0; k0 < p.ksteps && !*abort; k0 += p.segment, ++tile) {
+                    const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+                    if (!mbar_wait_bounded(tempty0 + 8 * buf, use ^ 1, abort, kWaitLimitNs)) {
+                        gave_up(3);
+                        break;
+                    }
+                    tc_fence_after();
+                    const int end = min(p.ksteps, k0 + p.segment);
+                    for (int k = k0; k < end; ++k, ++it) {
+                        const int s = it % kStages;
+                        if (!mbar_wait_bounded(full0 + 8 * s, (it / kStages) & 1, abort, kWaitLimitNs)) {
+                            gave_up(2);
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t st = smem_u32(smem + s * C::kStageBytes);
+                        const uint64_t a = umma_desc_k128_sw128(st), b = umma_desc_k128_sw128(st + 2 * kPiece);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            pair_mma(tmem + buf * kN, a + 2 * j, b + 2 * j, C::kIdesc, k > k0 || j > 0);
+                        pair_commit(empty0 + 8 * s);
+                    }
+                    pair_commit(tfull0 + 8 * buf);
+                }
+        } else if (warp >= 4) {
+            const int q = warp & 3, half = (int)(warp - 4) >> 2;
+            const uint32_t empty_bar = map_to_rank(tempty0, 0);
+            const float c = p.scale * kLog2e;
+            const bool dev = p.entropy != nullptr;
+            constexpr float kNone = -3.0e38f;
+            Sums s[C::kGroups];
+            int target[C::kGroups];
+#pragma unroll
+            for (int g = 0; g < C::kGroups; ++g) target[g] = p.row_target[half * (kN / 2) + g * 32 + (int)lane];
+            uint32_t tile = 0;
+            bool ok = true;
+            for (int v = pair; v < p.tiles && ok; v += pairs) {
+                const int word0 = v * kTile + (int)rank * kHalf + 32 * q;
+                const bool there = word0 + (int)lane < p.V;
+                float x[C::kGroups][32];
+                for (int k0 = 0; k0 < p.ksteps; k0 += p.segment, ++tile) {
+                    const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
+                        if (lane == 0) gave_up(4);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int g = 0; g < C::kGroups; ++g) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + buf * kN + half * (kN / 2) + g * 32, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[g][e] = k0 == 0 ? __uint_as_float(r[e]) : x[g][e] + __uint_as_float(r[e]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int g = 0; g < C::kGroups; ++g) {
+                    float w[32];
+                    // a target among this warp's words: its logit to its row
+                    uint32_t hits = __ballot_sync(0xffffffffu, target[g] >= word0 && target[g] < word0 + 32);
+                    while (hits) {
+                        const int j = __ffs((int)hits) - 1;
+                        hits &= hits - 1;
+                        const int owner = __shfl_sync(0xffffffffu, target[g], j) - word0;
+                        if ((int)lane == owner) p.picked[half * (kN / 2) + g * 32 + j] = pick32(x[g], j);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) w[e] = there ? x[g][e] : kNone;
+                    const float top = across(w, lane, [](float a, float b) { return fmaxf(a, b); }) * c;
+                    float d[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float a = fmaf(x[g][e], c, -__shfl_sync(0xffffffffu, top, e));
+                        w[e] = there ? ex2(a) : 0.f;
+                        d[e] = w[e] > 0.f ? w[e] * a : 0.f;
+                    }
+                    const auto plus = [](float a, float b) { return a + b; };
+                    const float sum = across(w, lane, plus), weighted = dev ? across(d, lane, plus) : 0.f;
+                    if (word0 < p.V) s[g].add(top, sum, weighted);
+                }
+            }
+            // this warp's part of its columns: one of 8 a pair
+            const int64_t size = (int64_t)8 * pairs * p.rows_pad, at = (int64_t)(8 * pair + 4 * (int)rank + q) * p.rows_pad;
+#pragma unroll
+            for (int g = 0; g < C::kGroups; ++g) {
+                float* part = p.part + at + half * (kN / 2) + g * 32 + lane;
+                part[0] = s[g].top, part[size] = s[g].sum;
+                if (dev) part[2 * size] = s[g].dev;
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 2) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
+    }
+}
+
 // ------------------------------------------------------------------ before and after the products
 
 __device__ __forceinline__ bool counts(const LogpParams& p, int64_t m) { return p.targets[m] >= 0 && p.targets[m] < p.V; }
@@ -552,7 +900,7 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
     __shared__ int place[kMostRows], before_w[8], all_w[8];
     __shared__ float largest_w[8];
     pdl_wait_then_release();
-    const int M = (int)p.M, m0 = blockIdx.x * rows, mine = min(rows, M - m0);
+    const int M = (int)p.M, m0 = blockIdx.x * rows, mine = max(0, min(rows, M - m0));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int before = 0, all = 0;
     float largest = 0.f;
@@ -610,47 +958,62 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
         uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.K);
         for (int i = lane; i < chunks; i += 32) dst[i] = ld_stream_v4(src + i);
     }
-    // up to the last tile's edge: no target, no gradient, and zeros (past M the copy engine fills them in)
-    const int edge = (all + kTile - 1) / kTile * kTile;
-    for (int at = all + blockIdx.x; at < edge; at += gridDim.x) {
-        if (threadIdx.x == 0) {
-            p.row_target[at] = -1;
-            if (kBackward) p.row_g[at] = 0.f, p.row_ge[at] = 0.f, p.row_lse[at] = 0.f, p.row_entropy[at] = 0.f;
-        }
-        if (at < M) {
-            uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.K);
-            for (int i = threadIdx.x; i < chunks; i += kRowThreads) dst[i] = make_uint4(0, 0, 0, 0);
-        }
+    // up to the last tile's edge no target and no gradient; hidden states of zeros up to the
+    // last 64 rows' end (past M the copy engine fills them in; further ones are not loaded),
+    // for a few rows up to all of their columns' (which is faster)
+    const int edge = (all + kTile - 1) / kTile * kTile, zeros = p.zeros ? p.zeros : min(M, (all + 63) / 64 * 64);
+    if (blockIdx.x == 0 && all + (int)threadIdx.x < edge) {
+        const int at = all + threadIdx.x;
+        p.row_target[at] = -1;
+        if (kBackward) p.row_g[at] = 0.f, p.row_ge[at] = 0.f, p.row_lse[at] = 0.f, p.row_entropy[at] = 0.f;
+    }
+    for (int at = all + blockIdx.x; at < zeros; at += gridDim.x) {
+        uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.K);
+        for (int i = threadIdx.x; i < chunks; i += kRowThreads) dst[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
-// Joins a row's tiles: a row a lane, a part of the tiles a warp.
-constexpr int kJoinWarps = 16;
+// Joins a row's tiles: eight rows a CTA (a sector of each array), a 64th of the tiles a thread.
+constexpr int kJoinThreads = 512, kJoinRows = 8;
 
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(kJoinThreads)
 logp_join_kernel(const __grid_constant__ LogpParams p) {
-    __shared__ Sums part[kJoinWarps][32];
+    __shared__ Sums part[kJoinThreads / 32][kJoinRows];
     pdl_wait_then_release();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int live = *p.live, m = blockIdx.x * 32 + lane;
-    if (blockIdx.x * 32 >= live) return;
-    const float c = p.scale * kLog2e, c_rest = fmaf(p.scale, kLog2e, -c) + p.scale * kLog2eRest;
-    const int64_t size = (int64_t)p.tiles * p.rows_pad;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x % kJoinRows;
+    const int live = *p.live, m = blockIdx.x * kJoinRows + r;
+    if (blockIdx.x * kJoinRows >= live) return;
+    const int64_t size = (int64_t)p.parts * p.rows_pad;
+    const bool dev = p.entropy != nullptr;
     Sums s;
-    if (m < live)
-        for (int t = warp; t < p.tiles; t += kJoinWarps) {
-            const float* at = p.part + (int64_t)t * p.rows_pad + m;
-            add_sums(s, at[0], at[size], p.entropy ? at[2 * size] : 0.f, c, c_rest);
+    if (m < live) {
+        constexpr int kStride = kJoinThreads / kJoinRows;
+        for (int t = threadIdx.x / kJoinRows; t < p.parts; t += 4 * kStride) {
+            float v[4][3];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool there = t + u * kStride < p.parts;
+                const float* at = p.part + (int64_t)(t + u * kStride) * p.rows_pad + m;
+                v[u][0] = there ? at[0] : -3.0e38f, v[u][1] = there ? at[size] : 0.f, v[u][2] = there && dev ? at[2 * size] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s.add(v[u][0], v[u][1], v[u][2]);
         }
-    part[warp][lane] = s;
+    }
+#pragma unroll
+    for (int o = kJoinRows; o < 32; o *= 2)
+        s.add(__shfl_xor_sync(0xffffffffu, s.top, o), __shfl_xor_sync(0xffffffffu, s.sum, o),
+              __shfl_xor_sync(0xffffffffu, s.dev, o));
+    if (lane < kJoinRows) part[warp][lane] = s;
     __syncthreads();
-    if (warp > 0 || m >= live) return;
-    for (int w = 1; w < kJoinWarps; ++w) add_sums(s, part[w][lane].top, part[w][lane].sum, part[w][lane].dev, c, c_rest);
+    if (threadIdx.x >= kJoinRows || m >= live) return;
+    for (int w = 1; w < kJoinThreads / 32; ++w) s.add(part[w][r].top, part[w][r].sum, part[w][r].dev);
     const float ls = logf(s.sum);
+    const double lse = (double)s.top * kLn2 + (double)ls;
     const int row = p.row_of[m];
-    p.logp[row] = (float)((double)p.scale * ((double)p.picked[m] - (double)s.top) - (double)ls);
-    p.lse[row] = (float)((double)p.scale * (double)s.top + (double)ls);
-    if (p.entropy) p.entropy[row] = ls - p.scale * s.dev / s.sum;
+    p.logp[row] = (float)((double)p.scale * (double)p.picked[m] - lse);
+    p.lse[row] = (float)lse;
+    if (dev) p.entropy[row] = ls - (float)kLn2 * s.dev / s.sum;
 }
 
 // dH from its fp32 sums, a row a CTA
@@ -674,6 +1037,8 @@ grad_h_kernel(const __grid_constant__ LogpParams p) {
 
 // ------------------------------------------------------------------ host
 
+constexpr int64_t kFewRows = 128;
+
 constexpr int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 // A workspace's parts, 256 bytes apart.
@@ -692,13 +1057,14 @@ void lay_rows(Arena& a, LogpParams& p) {
     p.rows_pad = (int)up(p.M, kTile);
     p.live = a.take<int>(1), p.largest = a.take<float>(1);
     p.row_of = a.take<int>(p.rows_pad), p.row_target = a.take<int>(p.rows_pad);
-    p.rows_h = a.take<uint16_t>(p.M * p.K);
+    p.rows_h = a.take<uint16_t>(std::max<int64_t>(p.M, kFewRows) * p.K);
 }
-void lay_forward(Arena& a, LogpParams& p) {
+void lay_forward(Arena& a, LogpParams& p, int pairs) {
     lay_rows(a, p);
     p.tiles = (int)((p.V + kTile - 1) / kTile);
     p.picked = a.take<float>(p.rows_pad);
-    p.part = a.take<float>(3 * (int64_t)p.tiles * p.rows_pad);
+    p.parts = p.M <= kFewRows ? std::max(8 * pairs, 2 * p.tiles) : 2 * p.tiles;
+    p.part = a.take<float>(3 * (int64_t)p.parts * p.rows_pad);
 }
 
 // The backward's pieces of the vocabulary: D of a piece is at most 128 MB, about what stays
@@ -732,12 +1098,12 @@ void lay_backward(Arena& a, LogpParams& p, int pairs) {
     p.acc = a.take<float>((int64_t)p.split * p.rows_pad * p.K);
 }
 
-template <typename K>
-cudaError_t launch_pairs(K kernel, int pairs, cudaStream_t st, const Maps& maps, const LogpParams& p) {
+cudaError_t launch_clusters(void (*kernel)(Maps, LogpParams), int pairs, int threads, int smem, cudaStream_t st,
+                            const Maps& maps, const LogpParams& p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -746,30 +1112,55 @@ cudaError_t launch_pairs(K kernel, int pairs, cudaStream_t st, const Maps& maps,
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
+template <Mode kMode>
+cudaError_t launch_pairs(int pairs, cudaStream_t st, const Maps& maps, const LogpParams& p) {
+    return launch_clusters(logp_pair_kernel<kMode>, pairs, Config<kMode>::kThreads, Config<kMode>::kSmemBytes, st, maps, p);
+}
+template <int kN>
+cudaError_t launch_few(int pairs, cudaStream_t st, const Maps& maps, const LogpParams& p) {
+    using C = FewConfig<kN>;
+    return launch_clusters(logp_few_kernel<kN>, std::min(pairs, p.tiles), C::kThreads, C::kSmemBytes, st, maps, p);
+}
 
+int pairs_of(void (*kernel)(Maps, LogpParams), int threads, int smem, int regs) {
+    cudaFuncAttributes fa;
+    // a split of registers (regs > 0) is made for just that many a thread at launch: with
+    // others the threads' part could wait for registers for ever
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || (regs && fa.numRegs != regs) ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 512);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
 // Pairs of CTAs that run at once on the current device; 0: the kernels do not run there.
 int pairs_here() {
-    static int known[64] = {};
+    static std::atomic<int> known[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (!known[dev]) {
-        void (*all[])(Maps, LogpParams) = {logp_pair_kernel<kLogp>, logp_pair_kernel<kGrad>, logp_pair_kernel<kBack>};
-        for (auto* f : all)
-            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return 0;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * 512);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmemBytes;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = 2, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, logp_pair_kernel<kLogp>, &cfg) != cudaSuccess || n <= 0) return 0;
-        known[dev] = n;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (!n) {
+        using A = Config<kLogp>;
+        using G = Config<kGrad>;
+        using B = Config<kBack>;
+        using F = FewConfig<64>;
+        using E = FewConfig<128>;
+        n = std::min({pairs_of(logp_pair_kernel<kLogp>, A::kThreads, A::kSmemBytes, kLaunchRegs),
+                      pairs_of(logp_pair_kernel<kGrad>, G::kThreads, G::kSmemBytes, 0),
+                      pairs_of(logp_pair_kernel<kBack>, B::kThreads, B::kSmemBytes, 0),
+                      pairs_of(logp_few_kernel<64>, F::kThreads, F::kSmemBytes, 0),
+                      pairs_of(logp_few_kernel<128>, E::kThreads, E::kSmemBytes, 0), num_sms() / 2});
+        known[dev].store(n, std::memory_order_relaxed);
     }
-    return known[dev];
+    return n;
 }
 
 // 64 x 64 boxes of a row-major bf16 matrix, rows 128 bytes under the 128-byte swizzle, zeros outside
@@ -779,7 +1170,8 @@ bool load_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
 
 cudaError_t launch_rows(const LogpParams& p, bool backward, cudaStream_t st) {
     const int rows = (int)std::max<int64_t>(16, (p.M + 4095) / 4096);
-    const dim3 grid((unsigned)((p.M + rows - 1) / rows));
+    // (for a few rows some more CTAs, for the zeros)
+    const dim3 grid((unsigned)std::max<int64_t>((p.M + rows - 1) / rows, p.zeros / 4));
     return backward ? launch_pdl(rows_kernel<true>, grid, dim3(kRowThreads), 0, st, p, rows)
                     : launch_pdl(rows_kernel<false>, grid, dim3(kRowThreads), 0, st, p, rows);
 }
@@ -799,7 +1191,7 @@ size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K) {
     LogpParams p{};
     p.M = M, p.V = V, p.K = K;
     Arena a{nullptr};
-    lay_forward(a, p);
+    lay_forward(a, p, pairs_or_default());
     return a.used;
 }
 
@@ -814,18 +1206,27 @@ size_t linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
 
 cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st) {
     const int pairs = pairs_here();
-    if (!pairs) return cudaErrorInvalidDeviceFunction;
+    if (!pairs || pairs > pairs_or_default()) return cudaErrorInvalidDeviceFunction;
     Arena a{static_cast<uint8_t*>(ws)};
-    lay_forward(a, p);
+    lay_forward(a, p, pairs_or_default());
     p.err = device_error_word();
     p.ksteps = (int)((p.K + kStep - 1) / kStep), p.group = group_of(p.K);
+    const int segments = (p.ksteps + kSegment - 1) / kSegment;
+    p.segment = (p.ksteps + segments - 1) / segments;
+    const bool few = p.M <= kFewRows;
+    if (few) p.zeros = p.M <= 64 ? 64 : 128, p.parts = 8 * std::min(pairs, p.tiles);
     Maps maps{};
-    if (!p.err || !load_map(&maps.h, p.rows_h, p.M, p.K, p.K) || !load_map(&maps.w, p.W, p.V, p.K, p.ldw))
+    if (!p.err || !load_map(&maps.w, p.W, p.V, p.K, p.ldw) ||
+        !(few ? make_tmap_bf16_load(&maps.h, p.rows_h, (uint64_t)p.zeros, (uint64_t)p.K, (uint64_t)p.K, (uint32_t)p.zeros / 2)
+              : load_map(&maps.h, p.rows_h, p.M, p.K, p.K)))
         return cudaErrorInvalidValue;
     cudaError_t e = launch_rows(p, false, st);
-    if (e == cudaSuccess) e = launch_pairs(logp_pair_kernel<kLogp>, pairs, st, maps, p);
+    if (e == cudaSuccess)
+        e = !few         ? launch_pairs<kLogp>(pairs, st, maps, p)
+            : p.M <= 64 ? launch_few<64>(pairs, st, maps, p)
+                         : launch_few<128>(pairs, st, maps, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(logp_join_kernel, dim3((unsigned)((p.M + 31) / 32)), dim3(32 * kJoinWarps), 0, st, p);
+    return launch_pdl(logp_join_kernel, dim3((unsigned)((p.M + kJoinRows - 1) / kJoinRows)), dim3(kJoinThreads), 0, st, p);
 }
 
 cudaError_t launch_linear_logp_backward(LogpParams p, void* ws, cudaStream_t st) {
@@ -848,8 +1249,8 @@ cudaError_t launch_linear_logp_backward(LogpParams p, void* ws, cudaStream_t st)
     for (int64_t v = 0; v < p.V && e == cudaSuccess; v += p.piece) {
         const int64_t n = std::min(p.piece, p.V - v);
         p.first = (int)v, p.tiles = (int)((n + kTile - 1) / kTile), p.steps = (int)((n + kStep - 1) / kStep);
-        e = launch_pairs(logp_pair_kernel<kGrad>, pairs, st, maps, p);
-        if (e == cudaSuccess) e = launch_pairs(logp_pair_kernel<kBack>, pairs, st, maps, p);
+        e = launch_pairs<kGrad>(pairs, st, maps, p);
+        if (e == cudaSuccess) e = launch_pairs<kBack>(pairs, st, maps, p);
     }
     if (!p.dH || e != cudaSuccess) return e;
     return launch_pdl(grad_h_kernel, dim3((unsigned)std::min<int64_t>(p.M, 8 * num_sms())), dim3(256), 0, st, p);
