@@ -138,6 +138,7 @@ struct LogpParams {
     // the piece, tiles of K, row tiles a group, the piece's first row of W
     int tiles, ksteps, steps, ktiles, group, first;
     int segment, parts, zeros;        // steps of K summed in tensor memory, parts of a row's sums, rows_h's rows of a few
+    int pitch, whole;                 // values a row of rows_h; K is whole pieces of 64
 };
 size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K);
 size_t linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);
@@ -237,6 +238,11 @@ bool make_tmap_f16_load(CUtensorMap* m, const void* base, uint64_t rows, uint64_
 // with the 128-byte swizzle, zero fill out of range.
 bool make_tmap_bf16_load(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch_elems,
                          uint32_t box_rows);
+// bf16 rows of `pieces` pieces of 64 values (row pitch in elements), loaded in boxes of box_rows
+// rows of box_pieces pieces, a piece's rows one behind the other, with the 128-byte swizzle;
+// coordinates 0, row, piece; zero fill out of range.
+bool make_tmap_bf16_pieces(CUtensorMap* m, const void* base, uint64_t rows, uint64_t pieces, uint64_t pitch_elems,
+                           uint32_t box_rows, uint32_t box_pieces);
 // 4-D map of 8- or 16-bit values for loads of boxes whose rows are `swizzle` (64 or
 // 128) bytes, stored with that swizzle; zero fill out of range.  strides: bytes of
 // dimensions 1 .. 3.

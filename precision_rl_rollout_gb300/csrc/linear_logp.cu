@@ -48,16 +48,14 @@ constexpr int kOutBytes = 32 * 128;                     // a warp's staging
 
 enum Mode { kLogp, kGrad, kBack };
 
-// kLogp: eight warps for the threads' part, half of a row a thread, in registers that the
-// other warps let go of; nothing is staged.  kGrad, kBack: four, a row a thread.
+// Eight warps have the threads' part, half of a row a thread.  kLogp keeps it in registers,
+// which the other warps let go of, and stages nothing; the others stage what they write.
 template <Mode kMode>
 struct Config {
     static constexpr bool kForward = kMode == kLogp;
     static constexpr int kStages = kForward ? 6 : 5, kStageBytes = 4 * kPiece;   // two pieces of either operand
-    static constexpr int kEpiWarps = kForward ? 8 : 4, kThreads = 32 * (4 + kEpiWarps);
-    // boxes a warp stages at once: with one, each waits for the copy engine to have read the
-    // one before, 4 us a tile of dW
-    static constexpr int kOuts = kForward ? 0 : 4;
+    static constexpr int kEpiWarps = 8, kThreads = 32 * (4 + kEpiWarps);
+    static constexpr int kOuts = kForward ? 0 : 2;           // boxes a warp stages at once
     static constexpr int kOutOffset = kStages * kStageBytes;
     static constexpr int kBarOffset = kOutOffset + kEpiWarps * kOuts * kOutBytes;
     static constexpr int kSmemBytes = kBarOffset + 256 + 1024;
@@ -68,17 +66,25 @@ static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "the split
 
 // The tensor cores' fp32 sums lose a little to truncation at each step, towards zero: 5 of
 // 10^6 of a logit over 3584 products.  The forward takes them out of tensor memory every
-// 512 products at most and adds in registers, rounded to nearest (SEGMENT_FIGURES).  The gradient's logits meet a rounding of 2^-9 and are left as they are.
-constexpr int kSegment = 512 / kStep;
+// 896 products at most and adds in registers, rounded to nearest (SEGMENT_FIGURES).  The gradient's logits meet a rounding of 2^-9 and are left as they are.
+constexpr int kSegment = 896 / kStep, kFewSegment = 512 / kStep;
 
 // ------------------------------------------------------------------ pairs of CTAs
 
-// A 64 x 64 box into this CTA's shared memory, counted on the barrier of the pair's first CTA.
+// A box into this CTA's shared memory, counted on the barrier of the pair's first CTA.
 __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint64_t pol) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
         " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(pol)
+        : "memory");
+}
+__device__ __forceinline__ void pair_load_mn(uint32_t dst, const CUtensorMap* map, uint32_t bar, int piece, int row,
+                                             uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(piece), "r"(bar), "l"(pol)
         : "memory");
 }
 __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -121,8 +127,29 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// A ring's stage and the phase of its barriers, and whether the barrier that is waited for
+// next was seen complete already.  One thread issues the products and one or two the
+// loads; a wait that finds its barrier complete still takes 200 cycles before anything after
+// it is issued, and so each looks one stage ahead before it issues what it has.
+template <int kStages>
+struct Ring {
+    uint32_t s = 0, phase = 0;
+    bool ready = false;
+    __device__ __forceinline__ void next() {
+        if (++s == kStages) s = 0, phase ^= 1;
+    }
+    // bars: the barriers; flip: 0 for what is filled, 1 for what is emptied (free at first)
+    __device__ __forceinline__ void look(uint32_t bars, uint32_t flip) { ready = mbar_test(bars + 8 * s, phase ^ flip); }
+    __device__ __forceinline__ bool wait(uint32_t bars, uint32_t flip, const volatile int* abort) {
+        return ready || mbar_wait_bounded(bars + 8 * s, phase ^ flip, abort, kWaitLimitNs);
+    }
+};
+
+// Loads with the reduction inside are boxes of 64 values of 128 rows, or of 64 where no more
+// rows count; with the reduction outside 64 rows of two pieces of 64 values (*_mn; of one
+// where a row of W does not end with a piece).
 struct Maps {
-    CUtensorMap h, w, d, d_out, acc, dw;
+    CUtensorMap h, h64, h_mn, w, w_mn, d, d64, d_mn, d_out, acc, dw;
 };
 
 // ------------------------------------------------------------------ the work
@@ -141,6 +168,8 @@ __device__ __forceinline__ void tile_of(int u, int rows, int cols, int group, in
     c = left / here;
     r = g * group + left % here;
 }
+
+constexpr int kLeastSteps = 6;   // steps' time that writing a tile of dW takes all the same
 
 template <Mode kMode>
 struct Work {
@@ -176,7 +205,8 @@ struct Work {
             }
             const int full = (nh + pairs - 1 - pair) / pairs, wsteps = (live + kStep - 1) / kStep;
             const int j = i - full;                                                       // the how manieth of dW's
-            const int r = nh % pairs, extra = r && wsteps ? (p.steps / p.split + wsteps / 2) / wsteps : 0;
+            const int r = nh % pairs, cost = max(wsteps, kLeastSteps);
+            const int extra = r && wsteps ? (p.steps / p.split + cost / 2) / cost : 0;
             const int head = extra * (pairs - r);
             if (pair >= r && extra) {
                 const int w = pair - r + j * (pairs - r);
@@ -305,11 +335,6 @@ __device__ __forceinline__ float mask01(int e, int i) {
     return f;
 }
 
-// Wait until at most N of this thread's bulk groups have shared memory left to read.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N < 0 ? 0 : N) : "memory");
-}
 // A box of 32 rows of 128 bytes of a warp's own, one row a lane, staged under the 128-byte swizzle.
 __device__ __forceinline__ void stage16(uint8_t* out, int lane, int chunk, uint4 v) {
     *reinterpret_cast<uint4*>(out + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
@@ -366,58 +391,64 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
     Work<kMode> work(p);
     Unit u;
     if (kForward && warp < 4) regs_dec<kOtherRegs>();
-    if (warp == 0 && lane == 0) {
-        // ---------------- loads: this CTA's rows of both operands
-        const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+    if ((warp == 0 || warp == 3) && lane == 0) {
+        // ---------------- loads: this CTA's rows of the first operand, and by another warp
+        // of the second (an issued copy takes its thread some 100 cycles and the wait before
+        // it 200; one thread with four copies a stage took 600 where the products take 512)
+        const bool first = warp == 0;
+        const uint64_t policy = first || kMode == kBack ? policy_evict_last() : policy_evict_first();
         const uint32_t bar0 = map_to_rank(full0, 0);
+        Ring<kStages> ring;
         uint32_t it = 0;
         while (!*abort && work.next(u)) {
-            const CUtensorMap* ma = kMode != kBack ? &maps.h : &maps.d;
-            const CUtensorMap* mb = kMode != kBack || u.kind == 1 ? &maps.w : &maps.h;
-            const int a = u.a + (int)rank * kHalf, b = u.b + (int)rank * kHalf + (kMode != kBack ? p.first : 0);
+            const int a = u.a + (int)rank * kHalf, b = u.b + (int)rank * kHalf;
             // Rows past those that count: 64 of them at once are left as they are in shared
-            // memory (whatever that makes of their products reaches no other row, and nobody
-            // reads theirs), which is faster than filling in zeros: one row 309 -> 175 us.
+            // memory; whatever that makes of their products reaches no other row, and nobody
+            // reads theirs.
             const bool by_row = kMode != kBack || u.kind == 1;
             const int pieces = by_row ? min(2, max(0, (work.live - a + 63) / 64)) : 2;
             const int other = by_row ? min(2, max(0, (work.live - a - kHalf + 63) / 64)) : 2;
             const uint32_t bytes = (uint32_t)(4 + pieces + other) * kPiece;
             for (int k = 0; k < u.n; ++k, ++it) {
-                const int s = it % kStages;
-                if (!mbar_wait_bounded(empty0 + 8 * s, ((it / kStages) & 1) ^ 1, abort, kWaitLimitNs)) {
+                if (!ring.wait(empty0, 1, abort)) {
                     gave_up(1);
                     break;
                 }
-                const uint32_t dst = smem_u32(smem + s * C::kStageBytes), bar = bar0 + 8 * s;
-                if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+                const uint32_t s = ring.s, dst = smem_u32(smem + s * C::kStageBytes), bar = bar0 + 8 * s;
                 const int at = (u.k + k) * kStep;
-                if (by_row) {
-                    if (pieces > 0) pair_load(dst, ma, bar, at, a, keep);
-                    if (pieces > 1) pair_load(dst + kPiece, ma, bar, at, a + 64, keep);
+                ring.next();
+                ring.look(empty0, 1);
+                if (first) {
+                    if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
+                    if (!by_row) pair_load_mn(dst, &maps.d_mn, bar, a / 64, at, policy);
+                    else if (pieces == 2) pair_load(dst, kMode != kBack ? &maps.h : &maps.d, bar, at, a, policy);
+                    else if (pieces == 1) pair_load(dst, kMode != kBack ? &maps.h64 : &maps.d64, bar, at, a, policy);
+                } else if (kMode != kBack) {
+                    pair_load(dst + 2 * kPiece, &maps.w, bar, at, p.first + b, policy);
+                } else if (u.kind == 2) {
+                    pair_load_mn(dst + 2 * kPiece, &maps.h_mn, bar, b / 64, at, policy);
+                } else if (p.whole) {
+                    pair_load_mn(dst + 2 * kPiece, &maps.w_mn, bar, b / 64, p.first + at, policy);
                 } else {
-                    pair_load(dst, ma, bar, a, at, keep);
-                    pair_load(dst + kPiece, ma, bar, a + 64, at, keep);
-                }
-                if (kMode != kBack) {
-                    pair_load(dst + 2 * kPiece, mb, bar, at, b, once);
-                    pair_load(dst + 3 * kPiece, mb, bar, at, b + 64, once);
-                } else {
-                    const int y = u.kind == 1 ? p.first + at : at;
-                    pair_load(dst + 2 * kPiece, mb, bar, b, y, keep);
-                    pair_load(dst + 3 * kPiece, mb, bar, b + 64, y, keep);
+                    pair_load(dst + 2 * kPiece, &maps.w_mn, bar, b, p.first + at, policy);
+                    pair_load(dst + 3 * kPiece, &maps.w_mn, bar, b + 64, p.first + at, policy);
                 }
             }
         }
-        if (*abort && rank == 0)                         // both CTAs' copies in flight land before either ends
+        if (*abort && first && rank == 0)                // both CTAs' copies in flight land before either ends
             for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
                 mbar_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kWaitLimitNs);
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---------------- products, for both CTAs
-        uint32_t it = 0, tile = 0;
+        Ring<kStages> ring;
+        uint32_t tile = 0;
+        const uint32_t stages = smem_u32(smem);
         while (!*abort && work.next(u)) {
             const bool a_mn = kMode == kBack && u.kind == 2, b_mn = kMode == kBack;
             const uint32_t idesc = kIdesc | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-            const uint64_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+            const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+            const uint64_t a0 = a_mn ? desc_mn(stages) : umma_desc_k128_sw128(stages);
+            const uint64_t b0 = b_mn ? desc_mn(stages + 2 * kPiece) : umma_desc_k128_sw128(stages + 2 * kPiece);
             const int segment = kForward ? p.segment : u.n;
             for (int k0 = 0; k0 < u.n && !*abort; k0 += segment) {
                 const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
@@ -429,18 +460,19 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 tc_fence_after();
                 const uint32_t d = tmem + buf * kTile;
                 const int end = min(u.n, k0 + segment);
-                for (int k = k0; k < end; ++k, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait_bounded(full0 + 8 * s, (it / kStages) & 1, abort, kWaitLimitNs)) {
+                for (int k = k0; k < end; ++k) {
+                    if (!ring.wait(full0, 0, abort)) {
                         gave_up(2);
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * C::kStageBytes);
-                    const uint64_t ad = a_mn ? desc_mn(st) : umma_desc_k128_sw128(st);
-                    const uint64_t bd = b_mn ? desc_mn(st + 2 * kPiece) : umma_desc_k128_sw128(st + 2 * kPiece);
+                    const uint32_t s = ring.s;
+                    const uint64_t ad = a0 + s * (C::kStageBytes >> 4), bd = b0 + s * (C::kStageBytes >> 4);
+                    ring.next();
+                    ring.look(full0, 0);
+                    pair_mma(d, ad, bd, idesc, k > k0);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) pair_mma(d, ad + j * a_step, bd + j * b_step, idesc, k > k0 || j > 0);
+                    for (int j = 1; j < 4; ++j) pair_mma(d, ad + j * a_step, bd + j * b_step, idesc, 1);
                     pair_commit(empty0 + 8 * s);
                 }
                 pair_commit(tfull0 + 8 * buf);
@@ -497,31 +529,23 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
             }
         }
     } else if (!kForward && warp >= 4) {
-        // ---------------- the tile's threads' part: a row a thread
-        const int q = warp & 3, row = 32 * q + (int)lane;
-        uint8_t* const outs = smem + C::kOutOffset + q * C::kOuts * kOutBytes;
-        uint32_t box = 0;
-        // the next buffer, once the copy engine has read what was in it
-        auto next_out = [&]() {
-            if (lane == 0) bulk_wait_read<C::kOuts - 1>();
-            __syncwarp();
-            return outs + box++ % C::kOuts * kOutBytes;
-        };
+        // ---------------- the tile's threads' part: half of a row a thread
+        const int q = warp & 3, half = (int)(warp - 4) >> 2, row = 32 * q + (int)lane;
+        uint8_t* const out = smem + C::kOutOffset + (warp - 4) * C::kOuts * kOutBytes;
         const uint32_t empty_bar = map_to_rank(tempty0, 0);
-        const float c = p.scale * kLog2e;
+        const float c = p.scale * kLog2e, f = kMode == kBack ? *p.largest * p.scale : 0.f;
         uint32_t tile = 0;
         while (work.next(u)) {
             const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
             const int m = u.a + (int)rank * kHalf + row;                 // kGrad: the row among those that count
-            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile;
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile + half * kHalf;
             // per row, before the wait
             float g = 0.f, ge = 0.f, l2 = 0.f, plus = 0.f;
             int t = -1;
             if (kMode == kGrad) {
-                t = p.row_target[m] - p.first - u.b;
+                t = p.row_target[m] - p.first - u.b - half * kHalf;
                 g = p.row_g[m], ge = p.row_ge[m], l2 = p.row_lse[m] * kLog2e, plus = p.row_entropy[m];
             }
-            const float f = kMode == kBack ? *p.largest * p.scale : 0.f;
             if (u.n > 0) {
                 ++tile;
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
@@ -529,119 +553,104 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                     break;
                 }
                 tc_fence_after();
-            }
-            if constexpr (kMode == kGrad) {
-                const int cols = min(kTile, (int)(p.V - p.first) - u.b);
-                const bool entropy = p.ge != nullptr;
-#pragma unroll 1
-                for (int j = 0; j < kTile; j += 64) {
-                    uint32_t packed[32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(taddr + j + 32 * h, r);
-                        tmem_wait_ld();
-                        const int j0 = j + 32 * h;
-                        float v[32];
-                        const uint64_t cc = pk2(c, c), low = pk2(-l2, -l2), ng = pk2(-g, -g), ng2 = pk2(-ge, -ge);
-                        const uint64_t ln2 = pk2(0.69314718f, 0.69314718f), pl = pk2(plus, plus);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint64_t a = fma2(f32x2_pack(r[2 * e], r[2 * e + 1]), cc, low), pr = ex2_2(a);
-                            uint64_t d = mul2(ng, pr);
-                            if (entropy) d = fma2(mul2(ng2, pr), fma2(a, ln2, pl), d);
-                            const float2 two = f32x2_unpack(d);
-                            v[2 * e] = two.x, v[2 * e + 1] = two.y;
-                        }
-                        if (t >= j0 && t < j0 + 32) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = fmaf(g, mask01(e, t - j0), v[e]);
-                        }
-                        if (cols < j0 + 32) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (j0 + e >= cols) v[e] = 0.f;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) packed[16 * h + e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-                    }
-                    if (j == kTile - 64) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) pair_arrive(empty_bar + 8 * buf);
-                    }
-                    uint8_t* out = next_out();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        stage16(out, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&maps.d_out, smem_u32(out), u.b + j, u.a + (int)rank * kHalf + 32 * q);
-                        bulk_commit();
-                    }
-                }
             } else if (u.kind == 1) {
-                if (u.n == 0) continue;
+                continue;
+            }
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+            };
+            // the staging buffers, once the copy engine has read what was in them
+            auto clear = [&]() {
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+            };
+            const int y = u.a + (int)rank * kHalf + 32 * q, x = u.b + half * kHalf;   // the warp's first row and column
+            if (kMode == kBack && u.kind == 1) {
 #pragma unroll 1
-                for (int j = 0; j < kTile; j += 32) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(taddr + j, r);
+                for (int j = 0; j < kHalf; j += 64) {
+                    uint32_t r[64];
+                    tmem_ld_32x32b_x32(taddr + j, *reinterpret_cast<uint32_t(*)[32]>(r));
+                    tmem_ld_32x32b_x32(taddr + j + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
                     tmem_wait_ld();
-                    if (j == kTile - 32) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) pair_arrive(empty_bar + 8 * buf);
-                    }
-                    uint8_t* out = next_out();
+                    if (j + 64 == kHalf) release();
+                    clear();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) stage16(out, lane, e, make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]));
+                    for (int e = 0; e < 16; ++e)
+                        stage16(out + (e >> 3) * kOutBytes, lane, e & 7, make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]));
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        const int y = u.slot * p.rows_pad + u.a + (int)rank * kHalf + 32 * q;
-                        if (u.b + j < p.K) {
-                            if (p.first == 0) tma_store_2d(&maps.acc, smem_u32(out), u.b + j, y);
-                            else tma_add_2d(&maps.acc, smem_u32(out), u.b + j, y);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = x + j + 32 * h, to = u.slot * p.rows_pad + y;
+                            if (at >= p.K) break;
+                            if (p.first == 0) tma_store_2d(&maps.acc, smem_u32(out + h * kOutBytes), at, to);
+                            else tma_add_2d(&maps.acc, smem_u32(out + h * kOutBytes), at, to);
                         }
-                        bulk_commit();                                   // a group a buffer, empty or not
-                    }
-                }
-            } else {
-#pragma unroll 1
-                for (int j = 0; j < kTile; j += 64) {
-                    uint32_t packed[32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[32];
-                        if (u.n > 0) {
-                            tmem_ld_32x32b_x32(taddr + j + 32 * h, r);
-                            tmem_wait_ld();
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = 0;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            packed[16 * h + e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
-                    }
-                    if (j == kTile - 64 && u.n > 0) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) pair_arrive(empty_bar + 8 * buf);
-                    }
-                    uint8_t* out = next_out();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        stage16(out, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    const int y = p.first + u.a + (int)rank * kHalf + 32 * q;
-                    if (lane == 0) {
-                        if (u.b + j < p.K && y < p.V) tma_store_2d(&maps.dw, smem_u32(out), u.b + j, y);
                         bulk_commit();
                     }
                 }
+                continue;
+            }
+            const int cols = (int)min((int64_t)kTile, p.V - p.first - u.b) - half * kHalf;   // kGrad: words of this half
+            const bool entropy = p.ge != nullptr;
+#pragma unroll 1
+            for (int j = 0; j < kHalf; j += 64) {
+                uint32_t r[64], packed[32];
+                if (u.n > 0) {
+                    tmem_ld_32x32b_x32(taddr + j, *reinterpret_cast<uint32_t(*)[32]>(r));
+                    tmem_ld_32x32b_x32(taddr + j + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+                    tmem_wait_ld();
+                    if (j + 64 == kHalf) release();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) r[e] = 0;
+                }
+                if constexpr (kMode == kGrad) {
+                    const uint64_t cc = pk2(c, c), low = pk2(-l2, -l2), ng = pk2(-g, -g), ng2 = pk2(-ge, -ge);
+                    const uint64_t ln2 = pk2(0.69314718f, 0.69314718f), pl = pk2(plus, plus);
+                    float v[64];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const uint64_t a = fma2(f32x2_pack(r[2 * e], r[2 * e + 1]), cc, low), pr = ex2_2(a);
+                        uint64_t d = mul2(ng, pr);
+                        if (entropy) d = fma2(mul2(ng2, pr), fma2(a, ln2, pl), d);
+                        const float2 two = f32x2_unpack(d);
+                        v[2 * e] = two.x, v[2 * e + 1] = two.y;
+                    }
+                    if (t >= j && t < j + 64) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) v[e] = fmaf(g, mask01(e, t - j), v[e]);
+                    }
+                    if (cols < j + 64) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (j + e >= cols) v[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) packed[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) packed[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+                }
+                if (j == 0) clear();
+                uint8_t* const box = out + (j / 64) * kOutBytes;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    stage16(box, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t from = smem_u32(out + h * kOutBytes);
+                    if (kMode == kGrad) tma_store_2d(&maps.d_out, from, x + 64 * h, y);
+                    else if (x + 64 * h < p.K && p.first + y < p.V) tma_store_2d(&maps.dw, from, x + 64 * h, p.first + y);
+                }
+                bulk_commit();
             }
         }
         if (lane == 0) bulk_wait_all();
@@ -743,31 +752,36 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
         const uint32_t bar0 = map_to_rank(full0, 0);
         const int mine = pair < p.tiles ? (p.tiles - pair + pairs - 1) / pairs : 0;
         const uint32_t total = (uint32_t)mine * p.ksteps, early = min(total, (uint32_t)kStages);
-        auto load_w = [&](uint32_t i) {
-            const int s = i % kStages, at = (int)(i % p.ksteps) * kStep;
-            const int v = (pair + (int)(i / p.ksteps) * pairs) * kTile + (int)rank * kHalf;
+        auto load_w = [&](uint32_t s, int step, int tile) {
+            const int at = step * kStep, v = tile * kTile + (int)rank * kHalf;
             const uint32_t dst = smem_u32(smem + s * C::kStageBytes), bar = bar0 + 8 * s;
             if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * C::kStageBytes);
             pair_load(dst, &maps.w, bar, at, v, once);
-            pair_load(dst + kPiece, &maps.w, bar, at, v + 64, once);
         };
-        auto load_h = [&](uint32_t i) {
-            const int s = i % kStages, at = (int)(i % p.ksteps) * kStep;
+        auto load_h = [&](uint32_t s, int step) {
+            const int at = step * kStep;
             pair_load(smem_u32(smem + s * C::kStageBytes) + 2 * kPiece, &maps.h, bar0 + 8 * s, at, (int)rank * C::kRows, keep);
         };
         // (rows_kernel writes no W, and whatever came before it has ended)
-        for (uint32_t i = 0; i < early; ++i) load_w(i);
+        for (uint32_t i = 0; i < early; ++i) load_w(i, (int)(i % p.ksteps), pair + (int)(i / p.ksteps) * pairs);
         grid_dependency_wait();
         grid_launch_dependents();
-        for (uint32_t i = 0; i < early; ++i) load_h(i);
+        for (uint32_t i = 0; i < early; ++i) load_h(i, (int)(i % p.ksteps));
         uint32_t it = early;
+        int step = (int)(early % p.ksteps), tile = pair + (int)(early / p.ksteps) * pairs;
+        Ring<kStages> ring;
+        ring.s = early % kStages, ring.phase = early / kStages & 1;
         for (; it < total && !*abort; ++it) {
-            if (!mbar_wait_bounded(empty0 + 8 * (it % kStages), ((it / kStages) & 1) ^ 1, abort, kWaitLimitNs)) {
+            if (!ring.wait(empty0, 1, abort)) {
                 gave_up(1);
                 break;
             }
-            load_w(it);
-            load_h(it);
+            const uint32_t s = ring.s;
+            ring.next();
+            ring.look(empty0, 1);
+            load_w(s, step, tile);
+            load_h(s, step);
+            if (++step == p.ksteps) step = 0, tile += pairs;
         }
         if (*abort && rank == 0)
             for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
@@ -776,7 +790,9 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
         grid_dependency_wait();
         grid_launch_dependents();
         if (warp == 1 && lane == 0 && rank == 0) {
-            uint32_t it = 0, tile = 0;
+            Ring<kStages> ring;
+            uint32_t tile = 0;
+            const uint64_t a0 = umma_desc_k128_sw128(smem_u32(smem)), b0 = umma_desc_k128_sw128(smem_u32(smem) + 2 * kPiece);
             for (int v = pair; v < p.tiles && !*abort; v += pairs)
                 for (int k0 = 0; k0 < p.ksteps && !*abort; k0 += p.segment, ++tile) {
                     const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
@@ -786,18 +802,19 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
                     }
                     tc_fence_after();
                     const int end = min(p.ksteps, k0 + p.segment);
-                    for (int k = k0; k < end; ++k, ++it) {
-                        const int s = it % kStages;
-                        if (!mbar_wait_bounded(full0 + 8 * s, (it / kStages) & 1, abort, kWaitLimitNs)) {
+                    for (int k = k0; k < end; ++k) {
+                        if (!ring.wait(full0, 0, abort)) {
                             gave_up(2);
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t st = smem_u32(smem + s * C::kStageBytes);
-                        const uint64_t a = umma_desc_k128_sw128(st), b = umma_desc_k128_sw128(st + 2 * kPiece);
+                        const uint32_t s = ring.s;
+                        const uint64_t a = a0 + s * (C::kStageBytes >> 4), b = b0 + s * (C::kStageBytes >> 4);
+                        ring.next();
+                        ring.look(full0, 0);
+                        pair_mma(tmem + buf * kN, a, b, C::kIdesc, k > k0);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            pair_mma(tmem + buf * kN, a + 2 * j, b + 2 * j, C::kIdesc, k > k0 || j > 0);
+                        for (int j = 1; j < 4; ++j) pair_mma(tmem + buf * kN, a + 2 * j, b + 2 * j, C::kIdesc, 1);
                         pair_commit(empty0 + 8 * s);
                     }
                     pair_commit(tfull0 + 8 * buf);
@@ -955,8 +972,9 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
             }
         }
         const uint4* src = reinterpret_cast<const uint4*>(p.H + m * p.ldh);
-        uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.K);
+        uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.pitch);
         for (int i = lane; i < chunks; i += 32) dst[i] = ld_stream_v4(src + i);
+        for (int i = chunks + lane; i < p.pitch / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
     }
     // up to the last tile's edge no target and no gradient; hidden states of zeros up to the
     // last 64 rows' end (past M the copy engine fills them in; further ones are not loaded),
@@ -968,8 +986,8 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
         if (kBackward) p.row_g[at] = 0.f, p.row_ge[at] = 0.f, p.row_lse[at] = 0.f, p.row_entropy[at] = 0.f;
     }
     for (int at = all + blockIdx.x; at < zeros; at += gridDim.x) {
-        uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.K);
-        for (int i = threadIdx.x; i < chunks; i += kRowThreads) dst[i] = make_uint4(0, 0, 0, 0);
+        uint4* dst = reinterpret_cast<uint4*>(p.rows_h + (int64_t)at * p.pitch);
+        for (int i = threadIdx.x; i < p.pitch / 8; i += kRowThreads) dst[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -1057,7 +1075,8 @@ void lay_rows(Arena& a, LogpParams& p) {
     p.rows_pad = (int)up(p.M, kTile);
     p.live = a.take<int>(1), p.largest = a.take<float>(1);
     p.row_of = a.take<int>(p.rows_pad), p.row_target = a.take<int>(p.rows_pad);
-    p.rows_h = a.take<uint16_t>(std::max<int64_t>(p.M, kFewRows) * p.K);
+    p.pitch = (int)up(p.K, kStep);
+    p.rows_h = a.take<uint16_t>(std::max<int64_t>(p.M, kFewRows) * p.pitch);
 }
 void lay_forward(Arena& a, LogpParams& p, int pairs) {
     lay_rows(a, p);
@@ -1067,33 +1086,41 @@ void lay_forward(Arena& a, LogpParams& p, int pairs) {
     p.part = a.take<float>(3 * (int64_t)p.parts * p.rows_pad);
 }
 
-// The backward's pieces of the vocabulary: D of a piece is at most 128 MB, about what stays
-// in L2, but at least 4096 wide, so that its launches are long.
-int64_t piece_of(int64_t rows_pad, int64_t V) {
-    const int64_t most = std::max<int64_t>(up((64ll << 20) / rows_pad, kTile), 4096), n = (V + most - 1) / most;
-    return up((V + n - 1) / n, kTile);
-}
-// Parts of a piece that dH's tiles are cut into, summed apart: as many as make the fewest
-// steps for the pair that has the most, with some 8 steps' time for a tile's ends and a
-// hundredth for a part's sums.  The same whether dW is wanted too, whose tiles would fill
-// the gaps: dH has the same bits either way.
-int split_of(int64_t M, int64_t K, int64_t piece, int pairs) {
-    const int64_t tiles = (M + kTile - 1) / kTile * ((K + kTile - 1) / kTile), steps = piece / kStep;
-    int best = 1;
-    double least = 1e30;
-    for (int s = 1; s <= 16 && s * 8 <= steps; ++s) {
-        const double turns = (double)((tiles * s + pairs - 1) / pairs);
-        const double cost = turns * ((double)steps / s + 8.0) * (1.0 + 0.01 * s);
-        if (cost < least) least = cost, best = s;
+// The backward's pieces of the vocabulary, and the parts of a piece that dH's tiles are cut
+// into (summed apart).  Taken by what the pairs' longest share comes to, in steps: kGrad's
+// tiles in waves, then dH's, alone (once) and with dW's (twice), which fill the gaps; 8 steps' time
+// at a tile's ends, 40 a launch, a part's sums a fortieth.  The same whichever gradients are wanted, so
+// that dH has the same bits.  D of a piece is at most kMostD bytes, a fifth of what 4096 rows
+// of 152064 have: with 64 MB both gradients of those take 8.4 ms, with 128 8.2, 256 8.0, 512 7.9.
+constexpr int64_t kMostD = 256ll << 20;
+
+void plan(int64_t M, int64_t V, int64_t K, int pairs, int64_t& piece, int& split) {
+    const int64_t rows = (M + kTile - 1) / kTile, kt = (K + kTile - 1) / kTile, words = (V + kTile - 1) / kTile;
+    const int64_t most = std::max<int64_t>(kMostD / (2 * rows * kTile * kTile), 4), least = (words + most - 1) / most;
+    const double ksteps = (double)((K + kStep - 1) / kStep), wsteps = std::max<double>(rows * kTile / kStep, kLeastSteps);
+    double best = 1e30;
+    for (int64_t n = least; n <= std::min(words, least + 8); ++n) {
+        const int64_t w = (words + n - 1) / n, steps = w * kTile / kStep;
+        const int64_t launches = (words + w - 1) / w;
+        const double grad = (double)((rows * w + pairs - 1) / pairs) * (ksteps + 8);
+        for (int s = 1; s <= 16 && s * 8 <= steps; ++s) {
+            const double each = (double)steps / s + 8, turns = (double)((rows * kt * s + pairs - 1) / pairs);
+            const double alone = turns * each;
+            const double both = std::max(alone, ((double)(rows * kt * s) * each + (double)(w * kt) * (wsteps + 2)) / pairs + wsteps / 2);
+            const double cost = (double)launches * (3 * grad + (alone + 2 * both) * (1 + 0.025 * s) + 240);
+            if (cost < best) best = cost, piece = w * kTile, split = s;
+        }
+        if (steps < 8) {                                // a piece that is hardly one
+            const double cost = (double)launches * 3 * (grad + (double)((rows * kt + pairs - 1) / pairs) * (steps + 8) + 80);
+            if (cost < best) best = cost, piece = w * kTile, split = 1;
+        }
     }
-    return best;
 }
 void lay_backward(Arena& a, LogpParams& p, int pairs) {
     lay_rows(a, p);
     p.row_g = a.take<float>(p.rows_pad), p.row_ge = a.take<float>(p.rows_pad);
     p.row_lse = a.take<float>(p.rows_pad), p.row_entropy = a.take<float>(p.rows_pad);
-    p.piece = piece_of(p.rows_pad, p.V);
-    p.split = split_of(p.M, p.K, p.piece, pairs);
+    plan(p.M, p.V, p.K, pairs, p.piece, p.split);
     p.D = a.take<uint16_t>((int64_t)p.rows_pad * p.piece);
     p.acc = a.take<float>((int64_t)p.split * p.rows_pad * p.K);
 }
@@ -1163,9 +1190,12 @@ int pairs_here() {
     return n;
 }
 
-// 64 x 64 boxes of a row-major bf16 matrix, rows 128 bytes under the 128-byte swizzle, zeros outside
-bool load_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
-    return make_tmap_bf16_load(m, base, (uint64_t)rows, (uint64_t)cols, (uint64_t)pitch, 64);
+// 64 rows of two pieces of 64 values of a row-major bf16 matrix whose rows are whole pieces
+bool load_map_mn(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch) {
+    return make_tmap_bf16_pieces(m, base, (uint64_t)rows, (uint64_t)cols / 64, (uint64_t)pitch, 64, 2);
+}
+bool load_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows) {
+    return make_tmap_bf16_load(m, base, (uint64_t)rows, (uint64_t)cols, (uint64_t)pitch, box_rows);
 }
 
 cudaError_t launch_rows(const LogpParams& p, bool backward, cudaStream_t st) {
@@ -1211,14 +1241,14 @@ cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st) {
     lay_forward(a, p, pairs_or_default());
     p.err = device_error_word();
     p.ksteps = (int)((p.K + kStep - 1) / kStep), p.group = group_of(p.K);
-    const int segments = (p.ksteps + kSegment - 1) / kSegment;
-    p.segment = (p.ksteps + segments - 1) / segments;
     const bool few = p.M <= kFewRows;
+    const int most = few ? kFewSegment : kSegment, segments = (p.ksteps + most - 1) / most;
+    p.segment = (p.ksteps + segments - 1) / segments;
     if (few) p.zeros = p.M <= 64 ? 64 : 128, p.parts = 8 * std::min(pairs, p.tiles);
     Maps maps{};
-    if (!p.err || !load_map(&maps.w, p.W, p.V, p.K, p.ldw) ||
-        !(few ? make_tmap_bf16_load(&maps.h, p.rows_h, (uint64_t)p.zeros, (uint64_t)p.K, (uint64_t)p.K, (uint32_t)p.zeros / 2)
-              : load_map(&maps.h, p.rows_h, p.M, p.K, p.K)))
+    if (!p.err || !load_map(&maps.w, p.W, p.V, p.K, p.ldw, kHalf) ||
+        !load_map(&maps.h, p.rows_h, few ? p.zeros : p.M, p.pitch, p.pitch, few ? (uint32_t)p.zeros / 2 : kHalf) ||
+        (!few && !load_map(&maps.h64, p.rows_h, p.M, p.pitch, p.pitch, 64)))
         return cudaErrorInvalidValue;
     cudaError_t e = launch_rows(p, false, st);
     if (e == cudaSuccess)
@@ -1239,8 +1269,13 @@ cudaError_t launch_linear_logp_backward(LogpParams p, void* ws, cudaStream_t st)
     p.ksteps = (int)((p.K + kStep - 1) / kStep), p.group = group_of(p.K);
     p.ktiles = (int)((p.K + kTile - 1) / kTile);
     Maps maps{};
-    if (!p.err || !load_map(&maps.h, p.rows_h, p.M, p.K, p.K) || !load_map(&maps.w, p.W, p.V, p.K, p.ldw) ||
-        !load_map(&maps.d, p.D, p.rows_pad, p.piece, p.piece) ||
+    p.whole = p.K % 64 == 0;
+    if (!p.err || !load_map(&maps.h, p.rows_h, p.M, p.pitch, p.pitch, kHalf) ||
+        !load_map(&maps.h64, p.rows_h, p.M, p.pitch, p.pitch, 64) || !load_map_mn(&maps.h_mn, p.rows_h, p.M, p.pitch, p.pitch) ||
+        !load_map(&maps.w, p.W, p.V, p.K, p.ldw, kHalf) ||
+        !(p.whole ? load_map_mn(&maps.w_mn, p.W, p.V, p.K, p.ldw) : load_map(&maps.w_mn, p.W, p.V, p.K, p.ldw, 64)) ||
+        !load_map(&maps.d, p.D, p.rows_pad, p.piece, p.piece, kHalf) || !load_map(&maps.d64, p.D, p.rows_pad, p.piece, p.piece, 64) ||
+        !load_map_mn(&maps.d_mn, p.D, p.rows_pad, p.piece, p.piece) ||
         !make_tmap_bf16_store(&maps.d_out, p.D, (uint64_t)p.rows_pad, (uint64_t)p.piece, (uint64_t)p.piece, 64, 32) ||
         !make_tmap_f32_store(&maps.acc, p.acc, (uint64_t)p.split * p.rows_pad, (uint64_t)p.K, (uint64_t)p.K, 32, 32) ||
         (p.dW && !make_tmap_bf16_store(&maps.dw, p.dW, (uint64_t)p.V, (uint64_t)p.K, (uint64_t)p.K, 64, 32)))

@@ -98,6 +98,20 @@ bool make_tmap_bf16_load(CUtensorMap* m, const void* base, uint64_t rows, uint64
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_bf16_pieces(CUtensorMap* m, const void* base, uint64_t rows, uint64_t pieces, uint64_t pitch_elems,
+                           uint32_t box_rows, uint32_t box_pieces) {
+    auto enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {64, rows, pieces};
+    cuuint64_t strides[2] = {pitch_elems * 2, 128};
+    cuuint32_t box[3] = {64, box_rows, box_pieces};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_4d(CUtensorMap* m, const void* base, bool bytes, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
                   const uint32_t (&box)[4], int swizzle) {
     auto enc = get_encode_fn();
