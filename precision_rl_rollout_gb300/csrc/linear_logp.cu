@@ -61,7 +61,7 @@ struct Config {
     static constexpr int kSmemBytes = kBarOffset + 256 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 };
-constexpr int kLaunchRegs = 168, kOtherRegs = 40, kEpiRegs = 232;   // forward: registers a thread, at launch and after
+constexpr int kLaunchRegs = 168, kOtherRegs = 40, kEpiRegs = 232;   // kLogp: registers a thread, at launch and after
 static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "the split must fit the launch's registers");
 
 // The tensor cores' fp32 sums lose a little to truncation at each step, towards zero: 5 of
@@ -335,6 +335,12 @@ __device__ __forceinline__ float mask01(int e, int i) {
     return f;
 }
 
+// 64 columns of this thread's row
+__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, uint32_t (&r)[64]) {
+    tmem_ld_32x32b_x32(taddr, *reinterpret_cast<uint32_t(*)[32]>(r));
+    tmem_ld_32x32b_x32(taddr + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+    tmem_wait_ld();
+}
 // A box of 32 rows of 128 bytes of a warp's own, one row a lane, staged under the 128-byte swizzle.
 __device__ __forceinline__ void stage16(uint8_t* out, int lane, int chunk, uint4 v) {
     *reinterpret_cast<uint4*>(out + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
@@ -385,6 +391,18 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
     cluster_sync_all();                                  // both CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // W's part of the first tile into L2 while the kernel before ends, by where it is if
+    // enough rows count (elsewhere nobody is harmed)
+    if (kMode != kBack && warp == 3 && lane == 0) {
+        const int rows = (int)((p.M + kTile - 1) / kTile), pair = blockIdx.x >> 1;
+        if (pair < rows * p.tiles) {
+            int r, c;
+            const int groups = (rows + p.group - 1) / p.group;
+            tile_of(pair, rows, p.tiles, (rows + groups - 1) / groups, r, c);
+            for (int k = 0; k < min(p.ksteps, 16); ++k)
+                tma_prefetch_l2_2d(&maps.w, k * kStep, p.first + c * kTile + (int)rank * kHalf);
+        }
+    }
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -501,6 +519,8 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                     }
                     tc_fence_after();
                     const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile + half * kHalf;
+                    // 32 columns at a time: tensor memory serves these loads at the expense of
+                    // the products' sums, and four at once cost 4096 rows 2% (2544 -> 2614 us)
 #pragma unroll
                     for (int j = 0; j < kHalf; j += 32) {
                         uint32_t r[32];
@@ -567,14 +587,21 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 __syncwarp();
             };
             const int y = u.a + (int)rank * kHalf + 32 * q, x = u.b + half * kHalf;   // the warp's first row and column
+            // 64 columns from tensor memory, which is let go of after the last of them
+            auto take = [&](int j, uint32_t (&r)[64]) {
+                if (u.n > 0) {
+                    tmem_ld_64(taddr + j, r);
+                    if (j + 64 == kHalf) release();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) r[e] = 0;
+                }
+            };
             if (kMode == kBack && u.kind == 1) {
 #pragma unroll 1
                 for (int j = 0; j < kHalf; j += 64) {
                     uint32_t r[64];
-                    tmem_ld_32x32b_x32(taddr + j, *reinterpret_cast<uint32_t(*)[32]>(r));
-                    tmem_ld_32x32b_x32(taddr + j + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
-                    tmem_wait_ld();
-                    if (j + 64 == kHalf) release();
+                    take(j, r);
                     clear();
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -599,15 +626,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
 #pragma unroll 1
             for (int j = 0; j < kHalf; j += 64) {
                 uint32_t r[64], packed[32];
-                if (u.n > 0) {
-                    tmem_ld_32x32b_x32(taddr + j, *reinterpret_cast<uint32_t(*)[32]>(r));
-                    tmem_ld_32x32b_x32(taddr + j + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
-                    tmem_wait_ld();
-                    if (j + 64 == kHalf) release();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) r[e] = 0;
-                }
+                take(j, r);
                 if constexpr (kMode == kGrad) {
                     const uint64_t cc = pk2(c, c), low = pk2(-l2, -l2), ng = pk2(-g, -g), ng2 = pk2(-ge, -ge);
                     const uint64_t ln2 = pk2(0.69314718f, 0.69314718f), pl = pk2(plus, plus);
@@ -1199,7 +1218,10 @@ bool load_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
 }
 
 cudaError_t launch_rows(const LogpParams& p, bool backward, cudaStream_t st) {
-    const int rows = (int)std::max<int64_t>(16, (p.M + 4095) / 4096);
+    // rows a CTA: four up to a CTA an SM, then to sixteen; every CTA goes over all targets,
+    // so not more than 4096 CTAs
+    const int64_t even = (p.M + num_sms() - 1) / num_sms();
+    const int rows = (int)std::max<int64_t>(std::min<int64_t>(std::max<int64_t>(even, 4), 16), (p.M + 4095) / 4096);
     // (for a few rows some more CTAs, for the zeros)
     const dim3 grid((unsigned)std::max<int64_t>((p.M + rows - 1) / rows, p.zeros / 4));
     return backward ? launch_pdl(rows_kernel<true>, grid, dim3(kRowThreads), 0, st, p, rows)
