@@ -137,7 +137,7 @@ struct LogpParams {
     // set by the launchers: tiles of the vocabulary, steps of the reduction over K and over
     // the piece, tiles of K, row tiles a group, the piece's first row of W
     int tiles, ksteps, steps, ktiles, group, first;
-    int segment, parts, zeros;        // steps of K summed in tensor memory, parts of a row's sums, rows_h's rows of a few
+    int segment, parts;               // steps of K summed in tensor memory, parts of a row's sums
     int pitch, whole;                 // values a row of rows_h; K is whole pieces of 64
 };
 size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K);

@@ -694,7 +694,8 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
 // 152064 x 5120 took 272 us).  A thread has a word of the vocabulary and 32 columns at a time; a
 // column's maximum and sums over a warp's 32 words meet by exchanges that halve the
 // columns at each step, so that lane l ends up with column l, whose sums it keeps over
-// all of its warp's tiles.  W's first stages are loaded before the wait for rows_kernel.
+// all of its warp's tiles.  Columns do not meet, so H is read as it lies, rows that do not
+// count (and what they hold) among the others: nothing is brought together first.
 template <int kN>
 struct FewConfig {
     static constexpr int kRows = kN / 2;                                  // of H, a CTA's
@@ -765,49 +766,33 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
+    grid_dependency_wait();
+    grid_launch_dependents();
     if (warp == 0 && lane == 0) {
-        // ---------------- loads; step i of this pair: step i % ksteps of its tile i / ksteps
+        // ---------------- loads
         const uint64_t keep = policy_evict_last(), once = policy_evict_first();
         const uint32_t bar0 = map_to_rank(full0, 0);
-        const int mine = pair < p.tiles ? (p.tiles - pair + pairs - 1) / pairs : 0;
-        const uint32_t total = (uint32_t)mine * p.ksteps, early = min(total, (uint32_t)kStages);
-        auto load_w = [&](uint32_t s, int step, int tile) {
-            const int at = step * kStep, v = tile * kTile + (int)rank * kHalf;
-            const uint32_t dst = smem_u32(smem + s * C::kStageBytes), bar = bar0 + 8 * s;
-            if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * C::kStageBytes);
-            pair_load(dst, &maps.w, bar, at, v, once);
-        };
-        auto load_h = [&](uint32_t s, int step) {
-            const int at = step * kStep;
-            pair_load(smem_u32(smem + s * C::kStageBytes) + 2 * kPiece, &maps.h, bar0 + 8 * s, at, (int)rank * C::kRows, keep);
-        };
-        // (rows_kernel writes no W, and whatever came before it has ended)
-        for (uint32_t i = 0; i < early; ++i) load_w(i, (int)(i % p.ksteps), pair + (int)(i / p.ksteps) * pairs);
-        grid_dependency_wait();
-        grid_launch_dependents();
-        for (uint32_t i = 0; i < early; ++i) load_h(i, (int)(i % p.ksteps));
-        uint32_t it = early;
-        int step = (int)(early % p.ksteps), tile = pair + (int)(early / p.ksteps) * pairs;
+        const uint32_t total = pair < p.tiles ? (uint32_t)((p.tiles - pair + pairs - 1) / pairs) * p.ksteps : 0;
+        int step = 0, tile = pair;
+        uint32_t it = 0;
         Ring<kStages> ring;
-        ring.s = early % kStages, ring.phase = early / kStages & 1;
         for (; it < total && !*abort; ++it) {
             if (!ring.wait(empty0, 1, abort)) {
                 gave_up(1);
                 break;
             }
-            const uint32_t s = ring.s;
+            const uint32_t s = ring.s, dst = smem_u32(smem + s * C::kStageBytes), bar = bar0 + 8 * s;
             ring.next();
             ring.look(empty0, 1);
-            load_w(s, step, tile);
-            load_h(s, step);
+            if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * C::kStageBytes);
+            pair_load(dst, &maps.w, bar, step * kStep, tile * kTile + (int)rank * kHalf, once);
+            pair_load(dst + 2 * kPiece, &maps.h, bar, step * kStep, (int)rank * C::kRows, keep);
             if (++step == p.ksteps) step = 0, tile += pairs;
         }
         if (*abort && rank == 0)
             for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
                 mbar_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kWaitLimitNs);
     } else {
-        grid_dependency_wait();
-        grid_launch_dependents();
         if (warp == 1 && lane == 0 && rank == 0) {
             Ring<kStages> ring;
             uint32_t tile = 0;
@@ -847,7 +832,10 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
             Sums s[C::kGroups];
             int target[C::kGroups];
 #pragma unroll
-            for (int g = 0; g < C::kGroups; ++g) target[g] = p.row_target[half * (kN / 2) + g * 32 + (int)lane];
+            for (int g = 0; g < C::kGroups; ++g) {
+                const int m = half * (kN / 2) + g * 32 + (int)lane;
+                target[g] = m < p.M ? p.targets[m] : -1;
+            }
             uint32_t tile = 0;
             bool ok = true;
             for (int v = pair; v < p.tiles && ok; v += pairs) {
@@ -936,7 +924,7 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
     __shared__ int place[kMostRows], before_w[8], all_w[8];
     __shared__ float largest_w[8];
     pdl_wait_then_release();
-    const int M = (int)p.M, m0 = blockIdx.x * rows, mine = max(0, min(rows, M - m0));
+    const int M = (int)p.M, m0 = blockIdx.x * rows, mine = min(rows, M - m0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int before = 0, all = 0;
     float largest = 0.f;
@@ -996,9 +984,8 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
         for (int i = chunks + lane; i < p.pitch / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
     }
     // up to the last tile's edge no target and no gradient; hidden states of zeros up to the
-    // last 64 rows' end (past M the copy engine fills them in; further ones are not loaded),
-    // for a few rows up to all of their columns' (which is faster)
-    const int edge = (all + kTile - 1) / kTile * kTile, zeros = p.zeros ? p.zeros : min(M, (all + 63) / 64 * 64);
+    // last 64 rows' end (past M the copy engine fills them in; further ones are not loaded)
+    const int edge = (all + kTile - 1) / kTile * kTile, zeros = min(M, (all + 63) / 64 * 64);
     if (blockIdx.x == 0 && all + (int)threadIdx.x < edge) {
         const int at = all + threadIdx.x;
         p.row_target[at] = -1;
@@ -1013,13 +1000,14 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
 // Joins a row's tiles: eight rows a CTA (a sector of each array), a 64th of the tiles a thread.
 constexpr int kJoinThreads = 512, kJoinRows = 8;
 
+template <bool kFew>
 __global__ void __launch_bounds__(kJoinThreads)
 logp_join_kernel(const __grid_constant__ LogpParams p) {
     __shared__ Sums part[kJoinThreads / 32][kJoinRows];
     pdl_wait_then_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x % kJoinRows;
-    const int live = *p.live, m = blockIdx.x * kJoinRows + r;
-    if (blockIdx.x * kJoinRows >= live) return;
+    const int live = kFew ? (int)p.M : *p.live, m = blockIdx.x * kJoinRows + r;
+    if ((int)blockIdx.x * kJoinRows >= live) return;
     const int64_t size = (int64_t)p.parts * p.rows_pad;
     const bool dev = p.entropy != nullptr;
     Sums s;
@@ -1047,7 +1035,12 @@ logp_join_kernel(const __grid_constant__ LogpParams p) {
     for (int w = 1; w < kJoinThreads / 32; ++w) s.add(part[w][r].top, part[w][r].sum, part[w][r].dev);
     const float ls = logf(s.sum);
     const double lse = (double)s.top * kLn2 + (double)ls;
-    const int row = p.row_of[m];
+    const int row = kFew ? m : p.row_of[m];
+    if (kFew && !counts(p, m)) {
+        p.logp[row] = 0.f, p.lse[row] = 0.f;
+        if (dev) p.entropy[row] = 0.f;
+        return;
+    }
     p.logp[row] = (float)((double)p.scale * (double)p.picked[m] - lse);
     p.lse[row] = (float)lse;
     if (dev) p.entropy[row] = ls - (float)kLn2 * s.dev / s.sum;
@@ -1095,13 +1088,18 @@ void lay_rows(Arena& a, LogpParams& p) {
     p.live = a.take<int>(1), p.largest = a.take<float>(1);
     p.row_of = a.take<int>(p.rows_pad), p.row_target = a.take<int>(p.rows_pad);
     p.pitch = (int)up(p.K, kStep);
-    p.rows_h = a.take<uint16_t>(std::max<int64_t>(p.M, kFewRows) * p.pitch);
+    p.rows_h = a.take<uint16_t>(p.M * p.pitch);
 }
 void lay_forward(Arena& a, LogpParams& p, int pairs) {
-    lay_rows(a, p);
     p.tiles = (int)((p.V + kTile - 1) / kTile);
+    if (p.M <= kFewRows) {
+        p.rows_pad = kFewRows;
+        p.parts = 8 * std::min(pairs, p.tiles);
+    } else {
+        lay_rows(a, p);
+        p.parts = 2 * p.tiles;
+    }
     p.picked = a.take<float>(p.rows_pad);
-    p.parts = p.M <= kFewRows ? std::max(8 * pairs, 2 * p.tiles) : 2 * p.tiles;
     p.part = a.take<float>(3 * (int64_t)p.parts * p.rows_pad);
 }
 
@@ -1222,8 +1220,7 @@ cudaError_t launch_rows(const LogpParams& p, bool backward, cudaStream_t st) {
     // so not more than 4096 CTAs
     const int64_t even = (p.M + num_sms() - 1) / num_sms();
     const int rows = (int)std::max<int64_t>(std::min<int64_t>(std::max<int64_t>(even, 4), 16), (p.M + 4095) / 4096);
-    // (for a few rows some more CTAs, for the zeros)
-    const dim3 grid((unsigned)std::max<int64_t>((p.M + rows - 1) / rows, p.zeros / 4));
+    const dim3 grid((unsigned)((p.M + rows - 1) / rows));
     return backward ? launch_pdl(rows_kernel<true>, grid, dim3(kRowThreads), 0, st, p, rows)
                     : launch_pdl(rows_kernel<false>, grid, dim3(kRowThreads), 0, st, p, rows);
 }
@@ -1266,19 +1263,23 @@ cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st) {
     const bool few = p.M <= kFewRows;
     const int most = few ? kFewSegment : kSegment, segments = (p.ksteps + most - 1) / most;
     p.segment = (p.ksteps + segments - 1) / segments;
-    if (few) p.zeros = p.M <= 64 ? 64 : 128, p.parts = 8 * std::min(pairs, p.tiles);
     Maps maps{};
-    if (!p.err || !load_map(&maps.w, p.W, p.V, p.K, p.ldw, kHalf) ||
-        !load_map(&maps.h, p.rows_h, few ? p.zeros : p.M, p.pitch, p.pitch, few ? (uint32_t)p.zeros / 2 : kHalf) ||
-        (!few && !load_map(&maps.h64, p.rows_h, p.M, p.pitch, p.pitch, 64)))
+    if (!p.err || !load_map(&maps.w, p.W, p.V, p.K, p.ldw, kHalf)) return cudaErrorInvalidValue;
+    if (few) {
+        // (as many pairs as the parts are laid out for)
+        const bool least = p.M <= 64;
+        if (!load_map(&maps.h, p.H, p.M, p.K, p.ldh, least ? 32 : 64)) return cudaErrorInvalidValue;
+        p.parts = 8 * std::min(pairs, p.tiles);
+        const cudaError_t e = least ? launch_few<64>(pairs, st, maps, p) : launch_few<128>(pairs, st, maps, p);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(logp_join_kernel<true>, dim3((unsigned)((p.M + kJoinRows - 1) / kJoinRows)), dim3(kJoinThreads), 0, st, p);
+    }
+    if (!load_map(&maps.h, p.rows_h, p.M, p.pitch, p.pitch, kHalf) || !load_map(&maps.h64, p.rows_h, p.M, p.pitch, p.pitch, 64))
         return cudaErrorInvalidValue;
     cudaError_t e = launch_rows(p, false, st);
-    if (e == cudaSuccess)
-        e = !few         ? launch_pairs<kLogp>(pairs, st, maps, p)
-            : p.M <= 64 ? launch_few<64>(pairs, st, maps, p)
-                         : launch_few<128>(pairs, st, maps, p);
+    if (e == cudaSuccess) e = launch_pairs<kLogp>(pairs, st, maps, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(logp_join_kernel, dim3((unsigned)((p.M + kJoinRows - 1) / kJoinRows)), dim3(kJoinThreads), 0, st, p);
+    return launch_pdl(logp_join_kernel<false>, dim3((unsigned)((p.M + kJoinRows - 1) / kJoinRows)), dim3(kJoinThreads), 0, st, p);
 }
 
 cudaError_t launch_linear_logp_backward(LogpParams p, void* ws, cudaStream_t st) {
