@@ -174,9 +174,9 @@ constexpr int kLeastSteps = 6;   // steps' time that writing a tile of dW takes 
 template <Mode kMode>
 struct Work {
     const LogpParams& p;
-    int rows, live, pair, pairs, i;
+    int rows, live, pair, pairs, i, phase;
 
-    __device__ __forceinline__ Work(const LogpParams& p_) : p(p_), i(0) {
+    __device__ __forceinline__ Work(const LogpParams& p_) : p(p_), i(0), phase(0) {
         live = *p.live;
         rows = (live + kTile - 1) / kTile;
         pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -191,38 +191,36 @@ struct Work {
             u = Unit{0, r * kTile, c * kTile, 0, p.ksteps, c};
             return true;
         } else {
-            // dH's units in turn, then dW's: pairs that have one unit of dH less take as
-            // many of dW as last as long first, the others follow in turn
+            // dH's units and dW's in turn: pairs that have one unit of dH less take as many of
+            // dW as last as long, the others follow in turn.  With few rows dW's are bound by
+            // what HBM writes (4 TB/s), dH's by the products and by reading, and every other
+            // pair takes dW's first, so that the two go on beside each other (500 rows of
+            // 32000 x 1024 103 -> 99 us, one of 152064 x 3584 728 -> 696); with more, each is
+            // better off with L2 to itself (1000 rows of 50257 x 896 220, beside each other 228,
+            // 4096 of 152064 x 3584 7930 and 8270).
             const int kt = p.ktiles;
             const int nh = p.dH ? rows * kt * p.split : 0, nw = p.dW ? p.tiles * kt : 0;
-            int at = pair + i * pairs;
-            if (at < nh) {
+            const int wsteps = (live + kStep - 1) / kStep;
+            for (; phase < 2; ++phase, i = 0) {
+                if ((phase ^ (wsteps < 10 ? pair : 0)) & 1) {
+                    const int r = nh % pairs, cost = max(wsteps, kLeastSteps);
+                    const int extra = r && wsteps ? (p.steps / p.split + cost / 2) / cost : 0, head = extra * (pairs - r);
+                    int at = head + pair + i * pairs;
+                    if (pair >= r && extra) at = i < extra ? pair - r + i * (pairs - r) : head + pair + (i - extra) * pairs;
+                    if (at >= nw) continue;
+                    ++i;
+                    u = Unit{2, at / kt * kTile, at % kt * kTile, 0, wsteps, 0};
+                    return true;
+                }
+                const int at = pair + i * pairs;
+                if (at >= nh) continue;
                 ++i;
                 const int s = at / (rows * kt), t = at - s * rows * kt;
                 const int k = s * p.steps / p.split, end = (s + 1) * p.steps / p.split;
                 u = Unit{1, t / kt * kTile, t % kt * kTile, k, end - k, s};
                 return true;
             }
-            const int full = (nh + pairs - 1 - pair) / pairs, wsteps = (live + kStep - 1) / kStep;
-            const int j = i - full;                                                       // the how manieth of dW's
-            const int r = nh % pairs, cost = max(wsteps, kLeastSteps);
-            const int extra = r && wsteps ? (p.steps / p.split + cost / 2) / cost : 0;
-            const int head = extra * (pairs - r);
-            if (pair >= r && extra) {
-                const int w = pair - r + j * (pairs - r);
-                if (j < extra) {
-                    if (w >= nw) return false;
-                    at = w;
-                } else {
-                    at = head + pair + (j - extra) * pairs;
-                }
-            } else {
-                at = head + pair + j * pairs;
-            }
-            if (at >= nw) return false;
-            ++i;
-            u = Unit{2, at / kt * kTile, at % kt * kTile, 0, wsteps, 0};
-            return true;
+            return false;
         }
     }
 };
@@ -792,111 +790,109 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
         if (*abort && rank == 0)
             for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
                 mbar_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kWaitLimitNs);
-    } else {
-        if (warp == 1 && lane == 0 && rank == 0) {
-            Ring<kStages> ring;
-            uint32_t tile = 0;
-            const uint64_t a0 = umma_desc_k128_sw128(smem_u32(smem)), b0 = umma_desc_k128_sw128(smem_u32(smem) + 2 * kPiece);
-            for (int v = pair; v < p.tiles && !*abort; v += pairs)
-                for (int k0 = 0; k0 < p.ksteps && !*abort; k0 += p.segment, ++tile) {
-                    const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
-                    if (!mbar_wait_bounded(tempty0 + 8 * buf, use ^ 1, abort, kWaitLimitNs)) {
-                        gave_up(3);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        Ring<kStages> ring;
+        uint32_t tile = 0;
+        const uint64_t a0 = umma_desc_k128_sw128(smem_u32(smem)), b0 = umma_desc_k128_sw128(smem_u32(smem) + 2 * kPiece);
+        for (int v = pair; v < p.tiles && !*abort; v += pairs)
+            for (int k0 = 0; k0 < p.ksteps && !*abort; k0 += p.segment, ++tile) {
+                const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+                if (!mbar_wait_bounded(tempty0 + 8 * buf, use ^ 1, abort, kWaitLimitNs)) {
+                    gave_up(3);
+                    break;
+                }
+                tc_fence_after();
+                const int end = min(p.ksteps, k0 + p.segment);
+                for (int k = k0; k < end; ++k) {
+                    if (!ring.wait(full0, 0, abort)) {
+                        gave_up(2);
                         break;
                     }
                     tc_fence_after();
-                    const int end = min(p.ksteps, k0 + p.segment);
-                    for (int k = k0; k < end; ++k) {
-                        if (!ring.wait(full0, 0, abort)) {
-                            gave_up(2);
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t s = ring.s;
-                        const uint64_t a = a0 + s * (C::kStageBytes >> 4), b = b0 + s * (C::kStageBytes >> 4);
-                        ring.next();
-                        ring.look(full0, 0);
-                        pair_mma(tmem + buf * kN, a, b, C::kIdesc, k > k0);
+                    const uint32_t s = ring.s;
+                    const uint64_t a = a0 + s * (C::kStageBytes >> 4), b = b0 + s * (C::kStageBytes >> 4);
+                    ring.next();
+                    ring.look(full0, 0);
+                    pair_mma(tmem + buf * kN, a, b, C::kIdesc, k > k0);
 #pragma unroll
-                        for (int j = 1; j < 4; ++j) pair_mma(tmem + buf * kN, a + 2 * j, b + 2 * j, C::kIdesc, 1);
-                        pair_commit(empty0 + 8 * s);
-                    }
-                    pair_commit(tfull0 + 8 * buf);
+                    for (int j = 1; j < 4; ++j) pair_mma(tmem + buf * kN, a + 2 * j, b + 2 * j, C::kIdesc, 1);
+                    pair_commit(empty0 + 8 * s);
                 }
-        } else if (warp >= 4) {
-            const int q = warp & 3, half = (int)(warp - 4) >> 2;
-            const uint32_t empty_bar = map_to_rank(tempty0, 0);
-            const float c = p.scale * kLog2e;
-            const bool dev = p.entropy != nullptr;
-            constexpr float kNone = -3.0e38f;
-            Sums s[C::kGroups];
-            int target[C::kGroups];
-#pragma unroll
-            for (int g = 0; g < C::kGroups; ++g) {
-                const int m = half * (kN / 2) + g * 32 + (int)lane;
-                target[g] = m < p.M ? p.targets[m] : -1;
+                pair_commit(tfull0 + 8 * buf);
             }
-            uint32_t tile = 0;
-            bool ok = true;
-            for (int v = pair; v < p.tiles && ok; v += pairs) {
-                const int word0 = v * kTile + (int)rank * kHalf + 32 * q;
-                const bool there = word0 + (int)lane < p.V;
-                float x[C::kGroups][32];
-                for (int k0 = 0; k0 < p.ksteps; k0 += p.segment, ++tile) {
-                    const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
-                        if (lane == 0) gave_up(4);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+    } else if (warp >= 4) {
+        const int q = warp & 3, half = (int)(warp - 4) >> 2;
+        const uint32_t empty_bar = map_to_rank(tempty0, 0);
+        const float c = p.scale * kLog2e;
+        const bool dev = p.entropy != nullptr;
+        constexpr float kNone = -3.0e38f;
+        Sums s[C::kGroups];
+        int target[C::kGroups];
 #pragma unroll
-                    for (int g = 0; g < C::kGroups; ++g) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + buf * kN + half * (kN / 2) + g * 32, r);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[g][e] = k0 == 0 ? __uint_as_float(r[e]) : x[g][e] + __uint_as_float(r[e]);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+        for (int g = 0; g < C::kGroups; ++g) {
+            const int m = half * (kN / 2) + g * 32 + (int)lane;
+            target[g] = m < p.M ? p.targets[m] : -1;
+        }
+        uint32_t tile = 0;
+        bool ok = true;
+        for (int v = pair; v < p.tiles && ok; v += pairs) {
+            const int word0 = v * kTile + (int)rank * kHalf + 32 * q;
+            const bool there = word0 + (int)lane < p.V;
+            float x[C::kGroups][32];
+            for (int k0 = 0; k0 < p.ksteps; k0 += p.segment, ++tile) {
+                const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
+                    if (lane == 0) gave_up(4);
+                    ok = false;
+                    break;
                 }
-                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
                 for (int g = 0; g < C::kGroups; ++g) {
-                    float w[32];
-                    // a target among this warp's words: its logit to its row
-                    uint32_t hits = __ballot_sync(0xffffffffu, target[g] >= word0 && target[g] < word0 + 32);
-                    while (hits) {
-                        const int j = __ffs((int)hits) - 1;
-                        hits &= hits - 1;
-                        const int owner = __shfl_sync(0xffffffffu, target[g], j) - word0;
-                        if ((int)lane == owner) p.picked[half * (kN / 2) + g * 32 + j] = pick32(x[g], j);
-                    }
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + buf * kN + half * (kN / 2) + g * 32, r);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) w[e] = there ? x[g][e] : kNone;
-                    const float top = across(w, lane, [](float a, float b) { return fmaxf(a, b); }) * c;
-                    float d[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float a = fmaf(x[g][e], c, -__shfl_sync(0xffffffffu, top, e));
-                        w[e] = there ? ex2(a) : 0.f;
-                        d[e] = w[e] > 0.f ? w[e] * a : 0.f;
-                    }
-                    const auto plus = [](float a, float b) { return a + b; };
-                    const float sum = across(w, lane, plus), weighted = dev ? across(d, lane, plus) : 0.f;
-                    if (word0 < p.V) s[g].add(top, sum, weighted);
+                    for (int e = 0; e < 32; ++e) x[g][e] = k0 == 0 ? __uint_as_float(r[e]) : x[g][e] + __uint_as_float(r[e]);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) pair_arrive(empty_bar + 8 * buf);
             }
-            // this warp's part of its columns: one of 8 a pair
-            const int64_t size = (int64_t)8 * pairs * p.rows_pad, at = (int64_t)(8 * pair + 4 * (int)rank + q) * p.rows_pad;
+            if (!ok) break;
 #pragma unroll
             for (int g = 0; g < C::kGroups; ++g) {
-                float* part = p.part + at + half * (kN / 2) + g * 32 + lane;
-                part[0] = s[g].top, part[size] = s[g].sum;
-                if (dev) part[2 * size] = s[g].dev;
+                float w[32];
+                // a target among this warp's words: its logit to its row
+                uint32_t hits = __ballot_sync(0xffffffffu, target[g] >= word0 && target[g] < word0 + 32);
+                while (hits) {
+                    const int j = __ffs((int)hits) - 1;
+                    hits &= hits - 1;
+                    const int owner = __shfl_sync(0xffffffffu, target[g], j) - word0;
+                    if ((int)lane == owner) p.picked[half * (kN / 2) + g * 32 + j] = pick32(x[g], j);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] = there ? x[g][e] : kNone;
+                const float top = across(w, lane, [](float a, float b) { return fmaxf(a, b); }) * c;
+                float d[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float a = fmaf(x[g][e], c, -__shfl_sync(0xffffffffu, top, e));
+                    w[e] = there ? ex2(a) : 0.f;
+                    d[e] = w[e] > 0.f ? w[e] * a : 0.f;
+                }
+                const auto plus = [](float a, float b) { return a + b; };
+                const float sum = across(w, lane, plus), weighted = dev ? across(d, lane, plus) : 0.f;
+                if (word0 < p.V) s[g].add(top, sum, weighted);
             }
+        }
+        // this warp's part of its columns: one of 8 a pair
+        const int64_t size = (int64_t)8 * pairs * p.rows_pad, at = (int64_t)(8 * pair + 4 * (int)rank + q) * p.rows_pad;
+#pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) {
+            float* part = p.part + at + half * (kN / 2) + g * 32 + lane;
+            part[0] = s[g].top, part[size] = s[g].sum;
+            if (dev) part[2 * size] = s[g].dev;
         }
     }
     __syncwarp();
