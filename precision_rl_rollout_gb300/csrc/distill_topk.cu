@@ -33,7 +33,7 @@ namespace fp8rl {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kMostRanks = 16, kFlight = 4;
+constexpr int kMostRanks = 16, kFlight = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eRest = 1.9259629911266175e-8f;   // log2(e) - kLog2e
 constexpr double kLn2 = 0.6931471805599453;
@@ -204,7 +204,7 @@ __device__ __forceinline__ uint4 load16(const void* p) {
     return v;
 }
 // kFlight loads of a thread, those past the end kLowest
-template <typename T>
+template <int kThreads, typename T>
 __device__ __forceinline__ void fetch(Chunk<T> (&b)[kFlight], const T* X, int at, int end) {
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
@@ -220,6 +220,7 @@ __device__ __forceinline__ void fetch(Chunk<T> (&b)[kFlight], const T* X, int at
 // logit and the student's are under way while the row's first logits are.  What is left
 // to do with them then is one warp's: this GPU's 64-bit arithmetic is slow, and eight warps
 // each with the same few steps of it took a CTA 2 us.
+template <int kThreads>
 struct Entries {
     int32_t* id;       // [k], -1 where the entry names no token
     float* q;          // [k], the teacher's logit, then its probability
@@ -325,13 +326,13 @@ struct Sum {
     }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4)
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint64_t parts[kMostRanks];              // of the cluster's CTAs, in its first one's
+    constexpr int N = Chunk<T>::N, kWarps = kThreads / 32;
     __shared__ Sum warps[kWarps];
-    constexpr int N = Chunk<T>::N;
     if (ranks > 1) sm100::cluster_arrive();              // all have started (waited for below)
     pdl_wait_then_release();
     const int rank = (int)(blockIdx.x % (unsigned)ranks), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -341,9 +342,9 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
     int at = (int)((int64_t)chunks * rank / ranks);
     const int end = (int)((int64_t)chunks * (rank + 1) / ranks);
     at += threadIdx.x;
-    Entries n(smem, p, m);
+    Entries<kThreads> n(smem, p, m);
     Chunk<T> now[kFlight];
-    fetch(now, X, at, end);
+    fetch<kThreads>(now, X, at, end);
     const bool apart = p.rest_lse != nullptr;
     n.load(p, X, apart);
     const bool nobody = !n.any;
@@ -352,7 +353,7 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
     const uint8_t* named = reinterpret_cast<const uint8_t*>(n.bits);
     for (; at < end && !nobody; at += kFlight * kThreads) {
         Chunk<T> next[kFlight];
-        fetch(next, X, at + kFlight * kThreads, end);
+        fetch<kThreads>(next, X, at + kFlight * kThreads, end);
         float most = s.top;
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
@@ -455,8 +456,8 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4)
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float factors[5];                         // outside: a exp(y - r); inside: g (Q exp(y - l) - q)
@@ -471,9 +472,9 @@ distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
     // this CTA's logits, the last one's with what is past the last whole 16 bytes
     const int64_t lo = (int64_t)from * N, hi = rank == ranks - 1 ? p.V : (int64_t)end * N;
     int at = from + (int)threadIdx.x;
-    Entries n(smem, p, m);
+    Entries<kThreads> n(smem, p, m);
     Chunk<T> now[kFlight];
-    fetch(now, X, at, end);
+    fetch<kThreads>(now, X, at, end);
     n.load(p, X, true);
     n.settle(p);                                         // the entries' logits are read before any of this CTA's is overwritten
     __syncthreads();
@@ -499,7 +500,7 @@ distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
     auto grad = [&](float x) { return a * ex2(fmaf(x, c, -r2)); };
     for (; at < end; at += kFlight * kThreads) {
         Chunk<T> next[kFlight];
-        fetch(next, X, at + kFlight * kThreads, end);
+        fetch<kThreads>(next, X, at + kFlight * kThreads, end);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             const int g4 = at + u * kThreads;
@@ -522,8 +523,11 @@ distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
 }
 
 using Kernel = void(const DistillParams, int);
-Kernel* const kKernels[4] = {distill_kernel<float>, distill_kernel<uint16_t>, distill_grad_kernel<float>,
-                             distill_grad_kernel<uint16_t>};
+// [gradient][bf16][128 threads]
+Kernel* const kKernels[2][2][2] = {
+    {{distill_kernel<float, 256>, distill_kernel<float, 128>}, {distill_kernel<uint16_t, 256>, distill_kernel<uint16_t, 128>}},
+    {{distill_grad_kernel<float, 256>, distill_grad_kernel<float, 128>},
+     {distill_grad_kernel<uint16_t, 256>, distill_grad_kernel<uint16_t, 128>}}};
 
 // Clusters of 16 and more than 48 KB of shared memory have to be asked for, once a device.
 cudaError_t ask() {
@@ -531,40 +535,64 @@ cudaError_t ask() {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || (dev < 64 && ready.load(std::memory_order_relaxed) >> dev & 1)) return e;
-    for (Kernel* k : kKernels) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-        if (e != cudaSuccess) return e;
-    }
+    for (auto& some : kKernels)
+        for (auto& pair : some)
+            for (Kernel* k : pair) {
+                e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+                if (e != cudaSuccess) return e;
+            }
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     return e;
 }
 
-cudaError_t launch(Kernel* f, const DistillParams& p, int per_load, bool cluster, cudaStream_t st) {
-    const cudaError_t e = ask();
-    if (e != cudaSuccess) return e;
-    // CTAs a row: as many as make the least of the waves (four CTAs an SM; half a wave more
-    // where there is more than one) times a CTA's time, its bytes at its share of HBM's rate or
-    // at what its own loads in flight allow, and what comes before and after: some 2 us, with
-    // a cluster to join 4.5, in the gradient 1.5.  Measured (1, 2, 4, 8 CTAs a row, us): loss of
-    // 64 rows of 152064 bf16 20, 14, 13, 12, of 777 rows of 50257 27, 31, 43, 64, of 4096 of
-    // 152064 203, 247, 311, 452; gradient of the last 402, 392, 406, 481.  Clusters of 16 only
-    // with an SM a CTA, and each thread keeps two loads.
-    const int64_t sms = num_sms(), row = p.V / per_load * 16, bytes = cluster ? row : 2 * row;
+// Threads and CTAs a row.  Measured (us):
+// - loss, more rows than find a place at 256 threads (four CTAs an SM): 128 threads, a CTA a
+//   row, 777 rows of 50257 fp32 34 (256 threads 40), 1500 of 32000 bf16 29 (31), 4096 of 152064
+//   bf16 199 (205); two CTAs a row 41, 34, 213;
+// - gradient, more rows than SMs: 128 threads, two CTAs a row and up to 80 KB of logits each,
+//   4096 of 152064 bf16 383 (a CTA a row 405, 256 threads 401 and 391 with two), 2000 of them
+//   fp32 368 (389; 384, 376), 300 bf16 31.5 (43; 34, 32), 1500 of 32000 33.8 (37.9; 34.6, 39.6);
+// - otherwise 256 threads and as many CTAs as make the least of the waves (half a wave more
+//   where there is more than one) times a CTA's time: its bytes at its share of HBM's rate or
+//   at what its own loads in flight allow, and what comes before and after, some 2 us, with a
+//   cluster to join 4.5, in the gradient 1.5.  64 rows of 152064: loss 20, 14, 13, 12 with 1, 2, 4
+//   and 8 CTAs a row.  Clusters of 16 only with an SM a CTA; each thread keeps two loads.
+struct Shape {
+    int small, ranks;                                     // 128 threads; CTAs a row
+};
+Shape shape_of(bool backward, bool bf16, const DistillParams& p) {
+    const int64_t sms = num_sms(), row = p.V / (bf16 ? 8 : 4) * 16;
+    if (!backward && p.M > 4 * sms) return {1, 1};
     int ranks = 1;
+    if (backward && p.M > sms) {
+        while (ranks < kMostRanks && (row / ranks > 80 * 1024 || (ranks == 1 && row >= 2 * 32 * 128))) ranks *= 2;
+        return {1, ranks};
+    }
+    const double bytes = (double)(backward ? 2 * row : row);
     double least = 1e30;
     for (int r = 1; r <= kMostRanks; r *= 2) {
-        if (r > 1 && (row < (int64_t)r * 32 * kThreads || (r > 8 && r * p.M > sms))) break;
+        if (r > 1 && (row < (int64_t)r * 32 * 256 || (r > 8 && r * p.M > sms))) break;
         const int64_t ctas = r * p.M, slots = 4 * sms;
-        const double rate = std::min(cluster ? 20e3 : 36e3, 6.7e6 / (double)std::min(ctas, slots));   // bytes a us
+        const double rate = std::min(backward ? 36e3 : 20e3, 6.7e6 / (double)std::min(ctas, slots));   // bytes a us
         const double waves = ctas <= slots ? 1.0 : (double)ctas / slots + 0.5;
-        const double cost = waves * ((double)bytes / r / rate + (cluster ? r > 1 ? 4.5 : 2.0 : 1.5));
+        const double cost = waves * (bytes / r / rate + (backward ? 1.5 : r > 1 ? 4.5 : 2.0));
         if (cost < least) least = cost, ranks = r;
     }
+    return {0, ranks};
+}
+
+cudaError_t launch(bool backward, bool bf16, const DistillParams& p, cudaStream_t st) {
+    const cudaError_t e = ask();
+    if (e != cudaSuccess) return e;
+    const Shape shape = shape_of(backward, bf16, p);
+    const int small = shape.small, ranks = shape.ranks;
+    const bool cluster = !backward;
+    Kernel* const f = kKernels[backward][bf16][small];
     const size_t smem = smem_bytes(p.k, p.V, !cluster || p.rest_lse);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.M * ranks));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(256 >> small);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
@@ -580,7 +608,7 @@ cudaError_t launch(Kernel* f, const DistillParams& p, int per_load, bool cluster
 }  // namespace
 
 cudaError_t launch_distill_topk(const DistillParams& p, bool bf16, bool backward, cudaStream_t st) {
-    return launch(kKernels[2 * backward + bf16], p, bf16 ? 8 : 4, !backward, st);
+    return launch(backward, bf16, p, st);
 }
 
 }  // namespace fp8rl
