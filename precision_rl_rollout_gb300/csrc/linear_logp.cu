@@ -374,9 +374,20 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
         }
         *abort = 0;
         fence_mbar_init();
-        prefetch_tmap(&maps.h);
-        prefetch_tmap(&maps.w);
-        if (!kForward) prefetch_tmap(&maps.d);
+        if (kMode != kBack) {
+            prefetch_tmap(&maps.h);
+            prefetch_tmap(&maps.h64);
+            prefetch_tmap(&maps.w);
+            if (kMode == kGrad) prefetch_tmap(&maps.d_out);
+        } else {
+            prefetch_tmap(&maps.d);
+            prefetch_tmap(&maps.d64);
+            prefetch_tmap(&maps.w_mn);
+            prefetch_tmap(&maps.acc);
+            prefetch_tmap(&maps.d_mn);
+            prefetch_tmap(&maps.h_mn);
+            prefetch_tmap(&maps.dw);
+        }
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -909,6 +920,8 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
 
 __device__ __forceinline__ bool counts(const LogpParams& p, int64_t m) { return p.targets[m] >= 0 && p.targets[m] < p.V; }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // The rows that count, brought together: their hidden states, targets and gradients; zeros
 // for the results of the others.  Every CTA goes over all targets (they are in L2) to find
 // where its own rows go, so nothing is waited for.
@@ -924,11 +937,16 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int before = 0, all = 0;
     float largest = 0.f;
-    for (int m = threadIdx.x; m < M; m += kRowThreads)
-        if (counts(p, m)) {
+    for (int r = warp; r < mine; r += kRowThreads / 32)      // this CTA's rows on their way to L2
+        for (int i = lane * 64; i < p.K; i += 32 * 64) prefetch_l2(p.H + (m0 + r) * p.ldh + i);
+    for (int m = threadIdx.x; m < M; m += kRowThreads) {
+        const int t = p.targets[m];
+        const float g = kBackward ? fabsf(p.g[m]) : 0.f, e = kBackward && p.ge ? fabsf(p.ge[m]) : 0.f;
+        if (t >= 0 && t < p.V) {
             before += m < m0, ++all;
-            if (kBackward) largest = fmaxf(largest, fmaxf(fabsf(p.g[m]), p.ge ? fabsf(p.ge[m]) : 0.f));
+            largest = fmaxf(largest, fmaxf(g, e));
         }
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -1051,10 +1069,17 @@ grad_h_kernel(const __grid_constant__ LogpParams p) {
     for (int m = blockIdx.x; m < live; m += gridDim.x) {
         uint2* dst = reinterpret_cast<uint2*>(p.dH + (int64_t)p.row_of[m] * p.K);
         for (int i = threadIdx.x; i < (int)(p.K / 4); i += 256) {
-            float4 v = *reinterpret_cast<const float4*>(p.acc + (int64_t)m * p.K + 4 * i);
-            for (int s = 1; s < p.split; ++s) {
-                const float4 w = *reinterpret_cast<const float4*>(p.acc + ((int64_t)s * p.rows_pad + m) * p.K + 4 * i);
-                v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+            const float* at = p.acc + (int64_t)m * p.K + 4 * i;
+            const int64_t part = (int64_t)p.rows_pad * p.K;
+            float4 v = *reinterpret_cast<const float4*>(at);
+            for (int s = 1; s < p.split; s += 4) {           // four parts' loads in flight, added in their order
+                float4 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (s + j < p.split) w[j] = *reinterpret_cast<const float4*>(at + (s + j) * part);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (s + j < p.split) v.x += w[j].x, v.y += w[j].y, v.z += w[j].z, v.w += w[j].w;
             }
             dst[i] = make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
         }
