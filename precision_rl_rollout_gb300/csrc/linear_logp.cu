@@ -102,8 +102,10 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
         "h"((uint16_t)3)
         : "memory");
 }
+// What it hands over is tensor memory, which the tcgen05 fence before it orders; no other
+// memory, so no release at cluster scope (that waits for this thread's stores to global memory).
 __device__ __forceinline__ void pair_arrive(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
     asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
