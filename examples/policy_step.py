@@ -89,11 +89,11 @@ def main():
     for i in range(a.steps):
         p, d = policy_gradient(s), distill(s)
         n = s["counted"].sum().item()
-        objective = (p["weights"] * s["advantage"] * p["logp"]).sum().item() / n
-        print(f"step {i}: objective {objective:+.4f}, entropy {p['entropy'].sum().item() / n:.4f}, mean weight "
+        objective = (p["weights"] * s["advantage"]).sum().item() / n
+        print(f"step {i}: weighted advantage {objective:+.4f}, entropy {p['entropy'].sum().item() / n:.4f}, mean weight "
               f"{p['stats'][2].item() / n:.4f}, student's divergence {(d['loss'] * d['g']).sum().item():.4f}")
-        s["W"] -= 0.5 * p["dW"]
-        s["student_W"] -= 2.0 * d["dW"]
+        s["W"] -= 0.05 * p["dW"]
+        s["student_W"] -= 0.5 * d["dW"]
     assert fb.fp8rl_check_device_error() == 0
 
 

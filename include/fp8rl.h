@@ -554,9 +554,11 @@ int fp8rl_spec_verify(const void* P, int64_t p_seq, int64_t p_step, const void* 
  * K  a multiple of 8 (FP8RL_ERR_SHAPE); V any number.
  * targets int32 [M]; logp, lse fp32 [M]; entropy fp32 [M] or NULL.
  * scale: finite and > 0 (FP8RL_ERR_UNSUPPORTED).
+ * Up to 128 rows are one pass over W that HBM bounds; the rows that do not count cost
+ * nothing above that.
  * workspace: at least fp8rl_linear_logp_workspace_bytes(M, V, K) bytes, 16-byte
  *     aligned, no zeroing, nothing kept between calls; calls in flight at once need
- *     their own.
+ *     their own.  (Above 128 rows a copy of H and 12 bytes a row for 128 words.)
  * Limits: M, V <= 2^21, K <= 65536, ld <= 2^32 (FP8RL_ERR_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 size_t fp8rl_linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K);
@@ -573,7 +575,10 @@ int fp8rl_linear_logp(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t
  * lse, entropy fp32 [M]: the forward's (entropy only with g_entropy).
  * g_logp fp32 [M]; g_entropy fp32 [M] or NULL.
  * dH bf16 [M][K], dW bf16 [V][K], contiguous, 16-byte aligned; either may be NULL (not
- *     wanted: a frozen head, a frozen trunk), not both.  Overwritten, not added to.
+ *     wanted: a frozen head, a frozen trunk), not both.  Overwritten, not added to; they
+ *     must not overlap an input.  dH has the same bits whether dW is wanted or not.
+ * workspace: fp8rl_linear_logp_backward_workspace_bytes: a copy of H, D of one piece (up
+ *     to 256 MB, or 1024 words of the vocabulary), and fp32 sums of dH.
  * With M == 0 dW is set to 0.  Everything else as for fp8rl_linear_logp.
  * ---------------------------------------------------------------------- */
 size_t fp8rl_linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);

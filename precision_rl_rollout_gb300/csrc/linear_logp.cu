@@ -11,8 +11,9 @@
 //
 // All products are tiles of 256 x 256 by a pair of CTAs (tcgen05.mma.cta_group::2, bf16,
 // sums in tensor memory, fp32): each CTA stages 128 rows of either operand, 64 of the
-// reduction a stage, six stages, and has 128 of the tile's rows in its tensor memory, two
-// tiles of them, so that one tile's threads' part runs under the next one's products.
+// reduction a stage, and has 128 of the tile's rows in its tensor memory, two tiles of them,
+// so that one tile's threads' part runs under the next one's products.  Up to 128 rows the
+// forward is a pass over W, and the roles change (logp_few_kernel).
 //
 // Forward (kLogp): tile by tile each row leaves a maximum, its sum of exponentials and
 // of weighted differences (12 bytes for 128 logits); logp_join_kernel joins a row's tiles.
@@ -22,6 +23,14 @@
 // reduction outside: MN-major) into fp32 sums of dH that the pieces add to, and its
 // transpose with H (both MN-major) into the piece's rows of dW.  Nothing is transposed in
 // memory, and each sum of dH is added to once a launch, so results do not depend on order.
+//
+// What bounds it: the tensor cores, and for long calls the power they draw.  8192 rows, 5734 of
+// them counted, 152064 words x 3584: 3.63 ms alone, 1.72 PFLOP/s (90% of the measured 1.92),
+// 3.75 among others, where the clocks fall to 1.6 GHz and a library's product of this size
+// makes 1.83; the tensor pipe is 88% active (2048 rows x 65536, profiled).  Both gradients of
+// 2731 of 4096 rows: 4.95 and 5.55 ms, 1.80 and 1.61 PFLOP/s, pipe 84%.  One row 174 us, 48
+// rows x 5120 243: 6.3 and 6.4 TB/s.  With few rows the gradient is bound by writing dW (a
+// stream of writes alone makes 4 TB/s): one row 0.70 ms.
 #include <math.h>
 
 #include <algorithm>
@@ -64,9 +73,12 @@ struct Config {
 constexpr int kLaunchRegs = 168, kOtherRegs = 40, kEpiRegs = 232;   // kLogp: registers a thread, at launch and after
 static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "the split must fit the launch's registers");
 
-// The tensor cores' fp32 sums lose a little to truncation at each step, towards zero: 5 of
-// 10^6 of a logit over 3584 products.  The forward takes them out of tensor memory every
-// 896 products at most and adds in registers, rounded to nearest (SEGMENT_FIGURES).  The gradient's logits meet a rounding of 2^-9 and are left as they are.
+// The tensor cores' fp32 sums lose more at each step than rounding to nearest would, and the
+// loss grows with the steps: 3.1e-6 of the log-probabilities over 3584 products (against 64 bits;
+// 32-bit torch 4.5e-7).  The forward takes the sums out of tensor memory every 896 products
+// at most and adds in registers: 6.9e-7.  Every 512 it is 3.6e-7, but 8% slower, since tensor
+// memory serves these reads at the products' expense; few rows, bound by HBM, are taken out
+// so often.  The gradient's logits meet a rounding of 2^-8 and are left as they are.
 constexpr int kSegment = 896 / kStep, kFewSegment = 512 / kStep;
 
 // ------------------------------------------------------------------ pairs of CTAs

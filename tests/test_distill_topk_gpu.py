@@ -7,7 +7,8 @@ from precision_rl_rollout_gb300 import binding as fb
 
 pytestmark = pytest.mark.gpu
 
-SIZES = [(1, 1, 1), (1, 152064, 64), (2, 37, 5), (3, 1000, 20), (16, 4096, 1), (5, 4097, 300), (130, 2049, 8), (33, 50257, 100),
+# from 153 rows (gradient) and 609 (loss) on CTAs are smaller
+SIZES = [(700, 2000, 300), (1300, 4099, 7), (200, 40000, 200), (1, 1, 1), (1, 152064, 64), (2, 37, 5), (3, 1000, 20), (16, 4096, 1), (5, 4097, 300), (130, 2049, 8), (33, 50257, 100),
          (7, 1100, 1024), (40, 513, 64), (20, 30001, 33)]
 
 

@@ -7,8 +7,10 @@ from precision_rl_rollout_gb300 import binding as fb
 
 pytestmark = pytest.mark.gpu
 
-# (M, V, K): one row, one word, tiles and their edges, odd vocabularies, short and long products
-SIZES = [(1, 1, 8), (1, 1000, 64), (2, 130, 72), (31, 513, 136), (32, 40000, 64), (33, 257, 200), (64, 128, 8), (130, 515, 264),
+# (M, V, K): one row, one word, tiles and their edges, few rows and more (from 65 and 129 on other
+# kernels), odd vocabularies, short and long products, a vocabulary in several pieces
+SIZES = [(65, 300, 128), (128, 1000, 192), (129, 600, 64), (3, 300, 65536), (150, 520, 16392), (70001, 3000, 64),
+         (1, 1, 8), (1, 1000, 64), (2, 130, 72), (31, 513, 136), (32, 40000, 64), (33, 257, 200), (64, 128, 8), (130, 515, 264),
          (255, 2049, 512), (256, 256, 256), (257, 4100, 1024), (700, 1537, 328), (1025, 300, 96), (5, 7, 4104)]
 
 
