@@ -138,7 +138,7 @@ struct LogpParams {
     // the piece, tiles of K, row tiles a group, the piece's first row of W
     int tiles, ksteps, steps, ktiles, group, first;
     int segment, parts;               // steps of K summed in tensor memory, parts of a row's sums
-    int pitch, whole;                 // values a row of rows_h; K is whole pieces of 64
+    int pitch, whole, few_box;        // values a row of rows_h; K is whole pieces of 64; rows a box of a few rows' H
 };
 size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K);
 size_t linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K);

@@ -77,9 +77,10 @@ static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "the split
 // loss grows with the steps: 3.1e-6 of the log-probabilities over 3584 products (against 64 bits;
 // 32-bit torch 4.5e-7).  The forward takes the sums out of tensor memory every 896 products
 // at most and adds in registers: 6.9e-7.  Every 512 it is 3.6e-7, but 8% slower, since tensor
-// memory serves these reads at the products' expense; few rows, bound by HBM, are taken out
-// so often.  The gradient's logits meet a rounding of 2^-8 and are left as they are.
-constexpr int kSegment = 896 / kStep, kFewSegment = 512 / kStep;
+// memory serves these reads at the products' expense.  Few rows, bound by HBM, every 256:
+// 1.1e-7, and 0 to 3% slower than every 512 with 2.1e-7.  The gradient's logits meet a rounding
+// of 2^-8 and are left as they are.
+constexpr int kSegment = 896 / kStep, kFewSegment = 256 / kStep;
 
 // ------------------------------------------------------------------ pairs of CTAs
 
@@ -796,6 +797,8 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
         const uint64_t keep = policy_evict_last(), once = policy_evict_first();
         const uint32_t bar0 = map_to_rank(full0, 0);
         const uint32_t total = pair < p.tiles ? (uint32_t)((p.tiles - pair + pairs - 1) / pairs) * p.ksteps : 0;
+        // (H in boxes of few_box rows; where there are none shared memory is left as it is)
+        const uint32_t bytes = 4 * kPiece + (uint32_t)(p.few_box * 128) * (p.M > C::kRows ? 2 : 1);
         int step = 0, tile = pair;
         uint32_t it = 0;
         Ring<kStages> ring;
@@ -807,9 +810,9 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
             const uint32_t s = ring.s, dst = smem_u32(smem + s * C::kStageBytes), bar = bar0 + 8 * s;
             ring.next();
             ring.look(empty0, 1);
-            if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * C::kStageBytes);
+            if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, bytes);
             pair_load(dst, &maps.w, bar, step * kStep, tile * kTile + (int)rank * kHalf, once);
-            pair_load(dst + 2 * kPiece, &maps.h, bar, step * kStep, (int)rank * C::kRows, keep);
+            if ((int)rank * C::kRows < p.M) pair_load(dst + 2 * kPiece, &maps.h, bar, step * kStep, (int)rank * C::kRows, keep);
             if (++step == p.ksteps) step = 0, tile += pairs;
         }
         if (*abort && rank == 0)
@@ -1303,7 +1306,8 @@ cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st) {
     if (few) {
         // (as many pairs as the parts are laid out for)
         const bool least = p.M <= 64;
-        if (!load_map(&maps.h, p.H, p.M, p.K, p.ldh, least ? 32 : 64)) return cudaErrorInvalidValue;
+        p.few_box = (int)std::min<int64_t>(least ? 32 : 64, up(p.M, 8));
+        if (!load_map(&maps.h, p.H, p.M, p.K, p.ldh, (uint32_t)p.few_box)) return cudaErrorInvalidValue;
         p.parts = 8 * std::min(pairs, p.tiles);
         const cudaError_t e = least ? launch_few<64>(pairs, st, maps, p) : launch_few<128>(pairs, st, maps, p);
         if (e != cudaSuccess) return e;
