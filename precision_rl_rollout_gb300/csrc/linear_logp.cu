@@ -30,7 +30,7 @@
 // makes 1.83; the tensor pipe is 88% active (2048 rows x 65536, profiled).  Both gradients of
 // 2731 of 4096 rows: 4.95 and 5.55 ms, 1.80 and 1.61 PFLOP/s, pipe 84%.  One row 174 us, 48
 // rows x 5120 243: 6.3 and 6.4 TB/s.  With few rows the gradient is bound by writing dW (a
-// stream of writes alone makes 4 TB/s): one row 0.70 ms.
+// stream of writes alone makes 4 TB/s): one row 0.59 ms.
 #include <math.h>
 
 #include <algorithm>
@@ -136,6 +136,13 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
 // bf16 x bf16 -> fp32, 256 x 256; bits 15 and 16: A, B are MN-major
 constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (kTile >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
 
+// Two fp32 to bf16, rounded to nearest even, in one instruction: converted one by one, a
+// tile of dW's 64 values a thread take its CTA 1000 cycles.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -189,50 +196,61 @@ constexpr int kLeastSteps = 6;   // steps' time that writing a tile of dW takes 
 template <Mode kMode>
 struct Work {
     const LogpParams& p;
-    int rows, live, pair, pairs, i, phase;
+    int rows, live, pair, pairs, i = 0;
+    // kLogp, kGrad: row tiles a group.  kBack: units of dH and of dW, dH's a row of parts, steps
+    // of dW, units of dW taken first by pairs from `from` on, in all, which comes first, phase
+    int group = 1, nh = 0, nw = 0, part = 1, wsteps = 0, extra = 0, from = 0, head = 0, flip = 0, phase = 0;
 
-    __device__ __forceinline__ Work(const LogpParams& p_) : p(p_), i(0), phase(0) {
+    __device__ __forceinline__ Work(const LogpParams& p_) : p(p_) {
         live = *p.live;
         rows = (live + kTile - 1) / kTile;
         pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+        if constexpr (kMode != kBack) {
+            const int groups = max(1, (rows + p.group - 1) / p.group);
+            group = (rows + groups - 1) / groups;
+        } else {
+            // dH's units and dW's in turn: pairs that have one unit of dH less take as many of
+            // dW as last as long, the others follow in turn.  With few rows dW's are bound by
+            // what HBM writes (4 TB/s), dH's by the products and by reading, and every other
+            // pair takes dW's first, so that the two go on beside each other (before tiles of dW
+            // were written faster: 500 rows of 32000 x 1024 103 -> 99 us, one of 152064 x 3584
+            // 728 -> 696); with more, each is
+            // better off with L2 to itself (1000 rows of 50257 x 896 220, beside each other 228,
+            // 4096 of 152064 x 3584 7930 and 8270).
+            part = max(1, rows * p.ktiles);
+            nh = p.dH ? rows * p.ktiles * p.split : 0, nw = p.dW ? p.tiles * p.ktiles : 0;
+            wsteps = (live + kStep - 1) / kStep, from = nh % pairs;
+            const int cost = max(wsteps, kLeastSteps);
+            extra = from && wsteps ? (p.steps / p.split + cost / 2) / cost : 0, head = extra * (pairs - from);
+            flip = wsteps < 10 ? pair & 1 : 0;
+        }
     }
     __device__ __forceinline__ bool next(Unit& u) {
         if constexpr (kMode != kBack) {
             const int at = pair + i++ * pairs;
             if (at >= rows * p.tiles) return false;
             int r, c;
-            const int groups = (rows + p.group - 1) / p.group;
-            tile_of(at, rows, p.tiles, (rows + groups - 1) / max(groups, 1), r, c);
+            tile_of(at, rows, p.tiles, group, r, c);
             u = Unit{0, r * kTile, c * kTile, 0, p.ksteps, c};
             return true;
         } else {
-            // dH's units and dW's in turn: pairs that have one unit of dH less take as many of
-            // dW as last as long, the others follow in turn.  With few rows dW's are bound by
-            // what HBM writes (4 TB/s), dH's by the products and by reading, and every other
-            // pair takes dW's first, so that the two go on beside each other (500 rows of
-            // 32000 x 1024 103 -> 99 us, one of 152064 x 3584 728 -> 696); with more, each is
-            // better off with L2 to itself (1000 rows of 50257 x 896 220, beside each other 228,
-            // 4096 of 152064 x 3584 7930 and 8270).
-            const int kt = p.ktiles;
-            const int nh = p.dH ? rows * kt * p.split : 0, nw = p.dW ? p.tiles * kt : 0;
-            const int wsteps = (live + kStep - 1) / kStep;
             for (; phase < 2; ++phase, i = 0) {
-                if ((phase ^ (wsteps < 10 ? pair : 0)) & 1) {
-                    const int r = nh % pairs, cost = max(wsteps, kLeastSteps);
-                    const int extra = r && wsteps ? (p.steps / p.split + cost / 2) / cost : 0, head = extra * (pairs - r);
+                if (phase ^ flip) {
                     int at = head + pair + i * pairs;
-                    if (pair >= r && extra) at = i < extra ? pair - r + i * (pairs - r) : head + pair + (i - extra) * pairs;
+                    if (pair >= from && extra)
+                        at = i < extra ? pair - from + i * (pairs - from) : head + pair + (i - extra) * pairs;
                     if (at >= nw) continue;
                     ++i;
-                    u = Unit{2, at / kt * kTile, at % kt * kTile, 0, wsteps, 0};
+                    const int v = (int)((uint32_t)at / (uint32_t)p.ktiles);
+                    u = Unit{2, v * kTile, (at - v * p.ktiles) * kTile, 0, wsteps, 0};
                     return true;
                 }
                 const int at = pair + i * pairs;
                 if (at >= nh) continue;
                 ++i;
-                const int s = at / (rows * kt), t = at - s * rows * kt;
+                const int s = at / part, t = at - s * part, r = t / p.ktiles;
                 const int k = s * p.steps / p.split, end = (s + 1) * p.steps / p.split;
-                u = Unit{1, t / kt * kTile, t % kt * kTile, k, end - k, s};
+                u = Unit{1, r * kTile, (t - r * p.ktiles) * kTile, k, end - k, s};
                 return true;
             }
             return false;
@@ -673,10 +691,10 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                             if (j + e >= cols) v[e] = 0.f;
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) packed[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                    for (int e = 0; e < 32; ++e) packed[e] = pack2(v[2 * e], v[2 * e + 1]);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) packed[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+                    for (int e = 0; e < 32; ++e) packed[e] = pack2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
                 }
                 if (j == 0) clear();
                 uint8_t* const box = out + (j / 64) * kOutBytes;
@@ -1098,7 +1116,7 @@ grad_h_kernel(const __grid_constant__ LogpParams p) {
                 for (int j = 0; j < 4; ++j)
                     if (s + j < p.split) v.x += w[j].x, v.y += w[j].y, v.z += w[j].z, v.w += w[j].w;
             }
-            dst[i] = make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+            dst[i] = make_uint2(pack2(v.x * f, v.y * f), pack2(v.z * f, v.w * f));
         }
     }
 }
