@@ -629,6 +629,11 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 __syncwarp();
             };
             const int y = u.a + (int)rank * kHalf + 32 * q, x = u.b + half * kHalf;   // the warp's first row and column
+            // rows that nobody reads: past those that count, of D past the last 64 of them
+            if (u.kind != 2 && y >= (kMode == kGrad ? (work.live + 63) / 64 * 64 : work.live)) {
+                release();
+                continue;
+            }
             // 64 columns from tensor memory, which is let go of after the last of them
             auto take = [&](int j, uint32_t (&r)[64]) {
                 if (u.n > 0) {
