@@ -553,13 +553,14 @@ int fp8rl_spec_verify(const void* P, int64_t p_seq, int64_t p_step, const void* 
  * H  bf16 [M][ldh], W bf16 [V][ldw], ld >= K, ld % 8 == 0, 16-byte aligned.
  * K  a multiple of 8 (FP8RL_ERR_SHAPE); V any number.
  * targets int32 [M]; logp, lse fp32 [M]; entropy fp32 [M] or NULL.
- * scale: finite and > 0 (FP8RL_ERR_UNSUPPORTED).
+ * scale: > 0 and at most 2e38 (FP8RL_ERR_UNSUPPORTED).
  * Up to 128 rows are one pass over W that HBM bounds; the rows that do not count cost
  * nothing above that.
  * workspace: at least fp8rl_linear_logp_workspace_bytes(M, V, K) bytes, 16-byte
  *     aligned, no zeroing, nothing kept between calls; calls in flight at once need
  *     their own.  (Above 128 rows a copy of H and 12 bytes a row for 128 words.)
- * Limits: M, V <= 2^21, K <= 65536, ld <= 2^32 (FP8RL_ERR_UNSUPPORTED).
+ * Limits: M, V <= 2^21, K <= 65536, ld <= 2^32 (FP8RL_ERR_UNSUPPORTED; the workspace
+ * queries return 0 past them).
  * ---------------------------------------------------------------------- */
 size_t fp8rl_linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K);
 int fp8rl_linear_logp(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, const int32_t* targets,
@@ -608,7 +609,7 @@ int fp8rl_linear_logp_backward(const uint16_t* H, int64_t ldh, const uint16_t* W
  * X  fp32 or bf16 (dtype) [M][ldx], ldx >= V, 16-byte aligned, rows of a multiple of
  *    16 bytes.  indices int32 [M][k], T fp32 [M][k], teacher_lse fp32 [M] or NULL;
  *    loss, lse fp32 [M], rest_lse fp32 [M] or NULL.
- * scale: finite and > 0.  Limits: k <= 1024, V <= 2^20, M < 2^31
+ * scale: > 0 and at most 2e38.  Limits: k <= 1024, V <= 2^20, M < 2^31
  * (FP8RL_ERR_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 #define FP8RL_LOGITS_F32 0

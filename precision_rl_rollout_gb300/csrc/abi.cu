@@ -457,8 +457,8 @@ static int check_linear_logp(const uint16_t* H, int64_t ldh, const uint16_t* W, 
     if (M < 0 || V <= 0 || K <= 0 || K % 8 || ldh < K || ldw < K) return FP8RL_ERR_SHAPE;
     if (!W || (M > 0 && (!H || !targets))) return FP8RL_ERR_NULL;
     if (!aligned16(H) || !aligned16(W) || ldh % 8 || ldw % 8 || !aligned4(targets)) return FP8RL_ERR_ALIGN;
-    if (M > (1 << 21) || V > (1 << 21) || K > (1 << 16) || ldh > (1ll << 32) || ldw > (1ll << 32) || !(scale > 0.f) ||
-        scale > 3e38f)
+    if (M > kLogpRows || V > kLogpRows || K > kLogpK || ldh > (1ll << 32) || ldw > (1ll << 32) || !(scale > 0.f) ||
+        scale > 2e38f)
         return FP8RL_ERR_UNSUPPORTED;
     return FP8RL_OK;
 }
@@ -518,7 +518,7 @@ static int check_distill(const void* X, int64_t ldx, int dtype, const int32_t* i
     if (!aligned16(X) || ldx % (dtype == FP8RL_LOGITS_F32 ? 4 : 8) || !aligned4(indices) || !aligned4(T) ||
         !aligned4(teacher_lse) || !aligned4(lse) || !aligned4(rest_lse))
         return FP8RL_ERR_ALIGN;
-    if (M > INT32_MAX || V > (1 << 20) || k > 1024 || !(scale > 0.f) || scale > 3e38f) return FP8RL_ERR_UNSUPPORTED;
+    if (M > INT32_MAX || V > (1 << 20) || k > 1024 || !(scale > 0.f) || scale > 2e38f) return FP8RL_ERR_UNSUPPORTED;
     return FP8RL_OK;
 }
 

@@ -115,6 +115,7 @@ cudaError_t launch_spec_verify(const VerifyParams& p, bool bf16, cudaStream_t st
 
 // Log-probabilities of chosen tokens from hidden states and output matrix, and their
 // gradient (strides in elements).
+constexpr int64_t kLogpRows = 1 << 21, kLogpK = 1 << 16;   // the most rows, and words; the longest product
 struct LogpParams {
     const uint16_t *H, *W;
     const int32_t* targets;

@@ -312,17 +312,24 @@ __device__ __forceinline__ void sums_of(Sums& s, const uint64_t (&x)[kCols / 2],
             if (2 * j + 1 < n) most = fmaxf(most, v.y);
         }
     }
-    s.top = most * c;
+    s.top = fmaxf(most * c, -3.0e38f);                  // finite where every logit is -inf
     const uint64_t cc = pk2(c, c), low = pk2(-s.top, -s.top);
     uint64_t sum = 0, dev = 0;
-    if (n >= kCols) {
+    bool careful = n < kCols;
+    if (!careful) {
 #pragma unroll
         for (int j = 0; j < kCols / 2; ++j) {
             const uint64_t a = fma2(x[j], cc, low), e = ex2_2(a);
             sum = add2(sum, e);
             if (kDev) dev = fma2(e, a, dev);
         }
-    } else {
+        if (kDev) {                                     // 0 times a logit of -inf
+            const float2 d = f32x2_unpack(dev);
+            careful = isnan(d.x + d.y);
+        }
+    }
+    if (careful) {
+        sum = dev = 0;
 #pragma unroll
         for (int j = 0; j < kCols / 2; ++j) {
             const uint64_t a = fma2(x[j], cc, low);
@@ -668,7 +675,9 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 }
                 continue;
             }
-            const int cols = (int)min((int64_t)kTile, p.V - p.first - u.b) - half * kHalf;   // kGrad: words of this half
+            // kGrad: words of this half; none for a row past those that count (0 times what its
+            // logits come to would be NaN where W holds infinities)
+            const int cols = kMode == kGrad && m >= work.live ? 0 : (int)min((int64_t)kTile, p.V - p.first - u.b) - half * kHalf;
             const bool entropy = p.ge != nullptr;
 #pragma unroll 1
             for (int j = 0; j < kHalf; j += 64) {
@@ -924,7 +933,7 @@ logp_few_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpP
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) w[e] = there ? x[g][e] : kNone;
-                const float top = across(w, lane, [](float a, float b) { return fmaxf(a, b); }) * c;
+                const float top = fmaxf(across(w, lane, [](float a, float b) { return fmaxf(a, b); }) * c, kNone);
                 float d[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -984,7 +993,7 @@ rows_kernel(const __grid_constant__ LogpParams p, int rows) {
         const float g = kBackward ? fabsf(p.g[m]) : 0.f, e = kBackward && p.ge ? fabsf(p.ge[m]) : 0.f;
         if (t >= 0 && t < p.V) {
             before += m < m0, ++all;
-            largest = fmaxf(largest, fmaxf(g, e));
+            if (fmaxf(g, e) < INFINITY) largest = fmaxf(largest, fmaxf(g, e));   // an infinite one is its row's alone
         }
     }
 #pragma unroll
@@ -1297,7 +1306,7 @@ int pairs_or_default() {
 }  // namespace
 
 size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-    if (M <= 0 || V <= 0 || K <= 0) return 0;
+    if (M <= 0 || V <= 0 || K <= 0 || M > kLogpRows || V > kLogpRows || K > kLogpK) return 0;
     LogpParams p{};
     p.M = M, p.V = V, p.K = K;
     Arena a{nullptr};
@@ -1306,7 +1315,7 @@ size_t linear_logp_workspace_bytes(int64_t M, int64_t V, int64_t K) {
 }
 
 size_t linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-    if (M <= 0 || V <= 0 || K <= 0) return 0;
+    if (M <= 0 || V <= 0 || K <= 0 || M > kLogpRows || V > kLogpRows || K > kLogpK) return 0;
     LogpParams p{};
     p.M = M, p.V = V, p.K = K;
     Arena a{nullptr};

@@ -161,6 +161,36 @@ def test_same_token_and_zero_gradients(cuda_lib, M):
         ref.check(a, b)
 
 
+@pytest.mark.parametrize("M", [20, 128, 300])
+def test_words_of_minus_infinity(cuda_lib, M):
+    """Logits of -inf for every word of a tile and some of the next are probabilities of 0; no
+    row's gradient reaches their words."""
+    H, W, t, (g, _) = _inputs(M, 700, 64, 0.0)
+    H, t = (H.abs() + 0.125).to(torch.bfloat16), t.clamp(min=300)
+    W[:300] = float("-inf")
+    for scale in (0.5, 3.0):
+        out = fb.fp8rl_linear_logp(H, W, t, scale=scale, want_entropy=True)
+        finite = [ref.linear_logp(H, W[300:], t - 300, scale), ref.linear_logp_grad(H, W[300:], t - 300, g, None, scale)]
+        for a, b in zip(out, finite[0]):
+            ref.check(a, b)
+        _, dW = fb.fp8rl_linear_logp_backward(H, W, t, out[1], g, scale=scale, want_dH=False)
+        assert (dW[:300] == 0).all()
+        ref.check(dW[300:], finite[1][1])
+
+
+@pytest.mark.parametrize("what", [float("inf"), float("nan")])
+def test_a_broken_gradient_stays_in_its_row(cuda_lib, what):
+    H, W, t, (g, ge) = _inputs(300, 700, 64, 0.2)
+    broken, zero = g.clone(), g.clone()
+    t[5], broken[5], zero[5] = 3, what, 0.0
+    H[5] = 1.0
+    _, lse, ent = fb.fp8rl_linear_logp(H, W, t, want_entropy=True)
+    a, _ = fb.fp8rl_linear_logp_backward(H, W, t, lse, broken, entropy=ent, g_entropy=ge)
+    b, _ = fb.fp8rl_linear_logp_backward(H, W, t, lse, zero, entropy=ent, g_entropy=ge)
+    others = torch.arange(300, device="cuda") != 5
+    assert torch.equal(a[others], b[others]) and not torch.isfinite(a[5]).any()
+
+
 def test_offsets_past_32_bits(cuda_lib):
     """A matrix of more than 2^32 bytes and 2^31 values, the target in its last row."""
     V, K, M = 152064, 16384, 3

@@ -30,9 +30,10 @@ def test_linear_logp_validation(lib):
     need = lib.fp8rl_linear_logp_workspace_bytes(4, 100, 64)
     assert need > 0 and f(wb=need - 1) == 4 and f(ws=None) == 4
     assert f(M=(1 << 21) + 1) == 6 and f(V=(1 << 21) + 1) == 6 and f(K=65544, ldh=65544, ldw=65544) == 6
-    for scale in (0.0, -1.0, float("nan"), float("inf")):
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 2.1e38):
         assert f(scale=scale) == 6
-    for bad in ((0, 5, 8), (5, 0, 8), (5, 5, 0), (-1, 5, 8)):
+    for bad in ((0, 5, 8), (5, 0, 8), (5, 5, 0), (-1, 5, 8), ((1 << 21) + 1, 5, 8), (1 << 55, 5, 8), (1 << 62, 5, 8),
+                (5, 1 << 62, 8), (5, 5, 65544)):
         assert lib.fp8rl_linear_logp_workspace_bytes(*bad) == 0
         assert lib.fp8rl_linear_logp_backward_workspace_bytes(*bad) == 0
 
