@@ -69,11 +69,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 // exp(scale d) for d <= 0: the constant scale log2(e) in two parts, since its rounding alone
-// would be a change of temperature, some 1e-6 of the sum.
+// would be a change of temperature, some 1e-6 of the sum.  Both parts are positive, so that
+// both products of d = -inf (a lowest logit under one of 1e37) are -inf.
 struct Scale {
     float c, rest;
-    __device__ __forceinline__ explicit Scale(float scale)
-        : c(scale * kLog2e), rest(fmaf(scale, kLog2e, -(scale * kLog2e)) + scale * kLog2eRest) {}
+    __device__ __forceinline__ explicit Scale(float scale) : c(scale * kLog2e), rest(left(scale)) {
+        if (rest < 0.f) c = __uint_as_float(__float_as_uint(c) - 1), rest = left(scale);
+        rest = fmaxf(rest, 1e-45f);
+    }
+    __device__ __forceinline__ float left(float scale) const { return fmaf(scale, kLog2e, -c) + scale * kLog2eRest; }
     __device__ __forceinline__ float exp(float d) const { return ex2(fmaf(d, c, d * rest)); }
     // of two logits relative to a maximum, given as pairs with -top
     __device__ __forceinline__ uint64_t exp(uint64_t x, uint64_t low) const {
@@ -455,7 +459,8 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
                      (lane == 0 ? (double)s.top * scale : lane == 1 ? (double)top * scale : 0.0);
     const double lse = __shfl_sync(0xffffffffu, v, 1), log_qr = __shfl_sync(0xffffffffu, v, 2);
     if (lane == 0) {
-        double loss = far * scale + n.total * ((lse - (double)n.shift) - (double)n.shift_rest);
+        double loss = far * scale;
+        if (n.total != 0.0) loss += n.total * ((lse - (double)n.shift) - (double)n.shift_rest);
         if (qr > 0.0) loss += qr * (log_qr - (v - lse));
         p.loss[m] = (float)loss, p.lse[m] = (float)lse;
         if (p.rest_lse) p.rest_lse[m] = (float)v;

@@ -90,6 +90,39 @@ def test_infinite_and_extreme_logits(cuda_lib, dtype):
         _check(X, ids, T, lse, g, rest, not rest, 1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [0.3, 0.7, 1.0, 1.3])
+def test_a_lowest_logit_under_a_huge_one(cuda_lib, dtype, scale):
+    """Their difference is -inf in 32 bits, the second's share still 0; a row of masks alone costs nothing
+    where the teacher has no weight either."""
+    X, ids, T, lse, g = _inputs(9, 1000, 20, dtype, masked=0.0)
+    X, ids, T = X.clone(), ids.clone(), T.clone()
+    last = X.argsort(dim=1)
+    X[0, last[0, 500]], X[3, last[3, 999]] = 1e37, 3e37
+    X[0, last[0, :100]], X[3, last[3, 0]] = torch.finfo(dtype).min, torch.finfo(dtype).min
+    X[5] = float("-inf")
+    T[5] = float("-inf")
+    got = fb.fp8rl_distill_topk(X, ids, T, scale=scale)
+    want = ref.distill(X, ids, torch.where(torch.isinf(T), 0.0, T), None, False, scale)
+    keep = torch.arange(9, device="cuda") != 5
+    for a, b in zip(got, want):
+        ref.check(a[keep], tuple(x[keep] for x in b))
+    assert got[0][5].item() == 0.0
+
+
+@pytest.mark.parametrize("M", [1, 9, 700])
+def test_the_largest_vocabulary(cuda_lib, M):
+    """As many parts a row as there are, with the bits of 2^20 tokens in each one's shared memory."""
+    X, ids, T, lse, g = _inputs(M, 1 << 20, 1024 if M < 10 else 20, torch.bfloat16)
+    out = fb.fp8rl_distill_topk(X, ids, T, teacher_lse=lse, rest=True)
+    dX = fb.fp8rl_distill_topk_backward(X, ids, T, out[1], g, teacher_lse=lse, rest_lse=out[2])
+    few = slice(max(0, M - 9), M)
+    want = ref.distill(X[few], ids[few], T[few], lse[few], True)
+    for a, b in zip(out, want):
+        ref.check(a[few], b)
+    ref.check(dX[few], ref.distill_grad(X[few], ids[few], T[few], g[few], lse[few], True))
+
+
 def test_masked_token_of_the_teacher_costs_everything(cuda_lib):
     X, ids, T, lse, g = _inputs(1, 500, 4, torch.float32)
     X[0, ids[0, 0].long()] = float("-inf")
