@@ -62,9 +62,9 @@ enum Mode { kLogp, kGrad, kBack };
 template <Mode kMode>
 struct Config {
     static constexpr bool kForward = kMode == kLogp;
-    static constexpr int kStages = kForward ? 6 : 5, kStageBytes = 4 * kPiece;   // two pieces of either operand
+    static constexpr int kStages = kMode == kBack ? 5 : 6, kStageBytes = 4 * kPiece;   // two pieces of either operand
     static constexpr int kEpiWarps = 8, kThreads = 32 * (4 + kEpiWarps);
-    static constexpr int kOuts = kForward ? 0 : 2;           // boxes a warp stages at once
+    static constexpr int kOuts = kForward ? 0 : kMode == kGrad ? 1 : 2;           // boxes a warp stages at once
     static constexpr int kOutOffset = kStages * kStageBytes;
     static constexpr int kBarOffset = kOutOffset + kEpiWarps * kOuts * kOutBytes;
     static constexpr int kSmemBytes = kBarOffset + 256 + 1024;
@@ -710,21 +710,25 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
 #pragma unroll
                     for (int e = 0; e < 32; ++e) packed[e] = pack2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
                 }
-                if (j == 0) clear();
-                uint8_t* const box = out + (j / 64) * kOutBytes;
+                if (j == 0 || kMode == kGrad) clear();
+                uint8_t* const box = out + (kMode == kGrad ? 0 : (j / 64) * kOutBytes);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     stage16(box, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t from = smem_u32(out + h * kOutBytes);
-                    if (kMode == kGrad) tma_store_2d(&maps.d_out, from, x + 64 * h, y);
-                    else if (x + 64 * h < p.K && p.first + y < p.V) tma_store_2d(&maps.dw, from, x + 64 * h, p.first + y);
+                if (kMode == kGrad || j) {                       // kGrad a box at a time, dW two
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
+                if (kMode == kGrad && lane == 0) {
+                    tma_store_2d(&maps.d_out, smem_u32(box), x + j, y);
+                    bulk_commit();
+                }
+            }
+            if (kMode == kBack && lane == 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (x + 64 * h < p.K && p.first + y < p.V)
+                        tma_store_2d(&maps.dw, smem_u32(out + h * kOutBytes), x + 64 * h, p.first + y);
                 bulk_commit();
             }
         }
