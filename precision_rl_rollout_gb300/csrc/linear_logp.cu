@@ -62,9 +62,9 @@ enum Mode { kLogp, kGrad, kBack };
 template <Mode kMode>
 struct Config {
     static constexpr bool kForward = kMode == kLogp;
-    static constexpr int kStages = kMode == kBack ? 5 : 6, kStageBytes = 4 * kPiece;   // two pieces of either operand
+    static constexpr int kStages = 6, kStageBytes = 4 * kPiece;   // two pieces of either operand
     static constexpr int kEpiWarps = 8, kThreads = 32 * (4 + kEpiWarps);
-    static constexpr int kOuts = kForward ? 0 : kMode == kGrad ? 1 : 2;           // boxes a warp stages at once
+    static constexpr int kOuts = kForward ? 0 : 1;           // boxes a warp stages at once
     static constexpr int kOutOffset = kStages * kStageBytes;
     static constexpr int kBarOffset = kOutOffset + kEpiWarps * kOuts * kOutBytes;
     static constexpr int kSmemBytes = kBarOffset + 256 + 1024;
@@ -656,21 +656,20 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 for (int j = 0; j < kHalf; j += 64) {
                     uint32_t r[64];
                     take(j, r);
-                    clear();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        stage16(out + (e >> 3) * kOutBytes, lane, e & 7, make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]));
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
+                    for (int h = 0; h < 2; ++h) {
+                        clear();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int at = x + j + 32 * h, to = u.slot * p.rows_pad + y;
-                            if (at >= p.K) break;
-                            if (p.first == 0) tma_store_2d(&maps.acc, smem_u32(out + h * kOutBytes), at, to);
-                            else tma_add_2d(&maps.acc, smem_u32(out + h * kOutBytes), at, to);
+                        for (int e = 8 * h; e < 8 * h + 8; ++e)
+                            stage16(out, lane, e & 7, make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]));
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        const int at = x + j + 32 * h, to = u.slot * p.rows_pad + y;
+                        if (lane == 0 && at < p.K) {
+                            if (p.first == 0) tma_store_2d(&maps.acc, smem_u32(out), at, to);
+                            else tma_add_2d(&maps.acc, smem_u32(out), at, to);
+                            bulk_commit();
                         }
-                        bulk_commit();
                     }
                 }
                 continue;
@@ -710,26 +709,17 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
 #pragma unroll
                     for (int e = 0; e < 32; ++e) packed[e] = pack2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
                 }
-                if (j == 0 || kMode == kGrad) clear();
-                uint8_t* const box = out + (kMode == kGrad ? 0 : (j / 64) * kOutBytes);
+                clear();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    stage16(box, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
-                if (kMode == kGrad || j) {                       // kGrad a box at a time, dW two
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (kMode == kGrad && lane == 0) {
-                    tma_store_2d(&maps.d_out, smem_u32(box), x + j, y);
+                    stage16(out, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kMode == kGrad) tma_store_2d(&maps.d_out, smem_u32(out), x + j, y);
+                    else if (x + j < p.K && p.first + y < p.V) tma_store_2d(&maps.dw, smem_u32(out), x + j, p.first + y);
                     bulk_commit();
                 }
-            }
-            if (kMode == kBack && lane == 0) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (x + 64 * h < p.K && p.first + y < p.V)
-                        tma_store_2d(&maps.dw, smem_u32(out + h * kOutBytes), x + 64 * h, p.first + y);
-                bulk_commit();
             }
         }
         if (lane == 0) bulk_wait_all();
