@@ -24,13 +24,13 @@
 // transpose with H (both MN-major) into the piece's rows of dW.  Nothing is transposed in
 // memory, and each sum of dH is added to once a launch, so results do not depend on order.
 //
-// What bounds it: the tensor cores, and for long calls the power they draw.  8192 rows, 5734 of
-// them counted, 152064 words x 3584: 3.63 ms alone, 1.72 PFLOP/s (90% of the measured 1.92),
-// 3.75 among others, where the clocks fall to 1.6 GHz and a library's product of this size
-// makes 1.83; the tensor pipe is 88% active (2048 rows x 65536, profiled).  Both gradients of
-// 2731 of 4096 rows: 4.95 and 5.55 ms, 1.80 and 1.61 PFLOP/s, pipe 84%.  One row 174 us, 48
-// rows x 5120 243: 6.3 and 6.4 TB/s.  With few rows the gradient is bound by writing dW (a
-// stream of writes alone makes 4 TB/s): one row 0.59 ms.
+// What bounds it: the tensor cores, and for long calls the power they draw.  4096 rows of
+// 152064 words x 3584: 2.30 ms alone, 1.94 PFLOP/s (the measured peak is 1.92), 2.55 in a loop, where
+// the clocks fall to 1.6 GHz and a library's product of this size makes 1.83; 8192 rows, 5734 of
+// them counted, 3.8.  Both gradients of 4096 rows 7.7 ms (1.73 PFLOP/s), of 2731 among 4096 5.4, 4.75
+// alone.  Profiled on 2048 rows of 65536: kLogp 0.51 ms, kGrad 0.54, kBack 1.03, the tensor pipe 86 to
+// 89% active.  One row 161 us, 48 rows x 5120 228: 6.8 TB/s.  With few rows the gradient is
+// bound by writing dW (a stream of writes alone makes 4 TB/s): one row 0.56 ms.
 #include <math.h>
 
 #include <algorithm>
@@ -58,7 +58,9 @@ constexpr int kOutBytes = 32 * 128;                     // a warp's staging
 enum Mode { kLogp, kGrad, kBack };
 
 // Eight warps have the threads' part, half of a row a thread.  kLogp keeps it in registers,
-// which the other warps let go of, and stages nothing; the others stage what they write.
+// which the other warps let go of, and stages nothing; the others stage what they write, a box
+// a warp.  Six stages: with five, and two boxes, the gradients take 1 to 9% longer (500 rows of
+// 32000 x 1024 99 us for 91), with seven the forward up to 3%.
 template <Mode kMode>
 struct Config {
     static constexpr bool kForward = kMode == kLogp;
@@ -751,7 +753,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
 // products' 256, 128 a CTA, the rows that count their 64 or 128 columns, and nearly all of
 // shared memory holds W on its way (11 stages of 16 KB of it, 9 with 128 columns; with rows
 // on the other side it was 6, every product was made for 256 rows, and 48 rows of
-// 152064 x 5120 took 272 us).  A thread has a word of the vocabulary and 32 columns at a time; a
+// 152064 x 5120 took 272 us, 228 here).  A thread has a word of the vocabulary and 32 columns at a time; a
 // column's maximum and sums over a warp's 32 words meet by exchanges that halve the
 // columns at each step, so that lane l ends up with column l, whose sums it keeps over
 // all of its warp's tiles.  Columns do not meet, so H is read as it lies, rows that do not
