@@ -980,7 +980,8 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 // The rows that count, brought together: their hidden states, targets and gradients; zeros
 // for the results of the others.  Every CTA goes over all targets (they are in L2) to find
 // where its own rows go, so nothing is waited for.
-constexpr int kRowThreads = 256, kMostRows = 512;
+static_assert(kLogpRows <= 1024 * 2048, "rows a CTA");
+constexpr int kRowThreads = 256, kMostRows = 2048;
 
 template <bool kBackward>
 __global__ void __launch_bounds__(kRowThreads)
@@ -1293,9 +1294,9 @@ bool load_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
 
 cudaError_t launch_rows(const LogpParams& p, bool backward, cudaStream_t st) {
     // rows a CTA: four up to a CTA an SM, then to sixteen; every CTA goes over all targets,
-    // so not more than 4096 CTAs
+    // so not more than 1024 CTAs
     const int64_t even = (p.M + num_sms() - 1) / num_sms();
-    const int rows = (int)std::max<int64_t>(std::min<int64_t>(std::max<int64_t>(even, 4), 16), (p.M + 4095) / 4096);
+    const int rows = (int)std::max<int64_t>(std::min<int64_t>(std::max<int64_t>(even, 4), 16), (p.M + 1023) / 1024);
     const dim3 grid((unsigned)((p.M + rows - 1) / rows));
     return backward ? launch_pdl(rows_kernel<true>, grid, dim3(kRowThreads), 0, st, p, rows)
                     : launch_pdl(rows_kernel<false>, grid, dim3(kRowThreads), 0, st, p, rows);

@@ -191,6 +191,18 @@ def test_a_broken_gradient_stays_in_its_row(cuda_lib, what):
     assert torch.equal(a[others], b[others]) and not torch.isfinite(a[5]).any()
 
 
+@pytest.mark.parametrize("M,V,K", [(1 << 21, 9, 8), (2, 1 << 21, 64), (140, 1 << 21, 64)])
+def test_most_rows_and_words(cuda_lib, M, V, K):
+    H, W, t, (g, ge) = _inputs(M, V, K)
+    t[-1], H[-1] = V - 1, 1.0
+    out = fb.fp8rl_linear_logp(H, W, t, want_entropy=True)
+    for a, b in zip(out, ref.linear_logp(H, W, t)):
+        ref.check(a, b)
+    grads = fb.fp8rl_linear_logp_backward(H, W, t, out[1], g, entropy=out[2], g_entropy=ge)
+    for a, b in zip(grads, ref.linear_logp_grad(H, W, t, g, ge)):
+        ref.check(a, b)
+
+
 def test_offsets_past_32_bits(cuda_lib):
     """A matrix of more than 2^32 bytes and 2^31 values, the target in its last row."""
     V, K, M = 152064, 16384, 3
