@@ -30,7 +30,7 @@
 // them counted, 3.8.  Both gradients of 4096 rows 7.7 ms (1.73 PFLOP/s), of 2731 among 4096 5.4, 4.75
 // alone.  Profiled on 2048 rows of 65536: kLogp 0.51 ms, kGrad 0.54, kBack 1.03, the tensor pipe 86 to
 // 89% active.  One row 161 us, 48 rows x 5120 228: 6.8 TB/s.  With few rows the gradient is
-// bound by writing dW (a stream of writes alone makes 4 TB/s): one row 0.56 ms.
+// bound by writing dW (a stream of writes alone makes 4 TB/s): one row 0.55 ms.
 #include <math.h>
 
 #include <algorithm>
@@ -217,19 +217,19 @@ struct Work {
             group = (rows + groups - 1) / groups;
         } else {
             // dH's units and dW's in turn: pairs that have one unit of dH less take as many of
-            // dW as last as long, the others follow in turn.  With few rows dW's are bound by
-            // what HBM writes (4 TB/s), dH's by the products and by reading, and every other
-            // pair takes dW's first, so that the two go on beside each other (before tiles of dW
-            // were written faster: 500 rows of 32000 x 1024 103 -> 99 us, one of 152064 x 3584
-            // 728 -> 696); with more, each is
-            // better off with L2 to itself (1000 rows of 50257 x 896 220, beside each other 228,
-            // 4096 of 152064 x 3584 7930 and 8270).
+            // dW as last as long, the others follow in turn.  With few rows and a W not much larger
+            // than L2 every other pair takes dW's first, so that writing goes on beside reading and
+            // products (one after the other, then beside each other, us: 500 rows of 32000 x 1024 92 and
+            // 90, 200 of 32000 x 2048 105 and 101, 20 of it 92.7 and 91.1); else each is better off with L2
+            // and HBM to itself (20 rows of 50257 x 2048 129.6 and 131.6, of 152064 x 5120 754 and
+            // 797, one of 152064 x 3584 549 and 557, 1000 of 50257 x 896 198 and 210; 200 rows of 50257 to
+            // 100000 x 2048 would gain 1%).
             part = max(1, rows * p.ktiles);
             nh = p.dH ? rows * p.ktiles * p.split : 0, nw = p.dW ? p.tiles * p.ktiles : 0;
             wsteps = (live + kStep - 1) / kStep, from = nh % pairs;
             const int cost = max(wsteps, kLeastSteps);
             extra = from && wsteps ? (p.steps / p.split + cost / 2) / cost : 0, head = extra * (pairs - from);
-            flip = wsteps < 10 ? pair & 1 : 0;
+            flip = wsteps < 10 && p.V * p.K <= 80ll << 20 ? pair & 1 : 0;
         }
     }
     __device__ __forceinline__ bool next(Unit& u) {
