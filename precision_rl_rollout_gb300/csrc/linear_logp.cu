@@ -702,7 +702,11 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                     for (int e = 0; e < 32; ++e) {
                         const uint64_t a = fma2(f32x2_pack(r[2 * e], r[2 * e + 1]), cc, low), pr = ex2_2(a);
                         uint64_t d = mul2(ng, pr);
-                        if (entropy) d = fma2(mul2(ng2, pr), fma2(a, ln2, pl), d);
+                        if (entropy) {
+                            // log p times a p of 0 is 0 where the logit is -inf too (a NaN is in d already)
+                            const float2 l = f32x2_unpack(a);
+                            d = fma2(mul2(ng2, pr), fma2(pk2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), ln2, pl), d);
+                        }
                         const float2 two = f32x2_unpack(d);
                         v[2 * e] = two.x, v[2 * e + 1] = two.y;
                     }

@@ -1,0 +1,55 @@
+"""The trainer's losses where logits, weights or sums are at their ends: words of -inf under
+an entropy's gradient, rows of lowest logits, targets that the policy is sure of, long sums."""
+import pytest
+import torch
+
+import losses_ref as ref
+from precision_rl_rollout_gb300 import binding as fb
+
+pytestmark = pytest.mark.gpu
+
+
+def _head(M, V, K, seed=0, spread=2.5):
+    g = torch.Generator(device="cuda").manual_seed(seed + M + 7 * V + 13 * K)
+    H = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    W = (torch.randn((V, K), generator=g, device="cuda") * spread / K ** 0.5).to(torch.bfloat16)
+    t = torch.randint(0, V, (M,), generator=g, device="cuda", dtype=torch.int32)
+    return H, W, t, torch.randn(M, generator=g, device="cuda"), torch.randn(M, generator=g, device="cuda") * 0.1
+
+
+@pytest.mark.parametrize("M", [1, 20, 128, 300])
+@pytest.mark.parametrize("scale", [0.5, 3.0])
+def test_entropys_gradient_at_words_of_minus_infinity(cuda_lib, M, scale):
+    """Words whose logit is -inf in every row have a gradient of 0, in rows without an
+    entropy's gradient and with one; the other words' is as if those were not there."""
+    H, W, t, g, ge = _head(M, 700, 64)
+    H, t = (H.abs() + 0.125).to(torch.bfloat16), t.clamp(min=300)
+    W[:300] = float("-inf")
+    ge[::3] = 0.0
+    _, lse, ent = fb.fp8rl_linear_logp(H, W, t, scale=scale, want_entropy=True)
+    _, dW = fb.fp8rl_linear_logp_backward(H, W, t, lse, g, entropy=ent, g_entropy=ge, scale=scale, want_dH=False)
+    assert (dW[:300] == 0).all()
+    ref.check(dW[300:], ref.linear_logp_grad(H, W[300:], t - 300, g, ge, scale)[1], "dW")
+
+
+def test_a_row_with_one_word_of_minus_infinity(cuda_lib):
+    """One row's logit is -inf, the others' at that word are finite: its own part is 0."""
+    H, W, t, g, ge = _head(150, 300, 64)
+    W[7, 0], W[:, 1:8], H[:, 0] = -3.0e38, 0.0, 0.0       # only row 5 meets the word's lowest entry
+    H[5, 0] = 4.0                                          # -1.2e39 is -inf in 32 bits
+    t[5] = 3
+    _, lse, ent = fb.fp8rl_linear_logp(H, W, t, want_entropy=True)
+    _, dW = fb.fp8rl_linear_logp_backward(H, W, t, lse, g, entropy=ent, g_entropy=ge, want_dH=False)
+    W2 = W.clone()
+    W2[7, 0] = -1.0e4                                      # exp(-4e4) is 0 in 64 bits too
+    ref.check(dW, ref.linear_logp_grad(H, W2, t, g, ge)[1], "dW")
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_nan_passes_the_entropys_gradient(cuda_lib, M):
+    """A word of NaN stays NaN in the gradient of every row that counts."""
+    H, W, t, g, ge = _head(M, 300, 64)
+    W[40] = float("nan")
+    ones = torch.ones(M, device="cuda")
+    dH, _ = fb.fp8rl_linear_logp_backward(H, W, t, ones, g, entropy=ones, g_entropy=ge, want_dW=False)
+    assert dH.isnan().all()
