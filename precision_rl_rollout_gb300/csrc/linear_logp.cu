@@ -57,8 +57,8 @@ constexpr int kOutBytes = 32 * 128;                     // a warp's staging
 
 enum Mode { kLogp, kGrad, kBack };
 
-// Eight warps have the threads' part, half of a row a thread.  kLogp keeps it in registers,
-// which the other warps let go of, and stages nothing; the others stage what they write, a box
+// Eight warps have the threads' part, half of a row a thread.  kLogp and kGrad keep it in registers,
+// which the other warps let go of.  kLogp stages nothing; the others stage what they write, a box
 // a warp.  Six stages: with five, and two boxes, the gradients take 1 to 9% longer (500 rows of
 // 32000 x 1024 99 us for 91), with seven the forward up to 3%.
 template <Mode kMode>
@@ -72,7 +72,7 @@ struct Config {
     static constexpr int kSmemBytes = kBarOffset + 256 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 };
-constexpr int kLaunchRegs = 168, kOtherRegs = 40, kEpiRegs = 232;   // kLogp: registers a thread, at launch and after
+constexpr int kLaunchRegs = 168, kOtherRegs = 40, kEpiRegs = 232;   // kLogp, kGrad: registers a thread, at launch and after
 static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "the split must fit the launch's registers");
 
 // The tensor cores' fp32 sums lose more at each step than rounding to nearest would, and the
@@ -80,8 +80,12 @@ static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "the split
 // 32-bit torch 4.5e-7).  The forward takes the sums out of tensor memory every 896 products
 // at most and adds in registers: 6.9e-7.  Every 512 it is 3.6e-7, but 8% slower, since tensor
 // memory serves these reads at the products' expense.  Few rows, bound by HBM, every 256:
-// 1.1e-7, and 0 to 3% slower than every 512 with 2.1e-7.  The gradient's logits meet a rounding
-// of 2^-8 and are left as they are.
+// 1.1e-7, and 0 to 3% slower than every 512 with 2.1e-7.  The gradient's logits are summed in the
+// same steps, so that they have the bits of those that lse came from: a target's D is g (1 - p), and
+// an error that its logit has and lse has not is not relative to 1 - p.  Left in tensor memory for
+// all of 3584 products it was 6e-5 g, and dH of a row whose policy is sure to 1e-4 off by 1.5 times itself
+// (32-bit torch: 6e-3); now 5e-7 g and 1.5e-2.  Both gradients of 4096 rows take 1.7% longer (7.64 -> 7.77
+// ms), of one row 1%, dH alone 2 to 5%.
 constexpr int kSegment = 896 / kStep, kFewSegment = 256 / kStep;
 
 // ------------------------------------------------------------------ pairs of CTAs
@@ -391,6 +395,37 @@ __device__ __forceinline__ void stage16(uint8_t* out, int lane, int chunk, uint4
     *reinterpret_cast<uint4*>(out + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
 }
 
+// The logits of half of this thread's row: a tile's sums as they come out of tensor memory, `segment` of
+// its n steps at once, added up.  Where `wanted` is not set they are waited for and let go of
+// all the same.  False: a wait has run out.
+__device__ __forceinline__ bool take_logits(uint64_t (&x)[kHalf / 2], int n, int segment, bool wanted, uint32_t& tile,
+                                            uint32_t taddr, uint32_t tfull0, uint32_t empty_bar, const volatile int* abort) {
+    for (int k0 = 0; k0 < n; k0 += segment, ++tile) {
+        const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) return false;
+        tc_fence_after();
+        // 32 columns at a time: tensor memory serves these loads at the expense of
+        // the products' sums, and four at once cost 4096 rows 2% (2544 -> 2614 us)
+        if (wanted) {
+#pragma unroll
+            for (int j = 0; j < kHalf; j += 32) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(taddr + buf * kTile + j, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint64_t v = f32x2_pack(r[2 * e], r[2 * e + 1]);
+                    x[j / 2 + e] = k0 == 0 ? v : add2(x[j / 2 + e], v);
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane_id() == 0) pair_arrive(empty_bar + 8 * buf);
+    }
+    return true;
+}
+
 template <Mode kMode>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Config<kMode>::kThreads, 1)
 logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LogpParams p) {
@@ -464,7 +499,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
 
     Work<kMode> work(p);
     Unit u;
-    if (kForward && warp < 4) regs_dec<kOtherRegs>();
+    if (kMode != kBack && warp < 4) regs_dec<kOtherRegs>();
     if ((warp == 0 || warp == 3) && lane == 0) {
         // ---------------- loads: this CTA's rows of the first operand, and by another warp
         // of the second (an issued copy takes its thread some 100 cycles and the wait before
@@ -528,7 +563,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
             const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
             const uint64_t a0 = a_mn ? desc_mn(stages) : umma_desc_k128_sw128(stages);
             const uint64_t b0 = b_mn ? desc_mn(stages + 2 * kPiece) : umma_desc_k128_sw128(stages + 2 * kPiece);
-            const int segment = kForward ? p.segment : u.n;
+            const int segment = kMode != kBack ? p.segment : u.n;
             for (int k0 = 0; k0 < u.n && !*abort; k0 += segment) {
                 const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
                 ++tile;
@@ -565,39 +600,16 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
             const uint32_t empty_bar = map_to_rank(tempty0, 0);
             const float c = p.scale * kLog2e;
             const int64_t size = (int64_t)p.parts * p.rows_pad;
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + half * kHalf;
             uint32_t tile = 0;
-            bool ok = true;
-            while (ok && work.next(u)) {
+            while (work.next(u)) {
                 const int m = u.a + (int)rank * kHalf + row;             // the row among those that count
                 const int t = p.row_target[m] - u.b - half * kHalf, cols = (int)p.V - u.b - half * kHalf;
                 uint64_t x[kHalf / 2];
-                for (int k0 = 0; k0 < u.n; k0 += p.segment, ++tile) {
-                    const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
-                        if (lane == 0) gave_up(4);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile + half * kHalf;
-                    // 32 columns at a time: tensor memory serves these loads at the expense of
-                    // the products' sums, and four at once cost 4096 rows 2% (2544 -> 2614 us)
-#pragma unroll
-                    for (int j = 0; j < kHalf; j += 32) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(taddr + j, r);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint64_t v = f32x2_pack(r[2 * e], r[2 * e + 1]);
-                            x[j / 2 + e] = k0 == 0 ? v : add2(x[j / 2 + e], v);
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+                if (!take_logits(x, u.n, p.segment, true, tile, taddr, tfull0, empty_bar, abort)) {
+                    if (lane == 0) gave_up(4);
+                    break;
                 }
-                if (!ok) break;
                 Sums s;
                 if (cols > 0) {
                     if (p.entropy) sums_of<kHalf, true>(s, x, cols, c);
@@ -609,24 +621,88 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 if (p.entropy) part[2 * size] = s.dev;
             }
         }
-    } else if (!kForward && warp >= 4) {
+    } else if (kMode == kGrad && warp >= 4) {
         // ---------------- the tile's threads' part: half of a row a thread
-        const int q = warp & 3, half = (int)(warp - 4) >> 2, row = 32 * q + (int)lane;
+        if constexpr (kMode == kGrad) {
+            regs_inc<kEpiRegs>();
+            const int q = warp & 3, half = (int)(warp - 4) >> 2, row = 32 * q + (int)lane;
+            uint8_t* const out = smem + C::kOutOffset + (warp - 4) * C::kOuts * kOutBytes;
+            const uint32_t empty_bar = map_to_rank(tempty0, 0), taddr = tmem + ((uint32_t)(32 * q) << 16) + half * kHalf;
+            const float c = p.scale * kLog2e;
+            const bool entropy = p.ge != nullptr;
+            uint32_t tile = 0;
+            while (work.next(u)) {
+                const int y = u.a + (int)rank * kHalf + 32 * q, x0 = u.b + half * kHalf;   // the warp's first row and column
+                const int m = y + (int)lane;                             // the row among those that count
+                const int t = p.row_target[m] - p.first - x0;
+                const float g = p.row_g[m], ge = p.row_ge[m], l2 = p.row_lse[m] * kLog2e, plus = p.row_entropy[m];
+                // words of this half; none for a row past those that count (0 times what its
+                // logits come to would be NaN where W holds infinities)
+                const int cols = m >= work.live ? 0 : (int)min((int64_t)kTile, p.V - p.first - u.b) - half * kHalf;
+                // rows that nobody reads: past the last 64 of those that count
+                const bool wanted = y < (work.live + 63) / 64 * 64;
+                uint64_t x[kHalf / 2];
+                if (!take_logits(x, u.n, p.segment, wanted, tile, taddr, tfull0, empty_bar, abort)) {
+                    if (lane == 0) gave_up(4);
+                    break;
+                }
+                if (!wanted) continue;
+                const uint64_t cc = pk2(c, c), low = pk2(-l2, -l2), ng = pk2(-g, -g), ng2 = pk2(-ge, -ge);
+                const uint64_t ln2 = pk2(0.69314718f, 0.69314718f), pl = pk2(plus, plus);
+#pragma unroll
+                for (int j = 0; j < kHalf; j += 64) {
+                    float v[64];
+                    uint32_t packed[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const uint64_t a = fma2(x[j / 2 + e], cc, low), pr = ex2_2(a);
+                        uint64_t d = mul2(ng, pr);
+                        if (entropy) {
+                            // log p times a p of 0 is 0 where the logit is -inf too (a NaN is in d already)
+                            const float2 l = f32x2_unpack(a);
+                            d = fma2(mul2(ng2, pr), fma2(pk2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), ln2, pl), d);
+                        }
+                        const float2 two = f32x2_unpack(d);
+                        v[2 * e] = two.x, v[2 * e + 1] = two.y;
+                    }
+                    if (t >= j && t < j + 64) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) v[e] = fmaf(g, mask01(e, t - j), v[e]);
+                    }
+                    if (cols < j + 64) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (j + e >= cols) v[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) packed[e] = pack2(v[2 * e], v[2 * e + 1]);
+                    // the staging box, once the copy engine has read what was in it
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        stage16(out, lane, e, make_uint4(packed[4 * e], packed[4 * e + 1], packed[4 * e + 2], packed[4 * e + 3]));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&maps.d_out, smem_u32(out), x0 + j, y);
+                        bulk_commit();
+                    }
+                }
+            }
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
+        }
+    } else if (kMode == kBack && warp >= 4) {
+        // ---------------- the tile's threads' part: half of a row a thread
+        const int q = warp & 3, half = (int)(warp - 4) >> 2;
         uint8_t* const out = smem + C::kOutOffset + (warp - 4) * C::kOuts * kOutBytes;
         const uint32_t empty_bar = map_to_rank(tempty0, 0);
-        const float c = p.scale * kLog2e, f = kMode == kBack ? *p.largest * p.scale : 0.f;
+        const float f = kMode == kBack ? *p.largest * p.scale : 0.f;
         uint32_t tile = 0;
         while (work.next(u)) {
             const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
-            const int m = u.a + (int)rank * kHalf + row;                 // kGrad: the row among those that count
             const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile + half * kHalf;
-            // per row, before the wait
-            float g = 0.f, ge = 0.f, l2 = 0.f, plus = 0.f;
-            int t = -1;
-            if (kMode == kGrad) {
-                t = p.row_target[m] - p.first - u.b - half * kHalf;
-                g = p.row_g[m], ge = p.row_ge[m], l2 = p.row_lse[m] * kLog2e, plus = p.row_entropy[m];
-            }
             if (u.n > 0) {
                 ++tile;
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
@@ -642,14 +718,13 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 __syncwarp();
                 if (lane == 0) pair_arrive(empty_bar + 8 * buf);
             };
-            // the staging buffers, once the copy engine has read what was in them
+            // the staging box, once the copy engine has read what was in it
             auto clear = [&]() {
                 if (lane == 0) bulk_wait_read_all();
                 __syncwarp();
             };
             const int y = u.a + (int)rank * kHalf + 32 * q, x = u.b + half * kHalf;   // the warp's first row and column
-            // rows that nobody reads: past those that count, of D past the last 64 of them
-            if (u.kind != 2 && y >= (kMode == kGrad ? (work.live + 63) / 64 * 64 : work.live)) {
+            if (u.kind == 1 && y >= work.live) {             // rows that nobody reads: past those that count
                 release();
                 continue;
             }
@@ -663,7 +738,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                     for (int e = 0; e < 64; ++e) r[e] = 0;
                 }
             };
-            if (kMode == kBack && u.kind == 1) {
+            if (u.kind == 1) {
 #pragma unroll 1
                 for (int j = 0; j < kHalf; j += 64) {
                     uint32_t r[64];
@@ -686,45 +761,12 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 }
                 continue;
             }
-            // kGrad: words of this half; none for a row past those that count (0 times what its
-            // logits come to would be NaN where W holds infinities)
-            const int cols = kMode == kGrad && m >= work.live ? 0 : (int)min((int64_t)kTile, p.V - p.first - u.b) - half * kHalf;
-            const bool entropy = p.ge != nullptr;
 #pragma unroll 1
             for (int j = 0; j < kHalf; j += 64) {
                 uint32_t r[64], packed[32];
                 take(j, r);
-                if constexpr (kMode == kGrad) {
-                    const uint64_t cc = pk2(c, c), low = pk2(-l2, -l2), ng = pk2(-g, -g), ng2 = pk2(-ge, -ge);
-                    const uint64_t ln2 = pk2(0.69314718f, 0.69314718f), pl = pk2(plus, plus);
-                    float v[64];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const uint64_t a = fma2(f32x2_pack(r[2 * e], r[2 * e + 1]), cc, low), pr = ex2_2(a);
-                        uint64_t d = mul2(ng, pr);
-                        if (entropy) {
-                            // log p times a p of 0 is 0 where the logit is -inf too (a NaN is in d already)
-                            const float2 l = f32x2_unpack(a);
-                            d = fma2(mul2(ng2, pr), fma2(pk2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), ln2, pl), d);
-                        }
-                        const float2 two = f32x2_unpack(d);
-                        v[2 * e] = two.x, v[2 * e + 1] = two.y;
-                    }
-                    if (t >= j && t < j + 64) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) v[e] = fmaf(g, mask01(e, t - j), v[e]);
-                    }
-                    if (cols < j + 64) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            if (j + e >= cols) v[e] = 0.f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) packed[e] = pack2(v[2 * e], v[2 * e + 1]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) packed[e] = pack2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
-                }
+                for (int e = 0; e < 32; ++e) packed[e] = pack2(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
                 clear();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -732,8 +774,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (kMode == kGrad) tma_store_2d(&maps.d_out, smem_u32(out), x + j, y);
-                    else if (x + j < p.K && p.first + y < p.V) tma_store_2d(&maps.dw, smem_u32(out), x + j, p.first + y);
+                    if (x + j < p.K && p.first + y < p.V) tma_store_2d(&maps.dw, smem_u32(out), x + j, p.first + y);
                     bulk_commit();
                 }
             }
@@ -1251,7 +1292,7 @@ int pairs_of(void (*kernel)(Maps, LogpParams), int threads, int smem, int regs) 
     cudaFuncAttributes fa;
     // a split of registers (regs > 0) is made for just that many a thread at launch: with
     // others the threads' part could wait for registers for ever
-    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || (regs && fa.numRegs != regs) ||
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || (regs && up(fa.numRegs, 8) != regs) ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return 0;
     cudaLaunchConfig_t cfg = {};
@@ -1279,7 +1320,7 @@ int pairs_here() {
         using F = FewConfig<64>;
         using E = FewConfig<128>;
         n = std::min({pairs_of(logp_pair_kernel<kLogp>, A::kThreads, A::kSmemBytes, kLaunchRegs),
-                      pairs_of(logp_pair_kernel<kGrad>, G::kThreads, G::kSmemBytes, 0),
+                      pairs_of(logp_pair_kernel<kGrad>, G::kThreads, G::kSmemBytes, kLaunchRegs),
                       pairs_of(logp_pair_kernel<kBack>, B::kThreads, B::kSmemBytes, 0),
                       pairs_of(logp_few_kernel<64>, F::kThreads, F::kSmemBytes, 0),
                       pairs_of(logp_few_kernel<128>, E::kThreads, E::kSmemBytes, 0), num_sms() / 2});
@@ -1308,6 +1349,13 @@ cudaError_t launch_rows(const LogpParams& p, bool backward, cudaStream_t st) {
 
 // Row tiles whose hidden states take some 40 MB, a third of L2.
 int group_of(int64_t K) { return (int)std::max<int64_t>(1, (40ll << 20) / (kTile * K * 2)); }
+
+// Steps of the logits' products that are summed in tensor memory: the same in both directions,
+// so that the backward's logits have the bits of those that lse came from.
+int segment_of(const LogpParams& p) {
+    const int most = p.M <= kFewRows ? kFewSegment : kSegment, segments = (p.ksteps + most - 1) / most;
+    return (p.ksteps + segments - 1) / segments;
+}
 
 int pairs_or_default() {
     const int n = num_sms() / 2;
@@ -1342,8 +1390,7 @@ cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st) {
     p.err = device_error_word();
     p.ksteps = (int)((p.K + kStep - 1) / kStep), p.group = group_of(p.K);
     const bool few = p.M <= kFewRows;
-    const int most = few ? kFewSegment : kSegment, segments = (p.ksteps + most - 1) / most;
-    p.segment = (p.ksteps + segments - 1) / segments;
+    p.segment = segment_of(p);
     Maps maps{};
     if (!p.err || !load_map(&maps.w, p.W, p.V, p.K, p.ldw, kHalf)) return cudaErrorInvalidValue;
     if (few) {
@@ -1372,7 +1419,7 @@ cudaError_t launch_linear_logp_backward(LogpParams p, void* ws, cudaStream_t st)
     lay_backward(a, p, pairs_or_default());
     p.err = device_error_word();
     p.ksteps = (int)((p.K + kStep - 1) / kStep), p.group = group_of(p.K);
-    p.ktiles = (int)((p.K + kTile - 1) / kTile);
+    p.ktiles = (int)((p.K + kTile - 1) / kTile), p.segment = segment_of(p);
     Maps maps{};
     p.whole = p.K % 64 == 0;
     if (!p.err || !load_map(&maps.h, p.rows_h, p.M, p.pitch, p.pitch, kHalf) ||

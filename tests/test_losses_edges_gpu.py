@@ -53,3 +53,46 @@ def test_nan_passes_the_entropys_gradient(cuda_lib, M):
     ones = torch.ones(M, device="cuda")
     dH, _ = fb.fp8rl_linear_logp_backward(H, W, t, ones, g, entropy=ones, g_entropy=ge, want_dW=False)
     assert dH.isnan().all()
+
+
+def _sure(M, V, K, seed=0):
+    """Rows whose targets have from a thousandth to all but 1e-6 of the probability and less."""
+    H, W, t, g, ge = _head(M, V, K, seed)
+    w = W[t.long()].float()
+    lean = torch.linspace(4, 26, M, device="cuda")[:, None]
+    return (H.float() + lean * w / (w ** 2).sum(1, keepdim=True)).to(torch.bfloat16), W, t, g, ge
+
+
+@pytest.mark.parametrize("M", [100, 256])
+@pytest.mark.parametrize("K", [64, 1024, 3584, 16384])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradient_of_targets_that_are_all_but_sure(cuda_lib, M, K, entropy):
+    """A target's D is g (1 - p): what its logit and the log-sum are off by differently is not
+    relative to 1 - p.  In 32 bits that is the roundings of the log-sum and its product with
+    log2 e (2^-24 each), of the argument (2^-24) and the exponential (2^-22): below |lse| 2^-22 +
+    2^-21; with the entropy's gradient the same twice more (its logarithm, and the entropy's
+    own).  All else is relative: D's rounding and the result's (2^-8 each) and a
+    logit's error against the others', below 2^-12."""
+    H, W, t, g, ge = _sure(M, 2048, K)
+    x = H.double() @ W.double().T
+    lse = torch.logsumexp(x, dim=1)
+    logp = x - lse[:, None]
+    others = logp.exp().scatter_(1, t.long()[:, None], 0.0)
+    left = others.sum(1)                                   # 1 - p of the target
+    logp.scatter_(1, t.long()[:, None], torch.log1p(-left)[:, None])
+    p = logp.exp()
+    D = -g.double()[:, None] * others
+    D.scatter_(1, t.long()[:, None], (g.double() * left)[:, None])
+    e = ge.double()[:, None] if entropy else torch.zeros((M, 1), dtype=torch.float64, device="cuda")
+    ent = -(p * logp).sum(1, keepdim=True)
+    D = D - e * p * (logp + ent)
+    want = D @ W.double()
+    _, mine, mine_ent = fb.fp8rl_linear_logp(H, W, t, want_entropy=True)
+    kw = dict(entropy=mine_ent, g_entropy=ge) if entropy else {}
+    dH, _ = fb.fp8rl_linear_logp_backward(H, W, t, mine, g, want_dW=False, **kw)
+    most = W.double().norm(dim=1).max()
+    once = lse.abs() * 2.0 ** -22 + 2.0 ** -21
+    bound = most * ((g.double().abs() + 2 * e[:, 0].abs()) * once + D.abs().sum(1) * (2.0 ** -8 + 2.0 ** -12))
+    bound = bound * (1 + 2.0 ** -7) + want.norm(dim=1) * 2.0 ** -8
+    over = (dH.double() - want).norm(dim=1) / bound
+    assert left.min() < 1e-6 and left.max() > 0.1 and over.max() <= 1.0, over.max().item()
