@@ -87,6 +87,10 @@ static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "the split
 // (32-bit torch: 6e-3); now 5e-7 g and 1.5e-2.  Both gradients of 4096 rows take 1.7% longer (7.64 -> 7.77
 // ms), of one row 1%, dH alone 2 to 5%.
 constexpr int kSegment = 896 / kStep, kFewSegment = 256 / kStep;
+// kBack's sums run over rows (dW) or words (dH), and leave tensor memory once: 16 bits are
+// kept of them.  Past this many products a unit's sums are put together from parts of as many (see
+// the products): dW of 2^20 rows whose terms have one sign was off by 6.1e-3, its own rounding being 1.6e-3.
+constexpr int kBackSegment = 65536 / kStep;
 
 // ------------------------------------------------------------------ pairs of CTAs
 
@@ -554,8 +558,11 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 mbar_drain(full0 + 8 * (j % kStages), (j / kStages) & 1, kWaitLimitNs);
     } else if (warp == 1 && lane == 0 && rank == 0) {
         // ---------------- products, for both CTAs
+        // Tiles, or with kLogp and kGrad parts of one, take the two halves of tensor memory in turn.  With
+        // kBack a tile's first part stays in its half, and the others come into the other one,
+        // from where the threads add them to it.
         Ring<kStages> ring;
-        uint32_t tile = 0;
+        uint32_t tile = 0, used = 0;                     // used: of either half, the phase of its barriers
         const uint32_t stages = smem_u32(smem);
         while (!*abort && work.next(u)) {
             const bool a_mn = kMode == kBack && u.kind == 2, b_mn = kMode == kBack;
@@ -563,10 +570,11 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
             const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
             const uint64_t a0 = a_mn ? desc_mn(stages) : umma_desc_k128_sw128(stages);
             const uint64_t b0 = b_mn ? desc_mn(stages + 2 * kPiece) : umma_desc_k128_sw128(stages + 2 * kPiece);
-            const int segment = kMode != kBack ? p.segment : u.n;
+            const int segment = kMode != kBack ? p.segment : kBackSegment;
             for (int k0 = 0; k0 < u.n && !*abort; k0 += segment) {
-                const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
-                ++tile;
+                const uint32_t buf = (tile ^ (kMode == kBack && k0 > 0)) & 1, use = used >> buf & 1;
+                used ^= 1u << buf;
+                if (kMode != kBack) ++tile;
                 if (!mbar_wait_bounded(tempty0 + 8 * buf, use ^ 1, abort, kWaitLimitNs)) {
                     gave_up(3);
                     break;
@@ -591,6 +599,7 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
                 }
                 pair_commit(tfull0 + 8 * buf);
             }
+            if (kMode == kBack && u.n > 0) ++tile;
         }
     } else if (kForward && warp >= 4) {
         // ---------------- the tile's threads' part: half of a row a thread
@@ -699,25 +708,42 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
         uint8_t* const out = smem + C::kOutOffset + (warp - 4) * C::kOuts * kOutBytes;
         const uint32_t empty_bar = map_to_rank(tempty0, 0);
         const float f = kMode == kBack ? *p.largest * p.scale : 0.f;
-        uint32_t tile = 0;
+        uint32_t tile = 0, used = 0;
+        bool ok = true;
         while (work.next(u)) {
-            const uint32_t buf = tile & 1, use = (tile >> 1) & 1;
+            const uint32_t buf = tile & 1;
             const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + buf * kTile + half * kHalf;
-            if (u.n > 0) {
-                ++tile;
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * buf, use, abort, kWaitLimitNs))) {
-                    if (lane == 0) gave_up(4);
-                    break;
-                }
-                tc_fence_after();
-            } else if (u.kind == 1) {
-                continue;
-            }
-            auto release = [&]() {
+            if (u.n > 0) ++tile;
+            else if (u.kind == 1) continue;
+            auto release = [&](uint32_t b) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) pair_arrive(empty_bar + 8 * buf);
+                if (lane == 0) pair_arrive(empty_bar + 8 * b);
             };
+            for (int k0 = 0; k0 < u.n; k0 += kBackSegment) {
+                const uint32_t b = (buf ^ (k0 > 0)) & 1, use = used >> b & 1;
+                used ^= 1u << b;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(tfull0 + 8 * b, use, abort, kWaitLimitNs));
+                if (!ok) break;
+                tc_fence_after();
+                if (k0 == 0) continue;
+#pragma unroll 1
+                for (int j = 0; j < kHalf; j += 32) {
+                    uint32_t sum[32], more[32];
+                    tmem_ld_32x32b_x32(taddr + j, sum);
+                    tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + b * kTile + half * kHalf + j, more);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sum[e] = __float_as_uint(__uint_as_float(sum[e]) + __uint_as_float(more[e]));
+                    tmem_st_32x32b_x32(taddr + j, sum);
+                }
+                tmem_wait_st();
+                release(b);
+            }
+            if (!ok) {
+                if (lane == 0) gave_up(4);
+                break;
+            }
             // the staging box, once the copy engine has read what was in it
             auto clear = [&]() {
                 if (lane == 0) bulk_wait_read_all();
@@ -725,14 +751,14 @@ logp_pair_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Logp
             };
             const int y = u.a + (int)rank * kHalf + 32 * q, x = u.b + half * kHalf;   // the warp's first row and column
             if (u.kind == 1 && y >= work.live) {             // rows that nobody reads: past those that count
-                release();
+                release(buf);
                 continue;
             }
             // 64 columns from tensor memory, which is let go of after the last of them
             auto take = [&](int j, uint32_t (&r)[64]) {
                 if (u.n > 0) {
                     tmem_ld_64(taddr + j, r);
-                    if (j + 64 == kHalf) release();
+                    if (j + 64 == kHalf) release(buf);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 64; ++e) r[e] = 0;

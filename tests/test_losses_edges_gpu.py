@@ -96,3 +96,30 @@ def test_gradient_of_targets_that_are_all_but_sure(cuda_lib, M, K, entropy):
     bound = bound * (1 + 2.0 ** -7) + want.norm(dim=1) * 2.0 ** -8
     over = (dH.double() - want).norm(dim=1) / bound
     assert left.min() < 1e-6 and left.max() > 0.1 and over.max() <= 1.0, over.max().item()
+
+
+@pytest.mark.parametrize("M,V,K", [(1 << 20, 24, 8), (300001, 9, 72), (70000, 300, 64)])
+@pytest.mark.parametrize("sign", [False, True])
+def test_gradient_over_many_rows(cuda_lib, M, V, K, sign):
+    """dW sums over the rows that count.  With terms of one sign (sign) what a sum's steps lose
+    adds up, and D's roundings (2^-8 each) do not: what is left is the result's rounding (2^-8 of
+    itself, 2^-8 / sqrt 3 of its binade at most in the norm), some 2^-12 of the longest sum held in one
+    place (65536 rows), and, at one in a few hundred of the terms' size, D's roundings.  Without, D's
+    roundings are some 2^-8 / sqrt 3 as well: the two together 2^-8 sqrt(2 / 3), at most."""
+    H, W, t, g, _ = _head(M, V, K)
+    if sign:
+        H, W, g = H.abs(), W.abs(), g.abs()
+    t[::5] = -1
+    _, lse = fb.fp8rl_linear_logp(H, W, t)
+    _, dW = fb.fp8rl_linear_logp_backward(H, W, t, lse, g, want_dH=False)
+    want = torch.zeros((V, K), dtype=torch.float64, device="cuda")
+    for i in range(0, M, 1 << 16):
+        rows = torch.arange(i, min(M, i + (1 << 16)), device="cuda")
+        rows = rows[t[rows] >= 0]
+        h = H[rows].double()
+        D = -torch.softmax(h @ W.double().T, dim=1)
+        D.scatter_add_(1, t[rows].long()[:, None], torch.ones((len(rows), 1), dtype=torch.float64, device="cuda"))
+        want += (D * g[rows].double()[:, None]).T @ h
+    off = ((dW.double() - want).norm() / want.norm()).item()
+    assert off <= 2.0 ** -8 * ((1 / 3) ** 0.5 + 2.0 ** -4 if sign else (2 / 3) ** 0.5 + 2.0 ** -4), off
+    assert fb.fp8rl_check_device_error() == 0
