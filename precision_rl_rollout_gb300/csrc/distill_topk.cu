@@ -10,7 +10,9 @@
 // (no q_r without the rest), lse_r the log-sum outside.
 //
 // The loss is a difference of near terms once the student is close, so the logarithms
-// are taken to 1e-9 and meet in 64 bits; the sums of exponentials are fp32 relative to a maximum.  With the rest
+// are taken to 1e-9 and meet in 64 bits; the sums of exponentials are fp32 relative to a maximum.
+// Logits enter it relative to the sums' references alone, so neither logits that share a large
+// part nor rows of nothing but a mask's value lose anything to them.  With the rest
 // the pass over the logits sums the tokens outside, relative to their own maximum, and the
 // entries are added to that: a difference, or one maximum for both, would lose a small rest.
 // The gradient outside is exp(y_v - lse_r) (Q exp(lse_r - lse) - q_r), no factor above 1.
@@ -37,7 +39,7 @@ constexpr int kMostRanks = 16, kFlight = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eRest = 1.9259629911266175e-8f;   // log2(e) - kLog2e
 constexpr double kLn2 = 0.6931471805599453;
-constexpr float kLowest = -3.3895314e38f;              // the lowest finite bf16
+constexpr float kLowest = -3.40282347e38f;             // the lowest of fp32: nothing seen yet
 
 // Two fp32 to bf16, rounded to nearest even, in one instruction (one by one they are slow).
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -122,12 +124,21 @@ __device__ __forceinline__ double log64(double v) {
     return (double)((int)(b >> 23) - 127) * kLn2 + n.log + (double)(r + (series + lost / s));
 }
 
+// (a - b) - (c - d), off by a rounding of the result and some 2^-46 of either difference
+__device__ __forceinline__ float apart_of(float a, float b, float c, float d) {
+    const float s = a - b, u = c - d;
+    if (!(fabsf(s) < INFINITY)) return s - u;
+    const float sb = s - a, ub = u - c;
+    const float se = (a - (s - sb)) + (-b - sb), ue = (c - (u - ub)) + (-d - ub);
+    return (s - u) + (se - ue);
+}
+
 // exp(scale t - shift) as fp32, shift in two parts: what the argument's roundings lose, to
 // first order
 __device__ __forceinline__ float exp_less(float t, float scale, float shift, float shift_rest) {
     const float y = t * scale, rest = fmaf(t, scale, -y), hi = y - shift, back = hi - y;
-    const float lo = (y - (hi - back)) + (-shift - back) + (rest - shift_rest);
-    return hi < -104.f ? 0.f : expf(hi) * (1.f + lo);
+    const float lo = (y - (hi - back)) + (-shift - back) + (rest - shift_rest), arg = hi + lo;
+    return hi < -104.f ? 0.f : expf(arg) * (1.f + (lo - (arg - hi)));
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -152,16 +163,12 @@ struct Chunk;
 template <>
 struct Chunk<uint16_t> {
     static constexpr int N = 8;
-    static constexpr uint32_t kPad = 0xFF7FFF7Fu;              // kLowest twice
+    static constexpr uint32_t kPad = 0xFF80FF80u;              // -inf twice
     uint32_t w[4];
     __device__ __forceinline__ void drop(uint32_t those) {     // as if they were not there
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (those >> e & 1) w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | 0xFF7F0000u : (w[e >> 1] & 0xFFFF0000u) | 0xFF7Fu;
-    }
-    __device__ __forceinline__ void clamp() {                  // -inf to kLowest, NaN kept
-#pragma unroll
-        for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(kPad));
+            if (those >> e & 1) w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | 0xFF800000u : (w[e >> 1] & 0xFFFF0000u) | 0xFF80u;
     }
     __device__ __forceinline__ float most() const {
         uint32_t a, b;
@@ -182,20 +189,12 @@ struct Chunk<uint16_t> {
 template <>
 struct Chunk<float> {
     static constexpr int N = 4;
-    static constexpr uint32_t kPad = 0xFF7F0000u;              // kLowest
+    static constexpr uint32_t kPad = 0xFF800000u;              // -inf
     uint32_t w[4];
     __device__ __forceinline__ void drop(uint32_t those) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (those >> e & 1) w[e] = kPad;
-    }
-    __device__ __forceinline__ void clamp() {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v = __uint_as_float(w[i]);
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(kLowest));
-            w[i] = __float_as_uint(v);
-        }
     }
     __device__ __forceinline__ float most() const { return fmaxf(fmaxf(at(0), at(1)), fmaxf(at(2), at(3))); }
     __device__ __forceinline__ float at(int e) const { return __uint_as_float(w[e]); }
@@ -213,7 +212,7 @@ __device__ __forceinline__ uint4 load16(const void* p) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
-// kFlight loads of a thread, those past the end kLowest
+// kFlight loads of a thread, those past the end -inf
 template <int kThreads, typename T>
 __device__ __forceinline__ void fetch(Chunk<T> (&b)[kFlight], const T* X, int at, int end) {
 #pragma unroll
@@ -242,6 +241,7 @@ struct Entries {
     bool every = false;            // every token is named
     double total;      // sum of q
     float shift, shift_rest;       // log q_i = scale t_i - shift
+    float center;                  // some t_i for which that is near 0
 
     __device__ __forceinline__ Entries(uint8_t* smem, const DistillParams& p, int64_t m) {
         id = reinterpret_cast<int32_t*>(smem);
@@ -295,6 +295,10 @@ struct Entries {
             for (int i = lane; i < p.k; i += 32)
                 if (id[i] >= 0) top = fmaxf(top, q[i]);
             top = warp_max(top);
+            if (fabsf(top) > 16777216.f && fabsf(top) < INFINITY) {   // past what shift and its rest can hold
+                for (int i = lane; i < p.k; i += 32) q[i] -= top;
+                top = 0.f;
+            }
             const float y = top * p.scale, rest = fmaf(top, p.scale, -y);
             for (int i = lane; i < p.k; i += 32)
                 if (id[i] >= 0) s += exp_less(q[i], p.scale, y, rest);
@@ -303,6 +307,8 @@ struct Entries {
             const double all = top > -INFINITY ? (double)top * (double)p.scale + log64((double)s) : 0.0;
             shift = (float)all, shift_rest = (float)(all - (double)shift);
         }
+        center = shift / p.scale;
+        if (!(fabsf(center) < INFINITY)) center = 0.f;
         double sum = 0.0;
         for (int i = lane; i < p.k; i += 32) {
             const float t = q[i], v = id[i] >= 0 ? exp_less(t, p.scale, shift, shift_rest) : 0.f;
@@ -372,7 +378,6 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
                 const uint32_t those = N == 8 ? named[g] : named[g >> 1] >> (g & 1) * 4 & 15u;
                 if (those) now[u].drop(those);
             }
-            now[u].clamp();
             most = fmaxf(most, now[u].most());
         }
         if (most > s.top) s.sum *= f.exp(s.top - most), s.top = most;
@@ -384,15 +389,13 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
             for (int e = 0; e < N / 2; ++e) part[u & 1] = add2(part[u & 1], f.exp(now[u].pair(e), low));
             now[u] = next[u];
         }
-        // kLowest stands for what is not there: where nothing else is, its terms are not either
         const float2 sums = sm100::f32x2_unpack(add2(part[0], part[1]));
-        const float more = sums.x + sums.y;
-        if (s.top > kLowest || isnan(more)) s.sum += more;
+        s.sum += sums.x + sums.y;                        // (terms of -inf are 0: the reference is finite)
     }
     const int last = chunks * N + (int)threadIdx.x;      // logits past the last whole 16 bytes
     if (rank == ranks - 1 && last < p.V && !nobody && !(apart && (n.bits[last >> 5] >> (last & 31) & 1))) {
         const float x = value(X, last);
-        if (x != -INFINITY) s.add(x, 1.f, f);
+        s.add(x, 1.f, f);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -427,41 +430,45 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
         }
         return;
     }
-    // loss = scale sum_i q_i (t_i - x_i) + sum_i q_i (lse - shift) + q_r (log q_r - lse_r + lse):
-    // the differences in fp32, their weighted sums and the log-sums in 64 bits
-    double far = 0.0;
-    n.weigh(p, m, [&](int i, float t, float q) {
-        if (q > 0.f) far += (double)(q * (t - n.x[i]));
-    });
-    far = warp_sum(far);
-    const double scale = (double)p.scale, qr = n.rest(p);
+    // In the rest's reading the log-sum is relative to the outside's reference, so that the
+    // whole's sum is that of the two: where the student is near, what the log-sums
+    // share cancels in the loss, and what they do not would stay.  Entries so far
+    // above that it would overflow: relative to their own maximum, and the outside
+    // adds nothing.
     float top = s.top, sum = 0.f;
     bool above = false;
     if (apart) {
-        // The entries, each token once, relative to the outside's reference, so that the
-        // whole's sum is that of the two: where the student is near, what the log-sums
-        // share cancels in the loss, and what they do not would stay.  Entries so far
-        // above that it would overflow: relative to their own maximum, and the outside
-        // adds nothing.
         float most = kLowest;
         for (int i = lane; i < p.k; i += 32)
             if (n.id[i] >= 0) most = fmaxf(most, n.x[i]);
         most = warp_max(most);
         above = s.sum == 0.f || (most - s.top) * p.scale > 60.f;
         if (above) top = most;
-        for (int i = lane; i < p.k; i += 32)
+    }
+    // loss = scale sum_i q_i ((t_i - center) - (x_i - top)) + sum_i q_i (lse - (shift - scale center))
+    //        + q_r (log q_r - (lse_r - lse)),
+    // lse relative to top where it stands behind q_i: the differences in fp32, their weighted sums and the log-sums in 64 bits
+    double far = 0.0;
+    n.weigh(p, m, [&](int i, float t, float q) {
+        if (q > 0.f) far += (double)(q * apart_of(t, n.x[i], n.center, top));
+    });
+    far = warp_sum(far);
+    const double scale = (double)p.scale, qr = n.rest(p);
+    if (apart) {
+        for (int i = lane; i < p.k; i += 32)             // the entries, each token once
             if (n.id[i] >= 0 && n.x[i] != -INFINITY && n.first(i)) sum += f.exp(n.x[i] - top);
         sum = warp_sum(sum);
     }
     // three logarithms by three lanes: of the sums outside and of all, of the rest
     const double all = isnan(s.sum) ? NAN : (double)sum + (above ? 0.0 : (double)s.sum);
-    const double v = log64(lane == 0 ? (double)s.sum : lane == 1 ? all : qr) +
-                     (lane == 0 ? (double)s.top * scale : lane == 1 ? (double)top * scale : 0.0);
-    const double lse = __shfl_sync(0xffffffffu, v, 1), log_qr = __shfl_sync(0xffffffffu, v, 2);
+    const double l = log64(lane == 0 ? (double)s.sum : lane == 1 ? all : qr);
+    const double whole = __shfl_sync(0xffffffffu, l, 1), log_qr = __shfl_sync(0xffffffffu, l, 2);
+    const double v = l + (double)(lane == 0 ? s.top : top) * scale, lse = __shfl_sync(0xffffffffu, v, 1);
     if (lane == 0) {
         double loss = far * scale;
-        if (n.total != 0.0) loss += n.total * ((lse - (double)n.shift) - (double)n.shift_rest);
-        if (qr > 0.0) loss += qr * (log_qr - (v - lse));
+        if (n.total != 0.0) loss += n.total * (whole - (((double)n.shift - scale * (double)n.center) + (double)n.shift_rest));
+        // (above, the outside's reference is another one)
+        if (qr > 0.0) loss += qr * (log_qr - (above ? v - lse : l - whole));
         p.loss[m] = (float)loss, p.lse[m] = (float)lse;
         if (p.rest_lse) p.rest_lse[m] = (float)v;
     }
