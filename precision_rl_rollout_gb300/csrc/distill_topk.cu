@@ -474,11 +474,55 @@ distill_kernel(const __grid_constant__ DistillParams p, int ranks) {
     }
 }
 
+// A row whose log-sums are too far from 0 for fp32 to tell its probabilities by them (masks
+// alone, or logits that share a large part): one CTA takes its maxima and sums again, of all tokens
+// and of those outside the entries, in passes of its own.  Rare, and written to be short.
+constexpr float kFarLse = 65536.f;                       // 2^-8 of a probability, bf16's own rounding
+
+template <typename T, int kThreads>
+__device__ __noinline__ void far_row(const T* X, T* D, int64_t V, float scale, const uint32_t* bits, const int32_t* id,
+                                     const float* q, int k, float g, float Q, float qr) {
+    __shared__ float all[kThreads / 32], out[kThreads / 32];
+    const int warp = threadIdx.x >> 5;
+    auto named = [&](int64_t v) { return bits[v >> 5] >> (v & 31) & 1; };
+    float top = kLowest, top_out = kLowest, sum = 0.f, sum_out = 0.f;
+    for (int64_t v = threadIdx.x; v < V; v += kThreads) {
+        const float x = value(X, v);
+        top = fmaxf(top, x);
+        if (!named(v)) top_out = fmaxf(top_out, x);
+    }
+    all[warp] = warp_max(top), out[warp] = warp_max(top_out);
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, all[w]), top_out = fmaxf(top_out, out[w]);
+    __syncthreads();
+    for (int64_t v = threadIdx.x; v < V; v += kThreads) {
+        const float x = value(X, v);
+        sum += expf((x - top) * scale);
+        if (!named(v)) sum_out += expf((x - top_out) * scale);
+    }
+    all[warp] = warp_sum(sum), out[warp] = warp_sum(sum_out);
+    __syncthreads();
+    sum = sum_out = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w) sum += all[w], sum_out += out[w];
+    const float a = Q / sum, b = qr > 0.f && sum_out > 0.f ? qr / sum_out : 0.f;
+    for (int64_t v = threadIdx.x; v < V; v += kThreads) {  // a thread's own logits, which D may overwrite
+        const float x = value(X, v);
+        float less = 0.f;
+        if (named(v)) {
+            for (int j = 0; j < k; ++j) less += id[j] == v ? q[j] : 0.f;
+        } else if (b != 0.f) {
+            less = b * expf((x - top_out) * scale);
+        }
+        put(D, v, g * (a * expf((x - top) * scale) - less));
+    }
+}
+
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
 distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float factors[5];                         // outside: a exp(y - r); inside: g (Q exp(y - l) - q)
+    __shared__ float factors[6];                         // outside: a exp(y - r); inside: g (Q exp(y - l) - q); q_r
+    __shared__ bool far;
     constexpr int N = Chunk<T>::N;
     pdl_wait_then_release();
     const int rank = (int)(blockIdx.x % (unsigned)ranks);
@@ -501,11 +545,13 @@ distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
         if (threadIdx.x == 0) {
             const float qr = (float)n.rest(p), lse = p.lse[m], g = p.g[m] * p.scale, Q = (float)n.total + qr;
             float a = g * Q, r2 = lse * kLog2e;
+            far = fabsf(lse) > kFarLse;
             if (qr > 0.f && p.rest_lse[m] > -INFINITY) {
                 const float rest = p.rest_lse[m];
+                far |= fabsf(rest) > kFarLse;
                 a = g * (Q * expf(rest - lse) - qr), r2 = rest * kLog2e;
             }
-            factors[0] = a, factors[1] = r2, factors[2] = g, factors[3] = Q, factors[4] = lse * kLog2e;
+            factors[0] = a, factors[1] = r2, factors[2] = g, factors[3] = Q, factors[4] = lse * kLog2e, factors[5] = qr;
         }
     }
     __syncthreads();
@@ -513,6 +559,10 @@ distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
     if (!n.any) {                                        // zeros, whatever the row holds
         for (; at < end; at += kThreads) __stcs(reinterpret_cast<uint4*>(D + (int64_t)at * N), make_uint4(0, 0, 0, 0));
         for (int64_t v = (int64_t)end * N + threadIdx.x; v < hi; v += kThreads) put(D, v, 0.f);
+        return;
+    }
+    if (far) {                                           // one CTA's, since D may be X
+        if (rank == 0) far_row<T, kThreads>(X, D, p.V, p.scale, n.bits, n.id, n.q, p.k, g, Q, factors[5]);
         return;
     }
     auto grad = [&](float x) { return a * ex2(fmaf(x, c, -r2)); };

@@ -126,3 +126,58 @@ def test_what_logits_share_costs_nothing(cuda_lib, dtype, student, teacher):
         got = fb.fp8rl_distill_topk(X, ids, T, teacher_lse=tl, rest=tl is not None, scale=0.8)
         for name, a, b in zip(("loss", "lse", "rest_lse"), got, _exact(X, ids, T, tl, tl is not None, 0.8)[0]):
             ref.check(a, b, name)
+
+
+def _check_grad(dX, X, ids, T, teacher_lse, g, scale, keep):
+    rest = teacher_lse is not None
+    out, p, share, q, qr = _exact(X, ids, T, teacher_lse, rest, scale)
+    inside = torch.zeros_like(p).scatter_(1, ids.long(), q)
+    Q = q.sum(1, keepdim=True)
+    dq = Q * 2.0 ** -20 + 2.0 ** -24
+    second = qr[:, None] * share if rest else torch.zeros_like(p)
+    Q = Q + qr[:, None] if rest else Q
+    f = g.double()[:, None] * scale
+    value = f * (p * Q - inside - second)
+    # by log-sums in fp32 up to 65536, past it by sums anew
+    sums = [x[0].abs()[:, None] for x in (out[1:] if rest else out[1:2])]
+    r = 2.0 ** -18 + sum(torch.where(s > 65536, 0.0, s) for s in sums) * 2.0 ** -21
+    bound = f.abs() * ((p * Q + second) * 2 * r + inside * 2.0 ** -19 + (p + share if rest else p) * dq)
+    half = 2.0 ** -8 if X.dtype == torch.bfloat16 else 2.0 ** -24
+    bound = bound * (1 + 2.0 ** -7) + value.abs() * half * (1 + 2.0 ** -7) + 1e-38
+    ref.check(dX[keep], (value[keep], bound[keep]), "dX")
+
+
+@pytest.mark.parametrize("M,V,k", SIZES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [0.5, 0.7, 1.0])
+def test_gradients_of_masks(cuda_lib, M, V, k, dtype, scale):
+    """Rows whose log-sums are a mask's value: softmax and its gradient are those of equal logits; in place too."""
+    X, ids, T, lse, kind, g = _rows(M, V, k, dtype, scale)
+    s = fb.fp8rl_distill_topk(X, ids, T, scale=scale)[1]
+    dX = fb.fp8rl_distill_topk_backward(X, ids, T, s, g, scale=scale)
+    _check_grad(dX, X, ids, T, None, g, scale, kind >= 0)
+    _, s, r = fb.fp8rl_distill_topk(X, ids, T, teacher_lse=lse, rest=True, scale=scale)
+    dX = fb.fp8rl_distill_topk_backward(X, ids, T, s, g, teacher_lse=lse, rest_lse=r, scale=scale)
+    _check_grad(dX, X, ids, T, lse, g, scale, (kind != 3) & (kind != 4))
+    wide = torch.zeros((M, -(-V // 8) * 8), dtype=dtype, device="cuda")
+    Y = wide[:, :V]
+    Y.copy_(X)
+    fb.fp8rl_distill_topk_backward(Y, ids, T, s, g, teacher_lse=lse, rest_lse=r, scale=scale, dX=Y)
+    assert torch.equal(Y, dX) and (wide[:, V:] == 0).all()
+    assert fb.fp8rl_check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shift", [300.0, -2e4, 7e4, -3e6, 1e9])
+def test_gradients_of_shifted_logits(cuda_lib, dtype, shift):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X = (torch.randn((30, 3000), generator=g, device="cuda") * 2.5).to(dtype)
+    T, ids = (X.float() + torch.randn((30, 3000), generator=g, device="cuda")).topk(30, dim=1)
+    T, ids, gl = T.contiguous(), ids.int().contiguous(), torch.randn(30, generator=g, device="cuda")
+    X = (X.float() + shift).to(dtype)
+    lse = (torch.logsumexp(T.double() * 0.8, dim=1) + 0.3).float()
+    _, s = fb.fp8rl_distill_topk(X, ids, T, scale=0.8)
+    _check_grad(fb.fp8rl_distill_topk_backward(X, ids, T, s, gl, scale=0.8), X, ids, T, None, gl, 0.8, gl == gl)
+    _, s, r = fb.fp8rl_distill_topk(X, ids, T, teacher_lse=lse, rest=True, scale=0.8)
+    dX = fb.fp8rl_distill_topk_backward(X, ids, T, s, gl, teacher_lse=lse, rest_lse=r, scale=0.8)
+    _check_grad(dX, X, ids, T, lse, gl, 0.8, gl == gl)
