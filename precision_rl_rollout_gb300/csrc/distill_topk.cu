@@ -556,7 +556,7 @@ distill_grad_kernel(const __grid_constant__ DistillParams p, int ranks) {
     }
     __syncthreads();
     const float c = p.scale * kLog2e, a = factors[0], r2 = factors[1], g = factors[2], Q = factors[3], l2 = factors[4];
-    if (!n.any) {                                        // zeros, whatever the row holds
+    if (!n.any || Q == 0.f) {                            // no entries, or none of any weight: zeros, whatever the row holds
         for (; at < end; at += kThreads) __stcs(reinterpret_cast<uint4*>(D + (int64_t)at * N), make_uint4(0, 0, 0, 0));
         for (int64_t v = (int64_t)end * N + threadIdx.x; v < hi; v += kThreads) put(D, v, 0.f);
         return;

@@ -181,3 +181,17 @@ def test_gradients_of_shifted_logits(cuda_lib, dtype, shift):
     _, s, r = fb.fp8rl_distill_topk(X, ids, T, teacher_lse=lse, rest=True, scale=0.8)
     dX = fb.fp8rl_distill_topk_backward(X, ids, T, s, gl, teacher_lse=lse, rest_lse=r, scale=0.8)
     _check_grad(dX, X, ids, T, lse, gl, 0.8, gl == gl)
+
+
+@pytest.mark.parametrize("M,V", [(4, 1003), (4, 152064), (700, 2000)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("whole", [False, True])
+def test_a_teacher_without_weight(cuda_lib, M, V, dtype, whole):
+    """Entries of -inf alone: the loss is 0, and so is the gradient, whatever the row's logits are."""
+    X, ids, T, lse, kind, g = _rows(M, V, 5, dtype, 1.0)
+    T[:] = float("-inf")
+    X[::4], X[1::4, 3], X[2::4] = float("-inf"), float("nan"), torch.finfo(dtype).min
+    tl = lse if whole else None
+    loss, s = fb.fp8rl_distill_topk(X, ids, T, teacher_lse=tl)
+    dX = fb.fp8rl_distill_topk_backward(X, ids, T, s, g, teacher_lse=tl)
+    assert (loss == 0).all() and (dX == 0).all()
