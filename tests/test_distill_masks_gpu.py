@@ -195,3 +195,32 @@ def test_a_teacher_without_weight(cuda_lib, M, V, dtype, whole):
     loss, s = fb.fp8rl_distill_topk(X, ids, T, teacher_lse=tl)
     dX = fb.fp8rl_distill_topk_backward(X, ids, T, s, g, teacher_lse=tl)
     assert (loss == 0).all() and (dX == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V,k", [(20000, 64), (152064, 64), (300, 300)])
+@pytest.mark.parametrize("rest", [False, True])
+def test_a_small_divergence(cuda_lib, dtype, V, k, rest):
+    """A student 0.004 from its teacher in every logit: losses of some 1e-6 to 1e-5, the differences of terms near
+    1.  With both cut to the entries a relative error of the student's sum is the loss's absolute one:
+    arguments (2^-24 of some 5, weighted) and exponentials (2^-22) that all err alike, 2^-20 at most.  With the
+    rest, errors that all of the sums share cancel: half of that."""
+    g = torch.Generator(device="cuda").manual_seed(V + k)
+    M = 64
+    X = (torch.randn((M, -(-V // 8) * 8), generator=g, device="cuda") * 2.5).to(dtype)[:, :V]
+    teacher = X.float() + 0.004 * torch.randn((M, V), generator=g, device="cuda")
+    T, ids = teacher.topk(k, dim=1)
+    if not rest:
+        X.masked_fill_(~torch.zeros((M, V), dtype=torch.bool, device="cuda").scatter_(1, ids, True), float("-inf"))
+    T, ids = T.contiguous(), ids.int().contiguous()
+    lse = torch.logsumexp(teacher.double(), dim=1).float() if rest else None
+    if rest and k == V:
+        # a teacher's log-sum in fp32 leaves a rest of up to 2^-22 to a class that no token is in; as in losses_ref it is none
+        want = ref.distill(X, ids, T, lse, True)[0][0]
+    else:
+        want = _exact(X, ids, T, lse, rest, 1.0)[0][0][0]
+    loss = fb.fp8rl_distill_topk(X, ids, T, teacher_lse=lse, rest=rest)[0].double()
+    bound = 2.0 ** -20 if not rest else 2.0 ** -21
+    if k < V or not rest:
+        assert want.median() > 2 * bound                   # so that a loss of 0 would not pass
+    assert ((loss - want).abs() <= bound + want.abs() * 2.0 ** -20).all(), (loss - want).abs().max().item()

@@ -123,3 +123,19 @@ def test_gradient_over_many_rows(cuda_lib, M, V, K, sign):
     off = ((dW.double() - want).norm() / want.norm()).item()
     assert off <= 2.0 ** -8 * ((1 / 3) ** 0.5 + 2.0 ** -4 if sign else (2 / 3) ** 0.5 + 2.0 ** -4), off
     assert fb.fp8rl_check_device_error() == 0
+
+
+@pytest.mark.parametrize("M", [40, 100, 300])
+@pytest.mark.parametrize("K", [3584, 5120, 16392])
+def test_log_probabilities_keep_their_precision(cuda_lib, M, K):
+    """In the norm.  A sum of n products in tensor memory goes through n / 16 steps, each of which drops
+    up to one unit of 2^-23 of what is summed so far, on average half of it: with sums that grow
+    evenly n / 64 units of 2^-23 of the whole; n is 256 at most up to 128 rows, 896 at
+    most above.  Two more units for the rest of a log-probability, twice all for an entropy, where the
+    errors meet weights p log p.  (A sum of all 3584 products would be off by 56 units.)"""
+    H, W, t, _, _ = _head(M, 3000, K)
+    out = fb.fp8rl_linear_logp(H, W, t, want_entropy=True)
+    units = (256 if M <= 128 else 896) / 64 + 2
+    for name, a, (value, _), times in zip(("logp", "lse", "entropy"), out, ref.linear_logp(H, W, t), (1, 1, 2)):
+        off = ((a.double() - value).norm() / value.norm()).item()
+        assert off <= times * units * 2.0 ** -23, (name, off / 2.0 ** -23)
