@@ -1333,24 +1333,27 @@ int pairs_of(void (*kernel)(Maps, LogpParams), int threads, int smem, int regs) 
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
-// Pairs of CTAs that run at once on the current device; 0: the kernels do not run there.
-int pairs_here() {
-    static std::atomic<int> known[64] = {};
+template <Mode kMode>
+int pairs_of_tiles() {
+    return pairs_of(logp_pair_kernel<kMode>, Config<kMode>::kThreads, Config<kMode>::kSmemBytes, kMode == kBack ? 0 : kLaunchRegs);
+}
+template <int kN>
+int pairs_of_few() {
+    return pairs_of(logp_few_kernel<kN>, FewConfig<kN>::kThreads, FewConfig<kN>::kSmemBytes, 0);
+}
+// Pairs of CTAs of one kind of call that run at once on the current device; 0: its kernels do
+// not run there (which says nothing of the others').
+enum Call { kFewCall, kForwardCall, kBackwardCall };
+int pairs_here(Call call) {
+    static std::atomic<int> known[3][64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int n = known[dev].load(std::memory_order_relaxed);
+    int n = known[call][dev].load(std::memory_order_relaxed);
     if (!n) {
-        using A = Config<kLogp>;
-        using G = Config<kGrad>;
-        using B = Config<kBack>;
-        using F = FewConfig<64>;
-        using E = FewConfig<128>;
-        n = std::min({pairs_of(logp_pair_kernel<kLogp>, A::kThreads, A::kSmemBytes, kLaunchRegs),
-                      pairs_of(logp_pair_kernel<kGrad>, G::kThreads, G::kSmemBytes, kLaunchRegs),
-                      pairs_of(logp_pair_kernel<kBack>, B::kThreads, B::kSmemBytes, 0),
-                      pairs_of(logp_few_kernel<64>, F::kThreads, F::kSmemBytes, 0),
-                      pairs_of(logp_few_kernel<128>, E::kThreads, E::kSmemBytes, 0), num_sms() / 2});
-        known[dev].store(n, std::memory_order_relaxed);
+        n = call == kFewCall ? std::min(pairs_of_few<64>(), pairs_of_few<128>())
+            : call == kForwardCall ? pairs_of_tiles<kLogp>() : std::min(pairs_of_tiles<kGrad>(), pairs_of_tiles<kBack>());
+        n = std::min(n, num_sms() / 2);
+        known[call][dev].store(n, std::memory_order_relaxed);
     }
     return n;
 }
@@ -1409,13 +1412,13 @@ size_t linear_logp_backward_workspace_bytes(int64_t M, int64_t V, int64_t K) {
 }
 
 cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st) {
-    const int pairs = pairs_here();
+    const bool few = p.M <= kFewRows;
+    const int pairs = pairs_here(few ? kFewCall : kForwardCall);
     if (!pairs || pairs > pairs_or_default()) return cudaErrorInvalidDeviceFunction;
     Arena a{static_cast<uint8_t*>(ws)};
     lay_forward(a, p, pairs_or_default());
     p.err = device_error_word();
     p.ksteps = (int)((p.K + kStep - 1) / kStep), p.group = group_of(p.K);
-    const bool few = p.M <= kFewRows;
     p.segment = segment_of(p);
     Maps maps{};
     if (!p.err || !load_map(&maps.w, p.W, p.V, p.K, p.ldw, kHalf)) return cudaErrorInvalidValue;
@@ -1439,7 +1442,7 @@ cudaError_t launch_linear_logp(LogpParams p, void* ws, cudaStream_t st) {
 
 cudaError_t launch_linear_logp_backward(LogpParams p, void* ws, cudaStream_t st) {
     if (p.M == 0) return p.dW ? cudaMemsetAsync(p.dW, 0, (size_t)(p.V * p.K) * 2, st) : cudaSuccess;
-    const int pairs = pairs_here();
+    const int pairs = pairs_here(kBackwardCall);
     if (!pairs) return cudaErrorInvalidDeviceFunction;
     Arena a{static_cast<uint8_t*>(ws)};
     lay_backward(a, p, pairs_or_default());
