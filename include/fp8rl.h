@@ -548,7 +548,8 @@ int fp8rl_spec_verify(const void* P, int64_t p_seq, int64_t p_step, const void* 
  *   lse[m] = log sum_v exp x_v,  logp[m] = x_t - lse[m],
  *   entropy[m] = - sum_v p_v log p_v,  p = exp(x - lse).
  * A row whose target is outside [0, V) (a prompt's, padding) does not count: its
- * results are 0, whatever the row of H holds (NaN included).
+ * results are 0, whatever the row of H holds (NaN included).  A logit of -inf is a probability of 0,
+ * here and in the gradient (of the entropy too).
  * bf16 products, summed in fp32; maxima, sums and results in fp32.  Deterministic.
  * H  bf16 [M][ldh], W bf16 [V][ldw], ld >= K, ld % 8 == 0, 16-byte aligned.
  * K  a multiple of 8 (FP8RL_ERR_SHAPE); V any number.
@@ -606,9 +607,10 @@ int fp8rl_linear_logp_backward(const uint16_t* H, int64_t ldh, const uint16_t* W
  *   loss[m] += q_r (log q_r - log p_r),  rest_lse[m] = log sum_outside exp y.
  * An entry whose token is outside [0, V) is none; a token named twice counts with both
  * entries.  A row without entries does not count: loss, lse and rest_lse are 0, whatever
- * its logits are.  Logits of -inf are probabilities of 0.
+ * its logits are.  Logits of -inf are probabilities of 0; any finite value is a logit, a mask's lowest one
+ * too (a row of nothing else is one of equal logits).
  * The loss is put together in 64 bits from fp32 sums, so that it keeps some 1e-7
- * absolute where the student is close.  Deterministic.
+ * absolute where the student is close, whatever part its logits share.  Deterministic.
  * X  fp32 or bf16 (dtype) [M][ldx], ldx >= V, 16-byte aligned, rows of a multiple of
  *    16 bytes.  indices int32 [M][k], T fp32 [M][k], teacher_lse fp32 [M] or NULL;
  *    loss, lse fp32 [M], rest_lse fp32 [M] or NULL.
@@ -624,8 +626,10 @@ int fp8rl_distill_topk(const void* X, int64_t ldx, int dtype, const int32_t* ind
 /* Its gradient: with Q = sum q_i (+ q_r),
  *   dX[m][v] = g_loss[m] * scale * (Q p_v - q_v)                            inside,
  *   dX[m][v] = g_loss[m] * scale * (Q p_v - q_r exp(y_v - rest_lse[m]))     outside
- * (without rest_lse no second term there); 0 in rows that do not count.  Computed in
- * fp32, rounded once to X's type.  lse, rest_lse: the forward's.
+ * (without rest_lse no second term there); 0 in rows that do not count, and where no entry has any weight.
+ * Computed in fp32, rounded once to X's type.  lse, rest_lse: the forward's.  fp32 holds them to 2^-24 of
+ * themselves, and so exp(y - lse); in a row where one of them is past 65536 in size (masks alone, logits
+ * that share that much) the sums are taken again, by one CTA that reads the row three times.
  * dX [M][lddx] of X's type, lddx >= V, aligned as X; it may be X with the same row
  * pitch, any other overlap is undefined.  Everything else as for fp8rl_distill_topk. */
 int fp8rl_distill_topk_backward(const void* X, int64_t ldx, int dtype, const int32_t* indices, const float* T,

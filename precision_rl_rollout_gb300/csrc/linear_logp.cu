@@ -25,12 +25,12 @@
 // memory, and each sum of dH is added to once a launch, so results do not depend on order.
 //
 // What bounds it: the tensor cores, and for long calls the power they draw.  4096 rows of
-// 152064 words x 3584: 2.30 ms alone, 1.94 PFLOP/s (the measured peak is 1.92), 2.55 in a loop, where
-// the clocks fall to 1.6 GHz and a library's product of this size makes 1.83; 8192 rows, 5734 of
-// them counted, 3.8.  Both gradients of 4096 rows 7.7 ms (1.73 PFLOP/s), of 2731 among 4096 5.4, 4.75
-// alone.  Profiled on 2048 rows of 65536: kLogp 0.51 ms, kGrad 0.54, kBack 1.03, the tensor pipe 86 to
-// 89% active.  One row 161 us, 48 rows x 5120 228: 6.8 TB/s.  With few rows the gradient is
-// bound by writing dW (a stream of writes alone makes 4 TB/s): one row 0.55 ms.
+// 152064 words x 3584: 2.30 ms alone, 1.94 PFLOP/s (the measured peak is 1.92), 2.6 in a loop, where
+// the clocks fall to 1.55 GHz and a library's product of this size makes 1.8; 8192 rows, 5734 of
+// them counted, 3.9.  Both gradients of 4096 rows 7.8 to 8.0 ms (1.67 to 1.72 PFLOP/s), of 2731 among 4096
+// 5.5, 4.86 alone.  Profiled on 2048 rows of 65536: kLogp 0.50 ms, kGrad 0.52, kBack 1.01, the tensor pipe
+// 84 to 89% active.  One row 161 to 164 us, 48 rows x 5120 228 to 233: the copy rate.  With few rows
+// the gradient is bound by writing dW (a stream of writes alone makes 4 TB/s): one row 0.55 ms.
 #include <math.h>
 
 #include <algorithm>
