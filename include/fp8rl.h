@@ -575,7 +575,7 @@ int fp8rl_linear_logp(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t
  * products as bf16 relative to the largest |g| and |e| of the call (2^-8 of itself);
  * the sums are fp32 and the gradients are rounded once to bf16.  Deterministic.
  * A target's D is g (1 - p): relative to itself down to a 1 - p of some 1e-3, below that off by the fp32
- * roundings of p, |lse| 2^-22 g at most, where lse is this library's for the same H, W, targets and scale (the
+ * roundings of p, (|lse| + 2) 2^-22 g at most, where lse is this library's for the same H, W, targets and scale (the
  * logits are then the same bits).
  * lse, entropy fp32 [M]: the forward's (entropy only with g_entropy).
  * g_logp fp32 [M]; g_entropy fp32 [M] or NULL.
